@@ -1,0 +1,164 @@
+// The handle behind the C ABI and the helpers every entry point uses: error
+// reporting, the stream-ordered workspace, TMA tensor-map encoding and the
+// device guard.  Shared by the translation units that implement the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <string>
+
+#include "../../include/gemm.h"
+
+struct gemm_ctx {
+    int device = 0;
+    int sm_count = 0;
+    int *d_status = nullptr;
+    void *ws = nullptr;
+    size_t ws_bytes = 0;
+    // Recorded on the caller's stream after every call that used the
+    // workspace; growth waits on it (stream-ordered) before the old buffer
+    // is released.
+    cudaEvent_t ws_event = nullptr;
+    bool ws_event_recorded = false;
+    std::string last_error;
+    std::string last_path;
+    int64_t launches = 0;
+    int force_repack = 0;
+    uint64_t timeout_ns = 4000000000ull;
+    int simt_group_m = 0;
+    int tc_group_m = 0;
+    int max_ctas = 0;
+    int simt_config = 0;  // 0: chosen per shape; else configuration index + 1
+    int elementwise = 0;  // FP32 unaligned operands: element-wise producer (1) or re-pack (0)
+    size_t ws_limit = 0;  // 0: none; else the workspace never grows beyond this many bytes
+    int split_k = 0;      // 0: chosen per shape; 1: never; n > 1: n K slices (FP32 path)
+    int stream_k = 0;     // FP32 tail: 0 chosen per shape, 1 slices, 2 stream-K
+    int simt_small = 0;   // FP32 small-problem kernel: 0 chosen per shape, 1 never, 2 always
+    int tc_cluster = 3;   // tensor-core mode: 1 one CTA per tile, 3 pair MMA
+    int tc_tma_store = 1; // tensor-core epilogue writes C with TMA stores when C allows it
+    int tc_slices = 0;    // pair MMA: K slices per ring stage (0: library's choice)
+    int ragged_tile = 0;  // grouped and 4-bit products: 0 chosen, else 1000 * CTAs + rows (GEMM_OPT_GROUPED_TILE)
+    int debug_drop = 0;   // test hook (GEMM_OPT_DEBUG_DROP_LOAD)
+    // gemm_run_host pipeline: copy streams and events (created on first use)
+    cudaStream_t copy_in = nullptr, copy_out = nullptr;
+    cudaEvent_t ev_start = nullptr, ev_done = nullptr;
+    cudaEvent_t ev_a[16] = {}, ev_b[8] = {}, ev_c[16 * 8] = {};  // row panels, column panels, blocks
+};
+
+namespace dg {
+
+constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;  // kernels index tiles with int
+constexpr int64_t kMaxLd = int64_t{1} << 36;
+
+// cuTensorMapEncodeTiled, looked up once by gemm_create.
+extern PFN_cuTensorMapEncodeTiled_v12000 g_encode;
+
+inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+inline int fail(gemm_ctx *h, int code, const std::string &msg)
+{
+    if (h) h->last_error = msg;
+    return code;
+}
+
+inline int cuda_fail(gemm_ctx *h, cudaError_t e, const char *what)
+{
+    cudaGetLastError();  // clear a non-sticky error so the next call starts clean
+    return fail(h, GEMM_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+inline bool tma_ready(const void *p, int64_t ld, int es)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
+}
+
+// Grows the workspace in stream order on `stream`: the stream first waits
+// for the last call that used the old buffer, then frees it and allocates
+// the new one from the device's stream-ordered pool.  Nothing waits on the
+// host, and work the caller queued on other streams is not held up.
+inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
+{
+    if (need <= h->ws_bytes) return GEMM_OK;
+    if (h->ws_limit > 0 && need > h->ws_limit) {
+        char msg[160];
+        std::snprintf(msg, sizeof msg, "workspace of %zu bytes needed, limit %zu (GEMM_OPT_WORKSPACE_LIMIT)", need,
+                      h->ws_limit);
+        return fail(h, GEMM_ERR_NOMEM, msg);
+    }
+    size_t grow = h->ws_bytes + h->ws_bytes / 2;
+    size_t bytes = need > grow ? need : grow;
+    bytes = (bytes + (size_t{2} << 20) - 1) & ~((size_t{2} << 20) - 1);
+    if (h->ws_limit > 0 && bytes > h->ws_limit) bytes = need;  // stay within the limit
+    cudaError_t e = cudaSuccess;
+    if (h->ws) {
+        // Earlier calls (on this or another stream) may still read the old buffer.
+        if (h->ws_event_recorded) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
+        if (e == cudaSuccess) e = cudaFreeAsync(h->ws, stream);
+        if (e != cudaSuccess) return cuda_fail(h, e, "stream-ordered release of the old workspace");
+    }
+    h->ws = nullptr;
+    h->ws_bytes = 0;
+    h->ws_event_recorded = false;
+    e = cudaMallocAsync(&h->ws, bytes, stream);
+    if (e != cudaSuccess) {
+        h->ws = nullptr;
+        cudaGetLastError();
+        return fail(h, GEMM_ERR_NOMEM, std::string("workspace cudaMallocAsync: ") + cudaGetErrorString(e));
+    }
+    h->ws_bytes = bytes;
+    return GEMM_OK;
+}
+
+// After a call whose launches read or write the workspace: its end on
+// `stream` is what the next growth waits for.
+inline int note_workspace_use(gemm_ctx *h, cudaStream_t stream)
+{
+    cudaError_t e = cudaEventRecord(h->ws_event, stream);
+    if (e != cudaSuccess) return cuda_fail(h, e, "workspace-use event");
+    h->ws_event_recorded = true;
+    return GEMM_OK;
+}
+
+inline int encode_2d(gemm_ctx *h, CUtensorMap *map, int es, const void *base, int64_t inner,
+              int64_t outer, int64_t ld, int box_inner, int box_outer,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapDataType dt = es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUresult r = g_encode(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char msg[160];
+        std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (%d) for a %lld x %lld operand",
+                      static_cast<int>(r), static_cast<long long>(outer), static_cast<long long>(inner));
+        return fail(h, GEMM_ERR_CUDA, msg);
+    }
+    return GEMM_OK;
+}
+
+class DeviceGuard {
+  public:
+    explicit DeviceGuard(int dev)
+    {
+        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
+        if (prev_ != dev) cudaSetDevice(dev);
+    }
+    ~DeviceGuard()
+    {
+        int cur = -1;
+        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
+    }
+
+  private:
+    int prev_ = -1;
+};
+
+}  // namespace dg

@@ -1,0 +1,751 @@
+// Grouped tensor-core products for sm_103a (tcgen05.mma): C_g = A_g · B_g over
+// ragged row groups, C_g = A_g^T · B_g over ragged contractions, with BF16,
+// TF32 or microscaled 4-bit (E2M1 x E8M0) operands and FP32 accumulation.
+//
+// Orientation.  The MMA's M side (128 tensor-memory lanes per CTA) carries the
+// index that runs along a row of C ("P", the columns of C), its N side the
+// rows of C ("Q").  N can be any multiple of 16 (32 for a CTA pair), so a
+// group's last tile shrinks the instruction to the rows that are left, and few
+// rows per expert do not pay for 128-row tiles.  In the epilogue a warp holds
+// 32 neighbouring columns of C and walks the rows: every store instruction
+// writes 32 neighbouring elements, at any pitch and alignment of C, and rows
+// of the next group are never touched.
+//
+// Roles, as in the dense tensor-core kernels: warp 0 TMA producer, warp 1 MMA
+// issuer, warps 2-5 epilogue (two accumulators, so the epilogue of a tile
+// overlaps the next tile's main loop); for 4-bit operands warps 6-9 move the
+// block scales from shared memory into tensor memory.
+//
+// Groups.  The offsets stay on the device.  Every CTA builds the running count
+// of its launch's tiles per group in shared memory (one load and a block scan,
+// beside the barrier set-up) and finds the group of tile u by bisection.
+// Offsets that decrease or leave [0, rows] are reported in the status word and
+// the launch computes nothing; reads of the offsets are clamped all the same,
+// so no tile reads or writes outside the operands.
+//
+// Ragged contraction.  The k rows of a group start anywhere and end inside a
+// stage.  Both operands are read through a view {column, y < BK, z} whose y
+// and z both step one row: the box at (y0 = n - BK, z = r) is zero for y < 0,
+// whatever lies there, and holds rows r .. r + n - 1 after that.  The order of
+// the k rows within a stage is the same for both operands, so zeros may come
+// first.
+#include <algorithm>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "ragged.h"
+
+namespace dg {
+namespace {
+
+constexpr int BP = kRaggedP;
+constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
+constexpr int MAX_STAGES = 12;
+constexpr int TMEM_COLS = 512;
+constexpr int NUM_BARS = 3 * MAX_STAGES + 2 + 2 + 2 + 1;
+// Accumulators at tensor-memory columns 0 and ACC1; for 4-bit operands the
+// scales of two stages live at SF_COL, so the second accumulator moves down
+// and, for tiles of more than ACC1_MX rows, overlaps the first (see epilogue).
+constexpr int ACC1 = 256, ACC1_MX = 208;
+constexpr int SF_COL = 464, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
+constexpr int SMEM_MAX = 227 * 1024;
+
+struct Params {
+    const long long *offsets;
+    int groups, rows, P, Q, K;
+    int bn, tiles_p, tiles_q, group_q;
+    int stages, stage_bytes, q_bytes, sf_bytes, table_bytes;
+    void *C;
+    long long ldc, stride_c;
+    int out_bf16, p_chunks, q_chunks;
+    int *status;
+    unsigned long long timeout_ns;
+    int debug_drop;
+};
+
+__device__ __forceinline__ void group_range(const Params &p, int g, int &lo, int &hi)
+{
+    if (p.offsets == nullptr) {
+        lo = 0;
+        hi = p.rows;
+        return;
+    }
+    const long long a = __ldg(p.offsets + g), b = __ldg(p.offsets + g + 1), r = p.rows;
+    const long long l = a < 0 ? 0 : a > r ? r : a;
+    const long long e = b < l ? l : b > r ? r : b;
+    lo = static_cast<int>(l);
+    hi = static_cast<int>(e);
+}
+
+// Whether the offsets rise within [0, rows].  All threads call it; block 0
+// reports offsets that do not, and every block then runs no tile.
+template <int NT>
+__device__ bool offsets_ok(const Params &p)
+{
+    int bad = 0;
+    if (p.offsets != nullptr)
+        for (int g = threadIdx.x; g < p.groups; g += NT) {
+            const long long a = __ldg(p.offsets + g), b = __ldg(p.offsets + g + 1);
+            if (a < 0 || b < a || b > p.rows) bad = 1;
+        }
+    bad = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kStatusBadOffsets);
+    return bad == 0;
+}
+
+// table[g] = tiles of the groups before g; table[groups] = all tiles.
+template <int NT>
+__device__ void build_table(const Params &p, int *table, int *warp_sum)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.groups + NT - 1) / NT;
+    const int g0 = min(p.groups, tid * per), g1 = min(p.groups, g0 + per);
+    int sum = 0;
+    for (int g = g0; g < g1; ++g) {
+        int lo, hi;
+        group_range(p, g, lo, hi);
+        sum += (hi - lo + p.bn - 1) / p.bn * p.tiles_p;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int g = g0; g < g1; ++g) {
+        int lo, hi;
+        group_range(p, g, lo, hi);
+        table[g] = before;
+        before += (hi - lo + p.bn - 1) / p.bn * p.tiles_p;
+    }
+    if (g0 < p.groups && g1 == p.groups) table[p.groups] = before;
+}
+
+struct Tile {
+    int g;    // group
+    int lo;   // its first row
+    int cnt;  // its rows
+    int pb;   // tile column index (units of ctas * 128 columns of C)
+    int q0;   // first row of the tile within the group's C
+    int qn;   // rows of the tile
+    int kt;   // ring stages of the contraction
+};
+
+template <int BK, bool RAGGED_K>
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u)
+{
+    Tile t;
+    int r, tiles_q;
+    if (RAGGED_K) {
+        const int per = p.tiles_p * p.tiles_q;
+        t.g = u / per;
+        r = u - t.g * per;
+        tiles_q = p.tiles_q;
+    } else {
+        int a = 0, b = p.groups;  // table[a] <= u < table[b]
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (table[m] <= u)
+                a = m;
+            else
+                b = m;
+        }
+        t.g = a;
+        r = u - table[a];
+        tiles_q = 0;
+    }
+    int hi;
+    group_range(p, t.g, t.lo, hi);
+    t.cnt = hi - t.lo;
+    if (!RAGGED_K) tiles_q = (t.cnt + p.bn - 1) / p.bn;
+    const int per = p.group_q * p.tiles_p;
+    const int grp = r / per;
+    const int first = grp * p.group_q;
+    const int gq = min(tiles_q - first, p.group_q);
+    const int rr = r - grp * per;
+    t.q0 = (first + rr % gq) * p.bn;
+    t.pb = rr / gq;
+    t.qn = min(p.bn, (RAGGED_K ? p.Q : t.cnt) - t.q0);
+    t.kt = ((RAGGED_K ? t.cnt : p.K) + BK - 1) / BK;
+    return t;
+}
+
+// MMA N of a tile: the rows that are left, in the granularity the instruction
+// takes.  The MN-major operand of a ragged contraction keeps whole chunks.
+template <int CG, bool RAGGED_K>
+__device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
+{
+    constexpr int G = CG == 2 ? 32 : 16;
+    return RAGGED_K ? p.bn : (t.qn + G - 1) / G * G;
+}
+
+template <int KIND, int CG, bool P_MN, bool RAGGED_K>
+__global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                  const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ, const Params p)
+{
+    constexpr bool MX = KIND == kRaggedMx4;
+    constexpr int THREADS = MX ? 320 : 192;
+    constexpr int ES = KIND == kRaggedBf16 ? 2 : 4;                 // bytes an element (not for 4-bit)
+    constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
+    constexpr int K_STEPS = 4;                                      // MMA instructions of a stage, 32 bytes of K each
+    constexpr int CHUNK = 128 / ES;                                 // MN-major: elements of a 128-byte row
+    constexpr int BOX_BYTES = BK * 128;                             // MN-major: one chunk of a stage
+    constexpr uint32_t MN_LAYOUT = ES == 2 ? kLayoutSw128 : kLayoutSw128Atom32;
+    constexpr uint32_t MN_SBO = ES == 2 ? 1024u : 512u;
+    constexpr bool Q_MN = RAGGED_K;
+    // Instruction descriptor without N.  BF16 / TF32: FP32 accumulator, operand
+    // formats, major-ness; 4-bit: E2M1 formats and E8M0 scales (the scale ids
+    // are added per instruction).
+    constexpr uint32_t FMT = KIND == kRaggedBf16 ? 1u : 2u;
+    constexpr uint32_t IDESC = MX ? (1u << 7) | (1u << 10) | (1u << 23) | (static_cast<uint32_t>((CG * BP) >> 4) << 24)
+                                  : (1u << 4) | (FMT << 7) | (FMT << 10) | ((P_MN ? 1u : 0u) << 15) |
+                                        ((Q_MN ? 1u : 0u) << 16) | (static_cast<uint32_t>((CG * BP) >> 4) << 24);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw_addr + pad;
+    const uint32_t ring = static_cast<uint32_t>(p.stages * p.stage_bytes);
+    int *table = reinterpret_cast<int *>(smem + ring);
+    const uint32_t bars = sbase + ring + p.table_bytes;
+    const uint32_t full_bar = bars;                       // [stages], used in the even CTA
+    const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;  // [stages]
+    const uint32_t sfull_bar = empty_bar + 8 * MAX_STAGES;  // [stages], scale bytes, each CTA its own
+    const uint32_t tfull_bar = sfull_bar + 8 * MAX_STAGES;  // [2]
+    const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
+    const uint32_t sready_bar = tempty_bar + 16;            // [2], scales in tensor memory, used in the even CTA
+    const uint32_t drain_bar = sready_bar + 16;
+    uint8_t *tail = smem + ring + p.table_bytes + NUM_BARS * 8;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
+    int *warp_sum = reinterpret_cast<int *>(tail + 16);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int first_unit = blockIdx.x / CG;
+    const int unit_step = gridDim.x / CG;
+    const int acc1 = MX ? ACC1_MX : ACC1;
+    const bool overlap = MX && p.bn > ACC1_MX;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full_bar + 8 * s, 1);
+            mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
+            mbar_init(sfull_bar + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar + 8 * b, 1);
+            mbar_init(tempty_bar + 8 * b, 4 * CG);  // the epilogue warps
+            mbar_init(sready_bar + 8 * b, 4 * CG);  // the scale warps
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        const uint32_t slot = smem_addr(const_cast<uint32_t *>(tmem_slot));
+        if (CG == 2) {
+            tmem_alloc_pair(slot, TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(slot, TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    const bool groups_ok = offsets_ok<THREADS>(p);
+    if (!RAGGED_K) build_table<THREADS>(p, table, warp_sum);
+    tc_fence_before_sync();
+    if (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const int num_units = !groups_ok ? 0 : RAGGED_K ? p.groups * p.tiles_p * p.tiles_q : table[p.groups];
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            if (RAGGED_K || p.K > 0) {
+                tma_prefetch_desc(&tmP);
+                tma_prefetch_desc(&tmQ);
+                if (MX) {
+                    tma_prefetch_desc(&tmSP);
+                    tma_prefetch_desc(&tmSQ);
+                }
+            }
+            const int q_cta = p.bn / CG;  // rows of Q this CTA stages
+            const uint32_t tx = static_cast<uint32_t>(CG * (P_BYTES + p.q_bytes));
+            const uint32_t sf_tx = static_cast<uint32_t>((BP + p.bn) * 16);
+            uint32_t it = 0, s = 0, ph = 0;
+            bool ok = true;
+            for (int u = first_unit; ok && u < num_units; u += unit_step) {
+                const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+                const int p0 = (t.pb * CG + static_cast<int>(rank)) * BP;
+                const int n_cta = mma_n<CG, RAGGED_K>(p, t) / CG;
+                const int qx = (RAGGED_K ? 0 : t.lo) + t.q0 + static_cast<int>(rank) * n_cta;
+                for (int kt = 0; kt < t.kt; ++kt, ++it) {
+                    if (!mbar_wait(empty_bar + 8 * s, ph ^ 1u, abort_flag, p.status, kWaitProducerEmpty,
+                                   p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb_local = full_bar + 8 * s;
+                    const uint32_t fb = CG == 2 ? mapa_shared(fb_local, 0) : fb_local;
+                    const uint32_t p_st = sbase + s * p.stage_bytes;
+                    const uint32_t q_st = p_st + P_BYTES;
+                    const uint32_t sfb = sfull_bar + 8 * s;
+                    if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                    if (MX) mbar_arrive_expect_tx(sfb, sf_tx);
+                    if (++s == static_cast<uint32_t>(p.stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (p.debug_drop && blockIdx.x == 0 && it == 0) continue;  // bytes that never come
+                    if (RAGGED_K) {
+                        // zeros, then rows [z, z + n) of the group
+                        const int n = min(BK, t.cnt - kt * BK);
+                        const int y = n - BK, z = t.lo + kt * BK;
+                        if (p.p_chunks) {
+                            if (CG == 2)
+                                tma_load_4d_pair(p_st, &tmP, fb, 0, y, z, p0 / CHUNK);
+                            else
+                                tma_load_4d(p_st, &tmP, fb, 0, y, z, p0 / CHUNK);
+                        } else {
+                            for (int j = 0; j < BP / CHUNK; ++j) {
+                                if (CG == 2)
+                                    tma_load_3d_pair(p_st + j * BOX_BYTES, &tmP, fb, p0 + j * CHUNK, y, z);
+                                else
+                                    tma_load_3d(p_st + j * BOX_BYTES, &tmP, fb, p0 + j * CHUNK, y, z);
+                            }
+                        }
+                        if (p.q_chunks) {
+                            if (CG == 2)
+                                tma_load_4d_pair(q_st, &tmQ, fb, 0, y, z, qx / CHUNK);
+                            else
+                                tma_load_4d(q_st, &tmQ, fb, 0, y, z, qx / CHUNK);
+                        } else {
+                            for (int j = 0; j < q_cta / CHUNK; ++j) {
+                                if (CG == 2)
+                                    tma_load_3d_pair(q_st + j * BOX_BYTES, &tmQ, fb, qx + j * CHUNK, y, z);
+                                else
+                                    tma_load_3d(q_st + j * BOX_BYTES, &tmQ, fb, qx + j * CHUNK, y, z);
+                            }
+                        }
+                        continue;
+                    }
+                    const int kx = MX ? kt * 128 : kt * BK;  // 4-bit views count bytes
+                    if (P_MN) {
+                        if (p.p_chunks) {
+                            if (CG == 2)
+                                tma_load_4d_pair(p_st, &tmP, fb, 0, kx, p0 / CHUNK, t.g);
+                            else
+                                tma_load_4d(p_st, &tmP, fb, 0, kx, p0 / CHUNK, t.g);
+                        } else {
+                            for (int j = 0; j < BP / CHUNK; ++j) {
+                                if (CG == 2)
+                                    tma_load_3d_pair(p_st + j * BOX_BYTES, &tmP, fb, p0 + j * CHUNK, kx, t.g);
+                                else
+                                    tma_load_3d(p_st + j * BOX_BYTES, &tmP, fb, p0 + j * CHUNK, kx, t.g);
+                            }
+                        }
+                    } else if (CG == 2) {
+                        tma_load_3d_pair(p_st, &tmP, fb, kx, p0, t.g);
+                    } else {
+                        tma_load_3d(p_st, &tmP, fb, kx, p0, t.g);
+                    }
+                    if (CG == 2)
+                        tma_load_2d_pair(q_st, &tmQ, fb, kx, qx);
+                    else
+                        tma_load_2d(q_st, &tmQ, fb, kx, qx);
+                    if (MX) {
+                        // 16 scale bytes cover two stages; each stage reads its half
+                        const uint32_t sf = q_st + p.q_bytes;
+                        tma_load_3d(sf, &tmSP, sfb, (kt >> 1) * 16, p0, t.g);
+                        tma_load_2d(sf + BP * 16, &tmSQ, sfb, (kt >> 1) * 16, t.lo + t.q0);
+                    }
+                }
+            }
+            // Stages issued last, oldest first: (s, ph) is the next one.
+            const uint32_t n = min(it, static_cast<uint32_t>(p.stages));
+            uint32_t ds = s >= n ? s - n : s + p.stages - n;
+            uint32_t dph = s >= n ? ph : ph ^ 1u;
+            for (uint32_t i = 0; i < n; ++i) {
+                int dummy = 0;
+                if (ok) {
+                    // every release must have landed before shared memory goes away
+                    mbar_wait(empty_bar + 8 * ds, dph, abort_flag, p.status, kWaitDrain, p.timeout_ns);
+                } else {
+                    // after an abort: leave no copy in flight (the even CTA's
+                    // barriers count both CTAs' operand bytes)
+                    if (leader) mbar_wait(full_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+                    if (MX) mbar_wait(sfull_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+                }
+                if (++ds == static_cast<uint32_t>(p.stages)) {
+                    ds = 0;
+                    dph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer (even CTA)
+        if (leader) {
+            uint32_t it = 0, s = 0, ph = 0, acc_it = 0;
+            bool ok = true, issued = false;
+            for (int u = first_unit; ok && u < num_units; u += unit_step, ++acc_it) {
+                const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+                const uint32_t abuf = acc_it & 1u;
+                const uint32_t idesc = IDESC | (static_cast<uint32_t>(mma_n<CG, RAGGED_K>(p, t) >> 3) << 17);
+                // The accumulator is free: tile i - 2 drained, or, where the two
+                // overlap, the columns tile i - 1 shares with this one.
+                const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
+                const uint32_t eph = overlap ? (acc_it & 1u) ^ 1u : ((acc_it >> 1) & 1u) ^ 1u;
+                if (!mbar_wait_warp(eb, eph, abort_flag, p.status, kWaitMmaTmemEmpty, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + abuf * acc1;
+                for (int kt = 0; kt < t.kt; ++kt, ++it) {
+                    if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t slot = it & 1u;
+                    if (MX && !mbar_wait_warp(sready_bar + 8 * slot, (it >> 1) & 1u, abort_flag, p.status,
+                                              kWaitMmaScale, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t p_st = sbase + s * p.stage_bytes;
+                    const uint32_t q_st = p_st + P_BYTES;
+                    uint64_t pd[K_STEPS], qd[K_STEPS];
+#pragma unroll
+                    for (int kk = 0; kk < K_STEPS; ++kk) {
+                        const int kr = kk * (32 / ES) * 128;  // MN-major: K rows of an instruction
+                        pd[kk] = P_MN ? smem_desc(p_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
+                                      : smem_desc(p_st + kk * 32, 16, 1024, kLayoutSw128);
+                        qd[kk] = Q_MN ? smem_desc(q_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
+                                      : smem_desc(q_st + kk * 32, 16, 1024, kLayoutSw128);
+                    }
+                    const uint32_t acc0 = kt > 0 ? 1u : 0u;
+                    const uint32_t sf = tmem_base + SF_COL + slot * SF_COLS;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < K_STEPS; ++kk) {
+                            const uint32_t acc = kk > 0 ? 1u : acc0;
+                            if (MX) {
+                                const uint32_t id = (kk & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
+                                const uint32_t sp = sf + (kk >> 1) * 4, sq = sf + 8 + (kk >> 1) * 8;
+                                if (CG == 2)
+                                    tc_mma_mx4_pair(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
+                                else
+                                    tc_mma_mx4(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
+                            } else if (KIND == kRaggedBf16) {
+                                if (CG == 2)
+                                    tc_mma_f16_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                else
+                                    tc_mma_f16(d_tmem, pd[kk], qd[kk], idesc, acc);
+                            } else {
+                                if (CG == 2)
+                                    tc_mma_tf32_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                else
+                                    tc_mma_tf32(d_tmem, pd[kk], qd[kk], idesc, acc);
+                            }
+                        }
+                        if (CG == 2)
+                            tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
+                        else
+                            tc_commit(empty_bar + 8 * s);
+                    }
+                    __syncwarp();
+                    issued = true;
+                    if (++s == static_cast<uint32_t>(p.stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if (CG == 2)
+                        tc_commit_pair_multicast(tfull_bar + 8 * abuf, 0x3);
+                    else
+                        tc_commit(tfull_bar + 8 * abuf);
+                }
+                __syncwarp();
+            }
+            if (!ok && issued && lane == 0) {
+                // Let every MMA already issued finish before TMEM is freed.
+                if (CG == 2)
+                    tc_commit_pair_multicast(drain_bar, 0x1);
+                else
+                    tc_commit(drain_bar);
+                int dummy = 0;
+                mbar_wait(drain_bar, 0, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+            }
+        }
+    } else if (warp < 6) {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        uint32_t acc_it = 0;
+        for (int u = first_unit; u < num_units; u += unit_step, ++acc_it) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+            const uint32_t abuf = acc_it & 1u;
+            if (!mbar_wait_warp(tfull_bar + 8 * abuf, (acc_it >> 1) & 1u, abort_flag, p.status, kWaitEpiTmemFull,
+                                p.timeout_ns))
+                break;
+            tc_fence_after_sync();
+            const int col = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32 + lane;
+            const long long first_row =
+                RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
+            const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * acc1;
+            // Chunks of 32 columns.  Overlapping accumulators share columns
+            // 208..255: the first one's chunks 6 and 7 and the second one's
+            // chunks 0 and 1, which go first and are handed over at once.
+            const int chunks = (t.qn + 31) / 32;
+            const int release = overlap ? 1 : chunks - 1;  // position after which the MMA warp may go on
+            const int order = overlap ? 8 : chunks;
+#pragma unroll 1
+            for (int i = 0; i < order; ++i) {
+                const int c = overlap && abuf == 0 ? (i + 6) & 7 : i;
+                uint32_t v[32];
+                if (c < chunks) {
+                    if (t.kt > 0) {
+                        tmem_load_32cols(t_row + c * 32, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;  // the empty sum
+                    }
+                }
+                if (i == release) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
+                        if (leader)
+                            mbar_arrive(eb);
+                        else
+                            mbar_arrive_cluster(mapa_shared(eb, 0));
+                    }
+                }
+                if (c < chunks && col < p.P) {
+                    const int n = t.qn - c * 32;
+                    const long long at = base + static_cast<long long>(c * 32) * p.ldc;
+                    if (p.out_bf16) {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                            if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
+                    } else {
+                        float *out = static_cast<float *>(p.C) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                            if (j < n) *out = __uint_as_float(v[j]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (MX) {
+        // ------------------------------------------------------ block scales
+        // Every scale warp writes all rows' words to its own lane quarter:
+        // lane l holds rows l, l + 32, ... of P and of Q.
+        const int q = warp & 3;
+        uint32_t it = 0, s = 0, ph = 0, ps = 0, pph = 0;  // ps: the stage two back
+        bool ok = true;
+        for (int u = first_unit; ok && u < num_units; u += unit_step) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+            for (int kt = 0; kt < t.kt; ++kt, ++it) {
+                if (!mbar_wait_warp(sfull_bar + 8 * s, ph, abort_flag, p.status, kWaitScaleSmem, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sf = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes + lane * 16 + (kt & 1) * 8;
+                uint32_t wp[8], wq[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(wp[i]), "=r"(wp[4 + i]) : "r"(sf + i * 512));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    wq[i] = wq[8 + i] = 0u;
+                    if (i * 32 < p.bn)
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(wq[i]), "=r"(wq[8 + i])
+                                     : "r"(sf + BP * 16 + i * 512));
+                }
+                // the MMAs that read this slot two stages ago are done
+                if (it >= 2) {
+                    if (!mbar_wait_warp(empty_bar + 8 * ps, pph, abort_flag, p.status, kWaitScaleTmem,
+                                        p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (++ps == static_cast<uint32_t>(p.stages)) {
+                        ps = 0;
+                        pph ^= 1u;
+                    }
+                    tc_fence_after_sync();
+                }
+                const uint32_t slot = it & 1u;
+                const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + SF_COL + slot * SF_COLS;
+                tmem_store_8cols(dst, wp);
+                tmem_store_16cols(dst + 8, wq);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(sready_bar + 8 * slot);
+                    else
+                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * slot, 0));
+                }
+                if (++s == static_cast<uint32_t>(p.stages)) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncwarp();
+    if (CG == 2)
+        cluster_sync();  // no CTA leaves while its peer may still target its shared memory
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if (CG == 2)
+            tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+template <int KIND, int CG, bool P_MN, bool RK>
+cudaError_t set_attrs()
+{
+    return cudaFuncSetAttribute(ragged_kernel<KIND, CG, P_MN, RK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SMEM_MAX);
+}
+
+template <int KIND, int CG, bool P_MN, bool RK>
+cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const CUtensorMap &tmSP,
+                       const CUtensorMap &tmSQ, const Params &p, int grid, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(KIND == kRaggedMx4 ? 320 : 192);
+    cfg.dynamicSmemBytes = SMEM_MAX;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK>, tmP, tmQ, tmSP, tmSQ, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_ragged()
+{
+    cudaError_t (*fns[])() = {
+        set_attrs<kRaggedBf16, 1, false, false>, set_attrs<kRaggedBf16, 2, false, false>,
+        set_attrs<kRaggedBf16, 1, true, false>,  set_attrs<kRaggedBf16, 2, true, false>,
+        set_attrs<kRaggedBf16, 1, true, true>,   set_attrs<kRaggedBf16, 2, true, true>,
+        set_attrs<kRaggedTf32, 1, false, false>, set_attrs<kRaggedTf32, 2, false, false>,
+        set_attrs<kRaggedTf32, 1, true, false>,  set_attrs<kRaggedTf32, 2, true, false>,
+        set_attrs<kRaggedTf32, 1, true, true>,   set_attrs<kRaggedTf32, 2, true, true>,
+        set_attrs<kRaggedMx4, 1, false, false>,  set_attrs<kRaggedMx4, 2, false, false>};
+    cudaError_t e = cudaSuccess;
+    for (auto f : fns)
+        if (e == cudaSuccess) e = f();
+    return e;
+}
+
+bool ragged_tile_ok(int ctas, int bn)
+{
+    return (ctas == 1 || ctas == 2) && (bn == 32 || bn == 64 || bn == 128 || bn == 256);
+}
+
+RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K)
+{
+    (void)kind;
+    (void)K;
+    RaggedTile t;
+    const int64_t avg = ragged_k ? Q : (rows + groups - 1) / groups;
+    t.bn = avg > 128 ? 256 : avg > 64 ? 128 : avg > 32 ? 64 : 32;
+    t.ctas = avg > 64 && P > BP ? 2 : 1;
+    if (ragged_k && t.bn < 128) t.bn = 128;
+    return t;
+}
+
+cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
+                          const CUtensorMap &tmQ, const CUtensorMap &tmSP, const CUtensorMap &tmSQ,
+                          const RaggedArgs &a, int sm_count, int max_ctas)
+{
+    Params p;
+    p.offsets = reinterpret_cast<const long long *>(a.offsets);
+    p.groups = a.groups;
+    p.rows = a.rows;
+    p.P = a.P;
+    p.Q = a.Q;
+    p.K = a.K;
+    p.bn = t.bn;
+    p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
+    p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
+    p.q_bytes = t.bn / t.ctas * 128;
+    p.sf_bytes = kind == kRaggedMx4 ? (BP + t.bn) * 16 : 0;
+    p.stage_bytes = (P_BYTES + p.q_bytes + p.sf_bytes + 1023) / 1024 * 1024;
+    p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
+    const int fixed = 1024 + p.table_bytes + NUM_BARS * 8 + 16 + 64;
+    p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);
+    p.C = a.C;
+    p.ldc = a.ldc;
+    p.stride_c = a.stride_c;
+    p.out_bf16 = a.out_bf16;
+    p.p_chunks = a.p_chunks;
+    p.q_chunks = a.q_chunks;
+    p.status = a.status;
+    p.timeout_ns = a.timeout_ns;
+    p.debug_drop = a.debug_drop;
+    p.group_q = 16;
+    // Upper bound of the tiles (the offsets are on the device).
+    const int64_t tiles_q = ragged_k ? int64_t{p.tiles_q} * a.groups
+                                     : (int64_t{a.rows} + t.bn - 1) / t.bn + std::min(a.groups, a.rows) - 1;
+    const int64_t units = std::max<int64_t>(1, tiles_q * p.tiles_p);
+    const int64_t slots = std::max(1, (max_ctas > 0 ? std::min(max_ctas, sm_count) : sm_count) / t.ctas);
+    const int grid = static_cast<int>(t.ctas * std::min(units, slots));
+    const bool pair = t.ctas == 2;
+#define DG_RAGGED(KIND, PMN, RK)                                                                  \
+    return pair ? launch_one<KIND, 2, PMN, RK>(tmP, tmQ, tmSP, tmSQ, p, grid, a.stream)           \
+                : launch_one<KIND, 1, PMN, RK>(tmP, tmQ, tmSP, tmSQ, p, grid, a.stream)
+    if (kind == kRaggedMx4) DG_RAGGED(kRaggedMx4, false, false);
+    if (kind == kRaggedTf32) {
+        if (ragged_k) DG_RAGGED(kRaggedTf32, true, true);
+        if (p_mn) DG_RAGGED(kRaggedTf32, true, false);
+        DG_RAGGED(kRaggedTf32, false, false);
+    }
+    if (ragged_k) DG_RAGGED(kRaggedBf16, true, true);
+    if (p_mn) DG_RAGGED(kRaggedBf16, true, false);
+    DG_RAGGED(kRaggedBf16, false, false);
+#undef DG_RAGGED
+}
+
+}  // namespace dg

@@ -5,10 +5,12 @@ The functions ``gemm_create``, ``gemm_run``, ``gemm_run_host``,
 ``gemm_set_option``, ``gemm_last_error_string``, ``gemm_status_string``,
 ``gemm_last_path``, ``gemm_launch_count``, ``gemm_version``,
 ``gemm_run_noalloc``, ``gemm_ladder_run``, ``gemm_ladder_name``,
-``gemm_peak_fma_run`` and ``gemm_peak_mma_run`` take and return the same
+``gemm_peak_fma_run`` and ``gemm_peak_mma_run``, and those of
+include/gemm_grouped.h and include/gemm_mx4.h, take and return the same
 plain values as their C counterparts (pointers as ints; the FLOP-count
 out-parameter of the peak calls is returned as a second value).  ``Gemm``
-wraps a handle for torch tensors.  Every GEMM step runs in the library's CUDA
+wraps a handle for torch tensors; ``Mx4`` holds a matrix in microscaled 4-bit
+floating point.  Every GEMM step runs in the library's CUDA
 kernels; there is no other code path, and calling anything here without the
 built library raises ``GemmLibraryMissing``.
 """
@@ -50,6 +52,10 @@ GEMM_OPT_WORKSPACE_LIMIT = 12
 GEMM_OPT_TC_STAGE_SLICES = 13
 GEMM_OPT_STREAM_K = 14
 GEMM_OPT_SIMT_SMALL = 15
+GEMM_OPT_GROUPED_TILE = 16
+
+GEMM_GROUPED_MAX_GROUPS = 4096
+GEMM_MX4_BLOCK = 32
 
 DTYPES = {"f32": GEMM_F32, "tf32": GEMM_TF32, "bf16": GEMM_BF16, "f32x3": GEMM_F32_3XTF32}
 LAYOUTS = {"row": GEMM_B_ROW_MAJOR, "col": GEMM_B_COL_MAJOR}
@@ -105,6 +111,27 @@ def load_library():
             "gemm_peak_fma_run": ([ci, i64, vp, vp, ctypes.POINTER(ctypes.c_double)], ci),
             "gemm_peak_mma_run": ([ci, i64, vp, ctypes.c_uint64, vp, ctypes.POINTER(ctypes.c_double)], ci),
         }
+        grouped = [ci, i64, i64, i64, i64, vp, vp, i64, vp, i64, i64, vp, i64, ci, ci]
+        wgrad = [i64, i64, i64, i64, vp, vp, i64, vp, i64, vp, i64, i64, ci, ci]
+        quantise = [ci, i64, i64, i64, vp, i64, i64, ci, vp, i64, vp, i64]
+        dequantise = [i64, i64, vp, i64, vp, i64, vp, i64, ci]
+        mx4 = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci]
+        mx4_grouped = [i64, i64, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci]
+        sig.update({
+            "gemm_grouped_run": ([vp, *grouped, vp], ci),
+            "gemm_grouped_wgrad": ([vp, *wgrad, vp], ci),
+            "gemm_grouped_validate": (grouped, ci),
+            "gemm_grouped_wgrad_validate": (wgrad, ci),
+            "gemm_mx4_code_pitch": ([i64], i64),
+            "gemm_mx4_scale_pitch": ([i64], i64),
+            "gemm_mx4_quantise": ([vp, *quantise, vp], ci),
+            "gemm_mx4_dequantise": ([vp, *dequantise, vp], ci),
+            "gemm_mx4_run": ([vp, *mx4, vp], ci),
+            "gemm_mx4_grouped_run": ([vp, *mx4_grouped, vp], ci),
+            "gemm_mx4_quantise_validate": (quantise, ci),
+            "gemm_mx4_dequantise_validate": (dequantise, ci),
+            "gemm_mx4_validate": (mx4_grouped, ci),
+        })
         for name, (argtypes, restype) in sig.items():
             fn = getattr(lib, name)
             fn.argtypes = argtypes
@@ -187,6 +214,60 @@ def gemm_noalloc_set_option(option, value) -> int:
     return load_library().gemm_noalloc_set_option(option, value)
 
 
+# include/gemm_grouped.h and include/gemm_mx4.h, argument for argument.
+
+def gemm_grouped_run(*args) -> int:
+    return load_library().gemm_grouped_run(*args)
+
+
+def gemm_grouped_wgrad(*args) -> int:
+    return load_library().gemm_grouped_wgrad(*args)
+
+
+def gemm_grouped_validate(*args) -> int:
+    return load_library().gemm_grouped_validate(*args)
+
+
+def gemm_grouped_wgrad_validate(*args) -> int:
+    return load_library().gemm_grouped_wgrad_validate(*args)
+
+
+def gemm_mx4_code_pitch(K) -> int:
+    return load_library().gemm_mx4_code_pitch(K)
+
+
+def gemm_mx4_scale_pitch(K) -> int:
+    return load_library().gemm_mx4_scale_pitch(K)
+
+
+def gemm_mx4_quantise(*args) -> int:
+    return load_library().gemm_mx4_quantise(*args)
+
+
+def gemm_mx4_dequantise(*args) -> int:
+    return load_library().gemm_mx4_dequantise(*args)
+
+
+def gemm_mx4_run(*args) -> int:
+    return load_library().gemm_mx4_run(*args)
+
+
+def gemm_mx4_grouped_run(*args) -> int:
+    return load_library().gemm_mx4_grouped_run(*args)
+
+
+def gemm_mx4_quantise_validate(*args) -> int:
+    return load_library().gemm_mx4_quantise_validate(*args)
+
+
+def gemm_mx4_dequantise_validate(*args) -> int:
+    return load_library().gemm_mx4_dequantise_validate(*args)
+
+
+def gemm_mx4_validate(*args) -> int:
+    return load_library().gemm_mx4_validate(*args)
+
+
 GEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 # Labelled benchmark suite (include/gemm_ladder.h): the pages' optimisation
@@ -263,6 +344,46 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+class Mx4:
+    """A matrix of rows x K elements in microscaled 4-bit floating point.
+
+    ``codes`` (rows x pitch bytes, two E2M1 codes a byte, the even element in
+    the low half) and ``scales`` (rows x pitch bytes, one E8M0 byte per 32
+    elements) are uint8 tensors; rows and pitches are multiples of 16 bytes
+    (``mx4_empty`` makes them so).  The expert matrices of a grouped product
+    follow one another along the rows."""
+
+    def __init__(self, codes, scales, K: int):
+        import torch
+        blocks = -(-K // GEMM_MX4_BLOCK)
+        for name, t, need in (("codes", codes, blocks * 16), ("scales", scales, blocks)):
+            if t.dtype != torch.uint8 or t.dim() != 2:
+                raise ValueError(f"{name} must be a 2-D uint8 tensor")
+            if t.shape[1] < need or (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name} must hold {need} bytes of each row, next to one another")
+        if codes.shape[0] != scales.shape[0] or codes.device != scales.device:
+            raise ValueError("codes and scales must have the same rows and device")
+        self.codes, self.scales, self.K = codes, scales, int(K)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _args(self):
+        return (self.codes.data_ptr(), Gemm._ld(self.codes), self.scales.data_ptr(), Gemm._ld(self.scales))
+
+
+def mx4_empty(rows: int, K: int, device="cuda") -> Mx4:
+    """Uninitialised ``Mx4`` storage for rows x K elements."""
+    import torch
+    return Mx4(torch.empty((rows, gemm_mx4_code_pitch(K)), dtype=torch.uint8, device=device),
+               torch.empty((rows, gemm_mx4_scale_pitch(K)), dtype=torch.uint8, device=device), K)
+
+
 class Gemm:
     """A library handle used with torch tensors.
 
@@ -337,6 +458,143 @@ class Gemm:
         self._check(gemm_run_host(self.handle, lb, M, N, K, A.data_ptr(), self._ld(A),
                                   B.data_ptr(), self._ld(B), C.data_ptr(), self._ld(C), dt,
                                   _stream_handle(stream)))
+        return C
+
+    @staticmethod
+    def _matrix(t, name):
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be 2-D with unit stride along rows")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"the rows of {name} overlap")
+        return max(t.stride(0), t.shape[1], 1)
+
+    @staticmethod
+    def _matrices(t, name):
+        """Row pitch and matrix stride of a 3-D tensor of matrices."""
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be 3-D (groups first) with unit stride along rows")
+        ld = max(t.stride(1), t.shape[2], 1) if t.shape[1] > 1 else max(t.shape[2], 1)
+        return ld, max(t.stride(0), t.shape[1] * ld if t.shape[0] <= 1 else 0)
+
+    def _on_device(self, **tensors):
+        for name, t in tensors.items():
+            if t.device.type != "cuda" or t.device.index not in (None, self.device):
+                raise ValueError(f"{name} is on {t.device}, the handle on cuda:{self.device}")
+
+    @staticmethod
+    def _offsets(offsets, groups):
+        import torch
+        if offsets.dtype != torch.int64 or tuple(offsets.shape) != (groups + 1,) or not offsets.is_contiguous():
+            raise ValueError(f"offsets must be a contiguous int64 tensor of {groups + 1} values")
+        return offsets.data_ptr()
+
+    @staticmethod
+    def _float_code(t, name):
+        import torch
+        codes = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16}
+        if t.dtype not in codes:
+            raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+        return codes[t.dtype]
+
+    @staticmethod
+    def _operand_dtype(dtype, **tensors):
+        import torch
+        dt = DTYPES.get(dtype, dtype)
+        want = torch.bfloat16 if dt == GEMM_BF16 else torch.float32
+        for name, t in tensors.items():
+            if t.dtype != want:
+                raise ValueError(f"{name} must be {want} for dtype {dtype!r}, not {t.dtype}")
+        return dt
+
+    def run_grouped(self, A, B, offsets, C, layout_b="row", dtype="bf16", stream=None):
+        """C[r] = A[r] · B[g] for the rows r of every group g.
+
+        A is (rows, K) with the rows sorted by group, ``offsets`` (groups + 1,)
+        int64 on the device, B (groups, K, N) for ``layout_b="row"`` or
+        (groups, N, K) for ``"col"``, C (rows, N) float32 or bfloat16.  Rows
+        outside [offsets[0], offsets[-1]) keep what C held.  ``dtype`` is
+        "bf16" or "tf32"."""
+        lb = LAYOUTS.get(layout_b, layout_b)
+        self._on_device(A=A, B=B, offsets=offsets, C=C)
+        dt = self._operand_dtype(dtype, A=A, B=B)
+        lda, ldc = self._matrix(A, "A"), self._matrix(C, "C")
+        ldb, stride_b = self._matrices(B, "B")
+        groups = B.shape[0]
+        (M, K), (Kb, N) = A.shape, (B.shape[1:] if lb == GEMM_B_ROW_MAJOR else (B.shape[2], B.shape[1]))
+        if Kb != K or tuple(C.shape) != (M, N):
+            raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)} ({layout_b}), C {tuple(C.shape)}")
+        self._check(gemm_grouped_run(self.handle, lb, groups, M, N, K, self._offsets(offsets, groups), A.data_ptr(),
+                                     lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt,
+                                     self._float_code(C, "C"), _stream_handle(stream)))
+        return C
+
+    def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None):
+        """C[g] = A_g^T · B_g over the rows of group g (zeros where it has none).
+
+        A is (rows, M), B (rows, N), C (groups, M, N) float32 or bfloat16: the
+        gradient of a row-major weight with A the input and B the output's
+        gradient, of a column-major weight with the two exchanged."""
+        self._on_device(A=A, B=B, offsets=offsets, C=C)
+        dt = self._operand_dtype(dtype, A=A, B=B)
+        lda, ldb = self._matrix(A, "A"), self._matrix(B, "B")
+        ldc, stride_c = self._matrices(C, "C")
+        groups, M, N = C.shape
+        if A.shape[0] != B.shape[0] or A.shape[1] != M or B.shape[1] != N:
+            raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+        self._check(gemm_grouped_wgrad(self.handle, groups, A.shape[0], M, N, self._offsets(offsets, groups),
+                                       A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
+                                       self._float_code(C, "C"), _stream_handle(stream)))
+        return C
+
+    def mx4_quantise(self, src, out: Mx4, layout="col", stream=None):
+        """Quantise ``src`` (float32 or bfloat16) along K into ``out``.
+
+        ``layout="col"``: src is (rows, K), or (batch, rows, K); ``"row"``:
+        (K, rows) or (batch, K, rows), turned on the way.  The matrices of a
+        batch follow one another along out's rows."""
+        lb = LAYOUTS.get(layout, layout)
+        self._on_device(src=src, out=out)
+        t = src if src.dim() == 3 else src.unsqueeze(0)
+        ld, stride = self._matrices(t, "src")
+        batch, rows, K = t.shape if lb == GEMM_B_COL_MAJOR else (t.shape[0], t.shape[2], t.shape[1])
+        if out.rows != batch * rows or out.K != K:
+            raise ValueError(f"out holds {out.rows} x {out.K}, src has {batch} x {rows} x {K}")
+        self._check(gemm_mx4_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride,
+                                      self._float_code(src, "src"), *out._args(), _stream_handle(stream)))
+        return out
+
+    def mx4_dequantise(self, q: Mx4, out, stream=None):
+        """The values ``q`` stands for, as float32 or bfloat16 (exact)."""
+        self._on_device(q=q, out=out)
+        if tuple(out.shape) != (q.rows, q.K):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(q.rows, q.K)}")
+        self._check(gemm_mx4_dequantise(self.handle, q.rows, q.K, *q._args(), out.data_ptr(),
+                                        self._matrix(out, "out"), self._float_code(out, "out"),
+                                        _stream_handle(stream)))
+        return out
+
+    def run_mx4(self, A: Mx4, B: Mx4, C, stream=None):
+        """C = A · B^T of two quantised matrices (M x K and N x K); C float32
+        or bfloat16."""
+        self._on_device(A=A, B=B, C=C)
+        if A.K != B.K or tuple(C.shape) != (A.rows, B.rows):
+            raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K}, C {tuple(C.shape)}")
+        self._check(gemm_mx4_run(self.handle, A.rows, B.rows, A.K, *A._args(), *B._args(), C.data_ptr(),
+                                 self._matrix(C, "C"), self._float_code(C, "C"), _stream_handle(stream)))
+        return C
+
+    def run_mx4_grouped(self, A: Mx4, B: Mx4, offsets, C, stream=None):
+        """``run_grouped`` of quantised operands: B holds the experts' N x K
+        matrices one after another, N = C's columns."""
+        self._on_device(A=A, B=B, offsets=offsets, C=C)
+        N = C.shape[1]
+        groups = offsets.shape[0] - 1
+        if A.K != B.K or C.shape[0] != A.rows or B.rows != groups * N:
+            raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K} for {groups} groups, "
+                             f"C {tuple(C.shape)}")
+        self._check(gemm_mx4_grouped_run(self.handle, groups, A.rows, N, A.K, self._offsets(offsets, groups),
+                                         *A._args(), *B._args(), C.data_ptr(), self._matrix(C, "C"),
+                                         self._float_code(C, "C"), _stream_handle(stream)))
         return C
 
     def sync_status(self, stream=None):
