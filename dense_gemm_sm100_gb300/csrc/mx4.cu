@@ -84,36 +84,72 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *s, int n, bool vec, f
     }
 }
 
+// One warp takes SEGS segments of 256 elements of a row: all its 16-byte loads
+// are issued before the first is used, so a full SM has 128 KB (BF16) on the
+// way.  Chunk w of the launch is row w / chunks, chunk w % chunks of it.
+constexpr int SEGS = 4;
+
+struct Chunk {
+    long long row;
+    int k;  // first element
+};
+
+__device__ __forceinline__ Chunk chunk_of(long long w, int chunks)
+{
+    Chunk c;
+    if (w < (1ll << 31)) {  // 32-bit division where it fits
+        const uint32_t r = static_cast<uint32_t>(w) / static_cast<uint32_t>(chunks);
+        c.row = r;
+        c.k = static_cast<int>(static_cast<uint32_t>(w) - r * chunks) * (SEGS * 256);
+    } else {
+        c.row = w / chunks;
+        c.k = static_cast<int>(w - c.row * chunks) * (SEGS * 256);
+    }
+    return c;
+}
+
 // Rows along K: four lanes share a block, eight elements each.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    quantise_rows_kernel(const T *src, long long ld, int rows_per, long long stride, long long rows, int K,
-                         int segs, int vec, uint8_t *codes, long long ldq, uint8_t *scales, long long lds)
+    quantise_rows_kernel(const T *src, long long ld, int rows_per, long long stride, long long total, int K,
+                         int chunks, int vec, uint8_t *codes, long long ldq, uint8_t *scales, long long lds)
 {
     const int lane = threadIdx.x & 31;
-    const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
+    const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+    if (w >= total) return;
+    const Chunk c = chunk_of(w, chunks);
     const int Kp = (K + 31) / 32 * 32;
-    for (long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); w < rows * segs;
-         w += warps) {
-        const long long row = w / segs;
-        const int k = static_cast<int>(w - row * segs) * 256 + lane * 8;
-        const T *s = src + (row / rows_per) * stride + (row % rows_per) * ld + k;
-        float v[8];
-        load8(s, K - k, vec != 0, v);
+    const T *s = src + c.row * ld;
+    if (stride) s = src + (c.row / rows_per) * stride + (c.row % rows_per) * ld;
+    float v[SEGS][8];
+#pragma unroll
+    for (int j = 0; j < SEGS; ++j) {
+        const int k = c.k + j * 256 + lane * 8;
+        load8(s + k, K - k, vec != 0, v[j]);
+    }
+    uint32_t byte[SEGS];
+#pragma unroll
+    for (int j = 0; j < SEGS; ++j) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7fffffffu);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t byte = scale_byte(m);
-        const float inv = inverse_scale(byte);
-        if (k < Kp) {
+        byte[j] = scale_byte(m);
+        const float inv = inverse_scale(byte[j]);
+        const int k = c.k + j * 256 + lane * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.0f : v[i] * inv;
-            *reinterpret_cast<uint32_t *>(codes + row * ldq + k / 2) = pack_e2m1(v);
-            if ((lane & 3) == 0) scales[row * lds + k / 32] = static_cast<uint8_t>(byte);
-        }
+        for (int i = 0; i < 8; ++i) v[j][i] = byte[j] == 255u ? 0.0f : v[j][i] * inv;
+        if (k < Kp) *reinterpret_cast<uint32_t *>(codes + c.row * ldq + k / 2) = pack_e2m1(v[j]);
     }
+    // the chunk's scale bytes, one a lane: segment lane / 8, block lane % 8
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < SEGS; ++j) {
+        const uint32_t t = __shfl_sync(0xffffffffu, byte[j], (lane & 7) * 4);
+        if ((lane >> 3) == j) mine = t;
+    }
+    if (c.k + lane * 32 < Kp) scales[c.row * lds + c.k / 32 + lane] = static_cast<uint8_t>(mine);
 }
 
 // K along the source's rows: one thread per block, neighbouring threads on
@@ -186,36 +222,43 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *d, int n, bool vec, const 
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    dequantise_kernel(const uint8_t *codes, long long ldq, const uint8_t *scales, long long lds, long long rows, int K,
-                      int segs, int vec, T *dst, long long ldd)
+    dequantise_kernel(const uint8_t *codes, long long ldq, const uint8_t *scales, long long lds, long long total, int K,
+                      int chunks, int vec, T *dst, long long ldd)
 {
     const int lane = threadIdx.x & 31;
-    const long long warps = static_cast<long long>(gridDim.x) * (THREADS / 32);
-    for (long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); w < rows * segs;
-         w += warps) {
-        const long long row = w / segs;
-        const int k = static_cast<int>(w - row * segs) * 256 + lane * 8;
-        if (k >= K) continue;
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(codes + row * ldq + k / 2));
-        const float scale = scale_value(__ldg(scales + row * lds + k / 32));
+    const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+    if (w >= total) return;
+    const Chunk ch = chunk_of(w, chunks);
+    uint32_t c[SEGS], byte[SEGS];
+#pragma unroll
+    for (int j = 0; j < SEGS; ++j) {
+        const int k = ch.k + j * 256 + lane * 8;
+        c[j] = byte[j] = 0;
+        if (k < K) {
+            c[j] = __ldg(reinterpret_cast<const uint32_t *>(codes + ch.row * ldq + k / 2));
+            byte[j] = __ldg(scales + ch.row * lds + k / 32);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < SEGS; ++j) {
+        const int k = ch.k + j * 256 + lane * 8;
+        if (k >= K) break;
+        const float scale = scale_value(byte[j]);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t q = (c >> (4 * i)) & 15u;
+            const uint32_t q = (c[j] >> (4 * i)) & 15u;
             // E2M1 magnitude: 0, 0.5, then (2 + mantissa) * 2^(exponent - 2)
             const float mag = (q & 7u) < 2u ? 0.5f * static_cast<float>(q & 1u)
                                             : __uint_as_float((((q & 6u) << 22) | ((q & 1u) << 22)) + (126u << 23));
             v[i] = ((q & 8u) ? -mag : mag) * scale;
         }
-        store8(dst + row * ldd + k, K - k, vec != 0, v);
+        store8(dst + ch.row * ldd + k, K - k, vec != 0, v);
     }
 }
 
-int warp_grid(int64_t warps, int sm_count)
-{
-    const int64_t blocks = (warps + THREADS / 32 - 1) / (THREADS / 32);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t{sm_count} * 8)));
-}
+// One warp per chunk; block counts pass 2^31 - 1 only for matrices beyond memory.
+int64_t chunk_blocks(int64_t chunks) { return (chunks + THREADS / 32 - 1) / (THREADS / 32); }
 
 template <typename T>
 cudaError_t quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const T *src, int64_t ld, int64_t stride,
@@ -224,27 +267,32 @@ cudaError_t quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const 
     const int64_t all = batch * rows;
     if (k_rows) {
         const int blocks = static_cast<int>((K + 31) / 32);
-        const int grid = warp_grid((all * blocks + 31) / 32, sm_count);
+        const int grid = static_cast<int>(std::min<int64_t>((all * blocks + THREADS - 1) / THREADS, int64_t{sm_count} * 8));
         quantise_cols_kernel<T><<<grid, THREADS, 0, stream>>>(src, ld, static_cast<int>(rows), stride, all,
                                                               static_cast<int>(K), blocks, codes, ldq, scales, lds);
         return cudaGetLastError();
     }
-    const int segs = static_cast<int>((K + 255) / 256);
+    const int chunks = static_cast<int>((K + SEGS * 256 - 1) / (SEGS * 256));
+    const int64_t grid = chunk_blocks(all * chunks);
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
     const int64_t align = 16 / static_cast<int64_t>(sizeof(T));
     const int vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % align == 0 && stride % align == 0;
-    quantise_rows_kernel<T><<<warp_grid(all * segs, sm_count), THREADS, 0, stream>>>(
-        src, ld, static_cast<int>(rows), stride, all, static_cast<int>(K), segs, vec, codes, ldq, scales, lds);
+    quantise_rows_kernel<T><<<static_cast<unsigned>(grid), THREADS, 0, stream>>>(
+        src, ld, static_cast<int>(rows), stride, all * chunks, static_cast<int>(K), chunks, vec, codes, ldq, scales,
+        lds);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds,
-                       T *dst, int64_t ldd, int sm_count, cudaStream_t stream)
+                       T *dst, int64_t ldd, cudaStream_t stream)
 {
-    const int segs = static_cast<int>((K + 255) / 256);
+    const int chunks = static_cast<int>((K + SEGS * 256 - 1) / (SEGS * 256));
+    const int64_t grid = chunk_blocks(rows * chunks);
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
     const int vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && (ldd * sizeof(T)) % 16 == 0;
-    dequantise_kernel<T><<<warp_grid(rows * segs, sm_count), THREADS, 0, stream>>>(
-        codes, ldq, scales, lds, rows, static_cast<int>(K), segs, vec, dst, ldd);
+    dequantise_kernel<T><<<static_cast<unsigned>(grid), THREADS, 0, stream>>>(
+        codes, ldq, scales, lds, rows * chunks, static_cast<int>(K), chunks, vec, dst, ldd);
     return cudaGetLastError();
 }
 
@@ -262,12 +310,11 @@ cudaError_t launch_mx4_quantise(bool k_rows, int64_t batch, int64_t rows, int64_
 }
 
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
-                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, int sm_count,
-                                  cudaStream_t stream)
+                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, cudaStream_t stream)
 {
     if (dst_bf16)
-        return dequantise(rows, K, codes, ldq, scales, lds, static_cast<__nv_bfloat16 *>(dst), ldd, sm_count, stream);
-    return dequantise(rows, K, codes, ldq, scales, lds, static_cast<float *>(dst), ldd, sm_count, stream);
+        return dequantise(rows, K, codes, ldq, scales, lds, static_cast<__nv_bfloat16 *>(dst), ldd, stream);
+    return dequantise(rows, K, codes, ldq, scales, lds, static_cast<float *>(dst), ldd, stream);
 }
 
 }  // namespace dg

@@ -344,6 +344,95 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# Argument marshalling of the grouped and 4-bit calls.  These run per call, in
+# front of kernels of a few microseconds, so each looks at a tensor's fields
+# once and nothing is imported or locked on the way.
+
+_float_codes = None
+
+
+def _type_code(t, name):
+    global _float_codes
+    if _float_codes is None:
+        import torch
+        _float_codes = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16}
+    code = _float_codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return code
+
+
+def _on_device(t, name, device):
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+
+
+def _matrix(t, name, device):
+    """(rows, columns, pitch, type code) of a 2-D operand on `device`."""
+    _on_device(t, name, device)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    if cols > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have unit stride along rows")
+    ld = cols if cols > 0 else 1
+    if rows > 1:
+        if stride[0] < cols:
+            raise ValueError(f"the rows of {name} overlap")
+        if stride[0] > ld:
+            ld = stride[0]
+    return rows, cols, ld, _type_code(t, name)
+
+
+def _matrices(t, name, device):
+    """(matrices, rows, columns, pitch, matrix stride, type code) of a 3-D one."""
+    _on_device(t, name, device)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D, matrices first")
+    n, rows, cols = shape
+    if cols > 1 and stride[2] != 1:
+        raise ValueError(f"{name} must have unit stride along rows")
+    ld = cols if cols > 0 else 1
+    if rows > 1:
+        if stride[1] < cols:
+            raise ValueError(f"the rows of {name} overlap")
+        if stride[1] > ld:
+            ld = stride[1]
+    return n, rows, cols, ld, (stride[0] if n > 1 else rows * ld), _type_code(t, name)
+
+
+def _offsets(t, groups, device):
+    import torch
+    _on_device(t, "offsets", device)
+    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != groups + 1 or (groups > 0 and t.stride(0) != 1):
+        raise ValueError(f"offsets must be a contiguous int64 tensor of {groups + 1} values")
+    return t.data_ptr()
+
+
+def _operand_types(dt, **codes):
+    want = GEMM_BF16 if dt == GEMM_BF16 else GEMM_F32
+    for name, code in codes.items():
+        if code != want:
+            raise ValueError(f"{name} must be {'bfloat16' if dt == GEMM_BF16 else 'float32'} for this dtype")
+
+
+_current_raw_stream = None
+
+
+def _raw_stream(stream, device):
+    """The caller's stream, or torch's current one on `device`, as a pointer."""
+    global _current_raw_stream
+    if stream is not None:
+        return _stream_handle(stream)
+    if _current_raw_stream is None:
+        import torch
+        _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _current_raw_stream(device)
+
+
 class Mx4:
     """A matrix of rows x K elements in microscaled 4-bit floating point.
 
@@ -364,17 +453,20 @@ class Mx4:
         if codes.shape[0] != scales.shape[0] or codes.device != scales.device:
             raise ValueError("codes and scales must have the same rows and device")
         self.codes, self.scales, self.K = codes, scales, int(K)
-
-    @property
-    def rows(self) -> int:
-        return self.codes.shape[0]
+        self.rows = codes.shape[0]
+        self._pitches = [max(t.stride(0), t.shape[1]) if self.rows > 1 else t.shape[1] for t in (codes, scales)]
+        if self.rows > 1 and (codes.stride(0) < blocks * 16 or scales.stride(0) < blocks):
+            raise ValueError("the rows of codes or scales overlap")
+        self._device = codes.get_device() if codes.is_cuda else None
 
     @property
     def device(self):
         return self.codes.device
 
-    def _args(self):
-        return (self.codes.data_ptr(), Gemm._ld(self.codes), self.scales.data_ptr(), Gemm._ld(self.scales))
+    def _args(self, device):
+        if self._device != device:
+            raise ValueError(f"a 4-bit operand is on {self.device}, the handle on cuda:{device}")
+        return self.codes.data_ptr(), self._pitches[0], self.scales.data_ptr(), self._pitches[1]
 
 
 def mx4_empty(rows: int, K: int, device="cuda") -> Mx4:
@@ -397,6 +489,7 @@ class Gemm:
     def __init__(self, device: int = 0):
         self.device = device
         self.handle = gemm_create(device)
+        self._lib = load_library()
 
     def close(self):
         if self.handle:
@@ -460,52 +553,6 @@ class Gemm:
                                   _stream_handle(stream)))
         return C
 
-    @staticmethod
-    def _matrix(t, name):
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be 2-D with unit stride along rows")
-        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-            raise ValueError(f"the rows of {name} overlap")
-        return max(t.stride(0), t.shape[1], 1)
-
-    @staticmethod
-    def _matrices(t, name):
-        """Row pitch and matrix stride of a 3-D tensor of matrices."""
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be 3-D (groups first) with unit stride along rows")
-        ld = max(t.stride(1), t.shape[2], 1) if t.shape[1] > 1 else max(t.shape[2], 1)
-        return ld, max(t.stride(0), t.shape[1] * ld if t.shape[0] <= 1 else 0)
-
-    def _on_device(self, **tensors):
-        for name, t in tensors.items():
-            if t.device.type != "cuda" or t.device.index not in (None, self.device):
-                raise ValueError(f"{name} is on {t.device}, the handle on cuda:{self.device}")
-
-    @staticmethod
-    def _offsets(offsets, groups):
-        import torch
-        if offsets.dtype != torch.int64 or tuple(offsets.shape) != (groups + 1,) or not offsets.is_contiguous():
-            raise ValueError(f"offsets must be a contiguous int64 tensor of {groups + 1} values")
-        return offsets.data_ptr()
-
-    @staticmethod
-    def _float_code(t, name):
-        import torch
-        codes = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16}
-        if t.dtype not in codes:
-            raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
-        return codes[t.dtype]
-
-    @staticmethod
-    def _operand_dtype(dtype, **tensors):
-        import torch
-        dt = DTYPES.get(dtype, dtype)
-        want = torch.bfloat16 if dt == GEMM_BF16 else torch.float32
-        for name, t in tensors.items():
-            if t.dtype != want:
-                raise ValueError(f"{name} must be {want} for dtype {dtype!r}, not {t.dtype}")
-        return dt
-
     def run_grouped(self, A, B, offsets, C, layout_b="row", dtype="bf16", stream=None):
         """C[r] = A[r] · B[g] for the rows r of every group g.
 
@@ -515,17 +562,20 @@ class Gemm:
         outside [offsets[0], offsets[-1]) keep what C held.  ``dtype`` is
         "bf16" or "tf32"."""
         lb = LAYOUTS.get(layout_b, layout_b)
-        self._on_device(A=A, B=B, offsets=offsets, C=C)
-        dt = self._operand_dtype(dtype, A=A, B=B)
-        lda, ldc = self._matrix(A, "A"), self._matrix(C, "C")
-        ldb, stride_b = self._matrices(B, "B")
-        groups = B.shape[0]
-        (M, K), (Kb, N) = A.shape, (B.shape[1:] if lb == GEMM_B_ROW_MAJOR else (B.shape[2], B.shape[1]))
-        if Kb != K or tuple(C.shape) != (M, N):
+        dt = DTYPES.get(dtype, dtype)
+        dev = self.device
+        M, K, lda, a_type = _matrix(A, "A", dev)
+        rows, N, ldc, c_type = _matrix(C, "C", dev)
+        groups, d1, d2, ldb, stride_b, b_type = _matrices(B, "B", dev)
+        Kb, Nb = (d1, d2) if lb == GEMM_B_ROW_MAJOR else (d2, d1)
+        if Kb != K or Nb != N or rows != M:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)} ({layout_b}), C {tuple(C.shape)}")
-        self._check(gemm_grouped_run(self.handle, lb, groups, M, N, K, self._offsets(offsets, groups), A.data_ptr(),
-                                     lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt,
-                                     self._float_code(C, "C"), _stream_handle(stream)))
+        _operand_types(dt, A=a_type, B=b_type)
+        rc = self._lib.gemm_grouped_run(self.handle, lb, groups, M, N, K, _offsets(offsets, groups, dev), A.data_ptr(),
+                                        lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt, c_type,
+                                        _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return C
 
     def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None):
@@ -534,16 +584,19 @@ class Gemm:
         A is (rows, M), B (rows, N), C (groups, M, N) float32 or bfloat16: the
         gradient of a row-major weight with A the input and B the output's
         gradient, of a column-major weight with the two exchanged."""
-        self._on_device(A=A, B=B, offsets=offsets, C=C)
-        dt = self._operand_dtype(dtype, A=A, B=B)
-        lda, ldb = self._matrix(A, "A"), self._matrix(B, "B")
-        ldc, stride_c = self._matrices(C, "C")
-        groups, M, N = C.shape
-        if A.shape[0] != B.shape[0] or A.shape[1] != M or B.shape[1] != N:
+        dt = DTYPES.get(dtype, dtype)
+        dev = self.device
+        rows, M, lda, a_type = _matrix(A, "A", dev)
+        rows_b, N, ldb, b_type = _matrix(B, "B", dev)
+        groups, Mc, Nc, ldc, stride_c, c_type = _matrices(C, "C", dev)
+        if rows_b != rows or Mc != M or Nc != N:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
-        self._check(gemm_grouped_wgrad(self.handle, groups, A.shape[0], M, N, self._offsets(offsets, groups),
-                                       A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
-                                       self._float_code(C, "C"), _stream_handle(stream)))
+        _operand_types(dt, A=a_type, B=b_type)
+        rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
+                                          A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
+                                          c_type, _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return C
 
     def mx4_quantise(self, src, out: Mx4, layout="col", stream=None):
@@ -553,48 +606,60 @@ class Gemm:
         (K, rows) or (batch, K, rows), turned on the way.  The matrices of a
         batch follow one another along out's rows."""
         lb = LAYOUTS.get(layout, layout)
-        self._on_device(src=src, out=out)
-        t = src if src.dim() == 3 else src.unsqueeze(0)
-        ld, stride = self._matrices(t, "src")
-        batch, rows, K = t.shape if lb == GEMM_B_COL_MAJOR else (t.shape[0], t.shape[2], t.shape[1])
+        dev = self.device
+        if src.dim() == 3:
+            batch, d1, d2, ld, stride, s_type = _matrices(src, "src", dev)
+        else:
+            d1, d2, ld, s_type = _matrix(src, "src", dev)
+            batch, stride = 1, 0
+        rows, K = (d1, d2) if lb == GEMM_B_COL_MAJOR else (d2, d1)
         if out.rows != batch * rows or out.K != K:
             raise ValueError(f"out holds {out.rows} x {out.K}, src has {batch} x {rows} x {K}")
-        self._check(gemm_mx4_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride,
-                                      self._float_code(src, "src"), *out._args(), _stream_handle(stream)))
+        rc = self._lib.gemm_mx4_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride, s_type,
+                                         *out._args(dev), _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return out
 
     def mx4_dequantise(self, q: Mx4, out, stream=None):
         """The values ``q`` stands for, as float32 or bfloat16 (exact)."""
-        self._on_device(q=q, out=out)
-        if tuple(out.shape) != (q.rows, q.K):
+        dev = self.device
+        rows, K, ld, o_type = _matrix(out, "out", dev)
+        if rows != q.rows or K != q.K:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(q.rows, q.K)}")
-        self._check(gemm_mx4_dequantise(self.handle, q.rows, q.K, *q._args(), out.data_ptr(),
-                                        self._matrix(out, "out"), self._float_code(out, "out"),
-                                        _stream_handle(stream)))
+        rc = self._lib.gemm_mx4_dequantise(self.handle, rows, K, *q._args(dev), out.data_ptr(), ld, o_type,
+                                           _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return out
 
     def run_mx4(self, A: Mx4, B: Mx4, C, stream=None):
         """C = A · B^T of two quantised matrices (M x K and N x K); C float32
         or bfloat16."""
-        self._on_device(A=A, B=B, C=C)
-        if A.K != B.K or tuple(C.shape) != (A.rows, B.rows):
+        dev = self.device
+        M, N, ldc, c_type = _matrix(C, "C", dev)
+        if A.K != B.K or M != A.rows or N != B.rows:
             raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K}, C {tuple(C.shape)}")
-        self._check(gemm_mx4_run(self.handle, A.rows, B.rows, A.K, *A._args(), *B._args(), C.data_ptr(),
-                                 self._matrix(C, "C"), self._float_code(C, "C"), _stream_handle(stream)))
+        rc = self._lib.gemm_mx4_run(self.handle, M, N, A.K, *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
+                                    _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return C
 
     def run_mx4_grouped(self, A: Mx4, B: Mx4, offsets, C, stream=None):
         """``run_grouped`` of quantised operands: B holds the experts' N x K
         matrices one after another, N = C's columns."""
-        self._on_device(A=A, B=B, offsets=offsets, C=C)
-        N = C.shape[1]
+        dev = self.device
+        M, N, ldc, c_type = _matrix(C, "C", dev)
         groups = offsets.shape[0] - 1
-        if A.K != B.K or C.shape[0] != A.rows or B.rows != groups * N:
+        if A.K != B.K or M != A.rows or B.rows != groups * N:
             raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K} for {groups} groups, "
                              f"C {tuple(C.shape)}")
-        self._check(gemm_mx4_grouped_run(self.handle, groups, A.rows, N, A.K, self._offsets(offsets, groups),
-                                         *A._args(), *B._args(), C.data_ptr(), self._matrix(C, "C"),
-                                         self._float_code(C, "C"), _stream_handle(stream)))
+        rc = self._lib.gemm_mx4_grouped_run(self.handle, groups, M, N, A.K, _offsets(offsets, groups, dev),
+                                            *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
+                                            _raw_stream(stream, dev))
+        if rc:
+            self._check(rc)
         return C
 
     def sync_status(self, stream=None):
