@@ -45,111 +45,150 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte)
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-// 2^(byte - 127); the lowest is subnormal, 0xFF is NaN.
-__device__ __forceinline__ float scale_value(uint32_t byte)
-{
-    return byte == 255u ? __uint_as_float(0x7fffffffu) : byte == 0u ? __uint_as_float(1u << 22) : __uint_as_float(byte << 23);
-}
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// 8 elements of a row; vec: 16-byte loads are allowed.
-__device__ __forceinline__ void load8(const float *s, int n, bool vec, float (&v)[8])
-{
-    if (vec && n >= 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(s));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(s) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(s + i) : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16 *s, int n, bool vec, float (&v)[8])
-{
-    if (vec && n >= 8) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(s));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(s[i]) : 0.0f;
-    }
-}
-
-// One warp takes SEGS segments of 256 elements of a row: all its 16-byte loads
-// are issued before the first is used, so a full SM has 128 KB (BF16) on the
-// way.  Chunk w of the launch is row w / chunks, chunk w % chunks of it.
-constexpr int SEGS = 4;
-
-struct Chunk {
-    long long row;
-    int k;  // first element
+// 8 elements of a row as they are loaded (vec: 16-byte loads are allowed), and
+// widened.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
 };
 
-__device__ __forceinline__ Chunk chunk_of(long long w, int chunks)
+__device__ __forceinline__ void load8(const float *s, int n, bool vec, Raw<float> &r)
 {
-    Chunk c;
-    if (w < (1ll << 31)) {  // 32-bit division where it fits
-        const uint32_t r = static_cast<uint32_t>(w) / static_cast<uint32_t>(chunks);
-        c.row = r;
-        c.k = static_cast<int>(static_cast<uint32_t>(w) - r * chunks) * (SEGS * 256);
+    if (vec && n >= 8) {
+        r.a = __ldg(reinterpret_cast<const float4 *>(s));
+        r.b = __ldg(reinterpret_cast<const float4 *>(s) + 1);
     } else {
-        c.row = w / chunks;
-        c.k = static_cast<int>(w - c.row * chunks) * (SEGS * 256);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(s + i) : 0.0f;
+        r.a = make_float4(v[0], v[1], v[2], v[3]);
+        r.b = make_float4(v[4], v[5], v[6], v[7]);
     }
-    return c;
 }
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *s, int n, bool vec, Raw<__nv_bfloat16> &r)
+{
+    if (vec && n >= 8) {
+        r.a = __ldg(reinterpret_cast<const uint4 *>(s));
+    } else {
+        const uint16_t *t = reinterpret_cast<const uint16_t *>(s);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (2 * i < n ? uint32_t{__ldg(t + 2 * i)} : 0u) | (2 * i + 1 < n ? uint32_t{__ldg(t + 2 * i + 1)} << 16 : 0u);
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__device__ __forceinline__ void widen(const Raw<float> &r, float (&v)[8])
+{
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
+    v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
+}
+
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16> &r, float (&v)[8])
+{
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// A warp takes chunks of SEGS segments of 256 elements of a row, 64 bytes a
+// lane, and issues the loads of its next chunk before it works on the present
+// one, so loads are on the way all the time.
+template <typename T>
+constexpr int kSegs = sizeof(T) == 2 ? 4 : 2;
+
+// Position of a warp in the rows x chunks grid, advanced by a fixed step
+// without division.
+struct Cursor {
+    long long row, step_row;
+    int chunk, step_chunk, chunks;
+    __device__ Cursor(long long first, long long step, int n) : chunks(n)
+    {
+        row = first / n;
+        chunk = static_cast<int>(first - row * n);
+        step_row = step / n;
+        step_chunk = static_cast<int>(step - step_row * n);
+    }
+    __device__ void next()
+    {
+        row += step_row;
+        chunk += step_chunk;
+        if (chunk >= chunks) {
+            chunk -= chunks;
+            ++row;
+        }
+    }
+};
 
 // Rows along K: four lanes share a block, eight elements each.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    quantise_rows_kernel(const T *src, long long ld, int rows_per, long long stride, long long total, int K,
+    quantise_rows_kernel(const T *src, long long ld, int rows_per, long long stride, long long rows, int K,
                          int chunks, int vec, uint8_t *codes, long long ldq, uint8_t *scales, long long lds)
 {
+    constexpr int SEGS = kSegs<T>;
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
-    if (w >= total) return;
-    const Chunk c = chunk_of(w, chunks);
+    Cursor at(static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5),
+              static_cast<long long>(gridDim.x) * (THREADS / 32), chunks);
     const int Kp = (K + 31) / 32 * 32;
-    const T *s = src + c.row * ld;
-    if (stride) s = src + (c.row / rows_per) * stride + (c.row % rows_per) * ld;
-    float v[SEGS][8];
+    Raw<T> next[SEGS];
+    const auto fetch = [&]() {
+        if (at.row >= rows) return;
+        const T *s = stride ? src + (at.row / rows_per) * stride + (at.row % rows_per) * ld : src + at.row * ld;
 #pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-        const int k = c.k + j * 256 + lane * 8;
-        load8(s + k, K - k, vec != 0, v[j]);
+        for (int j = 0; j < SEGS; ++j) {
+            const int k = (at.chunk * SEGS + j) * 256 + lane * 8;
+            load8(s + k, K - k, vec != 0, next[j]);
+        }
+    };
+    fetch();
+    while (at.row < rows) {
+        float v[SEGS][8];
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) widen(next[j], v[j]);
+        const long long row = at.row;
+        const int k0 = at.chunk * (SEGS * 256);
+        at.next();
+        fetch();
+        uint32_t byte[SEGS];
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            byte[j] = scale_byte(m);
+            const float inv = inverse_scale(byte[j]);
+            const int k = k0 + j * 256 + lane * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] *= inv;
+            if (k < Kp)
+                *reinterpret_cast<uint32_t *>(codes + row * ldq + k / 2) = byte[j] == 255u ? 0u : pack_e2m1(v[j]);
+        }
+        // the chunk's scale bytes, one a lane: segment lane / 8, block lane % 8
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) {
+            const uint32_t t = __shfl_sync(0xffffffffu, byte[j], (lane & 7) * 4);
+            if ((lane >> 3) == j) mine = t;
+        }
+        if (lane < SEGS * 8 && k0 + lane * 32 < Kp) scales[row * lds + k0 / 32 + lane] = static_cast<uint8_t>(mine);
     }
-    uint32_t byte[SEGS];
-#pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7fffffffu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        byte[j] = scale_byte(m);
-        const float inv = inverse_scale(byte[j]);
-        const int k = c.k + j * 256 + lane * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = byte[j] == 255u ? 0.0f : v[j][i] * inv;
-        if (k < Kp) *reinterpret_cast<uint32_t *>(codes + c.row * ldq + k / 2) = pack_e2m1(v[j]);
-    }
-    // the chunk's scale bytes, one a lane: segment lane / 8, block lane % 8
-    uint32_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-        const uint32_t t = __shfl_sync(0xffffffffu, byte[j], (lane & 7) * 4);
-        if ((lane >> 3) == j) mine = t;
-    }
-    if (c.k + lane * 32 < Kp) scales[c.row * lds + c.k / 32 + lane] = static_cast<uint8_t>(mine);
 }
 
 // K along the source's rows: one thread per block, neighbouring threads on
@@ -192,8 +231,33 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-__device__ __forceinline__ void store8(float *d, int n, bool vec, const float (&v)[8])
+// Eight codes as BF16 pairs.  A code's bits s, e e, m placed at the sign, the
+// two lowest exponent bits and the highest mantissa bit of a BF16 number are
+// its value times 2^-126 (the codes 0 and 0.5 as a zero and a subnormal), so
+// two exact multiplications, by 2^126 and by the scale, give the element.
+__device__ __forceinline__ void expand8(uint32_t c, __nv_bfloat162 scale, __nv_bfloat162 (&w)[4])
 {
+    const uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
+    const uint32_t up = 0x7e807e80u;  // 2^126 twice
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // byte i of `even` in the low half, of `odd` in the high half
+        const uint32_t t = __byte_perm(even, odd, 0x0400u + 0x1111u * i);
+        const uint32_t bits = ((t << 6) & 0x01c001c0u) | ((t << 12) & 0x80008000u);
+        w[i] = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&bits),
+                               *reinterpret_cast<const __nv_bfloat162 *>(&up)),
+                       scale);
+    }
+}
+
+__device__ __forceinline__ void store8(float *d, int n, bool vec, const __nv_bfloat162 (&w)[4])
+{
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __low2float(w[i]);
+        v[2 * i + 1] = __high2float(w[i]);
+    }
     if (vec && n >= 8) {
         reinterpret_cast<float4 *>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4 *>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -204,11 +268,8 @@ __device__ __forceinline__ void store8(float *d, int n, bool vec, const float (&
     }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *d, int n, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(__nv_bfloat16 *d, int n, bool vec, const __nv_bfloat162 (&w)[4])
 {
-    __nv_bfloat162 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     if (vec && n >= 8) {
         *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(w);
     } else {
@@ -222,43 +283,53 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *d, int n, bool vec, const 
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    dequantise_kernel(const uint8_t *codes, long long ldq, const uint8_t *scales, long long lds, long long total, int K,
+    dequantise_kernel(const uint8_t *codes, long long ldq, const uint8_t *scales, long long lds, long long rows, int K,
                       int chunks, int vec, T *dst, long long ldd)
 {
+    constexpr int SEGS = kSegs<T>;
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
-    if (w >= total) return;
-    const Chunk ch = chunk_of(w, chunks);
+    Cursor at(static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5),
+              static_cast<long long>(gridDim.x) * (THREADS / 32), chunks);
     uint32_t c[SEGS], byte[SEGS];
+    const auto fetch = [&]() {
+        if (at.row >= rows) return;
 #pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-        const int k = ch.k + j * 256 + lane * 8;
-        c[j] = byte[j] = 0;
-        if (k < K) {
-            c[j] = __ldg(reinterpret_cast<const uint32_t *>(codes + ch.row * ldq + k / 2));
-            byte[j] = __ldg(scales + ch.row * lds + k / 32);
+        for (int j = 0; j < SEGS; ++j) {
+            const int k = (at.chunk * SEGS + j) * 256 + lane * 8;
+            if (k < K) {
+                c[j] = __ldg(reinterpret_cast<const uint32_t *>(codes + at.row * ldq + k / 2));
+                byte[j] = __ldg(scales + at.row * lds + k / 32);
+            }
         }
-    }
+    };
+    fetch();
+    while (at.row < rows) {
+        uint32_t code[SEGS], s[SEGS];
 #pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-        const int k = ch.k + j * 256 + lane * 8;
-        if (k >= K) break;
-        const float scale = scale_value(byte[j]);
-        float v[8];
+        for (int j = 0; j < SEGS; ++j) code[j] = c[j], s[j] = byte[j];
+        T *d = dst + at.row * ldd;
+        const int k0 = at.chunk * (SEGS * 256);
+        at.next();
+        fetch();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t q = (c[j] >> (4 * i)) & 15u;
-            // E2M1 magnitude: 0, 0.5, then (2 + mantissa) * 2^(exponent - 2)
-            const float mag = (q & 7u) < 2u ? 0.5f * static_cast<float>(q & 1u)
-                                            : __uint_as_float((((q & 6u) << 22) | ((q & 1u) << 22)) + (126u << 23));
-            v[i] = ((q & 8u) ? -mag : mag) * scale;
+        for (int j = 0; j < SEGS; ++j) {
+            const int k = k0 + j * 256 + lane * 8;
+            if (k >= K) break;
+            const uint32_t sb = s[j] == 255u ? 0x7fffu : s[j] == 0u ? 0x0040u : s[j] << 7;  // the scale as BF16
+            const uint32_t both = sb * 0x00010001u;
+            __nv_bfloat162 w[4];
+            expand8(code[j], *reinterpret_cast<const __nv_bfloat162 *>(&both), w);
+            store8(d + k, K - k, vec != 0, w);
         }
-        store8(dst + ch.row * ldd + k, K - k, vec != 0, v);
     }
 }
 
-// One warp per chunk; block counts pass 2^31 - 1 only for matrices beyond memory.
-int64_t chunk_blocks(int64_t chunks) { return (chunks + THREADS / 32 - 1) / (THREADS / 32); }
+// Blocks of eight warps, one chunk a warp at least, eight blocks an SM at most.
+int chunk_grid(int64_t chunks, int sm_count)
+{
+    const int64_t blocks = (chunks + THREADS / 32 - 1) / (THREADS / 32);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t{sm_count} * 8)));
+}
 
 template <typename T>
 cudaError_t quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const T *src, int64_t ld, int64_t stride,
@@ -272,27 +343,22 @@ cudaError_t quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const 
                                                               static_cast<int>(K), blocks, codes, ldq, scales, lds);
         return cudaGetLastError();
     }
-    const int chunks = static_cast<int>((K + SEGS * 256 - 1) / (SEGS * 256));
-    const int64_t grid = chunk_blocks(all * chunks);
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const int chunks = static_cast<int>((K + kSegs<T> * 256 - 1) / (kSegs<T> * 256));
     const int64_t align = 16 / static_cast<int64_t>(sizeof(T));
     const int vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % align == 0 && stride % align == 0;
-    quantise_rows_kernel<T><<<static_cast<unsigned>(grid), THREADS, 0, stream>>>(
-        src, ld, static_cast<int>(rows), stride, all * chunks, static_cast<int>(K), chunks, vec, codes, ldq, scales,
-        lds);
+    quantise_rows_kernel<T><<<chunk_grid(all * chunks, sm_count), THREADS, 0, stream>>>(
+        src, ld, static_cast<int>(rows), stride, all, static_cast<int>(K), chunks, vec, codes, ldq, scales, lds);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds,
-                       T *dst, int64_t ldd, cudaStream_t stream)
+                       T *dst, int64_t ldd, int sm_count, cudaStream_t stream)
 {
-    const int chunks = static_cast<int>((K + SEGS * 256 - 1) / (SEGS * 256));
-    const int64_t grid = chunk_blocks(rows * chunks);
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const int chunks = static_cast<int>((K + kSegs<T> * 256 - 1) / (kSegs<T> * 256));
     const int vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && (ldd * sizeof(T)) % 16 == 0;
-    dequantise_kernel<T><<<static_cast<unsigned>(grid), THREADS, 0, stream>>>(
-        codes, ldq, scales, lds, rows * chunks, static_cast<int>(K), chunks, vec, dst, ldd);
+    dequantise_kernel<T><<<chunk_grid(rows * chunks, sm_count), THREADS, 0, stream>>>(
+        codes, ldq, scales, lds, rows, static_cast<int>(K), chunks, vec, dst, ldd);
     return cudaGetLastError();
 }
 
@@ -310,11 +376,12 @@ cudaError_t launch_mx4_quantise(bool k_rows, int64_t batch, int64_t rows, int64_
 }
 
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
-                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, cudaStream_t stream)
+                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, int sm_count,
+                                  cudaStream_t stream)
 {
     if (dst_bf16)
-        return dequantise(rows, K, codes, ldq, scales, lds, static_cast<__nv_bfloat16 *>(dst), ldd, stream);
-    return dequantise(rows, K, codes, ldq, scales, lds, static_cast<float *>(dst), ldd, stream);
+        return dequantise(rows, K, codes, ldq, scales, lds, static_cast<__nv_bfloat16 *>(dst), ldd, sm_count, stream);
+    return dequantise(rows, K, codes, ldq, scales, lds, static_cast<float *>(dst), ldd, sm_count, stream);
 }
 
 }  // namespace dg

@@ -17,9 +17,8 @@ enum WaitSite : int {
     kWaitMmaTmemEmpty = 4,
     kWaitEpiTmemFull = 5,
     kWaitDrain = 6,
-    kWaitScaleSmem = 7,
-    kWaitScaleTmem = 8,
-    kWaitMmaScale = 9,
+    kWaitScaleFull = 7,
+    kWaitMmaScale = 8,
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
@@ -489,28 +488,18 @@ __device__ __forceinline__ void tc_mma_mx4_pair(uint32_t d_tmem, uint64_t a_desc
         : "memory");
 }
 
-// 32 lanes x 8 (or 16) consecutive 32-bit columns, written from thread t's
-// registers to lane (lane base + t).
-__device__ __forceinline__ void tmem_store_8cols(uint32_t taddr, const uint32_t (&v)[8])
+// 32 rows x 16 bytes of shared memory (no swizzle, rows 16 bytes apart) into
+// four tensor-memory columns, the same in all four lane quarters; pair form:
+// in both CTAs, each from its own shared memory.  Runs in order with the MMAs
+// of the issuing thread, before and after it.
+__device__ __forceinline__ void tmem_copy_32x16b(uint32_t taddr, uint64_t desc)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t (&v)[16])
+__device__ __forceinline__ void tmem_copy_32x16b_pair(uint32_t taddr, uint64_t desc)
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, "
-        "%9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st()
-{
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
@@ -549,6 +538,7 @@ __device__ __forceinline__ void tmem_wait_ld()
 // stride-dimension byte offsets (all in 16-byte units), descriptor version 1,
 // and the layout type in bits 61..63.
 enum SmemLayout : uint32_t {
+    kLayoutNone = 0,
     kLayoutSw128 = 2,        // 128-byte swizzle, 16-byte atoms
     kLayoutSw128Atom32 = 1,  // 128-byte swizzle, 32-byte atoms (32-bit MN-major operands)
 };

@@ -13,8 +13,17 @@
 //
 // Roles, as in the dense tensor-core kernels: warp 0 TMA producer, warp 1 MMA
 // issuer, warps 2-5 epilogue (two accumulators, so the epilogue of a tile
-// overlaps the next tile's main loop); for 4-bit operands warps 6-9 move the
-// block scales from shared memory into tensor memory.
+// overlaps the next tile's main loop); for 4-bit operands warps 6-8 turn the
+// block scales.
+//
+// Block scales.  TMA brings 16 scale bytes of every row of the tile (a row's
+// scales are contiguous); the tensor core wants, for 128 rows and 128 elements
+// of K, one 4-byte word per row, row i in lane i % 32 of column i / 32.  A
+// scale warp per 128 rows regroups a stage's words to [lane][4] in shared
+// memory, and the MMA issuer copies them to tensor memory (tcgen05.cp) ahead
+// of the stage's MMAs, in order with them: nothing waits for an MMA to finish.
+// (Writing tensor memory from the scale warps, two stages deep, left the
+// tensor pipe 24 % busy: 417 us for 8192 x 14336 x 4096.)
 //
 // Groups.  The offsets stay on the device.  Every CTA builds the running count
 // of its launch's tiles per group in shared memory (one load and a block scan,
@@ -44,7 +53,7 @@ constexpr int BP = kRaggedP;
 constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_BARS = 3 * MAX_STAGES + 2 + 2 + 2 + 1;
+constexpr int NUM_BARS = 4 * MAX_STAGES + 2 + 2 + 1;
 // Accumulators at tensor-memory columns 0 and ACC1; for 4-bit operands the
 // scales of two stages live at SF_COL, so the second accumulator moves down
 // and, for tiles of more than ACC1_MX rows, overlaps the first (see epilogue).
@@ -56,7 +65,7 @@ struct Params {
     const long long *offsets;
     int groups, rows, P, Q, K;
     int bn, tiles_p, tiles_q, group_q;
-    int stages, stage_bytes, q_bytes, sf_bytes, table_bytes;
+    int stages, stage_bytes, q_bytes, table_bytes;
     void *C;
     long long ldc, stride_c;
     int out_bf16, p_chunks, q_chunks;
@@ -186,12 +195,12 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
 }
 
 template <int KIND, int CG, bool P_MN, bool RAGGED_K>
-__global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
+__global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
-    constexpr int THREADS = MX ? 320 : 192;
+    constexpr int THREADS = MX ? 288 : 192;
     constexpr int ES = KIND == kRaggedBf16 ? 2 : 4;                 // bytes an element (not for 4-bit)
     constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
     constexpr int K_STEPS = 4;                                      // MMA instructions of a stage, 32 bytes of K each
@@ -221,8 +230,8 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
     const uint32_t sfull_bar = empty_bar + 8 * MAX_STAGES;  // [stages], scale bytes, each CTA its own
     const uint32_t tfull_bar = sfull_bar + 8 * MAX_STAGES;  // [2]
     const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
-    const uint32_t sready_bar = tempty_bar + 16;            // [2], scales in tensor memory, used in the even CTA
-    const uint32_t drain_bar = sready_bar + 16;
+    const uint32_t sready_bar = tempty_bar + 16;            // [stages], scales regrouped, used in the even CTA
+    const uint32_t drain_bar = sready_bar + 8 * MAX_STAGES;
     uint8_t *tail = smem + ring + p.table_bytes + NUM_BARS * 8;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
@@ -242,11 +251,11 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
             mbar_init(full_bar + 8 * s, 1);
             mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
             mbar_init(sfull_bar + 8 * s, 1);
+            mbar_init(sready_bar + 8 * s, CG * (1 + (p.bn + 127) / 128));  // the scale warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
             mbar_init(tempty_bar + 8 * b, 4 * CG);  // the epilogue warps
-            mbar_init(sready_bar + 8 * b, 4 * CG);  // the scale warps
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -421,9 +430,8 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t slot = it & 1u;
-                    if (MX && !mbar_wait_warp(sready_bar + 8 * slot, (it >> 1) & 1u, abort_flag, p.status,
-                                              kWaitMmaScale, p.timeout_ns)) {
+                    if (MX && !mbar_wait_warp(sready_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaScale,
+                                              p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -440,8 +448,22 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
                                       : smem_desc(q_st + kk * 32, 16, 1024, kLayoutSw128);
                     }
                     const uint32_t acc0 = kt > 0 ? 1u : 0u;
-                    const uint32_t sf = tmem_base + SF_COL + slot * SF_COLS;
+                    const uint32_t sf = tmem_base + SF_COL + (it & 1u) * SF_COLS;
+                    const uint64_t sfd = smem_desc(q_st + p.q_bytes + (BP + p.bn) * 16, 0, 128, kLayoutNone);
                     if (elect_one()) {
+                        if (MX) {
+                            // 512-byte groups: P's two words, then the two words of each 128 rows of Q
+#pragma unroll
+                            for (int i = 0; i < 6; ++i) {
+                                const uint32_t dst = i < 2 ? sf + i * 4 : sf + 8 + (i & 1) * 8 + (i >> 2) * 4;
+                                if (i < 4 || p.bn > 128) {
+                                    if (CG == 2)
+                                        tmem_copy_32x16b_pair(dst, sfd + i * 32);
+                                    else
+                                        tmem_copy_32x16b(dst, sfd + i * 32);
+                                }
+                            }
+                        }
 #pragma unroll
                         for (int kk = 0; kk < K_STEPS; ++kk) {
                             const uint32_t acc = kk > 0 ? 1u : acc0;
@@ -559,58 +581,40 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 320 : 192, 1)
                 __syncwarp();
             }
         }
-    } else if (MX) {
+    } else if (MX && (warp - 7) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
-        // Every scale warp writes all rows' words to its own lane quarter:
-        // lane l holds rows l, l + 32, ... of P and of Q.
-        const int q = warp & 3;
-        uint32_t it = 0, s = 0, ph = 0, ps = 0, pph = 0;  // ps: the stage two back
+        // Warp 6: P's rows; warps 7 and 8: 128 rows of Q each.  Lane l takes
+        // rows l, l + 32, l + 64, l + 96 of its 128.
+        const int part = warp - 6;
+        uint32_t s = 0, ph = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
             const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
-            for (int kt = 0; kt < t.kt; ++kt, ++it) {
-                if (!mbar_wait_warp(sfull_bar + 8 * s, ph, abort_flag, p.status, kWaitScaleSmem, p.timeout_ns)) {
+            for (int kt = 0; kt < t.kt; ++kt) {
+                if (!mbar_wait_warp(sfull_bar + 8 * s, ph, abort_flag, p.status, kWaitScaleFull, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sf = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes + lane * 16 + (kt & 1) * 8;
-                uint32_t wp[8], wq[16];
+                const uint32_t raw = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes;
+                const uint32_t src = raw + part * 2048 + lane * 16 + (kt & 1) * 8;
+                const uint32_t dst = raw + (BP + p.bn) * 16 + part * 1024 + lane * 16;
+                uint32_t a[4], b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(wp[i]), "=r"(wp[4 + i]) : "r"(sf + i * 512));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    wq[i] = wq[8 + i] = 0u;
-                    if (i * 32 < p.bn)
-                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                     : "=r"(wq[i]), "=r"(wq[8 + i])
-                                     : "r"(sf + BP * 16 + i * 512));
-                }
-                // the MMAs that read this slot two stages ago are done
-                if (it >= 2) {
-                    if (!mbar_wait_warp(empty_bar + 8 * ps, pph, abort_flag, p.status, kWaitScaleTmem,
-                                        p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (++ps == static_cast<uint32_t>(p.stages)) {
-                        ps = 0;
-                        pph ^= 1u;
-                    }
-                    tc_fence_after_sync();
-                }
-                const uint32_t slot = it & 1u;
-                const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + SF_COL + slot * SF_COLS;
-                tmem_store_8cols(dst, wp);
-                tmem_store_16cols(dst + 8, wq);
-                tmem_wait_st();
-                tc_fence_before_sync();
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(src + i * 512));
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a[0]), "r"(a[1]), "r"(a[2]),
+                             "r"(a[3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(b[0]), "r"(b[1]),
+                             "r"(b[2]), "r"(b[3])
+                             : "memory");
+                fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
                     if (leader)
-                        mbar_arrive(sready_bar + 8 * slot);
+                        mbar_arrive(sready_bar + 8 * s);
                     else
-                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * slot, 0));
+                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * s, 0));
                 }
                 if (++s == static_cast<uint32_t>(p.stages)) {
                     s = 0;
@@ -648,7 +652,7 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const CUt
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(KIND == kRaggedMx4 ? 320 : 192);
+    cfg.blockDim = dim3(KIND == kRaggedMx4 ? 288 : 192);
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -711,8 +715,10 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
     p.q_bytes = t.bn / t.ctas * 128;
-    p.sf_bytes = kind == kRaggedMx4 ? (BP + t.bn) * 16 : 0;
-    p.stage_bytes = (P_BYTES + p.q_bytes + p.sf_bytes + 1023) / 1024 * 1024;
+    // 4-bit: 16 scale bytes a row as TMA brings them, then the regrouped words
+    // (512 bytes per 128 rows and word; a last group of Q reads rows past bn)
+    const int sf_bytes = kind == kRaggedMx4 ? (BP + t.bn) * 16 + 1024 * (1 + (t.bn + 127) / 128) : 0;
+    p.stage_bytes = (P_BYTES + p.q_bytes + sf_bytes + 1023) / 1024 * 1024;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
     const int fixed = 1024 + p.table_bytes + NUM_BARS * 8 + 16 + 64;
     p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);

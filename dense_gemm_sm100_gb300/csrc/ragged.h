@@ -72,6 +72,7 @@ cudaError_t launch_mx4_quantise(bool k_rows, int64_t batch, int64_t rows, int64_
                                 int64_t stride, bool src_bf16, uint8_t *codes, int64_t ldq, uint8_t *scales,
                                 int64_t lds, int sm_count, cudaStream_t stream);
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
-                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, cudaStream_t stream);
+                                  int64_t lds, void *dst, int64_t ldd, bool dst_bf16, int sm_count,
+                                  cudaStream_t stream);
 
 }  // namespace dg

@@ -587,7 +587,7 @@ int gemm_mx4_dequantise(gemm_handle_t h, int64_t rows, int64_t K, const void *co
     const cudaError_t e =
         dg::launch_mx4_dequantise(rows, K, static_cast<const uint8_t *>(codes), ldq,
                                   static_cast<const uint8_t *>(scales), lds, dst, ldd, dst_dtype == GEMM_BF16,
-                                  stream);
+                                  h->sm_count, stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "dequantisation launch");
     ++h->launches;
     h->last_path = "mx4_dequantise";
