@@ -17,7 +17,7 @@ enum WaitSite : int {
     kWaitMmaTmemEmpty = 4,
     kWaitEpiTmemFull = 5,
     kWaitDrain = 6,
-    kWaitScaleFull = 7,
+    kWaitScaleEmpty = 7,
     kWaitMmaScale = 8,
 };
 
@@ -160,6 +160,12 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr)
 __device__ __forceinline__ void sts_f4(uint32_t addr, float4 v)
 {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
 

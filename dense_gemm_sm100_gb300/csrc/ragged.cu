@@ -16,14 +16,16 @@
 // overlaps the next tile's main loop); for 4-bit operands warps 6-8 turn the
 // block scales.
 //
-// Block scales.  TMA brings 16 scale bytes of every row of the tile (a row's
-// scales are contiguous); the tensor core wants, for 128 rows and 128 elements
-// of K, one 4-byte word per row, row i in lane i % 32 of column i / 32.  A
-// scale warp per 128 rows regroups a stage's words to [lane][4] in shared
-// memory, and the MMA issuer copies them to tensor memory (tcgen05.cp) ahead
-// of the stage's MMAs, in order with them: nothing waits for an MMA to finish.
-// (Writing tensor memory from the scale warps, two stages deep, left the
-// tensor pipe 24 % busy: 417 us for 8192 x 14336 x 4096.)
+// Block scales.  A row's scales are contiguous bytes; the tensor core wants,
+// for 128 rows and 128 elements of K, one 4-byte word per row, row i in lane
+// i % 32 of column i / 32.  A scale warp per 128 rows loads 16 bytes of every
+// row (two ring stages) three steps ahead into registers, writes each stage's
+// words as [lane][4] to shared memory, and the MMA issuer copies them to tensor
+// memory (tcgen05.cp) ahead of the stage's MMAs, in order with them: nothing
+// waits for an MMA to finish.  Measured on 8192 x 14336 x 4096: 417 us with the
+// scale warps writing tensor memory two stages deep (tensor pipe 24 % busy);
+// 393 us with tcgen05.cp but TMA boxes of 16-byte rows, whose 384 rows a stage
+// keep TMA from the operands.
 //
 // Groups.  The offsets stay on the device.  Every CTA builds the running count
 // of its launch's tiles per group in shared memory (one load and a block scan,
@@ -53,7 +55,7 @@ constexpr int BP = kRaggedP;
 constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_BARS = 4 * MAX_STAGES + 2 + 2 + 1;
+constexpr int NUM_BARS = 3 * MAX_STAGES + 2 + 2 + 1;
 // Accumulators at tensor-memory columns 0 and ACC1; for 4-bit operands the
 // scales of two stages live at SF_COL, so the second accumulator moves down
 // and, for tiles of more than ACC1_MX rows, overlaps the first (see epilogue).
@@ -69,6 +71,10 @@ struct Params {
     void *C;
     long long ldc, stride_c;
     int out_bf16, p_chunks, q_chunks;
+    // 4-bit operands: scale bytes of P (groups of P rows) and Q, blocks of K
+    const uint8_t *scale_p, *scale_q;
+    long long lds_p, lds_q;
+    int blocks;
     int *status;
     unsigned long long timeout_ns;
     int debug_drop;
@@ -185,6 +191,31 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u
     return t;
 }
 
+// Walks a CTA's tiles in steps of two ring stages (16 scale bytes a row).
+// Every tile has a stage: not for K = 0.
+template <int BK, bool RAGGED_K>
+struct ScaleCursor {
+    const Params &p;
+    const int *table;
+    int u, num_units, unit_step, kt;
+    Tile t;
+    __device__ ScaleCursor(const Params &params, const int *tab, int first, int units, int step)
+        : p(params), table(tab), u(first), num_units(units), unit_step(step), kt(0)
+    {
+        if (valid()) t = tile_at<BK, RAGGED_K>(p, table, u);
+    }
+    __device__ bool valid() const { return u < num_units; }
+    __device__ void next()
+    {
+        kt += 2;
+        if (kt >= t.kt) {
+            kt = 0;
+            u += unit_step;
+            if (valid()) t = tile_at<BK, RAGGED_K>(p, table, u);
+        }
+    }
+};
+
 // MMA N of a tile: the rows that are left, in the granularity the instruction
 // takes.  The MN-major operand of a ragged contraction keeps whole chunks.
 template <int CG, bool RAGGED_K>
@@ -196,8 +227,7 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
 
 template <int KIND, int CG, bool P_MN, bool RAGGED_K>
 __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
-    ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                  const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ, const Params p)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
     constexpr int THREADS = MX ? 288 : 192;
@@ -227,8 +257,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     const uint32_t bars = sbase + ring + p.table_bytes;
     const uint32_t full_bar = bars;                       // [stages], used in the even CTA
     const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;  // [stages]
-    const uint32_t sfull_bar = empty_bar + 8 * MAX_STAGES;  // [stages], scale bytes, each CTA its own
-    const uint32_t tfull_bar = sfull_bar + 8 * MAX_STAGES;  // [2]
+    const uint32_t tfull_bar = empty_bar + 8 * MAX_STAGES;  // [2]
     const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
     const uint32_t sready_bar = tempty_bar + 16;            // [stages], scales regrouped, used in the even CTA
     const uint32_t drain_bar = sready_bar + 8 * MAX_STAGES;
@@ -250,7 +279,6 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar + 8 * s, 1);
             mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
-            mbar_init(sfull_bar + 8 * s, 1);
             mbar_init(sready_bar + 8 * s, CG * (1 + (p.bn + 127) / 128));  // the scale warps
         }
         for (int b = 0; b < 2; ++b) {
@@ -288,14 +316,9 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
             if (RAGGED_K || p.K > 0) {
                 tma_prefetch_desc(&tmP);
                 tma_prefetch_desc(&tmQ);
-                if (MX) {
-                    tma_prefetch_desc(&tmSP);
-                    tma_prefetch_desc(&tmSQ);
-                }
             }
             const int q_cta = p.bn / CG;  // rows of Q this CTA stages
             const uint32_t tx = static_cast<uint32_t>(CG * (P_BYTES + p.q_bytes));
-            const uint32_t sf_tx = static_cast<uint32_t>((BP + p.bn) * 16);
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
@@ -313,9 +336,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                     const uint32_t fb = CG == 2 ? mapa_shared(fb_local, 0) : fb_local;
                     const uint32_t p_st = sbase + s * p.stage_bytes;
                     const uint32_t q_st = p_st + P_BYTES;
-                    const uint32_t sfb = sfull_bar + 8 * s;
                     if (leader) mbar_arrive_expect_tx(fb_local, tx);
-                    if (MX) mbar_arrive_expect_tx(sfb, sf_tx);
                     if (++s == static_cast<uint32_t>(p.stages)) {
                         s = 0;
                         ph ^= 1u;
@@ -377,12 +398,6 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                         tma_load_2d_pair(q_st, &tmQ, fb, kx, qx);
                     else
                         tma_load_2d(q_st, &tmQ, fb, kx, qx);
-                    if (MX) {
-                        // 16 scale bytes cover two stages; each stage reads its half
-                        const uint32_t sf = q_st + p.q_bytes;
-                        tma_load_3d(sf, &tmSP, sfb, (kt >> 1) * 16, p0, t.g);
-                        tma_load_2d(sf + BP * 16, &tmSQ, sfb, (kt >> 1) * 16, t.lo + t.q0);
-                    }
                 }
             }
             // Stages issued last, oldest first: (s, ph) is the next one.
@@ -398,7 +413,6 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                     // after an abort: leave no copy in flight (the even CTA's
                     // barriers count both CTAs' operand bytes)
                     if (leader) mbar_wait(full_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
-                    if (MX) mbar_wait(sfull_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
                 }
                 if (++ds == static_cast<uint32_t>(p.stages)) {
                     ds = 0;
@@ -449,7 +463,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                     }
                     const uint32_t acc0 = kt > 0 ? 1u : 0u;
                     const uint32_t sf = tmem_base + SF_COL + (it & 1u) * SF_COLS;
-                    const uint64_t sfd = smem_desc(q_st + p.q_bytes + (BP + p.bn) * 16, 0, 128, kLayoutNone);
+                    const uint64_t sfd = smem_desc(q_st + p.q_bytes, 0, 128, kLayoutNone);
                     if (elect_one()) {
                         if (MX) {
                             // 512-byte groups: P's two words, then the two words of each 128 rows of Q
@@ -581,45 +595,83 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                 __syncwarp();
             }
         }
-    } else if (MX && (warp - 7) * 128 < p.bn) {
+    } else if (MX && p.K > 0 && (warp - 7) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
         // Warp 6: P's rows; warps 7 and 8: 128 rows of Q each.  Lane l takes
-        // rows l, l + 32, l + 64, l + 96 of its 128.
+        // rows l, l + 32, l + 64, l + 96 of its 128; out-of-range rows and
+        // blocks get scale byte 0 (their codes are zero).
         const int part = warp - 6;
+        ScaleCursor<BK, RAGGED_K> at(p, table, first_unit, num_units, unit_step);
+        constexpr int AHEAD = 3;
+        uint4 buf[AHEAD][4];
+        const auto fetch = [&](uint4(&d)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (!at.valid()) return;
+            const int first = part == 0 ? (at.t.pb * CG + static_cast<int>(rank)) * BP : at.t.q0 + (part - 1) * 128;
+            const int limit = part == 0 ? p.P : at.t.cnt;
+            const uint8_t *base = part == 0 ? p.scale_p + static_cast<long long>(at.t.g) * p.P * p.lds_p
+                                            : p.scale_q + static_cast<long long>(at.t.lo) * p.lds_q;
+            const long long ld = part == 0 ? p.lds_p : p.lds_q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = first + lane + 32 * i;
+                if (row < limit) d[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ld + at.kt * 8));
+            }
+            const int left = p.blocks - at.kt * 8;  // blocks of K among the 16 bytes
+            if (left < 16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int n = left - 4 * j;
+                        if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
+                    }
+                    d[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            at.next();
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) fetch(buf[i]);
         uint32_t s = 0, ph = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
-            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
-            for (int kt = 0; kt < t.kt; ++kt) {
-                if (!mbar_wait_warp(sfull_bar + 8 * s, ph, abort_flag, p.status, kWaitScaleFull, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t raw = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes;
-                const uint32_t src = raw + part * 2048 + lane * 16 + (kt & 1) * 8;
-                const uint32_t dst = raw + (BP + p.bn) * 16 + part * 1024 + lane * 16;
-                uint32_t a[4], b[4];
+            const int kts = tile_at<BK, RAGGED_K>(p, table, u).kt;
+            for (int kt = 0; ok && kt < kts; kt += 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a[i]), "=r"(b[i]) : "r"(src + i * 512));
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a[0]), "r"(a[1]), "r"(a[2]),
-                             "r"(a[3])
-                             : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(b[0]), "r"(b[1]),
-                             "r"(b[2]), "r"(b[3])
-                             : "memory");
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(sready_bar + 8 * s);
-                    else
-                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * s, 0));
+                for (int half = 0; half < 2; ++half) {
+                    if (kt + half >= kts) break;
+                    if (!mbar_wait_warp(empty_bar + 8 * s, ph ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
+                                        p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes + part * 1024 + lane * 16;
+                    const uint4(&r)[4] = buf[0];
+                    sts_u4(dst, half ? make_uint4(r[0].z, r[1].z, r[2].z, r[3].z)
+                                     : make_uint4(r[0].x, r[1].x, r[2].x, r[3].x));
+                    sts_u4(dst + 512, half ? make_uint4(r[0].w, r[1].w, r[2].w, r[3].w)
+                                           : make_uint4(r[0].y, r[1].y, r[2].y, r[3].y));
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive(sready_bar + 8 * s);
+                        else
+                            mbar_arrive_cluster(mapa_shared(sready_bar + 8 * s, 0));
+                    }
+                    if (++s == static_cast<uint32_t>(p.stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                if (++s == static_cast<uint32_t>(p.stages)) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+#pragma unroll
+                for (int i = 0; i + 1 < AHEAD; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) buf[i][j] = buf[i + 1][j];
+                fetch(buf[AHEAD - 1]);
             }
         }
     }
@@ -647,8 +699,8 @@ cudaError_t set_attrs()
 }
 
 template <int KIND, int CG, bool P_MN, bool RK>
-cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const CUtensorMap &tmSP,
-                       const CUtensorMap &tmSQ, const Params &p, int grid, cudaStream_t stream)
+cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Params &p, int grid,
+                       cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -662,7 +714,7 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const CUt
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK>, tmP, tmQ, tmSP, tmSQ, p);
+    return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK>, tmP, tmQ, p);
 }
 
 }  // namespace
@@ -701,8 +753,7 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
 }
 
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
-                          const CUtensorMap &tmQ, const CUtensorMap &tmSP, const CUtensorMap &tmSQ,
-                          const RaggedArgs &a, int sm_count, int max_ctas)
+                          const CUtensorMap &tmQ, const RaggedArgs &a, int sm_count, int max_ctas)
 {
     Params p;
     p.offsets = reinterpret_cast<const long long *>(a.offsets);
@@ -715,9 +766,8 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
     p.q_bytes = t.bn / t.ctas * 128;
-    // 4-bit: 16 scale bytes a row as TMA brings them, then the regrouped words
-    // (512 bytes per 128 rows and word; a last group of Q reads rows past bn)
-    const int sf_bytes = kind == kRaggedMx4 ? (BP + t.bn) * 16 + 1024 * (1 + (t.bn + 127) / 128) : 0;
+    // 4-bit: two scale words of each row, in groups of 128 rows
+    const int sf_bytes = kind == kRaggedMx4 ? 1024 * (1 + (t.bn + 127) / 128) : 0;
     p.stage_bytes = (P_BYTES + p.q_bytes + sf_bytes + 1023) / 1024 * 1024;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
     const int fixed = 1024 + p.table_bytes + NUM_BARS * 8 + 16 + 64;
@@ -728,6 +778,11 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.out_bf16 = a.out_bf16;
     p.p_chunks = a.p_chunks;
     p.q_chunks = a.q_chunks;
+    p.scale_p = a.scale_p;
+    p.scale_q = a.scale_q;
+    p.lds_p = a.lds_p;
+    p.lds_q = a.lds_q;
+    p.blocks = (a.K + kRaggedBlock - 1) / kRaggedBlock;
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
     p.debug_drop = a.debug_drop;
@@ -740,8 +795,8 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     const int grid = static_cast<int>(t.ctas * std::min(units, slots));
     const bool pair = t.ctas == 2;
 #define DG_RAGGED(KIND, PMN, RK)                                                                  \
-    return pair ? launch_one<KIND, 2, PMN, RK>(tmP, tmQ, tmSP, tmSQ, p, grid, a.stream)           \
-                : launch_one<KIND, 1, PMN, RK>(tmP, tmQ, tmSP, tmSQ, p, grid, a.stream)
+    return pair ? launch_one<KIND, 2, PMN, RK>(tmP, tmQ, p, grid, a.stream)                        \
+                : launch_one<KIND, 1, PMN, RK>(tmP, tmQ, p, grid, a.stream)
     if (kind == kRaggedMx4) DG_RAGGED(kRaggedMx4, false, false);
     if (kind == kRaggedTf32) {
         if (ragged_k) DG_RAGGED(kRaggedTf32, true, true);

@@ -33,6 +33,9 @@ struct RaggedArgs {
     int out_bf16 = 0;
     int p_chunks = 0;  // MN-major P: tmP is the view in 128-byte column chunks
     int q_chunks = 0;  // the same for Q (ragged_k)
+    // kRaggedMx4: scale bytes of B (rows of P, groups one after another) and A
+    const uint8_t *scale_p = nullptr, *scale_q = nullptr;
+    int64_t lds_p = 0, lds_q = 0;
     int *status = nullptr;
     uint64_t timeout_ns = 0;
     int debug_drop = 0;
@@ -59,11 +62,9 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
 inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : 64; }
 
 cudaError_t prepare_ragged();
-// tmP / tmQ: the operand views of ragged_api.cu; tmSP / tmSQ: scale bytes
-// (kRaggedMx4 only, else any map).
+// tmP / tmQ: the operand views of ragged_api.cu.
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
-                          const CUtensorMap &tmQ, const CUtensorMap &tmSP, const CUtensorMap &tmSQ,
-                          const RaggedArgs &a, int sm_count, int max_ctas);
+                          const CUtensorMap &tmQ, const RaggedArgs &a, int sm_count, int max_ctas);
 
 // Quantises `batch` matrices of `rows` x K elements (BF16 or FP32) to E2M1
 // codes and E8M0 scales, batch * rows output rows.  k_rows: element (r, k) is

@@ -373,22 +373,22 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     const int kind = dg::kRaggedMx4;
     const dg::RaggedTile t = tile_for(h, kind, false, rows, groups, N, 0, K);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
-    alignas(64) CUtensorMap tmP = {}, tmQ = {}, tmSP = {}, tmSQ = {};
+    alignas(64) CUtensorMap tmP = {}, tmQ = {};
     if (K > 0) {
         const int64_t Kp = round_up(K, GEMM_MX4_BLOCK);
         const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         int rc = encode_k_major(h, &tmP, u8, 1, bc, Kp / 2, N, bq, groups, N * bq, 128, dg::kRaggedP, sw, true,
                                 "the codes of B");
         if (!rc) rc = encode_k_major(h, &tmQ, u8, 1, ac, Kp / 2, rows, aq, 1, 0, 128, t.bn / t.ctas, sw, false,
                                      "the codes of A");
-        if (!rc) rc = encode_k_major(h, &tmSP, u8, 1, bs, Kp / 32, N, bl, groups, N * bl, 16, dg::kRaggedP, none, true,
-                                     "the scales of B");
-        if (!rc) rc = encode_k_major(h, &tmSQ, u8, 1, as, Kp / 32, rows, al, 1, 0, 16, t.bn, none, false,
-                                     "the scales of A");
         if (rc) return rc;
+        a.scale_p = static_cast<const uint8_t *>(bs);
+        a.lds_p = bl;
+        a.scale_q = static_cast<const uint8_t *>(as);
+        a.lds_q = al;
     }
-    const cudaError_t e = dg::launch_ragged(kind, false, false, t, tmP, tmQ, tmSP, tmSQ, a, h->sm_count, h->max_ctas);
+    const cudaError_t e = dg::launch_ragged(kind, false, false, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "4-bit product launch");
     ++h->launches;
     h->last_path = path_name(offsets ? "grouped" : "tc", kind, t, "");
@@ -465,7 +465,7 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
                                 CU_TENSOR_MAP_SWIZZLE_128B, false, "A");
         if (rc) return rc;
     }
-    const cudaError_t e = dg::launch_ragged(kind, false, row, t, tmP, tmQ, tmP, tmQ, a, h->sm_count, h->max_ctas);
+    const cudaError_t e = dg::launch_ragged(kind, false, row, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "grouped product launch");
     ++h->launches;
     h->last_path = path_name("grouped", kind, t, rest.c_str());
@@ -517,7 +517,7 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
         if (!rc) rc = encode_ragged_k(h, &tmQ, es, A, rows, M, lda, t.bn / t.ctas, a.q_chunks != 0);
         if (rc) return rc;
     }
-    const cudaError_t e = dg::launch_ragged(kind, true, true, t, tmP, tmQ, tmP, tmQ, a, h->sm_count, h->max_ctas);
+    const cudaError_t e = dg::launch_ragged(kind, true, true, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "weight gradient launch");
     ++h->launches;
     h->last_path = path_name("grouped", kind, t, rest.c_str());

@@ -14,7 +14,8 @@
  * with Kp = K rounded up to whole blocks; the codes of elements K .. Kp-1 must
  * be zero (gemm_mx4_quantise writes them so).  Both bases and both pitches are
  * multiples of 16 bytes (else GEMM_ERR_ALIGNMENT).  Bytes past Kp/2 and Kp/32
- * in a row are neither read nor written.
+ * in a row are not written and do not change results; of the scales, those in
+ * the last 16-byte piece may be read.
  *
  * gemm_mx4_quantise    Quantises `batch` matrices of `rows` x K elements of
  *                      type src_dtype (GEMM_F32 or GEMM_BF16) to batch * rows
