@@ -18,14 +18,13 @@
 //
 // Block scales.  A row's scales are contiguous bytes; the tensor core wants,
 // for 128 rows and 128 elements of K, one 4-byte word per row, row i in lane
-// i % 32 of column i / 32.  A scale warp per 128 rows loads 16 bytes of every
-// row (two ring stages) three steps ahead into registers, writes each stage's
-// words as [lane][4] to shared memory, and the MMA issuer copies them to tensor
-// memory (tcgen05.cp) ahead of the stage's MMAs, in order with them: nothing
-// waits for an MMA to finish.  Measured on 8192 x 14336 x 4096: 417 us with the
-// scale warps writing tensor memory two stages deep (tensor pipe 24 % busy);
-// 393 us with tcgen05.cp but TMA boxes of 16-byte rows, whose 384 rows a stage
-// keep TMA from the operands.
+// i % 32 of column i / 32.  A scale warp per 128 rows loads 64 bytes of every
+// row (the scales of SUP = 8 ring stages) into registers, regroups them to
+// [stage][word][lane][4] in one of two shared-memory slots, and the MMA issuer
+// copies a stage's words to tensor memory (tcgen05.cp) ahead of the stage's
+// MMAs, in order with them.  Eight stages at a time because the hand-over (a
+// proxy fence, and a release at cluster scope from the odd CTA of a pair) takes
+// about 1 us: once a stage it set the pace, 395 us for 8192 x 14336 x 4096.
 //
 // Groups.  The offsets stay on the device.  Every CTA builds the running count
 // of its launch's tiles per group in shared memory (one load and a block scan,
@@ -55,19 +54,21 @@ constexpr int BP = kRaggedP;
 constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_BARS = 3 * MAX_STAGES + 2 + 2 + 1;
+constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 2 + 2 + 1;
 // Accumulators at tensor-memory columns 0 and ACC1; for 4-bit operands the
 // scales of two stages live at SF_COL, so the second accumulator moves down
 // and, for tiles of more than ACC1_MX rows, overlaps the first (see epilogue).
 constexpr int ACC1 = 256, ACC1_MX = 208;
 constexpr int SF_COL = 464, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
+constexpr int SUP = 8;           // ring stages whose scales are handed over together
+constexpr int SF_PART = 1024;    // a stage's words of 128 rows
 constexpr int SMEM_MAX = 227 * 1024;
 
 struct Params {
     const long long *offsets;
     int groups, rows, P, Q, K;
     int bn, tiles_p, tiles_q, group_q;
-    int stages, stage_bytes, q_bytes, table_bytes;
+    int stages, stage_bytes, q_bytes, table_bytes, sf_parts;
     void *C;
     long long ldc, stride_c;
     int out_bf16, p_chunks, q_chunks;
@@ -191,31 +192,6 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u
     return t;
 }
 
-// Walks a CTA's tiles in steps of two ring stages (16 scale bytes a row).
-// Every tile has a stage: not for K = 0.
-template <int BK, bool RAGGED_K>
-struct ScaleCursor {
-    const Params &p;
-    const int *table;
-    int u, num_units, unit_step, kt;
-    Tile t;
-    __device__ ScaleCursor(const Params &params, const int *tab, int first, int units, int step)
-        : p(params), table(tab), u(first), num_units(units), unit_step(step), kt(0)
-    {
-        if (valid()) t = tile_at<BK, RAGGED_K>(p, table, u);
-    }
-    __device__ bool valid() const { return u < num_units; }
-    __device__ void next()
-    {
-        kt += 2;
-        if (kt >= t.kt) {
-            kt = 0;
-            u += unit_step;
-            if (valid()) t = tile_at<BK, RAGGED_K>(p, table, u);
-        }
-    }
-};
-
 // MMA N of a tile: the rows that are left, in the granularity the instruction
 // takes.  The MN-major operand of a ragged contraction keeps whole chunks.
 template <int CG, bool RAGGED_K>
@@ -253,15 +229,18 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = raw_addr + pad;
     const uint32_t ring = static_cast<uint32_t>(p.stages * p.stage_bytes);
-    int *table = reinterpret_cast<int *>(smem + ring);
-    const uint32_t bars = sbase + ring + p.table_bytes;
+    const uint32_t sf_slot = static_cast<uint32_t>(MX ? SUP * p.sf_parts * SF_PART : 0);  // scales of SUP stages
+    const uint32_t sf_base = sbase + ring;                                                 // [2]
+    int *table = reinterpret_cast<int *>(smem + ring + 2 * sf_slot);
+    const uint32_t bars = sf_base + 2 * sf_slot + p.table_bytes;
     const uint32_t full_bar = bars;                       // [stages], used in the even CTA
     const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;  // [stages]
     const uint32_t tfull_bar = empty_bar + 8 * MAX_STAGES;  // [2]
     const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
-    const uint32_t sready_bar = tempty_bar + 16;            // [stages], scales regrouped, used in the even CTA
-    const uint32_t drain_bar = sready_bar + 8 * MAX_STAGES;
-    uint8_t *tail = smem + ring + p.table_bytes + NUM_BARS * 8;
+    const uint32_t sready_bar = tempty_bar + 16;            // [2], scale slot filled, used in the even CTA
+    const uint32_t sfree_bar = sready_bar + 16;             // [2], scale slot read
+    const uint32_t drain_bar = sfree_bar + 16;
+    uint8_t *tail = smem + ring + 2 * sf_slot + p.table_bytes + NUM_BARS * 8;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
     int *warp_sum = reinterpret_cast<int *>(tail + 16);
@@ -279,11 +258,12 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar + 8 * s, 1);
             mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
-            mbar_init(sready_bar + 8 * s, CG * (1 + (p.bn + 127) / 128));  // the scale warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
             mbar_init(tempty_bar + 8 * b, 4 * CG);  // the epilogue warps
+            mbar_init(sready_bar + 8 * b, CG * p.sf_parts);  // the scale warps
+            mbar_init(sfree_bar + 8 * b, 1);                 // the MMA issuer's commit
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -423,7 +403,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (even CTA)
         if (leader) {
-            uint32_t it = 0, s = 0, ph = 0, acc_it = 0;
+            uint32_t it = 0, s = 0, ph = 0, acc_it = 0, sup = 0;
             bool ok = true, issued = false;
             for (int u = first_unit; ok && u < num_units; u += unit_step, ++acc_it) {
                 const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
@@ -444,8 +424,9 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                         ok = false;
                         break;
                     }
-                    if (MX && !mbar_wait_warp(sready_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaScale,
-                                              p.timeout_ns)) {
+                    if (MX && kt % SUP == 0 &&
+                        !mbar_wait_warp(sready_bar + 8 * (sup & 1u), (sup >> 1) & 1u, abort_flag, p.status,
+                                        kWaitMmaScale, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -463,7 +444,9 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                     }
                     const uint32_t acc0 = kt > 0 ? 1u : 0u;
                     const uint32_t sf = tmem_base + SF_COL + (it & 1u) * SF_COLS;
-                    const uint64_t sfd = smem_desc(q_st + p.q_bytes, 0, 128, kLayoutNone);
+                    const uint64_t sfd = smem_desc(
+                        sf_base + (sup & 1u) * sf_slot + static_cast<uint32_t>((kt % SUP) * p.sf_parts * SF_PART), 0,
+                        128, kLayoutNone);
                     if (elect_one()) {
                         if (MX) {
                             // 512-byte groups: P's two words, then the two words of each 128 rows of Q
@@ -504,8 +487,15 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                             tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
                         else
                             tc_commit(empty_bar + 8 * s);
+                        if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) {
+                            if (CG == 2)
+                                tc_commit_pair_multicast(sfree_bar + 8 * (sup & 1u), 0x3);
+                            else
+                                tc_commit(sfree_bar + 8 * (sup & 1u));
+                        }
                     }
                     __syncwarp();
+                    if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) ++sup;
                     issued = true;
                     if (++s == static_cast<uint32_t>(p.stages)) {
                         s = 0;
@@ -547,51 +537,57 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                 RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
             const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * acc1;
-            // Chunks of 32 columns.  Overlapping accumulators share columns
-            // 208..255: the first one's chunks 6 and 7 and the second one's
-            // chunks 0 and 1, which go first and are handed over at once.
             const int chunks = (t.qn + 31) / 32;
-            const int release = overlap ? 1 : chunks - 1;  // position after which the MMA warp may go on
-            const int order = overlap ? 8 : chunks;
+            const auto load = [&](int c, uint32_t(&v)[32]) {
+                if (c >= chunks) return;
+                if (t.kt > 0) {
+                    tmem_load_32cols(t_row + c * 32, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;  // the empty sum
+                }
+            };
+            const auto store = [&](int c, const uint32_t(&v)[32]) {
+                if (c >= chunks || col >= p.P) return;
+                const int n = t.qn - c * 32;
+                const long long at = base + static_cast<long long>(c * 32) * p.ldc;
+                if (p.out_bf16) {
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, out += p.ldc)
+                        if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
+                } else {
+                    float *out = static_cast<float *>(p.C) + at;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, out += p.ldc)
+                        if (j < n) *out = __uint_as_float(v[j]);
+                }
+            };
+            const auto release = [&](uint32_t bar) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(bar);
+                    else
+                        mbar_arrive_cluster(mapa_shared(bar, 0));
+                }
+            };
+            // Chunks of 32 columns, two at a time.  Overlapping accumulators
+            // share columns 208..255, the first one's chunks 6 and 7 and the
+            // second one's chunks 0 and 1: that pair goes first and is handed
+            // over before its stores.
+            uint32_t v[2][32];
+            const int pairs = overlap ? 4 : (chunks + 1) / 2;
 #pragma unroll 1
-            for (int i = 0; i < order; ++i) {
-                const int c = overlap && abuf == 0 ? (i + 6) & 7 : i;
-                uint32_t v[32];
-                if (c < chunks) {
-                    if (t.kt > 0) {
-                        tmem_load_32cols(t_row + c * 32, v);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0u;  // the empty sum
-                    }
-                }
-                if (i == release) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
-                        if (leader)
-                            mbar_arrive(eb);
-                        else
-                            mbar_arrive_cluster(mapa_shared(eb, 0));
-                    }
-                }
-                if (c < chunks && col < p.P) {
-                    const int n = t.qn - c * 32;
-                    const long long at = base + static_cast<long long>(c * 32) * p.ldc;
-                    if (p.out_bf16) {
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j, out += p.ldc)
-                            if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
-                    } else {
-                        float *out = static_cast<float *>(p.C) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j, out += p.ldc)
-                            if (j < n) *out = __uint_as_float(v[j]);
-                    }
-                }
+            for (int i = 0; i < pairs; ++i) {
+                const int c = 2 * (overlap && abuf == 0 ? (i + 3) & 3 : i);
+                load(c, v[0]);
+                load(c + 1, v[1]);
+                tmem_wait_ld();
+                if (overlap ? i == 0 : i == pairs - 1) release(overlap ? tempty_bar : tempty_bar + 8 * abuf);
+                store(c, v[0]);
+                store(c + 1, v[1]);
                 __syncwarp();
             }
         }
@@ -601,77 +597,61 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
         // rows l, l + 32, l + 64, l + 96 of its 128; out-of-range rows and
         // blocks get scale byte 0 (their codes are zero).
         const int part = warp - 6;
-        ScaleCursor<BK, RAGGED_K> at(p, table, first_unit, num_units, unit_step);
-        constexpr int AHEAD = 3;
-        uint4 buf[AHEAD][4];
-        const auto fetch = [&](uint4(&d)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (!at.valid()) return;
-            const int first = part == 0 ? (at.t.pb * CG + static_cast<int>(rank)) * BP : at.t.q0 + (part - 1) * 128;
-            const int limit = part == 0 ? p.P : at.t.cnt;
-            const uint8_t *base = part == 0 ? p.scale_p + static_cast<long long>(at.t.g) * p.P * p.lds_p
-                                            : p.scale_q + static_cast<long long>(at.t.lo) * p.lds_q;
-            const long long ld = part == 0 ? p.lds_p : p.lds_q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = first + lane + 32 * i;
-                if (row < limit) d[i] = __ldg(reinterpret_cast<const uint4 *>(base + row * ld + at.kt * 8));
-            }
-            const int left = p.blocks - at.kt * 8;  // blocks of K among the 16 bytes
-            if (left < 16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = left - 4 * j;
-                        if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
-                    }
-                    d[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            at.next();
-        };
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) fetch(buf[i]);
-        uint32_t s = 0, ph = 0;
+        uint32_t sup = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
-            const int kts = tile_at<BK, RAGGED_K>(p, table, u).kt;
-            for (int kt = 0; ok && kt < kts; kt += 2) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+            const int first = part == 0 ? (t.pb * CG + static_cast<int>(rank)) * BP : t.q0 + (part - 1) * 128;
+            const int limit = part == 0 ? p.P : t.cnt;
+            const long long ld = part == 0 ? p.lds_p : p.lds_q;
+            const uint8_t *base = (part == 0 ? p.scale_p + static_cast<long long>(t.g) * p.P * ld
+                                             : p.scale_q + static_cast<long long>(t.lo) * ld) +
+                                  (first + lane) * ld;
+            for (int k0 = 0; k0 < t.kt; k0 += SUP, ++sup) {
+                const int left = p.blocks - k0 * 8;  // blocks of K from here on; 16 to a 16-byte piece
+                uint4 r[SUP / 2][4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (kt + half >= kts) break;
-                    if (!mbar_wait_warp(empty_bar + 8 * s, ph ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
-                                        p.timeout_ns)) {
-                        ok = false;
-                        break;
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < SUP / 2; ++j) {
+                        r[j][i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (first + lane + 32 * i < limit && j * 16 < left)
+                            r[j][i] = __ldg(reinterpret_cast<const uint4 *>(base + 32 * i * ld + k0 * 8 + j * 16));
                     }
-                    const uint32_t dst = sbase + s * p.stage_bytes + P_BYTES + p.q_bytes + part * 1024 + lane * 16;
-                    const uint4(&r)[4] = buf[0];
-                    sts_u4(dst, half ? make_uint4(r[0].z, r[1].z, r[2].z, r[3].z)
-                                     : make_uint4(r[0].x, r[1].x, r[2].x, r[3].x));
-                    sts_u4(dst + 512, half ? make_uint4(r[0].w, r[1].w, r[2].w, r[3].w)
-                                           : make_uint4(r[0].y, r[1].y, r[2].y, r[3].y));
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader)
-                            mbar_arrive(sready_bar + 8 * s);
-                        else
-                            mbar_arrive_cluster(mapa_shared(sready_bar + 8 * s, 0));
-                    }
-                    if (++s == static_cast<uint32_t>(p.stages)) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                const uint32_t slot = sup & 1u;
+                if (!mbar_wait_warp(sfree_bar + 8 * slot, ((sup >> 1) & 1u) ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
+                                    p.timeout_ns)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t dst = sf_base + slot * sf_slot + part * SF_PART + lane * 16;
 #pragma unroll
-                for (int i = 0; i + 1 < AHEAD; ++i)
+                for (int j = 0; j < SUP / 2; ++j) {
+                    if (j * 16 >= left) break;
+                    uint32_t w[4][4];  // word, row
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) buf[i][j] = buf[i + 1][j];
-                fetch(buf[AHEAD - 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        w[0][i] = r[j][i].x, w[1][i] = r[j][i].y, w[2][i] = r[j][i].z, w[3][i] = r[j][i].w;
+                        if (left - j * 16 < 16)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int n = left - j * 16 - 4 * k;
+                                if (n < 4) w[k][i] = n <= 0 ? 0u : w[k][i] & ((1u << (8 * n)) - 1u);
+                            }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts_u4(dst + (2 * j + (k >> 1)) * p.sf_parts * SF_PART + (k & 1) * 512,
+                               make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]));
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(sready_bar + 8 * slot);
+                    else
+                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * slot, 0));
+                }
             }
         }
     }
@@ -766,11 +746,11 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
     p.q_bytes = t.bn / t.ctas * 128;
-    // 4-bit: two scale words of each row, in groups of 128 rows
-    const int sf_bytes = kind == kRaggedMx4 ? 1024 * (1 + (t.bn + 127) / 128) : 0;
-    p.stage_bytes = (P_BYTES + p.q_bytes + sf_bytes + 1023) / 1024 * 1024;
+    p.stage_bytes = P_BYTES + p.q_bytes;
+    p.sf_parts = 1 + (t.bn + 127) / 128;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
-    const int fixed = 1024 + p.table_bytes + NUM_BARS * 8 + 16 + 64;
+    const int sf_bytes = kind == kRaggedMx4 ? 2 * SUP * p.sf_parts * SF_PART : 0;
+    const int fixed = 1024 + sf_bytes + p.table_bytes + NUM_BARS * 8 + 16 + 64;
     p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);
     p.C = a.C;
     p.ldc = a.ldc;
