@@ -7,14 +7,18 @@
 // rows of C ("Q").  N can be any multiple of 16 (32 for a CTA pair), so a
 // group's last tile shrinks the instruction to the rows that are left, and few
 // rows per expert do not pay for 128-row tiles.  In the epilogue a warp holds
-// 32 neighbouring columns of C and walks the rows: every store instruction
-// writes 32 neighbouring elements, at any pitch and alignment of C, and rows
-// of the next group are never touched.
+// 32 neighbouring columns of C and walks the rows.  Where C's rows start on 16
+// bytes the warp turns 32 x 32 elements in shared memory and writes 16 bytes a
+// lane; else every store instruction writes 32 neighbouring elements, at any
+// pitch and alignment.  Either way a tile ends at its group's last row, and
+// rows of the next group are never touched.
 //
 // Roles, as in the dense tensor-core kernels: warp 0 TMA producer, warp 1 MMA
-// issuer, warps 2-5 epilogue (two accumulators, so the epilogue of a tile
-// overlaps the next tile's main loop); for 4-bit operands warps 6-8 turn the
-// block scales.
+// issuer, warps 2-9 epilogue (two accumulators, so the epilogue of a tile
+// overlaps the next tile's main loop; two warps a scheduler, because one warp
+// issues every fourth cycle at best: 4.6 us for a 128 x 256 tile with four
+// warps, which set the pace below K = 4096); for 4-bit operands warps 10-12
+// regroup the block scales.
 //
 // Block scales.  A row's scales are contiguous bytes; the tensor core wants,
 // for 128 rows and 128 elements of K, one 4-byte word per row, row i in lane
@@ -62,6 +66,9 @@ constexpr int ACC1 = 256, ACC1_MX = 208;
 constexpr int SF_COL = 464, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
 constexpr int SUP = 8;           // ring stages whose scales are handed over together
 constexpr int SF_PART = 1024;    // a stage's words of 128 rows
+constexpr int EPI_WARPS = 8;
+constexpr int EPI_BYTES = EPI_WARPS * 2048;  // a warp's staging: 32 x 32 BF16 or 16 x 32 FP32
+constexpr int WARPS = 2 + EPI_WARPS, WARPS_MX = WARPS + 3;
 constexpr int SMEM_MAX = 227 * 1024;
 
 struct Params {
@@ -72,6 +79,7 @@ struct Params {
     void *C;
     long long ldc, stride_c;
     int out_bf16, p_chunks, q_chunks;
+    int c_vec;  // 1: C is written in pieces of 16 bytes
     // 4-bit operands: scale bytes of P (groups of P rows) and Q, blocks of K
     const uint8_t *scale_p, *scale_q;
     long long lds_p, lds_q;
@@ -202,11 +210,11 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
 }
 
 template <int KIND, int CG, bool P_MN, bool RAGGED_K>
-__global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
+__global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
-    constexpr int THREADS = MX ? 288 : 192;
+    constexpr int THREADS = 32 * (MX ? WARPS_MX : WARPS);
     constexpr int ES = KIND == kRaggedBf16 ? 2 : 4;                 // bytes an element (not for 4-bit)
     constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
     constexpr int K_STEPS = 4;                                      // MMA instructions of a stage, 32 bytes of K each
@@ -231,8 +239,9 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     const uint32_t ring = static_cast<uint32_t>(p.stages * p.stage_bytes);
     const uint32_t sf_slot = static_cast<uint32_t>(MX ? SUP * p.sf_parts * SF_PART : 0);  // scales of SUP stages
     const uint32_t sf_base = sbase + ring;                                                 // [2]
-    int *table = reinterpret_cast<int *>(smem + ring + 2 * sf_slot);
-    const uint32_t bars = sf_base + 2 * sf_slot + p.table_bytes;
+    const uint32_t epi_base = sf_base + 2 * sf_slot;
+    int *table = reinterpret_cast<int *>(smem + ring + 2 * sf_slot + EPI_BYTES);
+    const uint32_t bars = epi_base + EPI_BYTES + p.table_bytes;
     const uint32_t full_bar = bars;                       // [stages], used in the even CTA
     const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;  // [stages]
     const uint32_t tfull_bar = empty_bar + 8 * MAX_STAGES;  // [2]
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
     const uint32_t sready_bar = tempty_bar + 16;            // [2], scale slot filled, used in the even CTA
     const uint32_t sfree_bar = sready_bar + 16;             // [2], scale slot read
     const uint32_t drain_bar = sfree_bar + 16;
-    uint8_t *tail = smem + ring + 2 * sf_slot + p.table_bytes + NUM_BARS * 8;
+    uint8_t *tail = smem + ring + 2 * sf_slot + EPI_BYTES + p.table_bytes + NUM_BARS * 8;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
     int *warp_sum = reinterpret_cast<int *>(tail + 16);
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
-            mbar_init(tempty_bar + 8 * b, 4 * CG);  // the epilogue warps
+            mbar_init(tempty_bar + 8 * b, EPI_WARPS * CG);
             mbar_init(sready_bar + 8 * b, CG * p.sf_parts);  // the scale warps
             mbar_init(sfree_bar + 8 * b, 1);                 // the MMA issuer's commit
         }
@@ -521,9 +530,11 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                 mbar_wait(drain_bar, 0, &dummy, nullptr, kWaitDrain, p.timeout_ns);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
-        const int q = warp & 3;
+        const int q = warp & 3;            // tensor-memory lane quarter
+        const int half = (warp - 2) >> 2;  // 0: even chunks of 32 rows of C, 1: odd ones
+        const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 2048;
         uint32_t acc_it = 0;
         for (int u = first_unit; u < num_units; u += unit_step, ++acc_it) {
             const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
@@ -532,10 +543,9 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                                 p.timeout_ns))
                 break;
             tc_fence_after_sync();
-            const int col = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32 + lane;
-            const long long first_row =
-                RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
-            const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col;
+            const int col0 = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32;  // the warp's first column
+            const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
+            const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col0;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * acc1;
             const int chunks = (t.qn + 31) / 32;
             const auto load = [&](int c, uint32_t(&v)[32]) {
@@ -548,55 +558,112 @@ __global__ void __launch_bounds__(KIND == kRaggedMx4 ? 288 : 192, 1)
                 }
             };
             const auto store = [&](int c, const uint32_t(&v)[32]) {
-                if (c >= chunks || col >= p.P) return;
-                const int n = t.qn - c * 32;
+                if (c >= chunks || col0 >= p.P) return;
+                const int n = t.qn - c * 32;  // rows left
                 const long long at = base + static_cast<long long>(c * 32) * p.ldc;
-                if (p.out_bf16) {
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
+                if (p.c_vec && p.out_bf16) {
+                    // words of two rows' neighbours, [row pair][column]
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, out += p.ldc)
-                        if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
-                } else {
-                    float *out = static_cast<float *>(p.C) + at;
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat162 w =
+                            __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + j * 128 + lane * 4),
+                                     "r"(*reinterpret_cast<const uint32_t *>(&w))
+                                     : "memory");
+                    }
+                    __syncwarp();
+                    // a lane: eight columns of two rows
+                    const int piece = (lane & 3) * 8;
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + (lane >> 2) * 2 * p.ldc + piece;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, out += p.ldc)
-                        if (j < n) *out = __uint_as_float(v[j]);
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = (i * 8 + (lane >> 2)) * 2;
+                        const uint32_t src = stage + (i * 8 + (lane >> 2)) * 128 + piece * 4;
+                        const uint4 a = lds_u4(src), b = lds_u4(src + 16);
+                        if (col0 + piece < p.P) {
+                            if (r < n)
+                                *reinterpret_cast<uint4 *>(out) =
+                                    make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                            if (r + 1 < n)
+                                *reinterpret_cast<uint4 *>(out + p.ldc) =
+                                    make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+                        }
+                        out += 16 * p.ldc;
+                    }
+                    __syncwarp();
+                } else if (p.c_vec) {
+                    const int piece = (lane & 7) * 4;
+                    float *out = static_cast<float *>(p.C) + at + (lane >> 3) * p.ldc + piece;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + j * 128 + lane * 4), "r"(v[h * 16 + j])
+                                         : "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = h * 16 + i * 4 + (lane >> 3);
+                            const uint4 x = lds_u4(stage + (i * 4 + (lane >> 3)) * 128 + piece * 4);
+                            if (r < n && col0 + piece < p.P) *reinterpret_cast<uint4 *>(out) = x;
+                            out += 4 * p.ldc;
+                        }
+                        __syncwarp();
+                    }
+                } else if (col0 + lane < p.P) {
+                    if (p.out_bf16) {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                            if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
+                    } else {
+                        float *out = static_cast<float *>(p.C) + at + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                            if (j < n) *out = __uint_as_float(v[j]);
+                    }
                 }
             };
-            const auto release = [&](uint32_t bar) {
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(bar);
-                    else
-                        mbar_arrive_cluster(mapa_shared(bar, 0));
-                }
-            };
-            // Chunks of 32 columns, two at a time.  Overlapping accumulators
-            // share columns 208..255, the first one's chunks 6 and 7 and the
-            // second one's chunks 0 and 1: that pair goes first and is handed
-            // over before its stores.
+            // A warp's chunks, two at a time.  Overlapping accumulators share
+            // columns 208..255, the first one's chunks 6 and 7 and the second
+            // one's chunks 0 and 1: those go first and are handed over before
+            // their stores.
             uint32_t v[2][32];
-            const int pairs = overlap ? 4 : (chunks + 1) / 2;
+            const int mine = overlap ? 4 : (chunks + 1 - half) / 2;
+            const int turn = overlap && abuf == 0 ? 3 : 0;
+            bool released = false;
 #pragma unroll 1
-            for (int i = 0; i < pairs; ++i) {
-                const int c = 2 * (overlap && abuf == 0 ? (i + 3) & 3 : i);
-                load(c, v[0]);
-                load(c + 1, v[1]);
+            for (int i = 0; i < mine || !released; i += 2) {
+                const int c0 = overlap ? 2 * ((i + turn) & 3) + half : 2 * i + half;
+                const int c1 = overlap ? 2 * ((i + 1 + turn) & 3) + half : 2 * (i + 1) + half;
+                load(c0, v[0]);
+                load(c1, v[1]);
                 tmem_wait_ld();
-                if (overlap ? i == 0 : i == pairs - 1) release(overlap ? tempty_bar : tempty_bar + 8 * abuf);
-                store(c, v[0]);
-                store(c + 1, v[1]);
-                __syncwarp();
+                if (!released && (overlap || i + 2 >= mine)) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
+                        if (leader)
+                            mbar_arrive(eb);
+                        else
+                            mbar_arrive_cluster(mapa_shared(eb, 0));
+                    }
+                    released = true;
+                }
+                store(c0, v[0]);
+                store(c1, v[1]);
             }
+            __syncwarp();
         }
-    } else if (MX && p.K > 0 && (warp - 7) * 128 < p.bn) {
+    } else if (MX && p.K > 0 && (warp - 2 - EPI_WARPS - 1) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
-        // Warp 6: P's rows; warps 7 and 8: 128 rows of Q each.  Lane l takes
+        // The first: P's rows; the others: 128 rows of Q each.  Lane l takes
         // rows l, l + 32, l + 64, l + 96 of its 128; out-of-range rows and
         // blocks get scale byte 0 (their codes are zero).
-        const int part = warp - 6;
+        const int part = warp - 2 - EPI_WARPS;
         uint32_t sup = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
@@ -684,7 +751,7 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Par
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(KIND == kRaggedMx4 ? 288 : 192);
+    cfg.blockDim = dim3(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS));
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -750,12 +817,16 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.sf_parts = 1 + (t.bn + 127) / 128;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
     const int sf_bytes = kind == kRaggedMx4 ? 2 * SUP * p.sf_parts * SF_PART : 0;
-    const int fixed = 1024 + sf_bytes + p.table_bytes + NUM_BARS * 8 + 16 + 64;
+    const int fixed = 1024 + sf_bytes + EPI_BYTES + p.table_bytes + NUM_BARS * 8 + 16 + 64;
     p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);
     p.C = a.C;
     p.ldc = a.ldc;
     p.stride_c = a.stride_c;
     p.out_bf16 = a.out_bf16;
+    // 16-byte pieces of C: aligned rows that hold whole pieces
+    const int eo = a.out_bf16 ? 2 : 4;
+    p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && (a.ldc * eo) % 16 == 0 && (a.stride_c * eo) % 16 == 0 &&
+              (int64_t{a.P} * eo) % 16 == 0;
     p.p_chunks = a.p_chunks;
     p.q_chunks = a.q_chunks;
     p.scale_p = a.scale_p;
