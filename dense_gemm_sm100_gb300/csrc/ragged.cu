@@ -59,11 +59,12 @@ constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 2 + 2 + 1;
-// Accumulators at tensor-memory columns 0 and ACC1; for 4-bit operands the
-// scales of two stages live at SF_COL, so the second accumulator moves down
-// and, for tiles of more than ACC1_MX rows, overlaps the first (see epilogue).
-constexpr int ACC1 = 256, ACC1_MX = 208;
-constexpr int SF_COL = 464, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
+// Accumulators at tensor-memory columns 0 and ACC1.  For 4-bit operands the
+// scales of two stages live at SF_COL, which leaves two accumulators of 224
+// rows.  (256 rows, the accumulators sharing 48 columns that the epilogue frees
+// first: 163 us for 8192 x 14336 x 4096, 2.5 us of every tile in that hand-over.)
+constexpr int ACC1 = 256, ACC1_MX = 224;
+constexpr int SF_COL = 448, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
 constexpr int SUP = 8;           // ring stages whose scales are handed over together
 constexpr int SF_PART = 1024;    // a stage's words of 128 rows
 constexpr int EPI_WARPS = 8;
@@ -261,7 +262,6 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     const int first_unit = blockIdx.x / CG;
     const int unit_step = gridDim.x / CG;
     const int acc1 = MX ? ACC1_MX : ACC1;
-    const bool overlap = MX && p.bn > ACC1_MX;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
             mbar_init(tempty_bar + 8 * b, EPI_WARPS * CG);
-            mbar_init(sready_bar + 8 * b, CG * p.sf_parts);  // the scale warps
+            mbar_init(sready_bar + 8 * b, p.sf_parts + (CG == 2 && leader ? 1 : 0));  // scale warps, the odd CTA
             mbar_init(sfree_bar + 8 * b, 1);                 // the MMA issuer's commit
         }
         mbar_init(drain_bar, 1);
@@ -418,11 +418,8 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
                 const uint32_t abuf = acc_it & 1u;
                 const uint32_t idesc = IDESC | (static_cast<uint32_t>(mma_n<CG, RAGGED_K>(p, t) >> 3) << 17);
-                // The accumulator is free: tile i - 2 drained, or, where the two
-                // overlap, the columns tile i - 1 shares with this one.
-                const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
-                const uint32_t eph = overlap ? (acc_it & 1u) ^ 1u : ((acc_it >> 1) & 1u) ^ 1u;
-                if (!mbar_wait_warp(eb, eph, abort_flag, p.status, kWaitMmaTmemEmpty, p.timeout_ns)) {
+                if (!mbar_wait_warp(tempty_bar + 8 * abuf, ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                                    kWaitMmaTmemEmpty, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -529,6 +526,24 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 int dummy = 0;
                 mbar_wait(drain_bar, 0, &dummy, nullptr, kWaitDrain, p.timeout_ns);
             }
+        } else if (MX) {
+            // The odd CTA's scale slots, announced to the issuer: the release
+            // at cluster scope takes about 1 us, which the scale warps are
+            // spared.
+            uint32_t sup = 0;
+            bool ok = true;
+            for (int u = first_unit; ok && u < num_units; u += unit_step) {
+                const int kts = tile_at<BK, RAGGED_K>(p, table, u).kt;
+                for (int k0 = 0; k0 < kts; k0 += SUP, ++sup) {
+                    if (!mbar_wait_warp(sready_bar + 8 * (sup & 1u), (sup >> 1) & 1u, abort_flag, p.status,
+                                        kWaitMmaScale, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(sready_bar + 8 * (sup & 1u), 0));
+                    __syncwarp();
+                }
+            }
         }
     } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------------ epilogue
@@ -626,32 +641,25 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                     }
                 }
             };
-            // A warp's chunks, two at a time.  Overlapping accumulators share
-            // columns 208..255, the first one's chunks 6 and 7 and the second
-            // one's chunks 0 and 1: those go first and are handed over before
-            // their stores.
+            // A warp's chunks, two at a time; the accumulator is free once the
+            // last are in registers.
             uint32_t v[2][32];
-            const int mine = overlap ? 4 : (chunks + 1 - half) / 2;
-            const int turn = overlap && abuf == 0 ? 3 : 0;
-            bool released = false;
+            const int mine = (chunks + 1 - half) / 2;
 #pragma unroll 1
-            for (int i = 0; i < mine || !released; i += 2) {
-                const int c0 = overlap ? 2 * ((i + turn) & 3) + half : 2 * i + half;
-                const int c1 = overlap ? 2 * ((i + 1 + turn) & 3) + half : 2 * (i + 1) + half;
+            for (int i = 0; i == 0 || i < mine; i += 2) {
+                const int c0 = 2 * i + half, c1 = c0 + 2;
                 load(c0, v[0]);
                 load(c1, v[1]);
                 tmem_wait_ld();
-                if (!released && (overlap || i + 2 >= mine)) {
+                if (i + 2 >= mine) {
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        const uint32_t eb = overlap ? tempty_bar : tempty_bar + 8 * abuf;
                         if (leader)
-                            mbar_arrive(eb);
+                            mbar_arrive(tempty_bar + 8 * abuf);
                         else
-                            mbar_arrive_cluster(mapa_shared(eb, 0));
+                            mbar_arrive_cluster(mapa_shared(tempty_bar + 8 * abuf, 0));
                     }
-                    released = true;
                 }
                 store(c0, v[0]);
                 store(c1, v[1]);
@@ -660,66 +668,76 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         }
     } else if (MX && p.K > 0 && (warp - 2 - EPI_WARPS - 1) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
-        // The first: P's rows; the others: 128 rows of Q each.  Lane l takes
-        // rows l, l + 32, l + 64, l + 96 of its 128; out-of-range rows and
-        // blocks get scale byte 0 (their codes are zero).
+        // The first: P's rows; the others: 128 rows of Q each.  Out-of-range
+        // rows and blocks get scale byte 0 (their codes are zero).
+        // The loads of the next hand-over are issued before the fence of the
+        // present one, so their latencies overlap.
         const int part = warp - 2 - EPI_WARPS;
-        uint32_t sup = 0;
-        bool ok = true;
-        for (int u = first_unit; ok && u < num_units; u += unit_step) {
+        const long long ld = part == 0 ? p.lds_p : p.lds_q;
+        int u = first_unit, k0 = 0, kts = 0, first = 0, limit = 0;
+        const uint8_t *base = nullptr;
+        // Lane l loads 16-byte piece l % 4 of rows l / 4, l / 4 + 8, ...: eight
+        // rows' 64 bytes an instruction, whole sectors.
+        const int piece = lane & 3, row8 = lane >> 2;
+        uint4 r[16];
+        const auto tile = [&]() {
+            if (u >= num_units) return;
             const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
-            const int first = part == 0 ? (t.pb * CG + static_cast<int>(rank)) * BP : t.q0 + (part - 1) * 128;
-            const int limit = part == 0 ? p.P : t.cnt;
-            const long long ld = part == 0 ? p.lds_p : p.lds_q;
-            const uint8_t *base = (part == 0 ? p.scale_p + static_cast<long long>(t.g) * p.P * ld
-                                             : p.scale_q + static_cast<long long>(t.lo) * ld) +
-                                  (first + lane) * ld;
-            for (int k0 = 0; k0 < t.kt; k0 += SUP, ++sup) {
-                const int left = p.blocks - k0 * 8;  // blocks of K from here on; 16 to a 16-byte piece
-                uint4 r[SUP / 2][4];
+            kts = t.kt;
+            first = (part == 0 ? (t.pb * CG + static_cast<int>(rank)) * BP : t.q0 + (part - 1) * 128) + row8;
+            limit = part == 0 ? p.P : t.cnt;
+            base = (part == 0 ? p.scale_p + static_cast<long long>(t.g) * p.P * ld
+                              : p.scale_q + static_cast<long long>(t.lo) * ld) +
+                   first * ld + piece * 16;
+        };
+        const auto fetch = [&]() {
+            const bool in_k = u < num_units && k0 * 8 + piece * 16 < p.blocks;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < SUP / 2; ++j) {
-                        r[j][i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (first + lane + 32 * i < limit && j * 16 < left)
-                            r[j][i] = __ldg(reinterpret_cast<const uint4 *>(base + 32 * i * ld + k0 * 8 + j * 16));
-                    }
-                const uint32_t slot = sup & 1u;
-                if (!mbar_wait_warp(sfree_bar + 8 * slot, ((sup >> 1) & 1u) ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
-                                    p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = sf_base + slot * sf_slot + part * SF_PART + lane * 16;
-#pragma unroll
-                for (int j = 0; j < SUP / 2; ++j) {
-                    if (j * 16 >= left) break;
-                    uint32_t w[4][4];  // word, row
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[0][i] = r[j][i].x, w[1][i] = r[j][i].y, w[2][i] = r[j][i].z, w[3][i] = r[j][i].w;
-                        if (left - j * 16 < 16)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int n = left - j * 16 - 4 * k;
-                                if (n < 4) w[k][i] = n <= 0 ? 0u : w[k][i] & ((1u << (8 * n)) - 1u);
-                            }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sts_u4(dst + (2 * j + (k >> 1)) * p.sf_parts * SF_PART + (k & 1) * 512,
-                               make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]));
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(sready_bar + 8 * slot);
-                    else
-                        mbar_arrive_cluster(mapa_shared(sready_bar + 8 * slot, 0));
-                }
+            for (int i = 0; i < 16; ++i) {
+                r[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (in_k && first + 8 * i < limit)
+                    r[i] = __ldg(reinterpret_cast<const uint4 *>(base + 8 * i * ld + k0 * 8));
             }
+        };
+        tile();
+        fetch();
+        for (uint32_t sup = 0; u < num_units; ++sup) {
+            const uint32_t slot = sup & 1u;
+            if (!mbar_wait_warp(sfree_bar + 8 * slot, ((sup >> 1) & 1u) ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
+                                p.timeout_ns))
+                break;
+            // word w of the piece: stage 2 * piece + w / 2, word w % 2 of row i * 8 + row8
+            const uint32_t stage_step = static_cast<uint32_t>(p.sf_parts * SF_PART);
+            const uint32_t dst = sf_base + slot * sf_slot + part * SF_PART + 2 * piece * stage_step + row8 * 16;
+            const int left = p.blocks - k0 * 8 - piece * 16;  // blocks of K from the piece on
+            const auto keep = [&](uint32_t w, int n) {        // the first n bytes of a word
+                return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
+            };
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                uint4 x = r[i];
+                if (left < 16) {
+                    x.x = keep(x.x, left);
+                    x.y = keep(x.y, left - 4);
+                    x.z = keep(x.z, left - 8);
+                    x.w = keep(x.w, left - 12);
+                }
+                const uint32_t at = dst + (i & 3) * 128 + (i >> 2) * 4;  // rows 32 * (i / 4) + 8 * (i % 4) + row8
+                sts_u32(at, x.x);
+                sts_u32(at + 512, x.y);
+                sts_u32(at + stage_step, x.z);
+                sts_u32(at + stage_step + 512, x.w);
+            }
+            k0 += SUP;
+            if (k0 >= kts) {
+                k0 = 0;
+                u += unit_step;
+                tile();
+            }
+            fetch();
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sready_bar + 8 * slot);
         }
     }
 
@@ -784,16 +802,15 @@ cudaError_t prepare_ragged()
 
 bool ragged_tile_ok(int ctas, int bn)
 {
-    return (ctas == 1 || ctas == 2) && (bn == 32 || bn == 64 || bn == 128 || bn == 256);
+    return (ctas == 1 || ctas == 2) && (bn == 32 || bn == 64 || bn == 128 || bn == 224 || bn == 256);
 }
 
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K)
 {
-    (void)kind;
     (void)K;
     RaggedTile t;
     const int64_t avg = ragged_k ? Q : (rows + groups - 1) / groups;
-    t.bn = avg > 128 ? 256 : avg > 64 ? 128 : avg > 32 ? 64 : 32;
+    t.bn = avg > 128 ? (kind == kRaggedMx4 ? ACC1_MX : 256) : avg > 64 ? 128 : avg > 32 ? 64 : 32;
     t.ctas = avg > 64 && P > BP ? 2 : 1;
     if (ragged_k && t.bn < 128) t.bn = 128;
     return t;

@@ -294,7 +294,8 @@ dg::RaggedTile tile_for(const gemm_ctx *h, int kind, bool ragged_k, int64_t rows
         dg::RaggedTile t;
         t.ctas = h->ragged_tile / 1000;
         t.bn = h->ragged_tile % 1000;
-        if (ragged_k) t.bn = std::max(t.bn, 128);  // whole 128-byte column chunks per CTA
+        if (ragged_k) t.bn = t.bn == 224 ? 256 : std::max(t.bn, 128);  // whole 128-byte column chunks per CTA
+        if (kind == dg::kRaggedMx4) t.bn = std::min(t.bn, 224);        // two accumulators beside the scales
         return t;
     }
     return dg::ragged_pick_tile(kind, ragged_k, rows, static_cast<int>(groups), P, Q, K);

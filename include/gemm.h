@@ -151,8 +151,9 @@ extern "C" {
 #define GEMM_OPT_SIMT_SMALL 15
 /* Tile of the grouped and 4-bit products (gemm_grouped.h, gemm_mx4.h): 0
  * (default) = chosen from the average rows of a group; else 1000 * CTAs + rows
- * with CTAs 1 or 2 (a pair) and rows 32, 64, 128 or 256 of C per tile of
- * 128 * CTAs columns (weight gradients take at least 128). */
+ * with CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile of
+ * 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at most
+ * 224). */
 #define GEMM_OPT_GROUPED_TILE 16
 
 typedef struct gemm_ctx *gemm_handle_t;
