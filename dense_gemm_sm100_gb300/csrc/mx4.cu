@@ -9,6 +9,7 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "ragged.h"
 
 namespace dg {
@@ -64,12 +65,12 @@ struct Raw<__nv_bfloat16> {
 __device__ __forceinline__ void load8(const float *s, int n, bool vec, Raw<float> &r)
 {
     if (vec && n >= 8) {
-        r.a = __ldg(reinterpret_cast<const float4 *>(s));
-        r.b = __ldg(reinterpret_cast<const float4 *>(s) + 1);
+        r.a = *reinterpret_cast<const float4 *>(s);
+        r.b = *(reinterpret_cast<const float4 *>(s) + 1);
     } else {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(s + i) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? *(s + i) : 0.0f;
         r.a = make_float4(v[0], v[1], v[2], v[3]);
         r.b = make_float4(v[4], v[5], v[6], v[7]);
     }
@@ -78,13 +79,13 @@ __device__ __forceinline__ void load8(const float *s, int n, bool vec, Raw<float
 __device__ __forceinline__ void load8(const __nv_bfloat16 *s, int n, bool vec, Raw<__nv_bfloat16> &r)
 {
     if (vec && n >= 8) {
-        r.a = __ldg(reinterpret_cast<const uint4 *>(s));
+        r.a = *reinterpret_cast<const uint4 *>(s);
     } else {
         const uint16_t *t = reinterpret_cast<const uint16_t *>(s);
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = (2 * i < n ? uint32_t{__ldg(t + 2 * i)} : 0u) | (2 * i + 1 < n ? uint32_t{__ldg(t + 2 * i + 1)} << 16 : 0u);
+            w[i] = (2 * i < n ? uint32_t{*(t + 2 * i)} : 0u) | (2 * i + 1 < n ? uint32_t{*(t + 2 * i + 1)} << 16 : 0u);
         r.a = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(THREADS)
                          int chunks, int vec, uint8_t *codes, long long ldq, uint8_t *scales, long long lds)
 {
     constexpr int SEGS = kSegs<T>;
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     Cursor at(static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5),
               static_cast<long long>(gridDim.x) * (THREADS / 32), chunks);
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(THREADS)
         }
         if (lane < SEGS * 8 && k0 + lane * 32 < Kp) scales[row * lds + k0 / 32 + lane] = static_cast<uint8_t>(mine);
     }
+    griddep_launch_dependents();
 }
 
 // K along the source's rows: one thread per block, neighbouring threads on
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(THREADS)
                          int blocks, uint8_t *codes, long long ldq, uint8_t *scales, long long lds)
 {
     const long long total = rows * blocks;
+    griddep_wait();
     for (long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; i < total;
          i += static_cast<long long>(gridDim.x) * THREADS) {
         // order: batch, block of K, row
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(THREADS)
         *reinterpret_cast<uint4 *>(codes + row * ldq + kb * 16) = make_uint4(out[0], out[1], out[2], out[3]);
         scales[row * lds + kb] = static_cast<uint8_t>(byte);
     }
+    griddep_launch_dependents();
 }
 
 // Eight codes as BF16 pairs.  A code's bits s, e e, m placed at the sign, the
@@ -287,6 +292,7 @@ __global__ void __launch_bounds__(THREADS)
                       int chunks, int vec, T *dst, long long ldd)
 {
     constexpr int SEGS = kSegs<T>;
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     Cursor at(static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5),
               static_cast<long long>(gridDim.x) * (THREADS / 32), chunks);
@@ -297,8 +303,8 @@ __global__ void __launch_bounds__(THREADS)
         for (int j = 0; j < SEGS; ++j) {
             const int k = (at.chunk * SEGS + j) * 256 + lane * 8;
             if (k < K) {
-                c[j] = __ldg(reinterpret_cast<const uint32_t *>(codes + at.row * ldq + k / 2));
-                byte[j] = __ldg(scales + at.row * lds + k / 32);
+                c[j] = *reinterpret_cast<const uint32_t *>(codes + at.row * ldq + k / 2);
+                byte[j] = *(scales + at.row * lds + k / 32);
             }
         }
     };
@@ -322,6 +328,25 @@ __global__ void __launch_bounds__(THREADS)
             store8(d + k, K - k, vec != 0, w);
         }
     }
+    griddep_launch_dependents();
+}
+
+// Launches that may start while the kernel before them on the stream ends
+// (each kernel waits for it before its first access to memory): a product
+// behind the quantisation of its operand then finds its set-up done.
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int grid, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 // Blocks of eight warps, one chunk a warp at least, eight blocks an SM at most.
@@ -339,16 +364,14 @@ cudaError_t quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const 
     if (k_rows) {
         const int blocks = static_cast<int>((K + 31) / 32);
         const int grid = static_cast<int>(std::min<int64_t>((all * blocks + THREADS - 1) / THREADS, int64_t{sm_count} * 8));
-        quantise_cols_kernel<T><<<grid, THREADS, 0, stream>>>(src, ld, static_cast<int>(rows), stride, all,
-                                                              static_cast<int>(K), blocks, codes, ldq, scales, lds);
-        return cudaGetLastError();
+        return launch(quantise_cols_kernel<T>, grid, stream, src, ld, rows, stride, all, K, blocks, codes, ldq, scales,
+                      lds);
     }
     const int chunks = static_cast<int>((K + kSegs<T> * 256 - 1) / (kSegs<T> * 256));
     const int64_t align = 16 / static_cast<int64_t>(sizeof(T));
     const int vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % align == 0 && stride % align == 0;
-    quantise_rows_kernel<T><<<chunk_grid(all * chunks, sm_count), THREADS, 0, stream>>>(
-        src, ld, static_cast<int>(rows), stride, all, static_cast<int>(K), chunks, vec, codes, ldq, scales, lds);
-    return cudaGetLastError();
+    return launch(quantise_rows_kernel<T>, chunk_grid(all * chunks, sm_count), stream, src, ld, rows, stride, all, K,
+                  chunks, vec, codes, ldq, scales, lds);
 }
 
 template <typename T>
@@ -357,9 +380,8 @@ cudaError_t dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ld
 {
     const int chunks = static_cast<int>((K + kSegs<T> * 256 - 1) / (kSegs<T> * 256));
     const int vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && (ldd * sizeof(T)) % 16 == 0;
-    dequantise_kernel<T><<<chunk_grid(rows * chunks, sm_count), THREADS, 0, stream>>>(
-        codes, ldq, scales, lds, rows, static_cast<int>(K), chunks, vec, dst, ldd);
-    return cudaGetLastError();
+    return launch(dequantise_kernel<T>, chunk_grid(rows * chunks, sm_count), stream, codes, ldq, scales, lds, rows, K,
+                  chunks, vec, dst, ldd);
 }
 
 }  // namespace

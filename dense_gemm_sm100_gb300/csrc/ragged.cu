@@ -97,59 +97,57 @@ __device__ __forceinline__ void group_range(const Params &p, int g, int &lo, int
         hi = p.rows;
         return;
     }
-    const long long a = __ldg(p.offsets + g), b = __ldg(p.offsets + g + 1), r = p.rows;
+    const long long a = *(p.offsets + g), b = *(p.offsets + g + 1), r = p.rows;
     const long long l = a < 0 ? 0 : a > r ? r : a;
     const long long e = b < l ? l : b > r ? r : b;
     lo = static_cast<int>(l);
     hi = static_cast<int>(e);
 }
 
-// Whether the offsets rise within [0, rows].  All threads call it; block 0
-// reports offsets that do not, and every block then runs no tile.
-template <int NT>
-__device__ bool offsets_ok(const Params &p)
-{
-    int bad = 0;
-    if (p.offsets != nullptr)
-        for (int g = threadIdx.x; g < p.groups; g += NT) {
-            const long long a = __ldg(p.offsets + g), b = __ldg(p.offsets + g + 1);
-            if (a < 0 || b < a || b > p.rows) bad = 1;
-        }
-    bad = __syncthreads_or(bad);
-    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kStatusBadOffsets);
-    return bad == 0;
-}
-
-// table[g] = tiles of the groups before g; table[groups] = all tiles.
-template <int NT>
-__device__ void build_table(const Params &p, int *table, int *warp_sum)
+// Whether the offsets rise within [0, rows], and, for ragged rows, table[g] =
+// tiles of the groups before g, table[groups] = all tiles.  All threads call
+// it; block 0 reports offsets that do not rise, and every block then runs no
+// tile.  Threads take contiguous runs of groups; up to NT groups are read once.
+template <int NT, bool TABLE>
+__device__ bool read_groups(const Params &p, int *table, int *warp_sum)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.groups + NT - 1) / NT;
     const int g0 = min(p.groups, tid * per), g1 = min(p.groups, g0 + per);
-    int sum = 0;
-    for (int g = g0; g < g1; ++g) {
+    const auto tiles = [&](int g) {
         int lo, hi;
         group_range(p, g, lo, hi);
-        sum += (hi - lo + p.bn - 1) / p.bn * p.tiles_p;
+        return (hi - lo + p.bn - 1) / p.bn * p.tiles_p;
+    };
+    int sum = 0, bad = 0, last = 0;
+    for (int g = g0; g < g1; ++g) {
+        if (p.offsets != nullptr) {
+            const long long a = *(p.offsets + g), b = *(p.offsets + g + 1);
+            if (a < 0 || b < a || b > p.rows) bad = 1;
+        }
+        if (TABLE) sum += last = tiles(g);
     }
     int inc = sum;
+    if (TABLE) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += v;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
     }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    for (int g = g0; g < g1; ++g) {
-        int lo, hi;
-        group_range(p, g, lo, hi);
-        table[g] = before;
-        before += (hi - lo + p.bn - 1) / p.bn * p.tiles_p;
+    bad = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0 && tid == 0) atomicCAS(p.status, 0, kStatusBadOffsets);
+    if (TABLE) {
+        int before = inc - sum;
+        for (int w = 0; w < warp; ++w) before += warp_sum[w];
+        for (int g = g0; g < g1; ++g) {
+            table[g] = before;
+            before += per == 1 ? last : tiles(g);
+        }
+        if (g0 < p.groups && g1 == p.groups) table[p.groups] = before;
     }
-    if (g0 < p.groups && g1 == p.groups) table[p.groups] = before;
+    return bad == 0;
 }
 
 struct Tile {
@@ -288,8 +286,16 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             tmem_relinquish();
         }
     }
-    const bool groups_ok = offsets_ok<THREADS>(p);
-    if (!RAGGED_K) build_table<THREADS>(p, table, warp_sum);
+    if (threadIdx.x == 0 && (RAGGED_K || p.K > 0)) {
+        tma_prefetch_desc(&tmP);
+        tma_prefetch_desc(&tmQ);
+    }
+    // Up to here the kernel may overlap the end of the one before it on the
+    // stream.  It does not ask for the next one early: a quantisation that
+    // starts beside this kernel finds the SMs unevenly free (8 us lost on
+    // 8192 x 14336 x 4096).
+    griddep_wait();
+    const bool groups_ok = read_groups<THREADS, !RAGGED_K>(p, table, warp_sum);
     tc_fence_before_sync();
     if (CG == 2)
         cluster_sync();
@@ -302,10 +308,6 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
-            if (RAGGED_K || p.K > 0) {
-                tma_prefetch_desc(&tmP);
-                tma_prefetch_desc(&tmQ);
-            }
             const int q_cta = p.bn / CG;  // rows of Q this CTA stages
             const uint32_t tx = static_cast<uint32_t>(CG * (P_BYTES + p.q_bytes));
             uint32_t it = 0, s = 0, ph = 0;
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             for (int i = 0; i < 16; ++i) {
                 r[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (in_k && first + 8 * i < limit)
-                    r[i] = __ldg(reinterpret_cast<const uint4 *>(base + 8 * i * ld + k0 * 8));
+                    r[i] = *reinterpret_cast<const uint4 *>(base + 8 * i * ld + k0 * 8);
             }
         };
         tile();
@@ -772,13 +774,15 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Par
     cfg.blockDim = dim3(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS));
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK>, tmP, tmQ, p);
 }
 
