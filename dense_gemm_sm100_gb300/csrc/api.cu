@@ -817,7 +817,10 @@ int gemm_set_option(gemm_handle_t h, int option, int64_t value)
         h->simt_small = static_cast<int>(value);
         return GEMM_OK;
     case GEMM_OPT_GROUPED_TILE:
-        if (value != 0 && !dg::ragged_tile_ok(static_cast<int>(value / 1000), static_cast<int>(value % 1000))) break;
+        if (value != 0 && (value < 0 || value >= 100000 ||
+                           !dg::ragged_tile_ok(static_cast<int>(value / 10000), static_cast<int>(value / 1000 % 10),
+                                               static_cast<int>(value % 1000))))
+            break;
         h->ragged_tile = static_cast<int>(value);
         return GEMM_OK;
     default:

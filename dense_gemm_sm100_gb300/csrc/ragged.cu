@@ -30,6 +30,21 @@
 // proxy fence, and a release at cluster scope from the odd CTA of a pair) takes
 // about 1 us: once a stage it set the pace, 395 us for 8192 x 14336 x 4096.
 //
+// Long FP32 sums.  The tensor core's FP32 accumulator drops the bits that do
+// not fit at every addition, an error that grows with their number (measured,
+// normal values, of the result's norm: 1.0e-6 for 64 additions, 4.4e-6 for 256;
+// FP32 multiply-adds 2.5e-7 and 6.1e-7).  For FP32 results of BF16 (TF32)
+// operands longer than 12 (8) ring stages, 48 (32) additions, the accumulator
+// therefore runs over that many stages at a time, and the epilogue warps add
+// the segments in registers, rounding to nearest (5e-7 at any K, for a tenth of
+// the rate at K = 4096).  BF16 results round by 2^-9 afterwards; sums of 4-bit
+// products have few bits and few additions (64 K elements each).
+//
+// Few tiles.  A launch with fewer tiles than SMs and a long contraction runs
+// each tile on a cluster of 2, 4 or 8 CTAs, each with its own range of K.  The
+// partial tiles stay in shared memory; every CTA of the cluster adds a share of
+// the rows over the cluster, in CTA order, and writes them.
+//
 // Groups.  The offsets stay on the device.  Every CTA builds the running count
 // of its launch's tiles per group in shared memory (one load and a block scan,
 // beside the barrier set-up) and finds the group of tile u by bisection.
@@ -46,6 +61,7 @@
 #include <algorithm>
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -75,7 +91,7 @@ constexpr int SMEM_MAX = 227 * 1024;
 struct Params {
     const long long *offsets;
     int groups, rows, P, Q, K;
-    int bn, tiles_p, tiles_q, group_q;
+    int bn, tiles_p, tiles_q, group_q, split;
     int stages, stage_bytes, q_bytes, table_bytes, sf_parts;
     void *C;
     long long ldc, stride_c;
@@ -157,11 +173,12 @@ struct Tile {
     int pb;   // tile column index (units of ctas * 128 columns of C)
     int q0;   // first row of the tile within the group's C
     int qn;   // rows of the tile
-    int kt;   // ring stages of the contraction
+    int ks;   // first ring stage of this CTA's share of the contraction
+    int kt;   // its stages
 };
 
 template <int BK, bool RAGGED_K>
-__device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u)
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u, int krank)
 {
     Tile t;
     int r, tiles_q;
@@ -195,7 +212,14 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u
     t.q0 = (first + rr % gq) * p.bn;
     t.pb = rr / gq;
     t.qn = min(p.bn, (RAGGED_K ? p.Q : t.cnt) - t.q0);
+    t.ks = 0;
     t.kt = ((RAGGED_K ? t.cnt : p.K) + BK - 1) / BK;
+    if (p.split > 1) {
+        // even shares: 16 scale bytes of 4-bit operands cover two stages
+        const int per = ((t.kt + p.split - 1) / p.split + 1) & ~1;
+        t.ks = min(t.kt, krank * per);
+        t.kt = min(t.kt - t.ks, per);
+    }
     return t;
 }
 
@@ -208,11 +232,16 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
     return RAGGED_K ? p.bn : (t.qn + G - 1) / G * G;
 }
 
-template <int KIND, int CG, bool P_MN, bool RAGGED_K>
+// Stages of a segment of a long FP32 sum.
+__host__ __device__ constexpr int seg_stages(int kind) { return kind == kRaggedTf32 ? 8 : 12; }
+
+// SUM: long FP32 sums (see above).
+template <int KIND, int CG, bool P_MN, bool RAGGED_K, bool SUM>
 __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
+    constexpr int SEG = seg_stages(KIND);
     constexpr int THREADS = 32 * (MX ? WARPS_MX : WARPS);
     constexpr int ES = KIND == kRaggedBf16 ? 2 : 4;                 // bytes an element (not for 4-bit)
     constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
@@ -257,8 +286,11 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     const int lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
-    const int first_unit = blockIdx.x / CG;
-    const int unit_step = gridDim.x / CG;
+    // With a split contraction the cluster's CTAs share a tile (CG = 1 only).
+    const int krank = CG == 1 && p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int per_unit = CG == 1 ? p.split : CG;
+    const int first_unit = blockIdx.x / per_unit;
+    const int unit_step = gridDim.x / per_unit;
     const int acc1 = MX ? ACC1_MX : ACC1;
 
     if (threadIdx.x == 0) {
@@ -313,7 +345,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
-                const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+                const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
                 const int p0 = (t.pb * CG + static_cast<int>(rank)) * BP;
                 const int n_cta = mma_n<CG, RAGGED_K>(p, t) / CG;
                 const int qx = (RAGGED_K ? 0 : t.lo) + t.q0 + static_cast<int>(rank) * n_cta;
@@ -335,8 +367,9 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                     if (p.debug_drop && blockIdx.x == 0 && it == 0) continue;  // bytes that never come
                     if (RAGGED_K) {
                         // zeros, then rows [z, z + n) of the group
-                        const int n = min(BK, t.cnt - kt * BK);
-                        const int y = n - BK, z = t.lo + kt * BK;
+                        const int k = (t.ks + kt) * BK;
+                        const int n = min(BK, t.cnt - k);
+                        const int y = n - BK, z = t.lo + k;
                         if (p.p_chunks) {
                             if (CG == 2)
                                 tma_load_4d_pair(p_st, &tmP, fb, 0, y, z, p0 / CHUNK);
@@ -365,7 +398,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                         }
                         continue;
                     }
-                    const int kx = MX ? kt * 128 : kt * BK;  // 4-bit views count bytes
+                    const int kx = (t.ks + kt) * (MX ? 128 : BK);  // 4-bit views count bytes
                     if (P_MN) {
                         if (p.p_chunks) {
                             if (CG == 2)
@@ -416,108 +449,115 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         if (leader) {
             uint32_t it = 0, s = 0, ph = 0, acc_it = 0, sup = 0;
             bool ok = true, issued = false;
-            for (int u = first_unit; ok && u < num_units; u += unit_step, ++acc_it) {
-                const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
-                const uint32_t abuf = acc_it & 1u;
+            for (int u = first_unit; ok && u < num_units; u += unit_step) {
+                const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
                 const uint32_t idesc = IDESC | (static_cast<uint32_t>(mma_n<CG, RAGGED_K>(p, t) >> 3) << 17);
-                if (!mbar_wait_warp(tempty_bar + 8 * abuf, ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
-                                    kWaitMmaTmemEmpty, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + abuf * acc1;
-                for (int kt = 0; kt < t.kt; ++kt, ++it) {
-                    if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (MX && kt % SUP == 0 &&
-                        !mbar_wait_warp(sready_bar + 8 * (sup & 1u), (sup >> 1) & 1u, abort_flag, p.status,
-                                        kWaitMmaScale, p.timeout_ns)) {
+                for (int seg0 = 0; seg0 == 0 || seg0 < t.kt; seg0 += SUM ? SEG : t.kt, ++acc_it) {
+                    const int seg1 = SUM ? min(t.kt, seg0 + SEG) : t.kt;
+                    const uint32_t abuf = acc_it & 1u;
+                    if (!mbar_wait_warp(tempty_bar + 8 * abuf, ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                                        kWaitMmaTmemEmpty, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t p_st = sbase + s * p.stage_bytes;
-                    const uint32_t q_st = p_st + P_BYTES;
-                    uint64_t pd[K_STEPS], qd[K_STEPS];
-#pragma unroll
-                    for (int kk = 0; kk < K_STEPS; ++kk) {
-                        const int kr = kk * (32 / ES) * 128;  // MN-major: K rows of an instruction
-                        pd[kk] = P_MN ? smem_desc(p_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
-                                      : smem_desc(p_st + kk * 32, 16, 1024, kLayoutSw128);
-                        qd[kk] = Q_MN ? smem_desc(q_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
-                                      : smem_desc(q_st + kk * 32, 16, 1024, kLayoutSw128);
-                    }
-                    const uint32_t acc0 = kt > 0 ? 1u : 0u;
-                    const uint32_t sf = tmem_base + SF_COL + (it & 1u) * SF_COLS;
-                    const uint64_t sfd = smem_desc(
-                        sf_base + (sup & 1u) * sf_slot + static_cast<uint32_t>((kt % SUP) * p.sf_parts * SF_PART), 0,
-                        128, kLayoutNone);
-                    if (elect_one()) {
-                        if (MX) {
-                            // 512-byte groups: P's two words, then the two words of each 128 rows of Q
-#pragma unroll
-                            for (int i = 0; i < 6; ++i) {
-                                const uint32_t dst = i < 2 ? sf + i * 4 : sf + 8 + (i & 1) * 8 + (i >> 2) * 4;
-                                if (i < 4 || p.bn > 128) {
-                                    if (CG == 2)
-                                        tmem_copy_32x16b_pair(dst, sfd + i * 32);
-                                    else
-                                        tmem_copy_32x16b(dst, sfd + i * 32);
+                    const uint32_t d_tmem = tmem_base + abuf * acc1;
+                    for (int kt = seg0; kt < seg1; ++kt, ++it) {
+                        if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        if (MX && kt % SUP == 0 &&
+                            !mbar_wait_warp(sready_bar + 8 * (sup & 1u), (sup >> 1) & 1u, abort_flag, p.status,
+                                            kWaitMmaScale, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t p_st = sbase + s * p.stage_bytes;
+                        const uint32_t q_st = p_st + P_BYTES;
+                        uint64_t pd[K_STEPS], qd[K_STEPS];
+    #pragma unroll
+                        for (int kk = 0; kk < K_STEPS; ++kk) {
+                            const int kr = kk * (32 / ES) * 128;  // MN-major: K rows of an instruction
+                            pd[kk] = P_MN ? smem_desc(p_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
+                                          : smem_desc(p_st + kk * 32, 16, 1024, kLayoutSw128);
+                            qd[kk] = Q_MN ? smem_desc(q_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
+                                          : smem_desc(q_st + kk * 32, 16, 1024, kLayoutSw128);
+                        }
+                        const uint32_t acc0 = kt > seg0 ? 1u : 0u;
+                        const uint32_t sf = tmem_base + SF_COL + (it & 1u) * SF_COLS;
+                        const uint64_t sfd = smem_desc(
+                            sf_base + (sup & 1u) * sf_slot + static_cast<uint32_t>((kt % SUP) * p.sf_parts * SF_PART), 0,
+                            128, kLayoutNone);
+                        if (elect_one()) {
+                            if (MX) {
+                                // 512-byte groups: P's two words, then the two words of each 128 rows of Q
+    #pragma unroll
+                                for (int i = 0; i < 6; ++i) {
+                                    const uint32_t dst = i < 2 ? sf + i * 4 : sf + 8 + (i & 1) * 8 + (i >> 2) * 4;
+                                    if (i < 4 || p.bn > 128) {
+                                        if (CG == 2)
+                                            tmem_copy_32x16b_pair(dst, sfd + i * 32);
+                                        else
+                                            tmem_copy_32x16b(dst, sfd + i * 32);
+                                    }
                                 }
                             }
-                        }
-#pragma unroll
-                        for (int kk = 0; kk < K_STEPS; ++kk) {
-                            const uint32_t acc = kk > 0 ? 1u : acc0;
-                            if (MX) {
-                                const uint32_t id = (kk & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
-                                const uint32_t sp = sf + (kk >> 1) * 4, sq = sf + 8 + (kk >> 1) * 8;
+    #pragma unroll
+                            for (int kk = 0; kk < K_STEPS; ++kk) {
+                                const uint32_t acc = kk > 0 ? 1u : acc0;
+                                if (MX) {
+                                    const uint32_t id = (kk & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
+                                    const uint32_t sp = sf + (kk >> 1) * 4, sq = sf + 8 + (kk >> 1) * 8;
+                                    if (CG == 2)
+                                        tc_mma_mx4_pair(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
+                                    else
+                                        tc_mma_mx4(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
+                                } else if (KIND == kRaggedBf16) {
+                                    if (CG == 2)
+                                        tc_mma_f16_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                    else
+                                        tc_mma_f16(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                } else {
+                                    if (CG == 2)
+                                        tc_mma_tf32_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                    else
+                                        tc_mma_tf32(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                }
+                            }
+                            if (CG == 2)
+                                tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
+                            else
+                                tc_commit(empty_bar + 8 * s);
+                            if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) {
                                 if (CG == 2)
-                                    tc_mma_mx4_pair(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
+                                    tc_commit_pair_multicast(sfree_bar + 8 * (sup & 1u), 0x3);
                                 else
-                                    tc_mma_mx4(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
-                            } else if (KIND == kRaggedBf16) {
-                                if (CG == 2)
-                                    tc_mma_f16_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
-                                else
-                                    tc_mma_f16(d_tmem, pd[kk], qd[kk], idesc, acc);
-                            } else {
-                                if (CG == 2)
-                                    tc_mma_tf32_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
-                                else
-                                    tc_mma_tf32(d_tmem, pd[kk], qd[kk], idesc, acc);
+                                    tc_commit(sfree_bar + 8 * (sup & 1u));
                             }
                         }
-                        if (CG == 2)
-                            tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
-                        else
-                            tc_commit(empty_bar + 8 * s);
-                        if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) {
-                            if (CG == 2)
-                                tc_commit_pair_multicast(sfree_bar + 8 * (sup & 1u), 0x3);
-                            else
-                                tc_commit(sfree_bar + 8 * (sup & 1u));
+                        __syncwarp();
+                        if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) ++sup;
+                        issued = true;
+                        if (++s == static_cast<uint32_t>(p.stages)) {
+                            s = 0;
+                            ph ^= 1u;
                         }
                     }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (CG == 2)
+                            tc_commit_pair_multicast(tfull_bar + 8 * abuf, 0x3);
+                        else
+                            tc_commit(tfull_bar + 8 * abuf);
+                    }
                     __syncwarp();
-                    if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) ++sup;
-                    issued = true;
-                    if (++s == static_cast<uint32_t>(p.stages)) {
-                        s = 0;
-                        ph ^= 1u;
+                    if (!SUM) {
+                        ++acc_it;
+                        break;
                     }
                 }
-                if (!ok) break;
-                if (elect_one()) {
-                    if (CG == 2)
-                        tc_commit_pair_multicast(tfull_bar + 8 * abuf, 0x3);
-                    else
-                        tc_commit(tfull_bar + 8 * abuf);
-                }
-                __syncwarp();
             }
             if (!ok && issued && lane == 0) {
                 // Let every MMA already issued finish before TMEM is freed.
@@ -535,7 +575,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             uint32_t sup = 0;
             bool ok = true;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
-                const int kts = tile_at<BK, RAGGED_K>(p, table, u).kt;
+                const int kts = tile_at<BK, RAGGED_K>(p, table, u, krank).kt;
                 for (int k0 = 0; k0 < kts; k0 += SUP, ++sup) {
                     if (!mbar_wait_warp(sready_bar + 8 * (sup & 1u), (sup >> 1) & 1u, abort_flag, p.status,
                                         kWaitMmaScale, p.timeout_ns)) {
@@ -553,118 +593,150 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         const int half = (warp - 2) >> 2;  // 0: even chunks of 32 rows of C, 1: odd ones
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 2048;
         uint32_t acc_it = 0;
-        for (int u = first_unit; u < num_units; u += unit_step, ++acc_it) {
-            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
-            const uint32_t abuf = acc_it & 1u;
-            if (!mbar_wait_warp(tfull_bar + 8 * abuf, (acc_it >> 1) & 1u, abort_flag, p.status, kWaitEpiTmemFull,
-                                p.timeout_ns))
-                break;
-            tc_fence_after_sync();
+        bool ok = true;
+        for (int u = first_unit; ok && u < num_units; u += unit_step) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
             const int col0 = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32;  // the warp's first column
             const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
             const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col0;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * acc1;
             const int chunks = (t.qn + 31) / 32;
-            const auto load = [&](int c, uint32_t(&v)[32]) {
-                if (c >= chunks) return;
+            const auto await = [&]() {
+                const uint32_t abuf = acc_it & 1u;
+                ok = mbar_wait_warp(tfull_bar + 8 * abuf, (acc_it >> 1) & 1u, abort_flag, p.status, kWaitEpiTmemFull,
+                                    p.timeout_ns);
+                tc_fence_after_sync();
+                return ok;
+            };
+            // The accumulator is in registers: hand it back to the MMA warp.
+            const auto release = [&]() {
+                const uint32_t bar = tempty_bar + 8 * (acc_it & 1u);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(bar);
+                    else
+                        mbar_arrive_cluster(mapa_shared(bar, 0));
+                }
+                ++acc_it;
+            };
+            const auto load = [&](int unit, uint32_t(&v)[16]) {
                 if (t.kt > 0) {
-                    tmem_load_32cols(t_row + c * 32, v);
+                    tmem_load_16cols(
+                        tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc_it & 1u) * acc1 + unit * 16, v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;  // the empty sum
+                    for (int j = 0; j < 16; ++j) v[j] = 0u;  // the empty sum
                 }
             };
-            const auto store = [&](int c, const uint32_t(&v)[32]) {
-                if (c >= chunks || col0 >= p.P) return;
-                const int n = t.qn - c * 32;  // rows left
-                const long long at = base + static_cast<long long>(c * 32) * p.ldc;
-                if (p.c_vec && p.out_bf16) {
+            // 16 rows of C from unit * 16 on, the warp's 32 columns.
+            const auto store = [&](int unit, const uint32_t(&v)[16]) {
+                if (CG == 1 && p.split > 1) {
+                    // this CTA's part of the sum, [row][128 columns], where the ring was
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sts_u32(sbase + (unit * 16 + j) * 512 + (q * 32 + lane) * 4, v[j]);
+                    return;
+                }
+                const int n = t.qn - unit * 16;  // rows left
+                if (n <= 0 || col0 >= p.P) return;
+                const long long at = base + static_cast<long long>(unit * 16) * p.ldc;
+                if (!SUM && p.c_vec && p.out_bf16) {
                     // words of two rows' neighbours, [row pair][column]
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         const __nv_bfloat162 w =
                             __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + j * 128 + lane * 4),
-                                     "r"(*reinterpret_cast<const uint32_t *>(&w))
-                                     : "memory");
+                        sts_u32(stage + j * 128 + lane * 4, *reinterpret_cast<const uint32_t *>(&w));
                     }
                     __syncwarp();
                     // a lane: eight columns of two rows
-                    const int piece = (lane & 3) * 8;
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + (lane >> 2) * 2 * p.ldc + piece;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = (i * 8 + (lane >> 2)) * 2;
-                        const uint32_t src = stage + (i * 8 + (lane >> 2)) * 128 + piece * 4;
-                        const uint4 a = lds_u4(src), b = lds_u4(src + 16);
-                        if (col0 + piece < p.P) {
-                            if (r < n)
-                                *reinterpret_cast<uint4 *>(out) =
-                                    make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
-                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
-                            if (r + 1 < n)
-                                *reinterpret_cast<uint4 *>(out + p.ldc) =
-                                    make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
-                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
-                        }
-                        out += 16 * p.ldc;
+                    const int piece = (lane & 3) * 8, r = (lane >> 2) * 2;
+                    const uint32_t src = stage + (lane >> 2) * 128 + piece * 4;
+                    const uint4 a = lds_u4(src), b = lds_u4(src + 16);
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + r * p.ldc + piece;
+                    if (col0 + piece < p.P) {
+                        if (r < n)
+                            *reinterpret_cast<uint4 *>(out) =
+                                make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                           __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                        if (r + 1 < n)
+                            *reinterpret_cast<uint4 *>(out + p.ldc) =
+                                make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                           __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
                     }
                     __syncwarp();
                 } else if (p.c_vec) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sts_u32(stage + j * 128 + lane * 4, v[j]);
+                    __syncwarp();
                     const int piece = (lane & 7) * 4;
                     float *out = static_cast<float *>(p.C) + at + (lane >> 3) * p.ldc + piece;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + j * 128 + lane * 4), "r"(v[h * 16 + j])
-                                         : "memory");
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = h * 16 + i * 4 + (lane >> 3);
-                            const uint4 x = lds_u4(stage + (i * 4 + (lane >> 3)) * 128 + piece * 4);
-                            if (r < n && col0 + piece < p.P) *reinterpret_cast<uint4 *>(out) = x;
-                            out += 4 * p.ldc;
-                        }
-                        __syncwarp();
+                    for (int i = 0; i < 4; ++i, out += 4 * p.ldc) {
+                        const int r = i * 4 + (lane >> 3);
+                        const uint4 x = lds_u4(stage + r * 128 + piece * 4);
+                        if (r < n && col0 + piece < p.P) *reinterpret_cast<uint4 *>(out) = x;
                     }
+                    __syncwarp();
                 } else if (col0 + lane < p.P) {
-                    if (p.out_bf16) {
+                    if (!SUM && p.out_bf16) {
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                        for (int j = 0; j < 16; ++j, out += p.ldc)
                             if (j < n) *out = __float2bfloat16_rn(__uint_as_float(v[j]));
                     } else {
                         float *out = static_cast<float *>(p.C) + at + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j, out += p.ldc)
+                        for (int j = 0; j < 16; ++j, out += p.ldc)
                             if (j < n) *out = __uint_as_float(v[j]);
                     }
                 }
             };
-            // A warp's chunks, two at a time; the accumulator is free once the
-            // last are in registers.
-            uint32_t v[2][32];
+            // This warp's chunks of 32 rows: half, half + 2, ...; unit k of them
+            // is 16 rows.
             const int mine = (chunks + 1 - half) / 2;
+            const auto unit_of = [&](int k) { return 4 * (k >> 1) + 2 * half + (k & 1); };
+            if (SUM) {
+                uint32_t sum[8][16];
+                for (int seg0 = 0; seg0 == 0 || seg0 < t.kt; seg0 += SEG) {
+                    if (!await()) break;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= 2 * mine) break;
+                        if (seg0 == 0) {
+                            load(unit_of(k), sum[k]);
+                        } else {
+                            uint32_t v[16];
+                            load(unit_of(k), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[k][j] = __float_as_uint(__uint_as_float(sum[k][j]) + __uint_as_float(v[j]));
+                        }
+                    }
+                    tmem_wait_ld();
+                    release();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < 2 * mine) store(unit_of(k), sum[k]);
+            } else {
+                if (!await()) break;
+                uint32_t v[2][16];
 #pragma unroll 1
-            for (int i = 0; i == 0 || i < mine; i += 2) {
-                const int c0 = 2 * i + half, c1 = c0 + 2;
-                load(c0, v[0]);
-                load(c1, v[1]);
-                tmem_wait_ld();
-                if (i + 2 >= mine) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader)
-                            mbar_arrive(tempty_bar + 8 * abuf);
-                        else
-                            mbar_arrive_cluster(mapa_shared(tempty_bar + 8 * abuf, 0));
+                for (int k = 0; k == 0 || k < 2 * mine; k += 2) {
+                    if (k < 2 * mine) {
+                        load(unit_of(k), v[0]);
+                        load(unit_of(k + 1), v[1]);
+                        tmem_wait_ld();
+                    }
+                    if (k + 2 >= 2 * mine) release();
+                    if (k < 2 * mine) {
+                        store(unit_of(k), v[0]);
+                        store(unit_of(k + 1), v[1]);
                     }
                 }
-                store(c0, v[0]);
-                store(c1, v[1]);
             }
             __syncwarp();
         }
@@ -676,7 +748,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         // present one, so their latencies overlap.
         const int part = warp - 2 - EPI_WARPS;
         const long long ld = part == 0 ? p.lds_p : p.lds_q;
-        int u = first_unit, k0 = 0, kts = 0, first = 0, limit = 0;
+        int u = first_unit, k0 = 0, kts = 0, first = 0, limit = 0, blocks = 0;
         const uint8_t *base = nullptr;
         // Lane l loads 16-byte piece l % 4 of rows l / 4, l / 4 + 8, ...: eight
         // rows' 64 bytes an instruction, whole sectors.
@@ -684,16 +756,17 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         uint4 r[16];
         const auto tile = [&]() {
             if (u >= num_units) return;
-            const Tile t = tile_at<BK, RAGGED_K>(p, table, u);
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
             kts = t.kt;
             first = (part == 0 ? (t.pb * CG + static_cast<int>(rank)) * BP : t.q0 + (part - 1) * 128) + row8;
             limit = part == 0 ? p.P : t.cnt;
             base = (part == 0 ? p.scale_p + static_cast<long long>(t.g) * p.P * ld
                               : p.scale_q + static_cast<long long>(t.lo) * ld) +
-                   first * ld + piece * 16;
+                   first * ld + t.ks * 8 + piece * 16;
+            blocks = p.blocks - t.ks * 8;
         };
         const auto fetch = [&]() {
-            const bool in_k = u < num_units && k0 * 8 + piece * 16 < p.blocks;
+            const bool in_k = u < num_units && k0 * 8 + piece * 16 < blocks;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 r[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -711,7 +784,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             // word w of the piece: stage 2 * piece + w / 2, word w % 2 of row i * 8 + row8
             const uint32_t stage_step = static_cast<uint32_t>(p.sf_parts * SF_PART);
             const uint32_t dst = sf_base + slot * sf_slot + part * SF_PART + 2 * piece * stage_step + row8 * 16;
-            const int left = p.blocks - k0 * 8 - piece * 16;  // blocks of K from the piece on
+            const int left = blocks - k0 * 8 - piece * 16;  // blocks of K from the piece on
             const auto keep = [&](uint32_t w, int n) {        // the first n bytes of a word
                 return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
             };
@@ -743,6 +816,53 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         }
     }
 
+    if (CG == 1 && p.split > 1) {
+        // Add the cluster's partial tiles, rows krank, krank + split, ... here,
+        // four columns a thread.
+        __syncwarp();
+        cluster_sync();
+        if (first_unit < num_units) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, first_unit, krank);
+            const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
+            const int piece = (threadIdx.x & 31) * 4;
+            const int col = t.pb * BP + piece;
+            for (int j = krank + p.split * warp; j < t.qn && col < p.P; j += p.split * (THREADS / 32)) {
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int r = 0; r < p.split; ++r) {
+                    const float4 y = lds_cluster_f4(mapa_shared(sbase + j * 512 + piece * 4, r));
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                const long long at = (RAGGED_K ? t.g * p.stride_c : 0) + (first_row + j) * p.ldc + col;
+                const float v[4] = {x.x, x.y, x.z, x.w};
+                if (p.out_bf16) {
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
+                    if (p.c_vec) {
+                        const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+                        *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(w);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (col + i < p.P) out[i] = __float2bfloat16_rn(v[i]);
+                    }
+                } else {
+                    float *out = static_cast<float *>(p.C) + at;
+                    if (p.c_vec) {
+                        *reinterpret_cast<float4 *>(out) = x;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (col + i < p.P) out[i] = v[i];
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its part
+    }
+
     tc_fence_before_sync();
     __syncwarp();
     if (CG == 2)
@@ -758,16 +878,15 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     }
 }
 
-template <int KIND, int CG, bool P_MN, bool RK>
+template <int KIND, int CG, bool P_MN, bool RK, bool SUM>
 cudaError_t set_attrs()
 {
-    return cudaFuncSetAttribute(ragged_kernel<KIND, CG, P_MN, RK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(ragged_kernel<KIND, CG, P_MN, RK, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 SMEM_MAX);
 }
 
-template <int KIND, int CG, bool P_MN, bool RK>
-cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Params &p, int grid,
-                       cudaStream_t stream)
+template <int KIND, int CG, bool P_MN, bool RK, bool SUM>
+cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Params &p, int grid, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -778,46 +897,158 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Par
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = CG == 1 ? p.split : CG;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK>, tmP, tmQ, p);
+    cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ragged_kernel<KIND, CG, P_MN, RK, SUM>, tmP, tmQ, p);
+}
+
+// The instantiation for a launch (op: apply<kind, ctas, P MN-major, ragged K, long FP32 sums>).
+template <int KIND, int CG, typename Op>
+cudaError_t dispatch_form(bool p_mn, bool ragged_k, bool sum, const Op &op)
+{
+    if (ragged_k) return sum ? op.template apply<KIND, CG, true, true, true>() : op.template apply<KIND, CG, true, true, false>();
+    if (p_mn) return sum ? op.template apply<KIND, CG, true, false, true>() : op.template apply<KIND, CG, true, false, false>();
+    return sum ? op.template apply<KIND, CG, false, false, true>() : op.template apply<KIND, CG, false, false, false>();
+}
+
+template <typename Op>
+cudaError_t dispatch(int kind, int ctas, bool p_mn, bool ragged_k, bool sum, const Op &op)
+{
+    if (kind == kRaggedMx4)
+        return ctas == 2 ? op.template apply<kRaggedMx4, 2, false, false, false>()
+                         : op.template apply<kRaggedMx4, 1, false, false, false>();
+    if (kind == kRaggedTf32)
+        return ctas == 2 ? dispatch_form<kRaggedTf32, 2>(p_mn, ragged_k, sum, op)
+                         : dispatch_form<kRaggedTf32, 1>(p_mn, ragged_k, sum, op);
+    return ctas == 2 ? dispatch_form<kRaggedBf16, 2>(p_mn, ragged_k, sum, op)
+                     : dispatch_form<kRaggedBf16, 1>(p_mn, ragged_k, sum, op);
+}
+
+struct SetAttrs {
+    template <int K, int CG, bool P, bool R, bool S>
+    cudaError_t apply() const
+    {
+        return set_attrs<K, CG, P, R, S>();
+    }
+};
+
+struct Launch {
+    const CUtensorMap &tmP, &tmQ;
+    const Params &p;
+    int grid;
+    cudaStream_t stream;
+    template <int K, int CG, bool P, bool R, bool S>
+    cudaError_t apply() const
+    {
+        return launch_one<K, CG, P, R, S>(tmP, tmQ, p, grid, stream);
+    }
+};
+
+// Tiles of a launch at most (row offsets are on the device): every busy group
+// adds at most one partial tile.
+int64_t max_units(bool ragged_k, int64_t rows, int64_t groups, int64_t P, int64_t Q, int ctas, int bn)
+{
+    const int64_t tiles_q =
+        ragged_k ? (Q + bn - 1) / bn * groups : (rows + bn - 1) / bn + std::max<int64_t>(0, std::min(groups, rows) - 1);
+    return std::max<int64_t>(1, tiles_q * ((P + ctas * BP - 1) / (ctas * BP)));
+}
+
+// Clusters of 2, 4 and 8 CTAs that run at the same time (the SMs of a cluster
+// share a GPC, so fewer than SMs / size); filled in by prepare_ragged.
+int g_clusters[3] = {};
+
+int max_clusters(int split) { return g_clusters[split == 2 ? 0 : split == 4 ? 1 : 2]; }
+
+cudaError_t query_clusters(int split, int *out)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(32 * WARPS_MX);
+    cfg.dynamicSmemBytes = SMEM_MAX;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(out, ragged_kernel<kRaggedMx4, 1, false, false, false>, &cfg);
 }
 
 }  // namespace
 
 cudaError_t prepare_ragged()
 {
-    cudaError_t (*fns[])() = {
-        set_attrs<kRaggedBf16, 1, false, false>, set_attrs<kRaggedBf16, 2, false, false>,
-        set_attrs<kRaggedBf16, 1, true, false>,  set_attrs<kRaggedBf16, 2, true, false>,
-        set_attrs<kRaggedBf16, 1, true, true>,   set_attrs<kRaggedBf16, 2, true, true>,
-        set_attrs<kRaggedTf32, 1, false, false>, set_attrs<kRaggedTf32, 2, false, false>,
-        set_attrs<kRaggedTf32, 1, true, false>,  set_attrs<kRaggedTf32, 2, true, false>,
-        set_attrs<kRaggedTf32, 1, true, true>,   set_attrs<kRaggedTf32, 2, true, true>,
-        set_attrs<kRaggedMx4, 1, false, false>,  set_attrs<kRaggedMx4, 2, false, false>};
     cudaError_t e = cudaSuccess;
-    for (auto f : fns)
-        if (e == cudaSuccess) e = f();
+    for (int kind : {kRaggedBf16, kRaggedTf32, kRaggedMx4})
+        for (int ctas = 1; ctas <= 2; ++ctas)
+            for (int form = 0; form < 3; ++form)
+                for (bool sum : {false, true})
+                    if (e == cudaSuccess) e = dispatch(kind, ctas, form > 0, form == 2, sum, SetAttrs());
+    for (int i = 0; i < 3; ++i)
+        if (e == cudaSuccess) e = query_clusters(2 << i, &g_clusters[i]);
     return e;
 }
 
-bool ragged_tile_ok(int ctas, int bn)
+bool ragged_tile_ok(int split, int ctas, int bn)
 {
-    return (ctas == 1 || ctas == 2) && (bn == 32 || bn == 64 || bn == 128 || bn == 224 || bn == 256);
+    if (!(bn == 32 || bn == 64 || bn == 128 || bn == 224 || bn == 256)) return false;
+    if (split <= 1) return split == 0 && (ctas == 1 || ctas == 2);
+    return (split == 2 || split == 4 || split == 8) && ctas == 1 && bn <= 128;
 }
 
-RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K)
+// Estimated time of each tile in cycles; the least wins.  A ring stage takes
+// its four MMA instructions (measured: 128 cycles at N = 256, 64 at 128, 48 at
+// 64, 40 at 32) or the arrival of its bytes (55 a cycle and SM measured),
+// whichever is longer; a tile its stages or its epilogue (12 cycles a row); a
+// launch the waves of tiles, one epilogue and 3 us, and at least its traffic at
+// 6.4 TB/s.  The type of C does not enter, so that a BF16 result is the FP32
+// result rounded.
+RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
+                            int sm_count, bool may_split)
 {
-    (void)K;
-    RaggedTile t;
-    const int64_t avg = ragged_k ? Q : (rows + groups - 1) / groups;
-    t.bn = avg > 128 ? (kind == kRaggedMx4 ? ACC1_MX : 256) : avg > 64 ? 128 : avg > 32 ? 64 : 32;
-    t.ctas = avg > 64 && P > BP ? 2 : 1;
-    if (ragged_k && t.bn < 128) t.bn = 128;
-    return t;
+    const double es = kind == kRaggedMx4 ? 17.0 / 32 : kind == kRaggedTf32 ? 4 : 2, eo = ragged_k ? 4 : 2;
+    const double busy = static_cast<double>(std::max<int64_t>(1, std::min<int64_t>(groups, rows)));
+    const double per_group = static_cast<double>(rows) / busy;
+    const int bk = ragged_bk(kind);
+    const int64_t k_len = ragged_k ? (rows + groups - 1) / groups : K;
+    const int64_t kt = std::max<int64_t>(1, (k_len + bk - 1) / bk);
+    const double bytes = ragged_k ? double(rows) * (P + Q) * es + double(groups) * P * Q * eo
+                                  : double(rows) * K * es + busy * P * K * es + double(rows) * P * eo;
+    RaggedTile best;
+    double best_t = 0;
+    for (int ctas = 1; ctas <= 2; ++ctas)
+        for (int bn : {32, 64, 128, kind == kRaggedMx4 ? ACC1_MX : 256})
+            for (int split = 1; split <= 8; split *= 2) {
+                if (ragged_k && bn < 128) continue;  // whole 128-byte column chunks per CTA
+                const int64_t units = max_units(ragged_k, rows, groups, P, Q, ctas, bn);
+                if (split > 1 && (!may_split || ctas > 1 || bn > 128 || units > max_clusters(split) || units * split > sm_count ||
+                                  kt < 4 * split))
+                    continue;
+                const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
+                const double stage = std::max(4 * mma, (P_BYTES + bn / ctas * 128) / 55.0) * (kind == kRaggedMx4 ? 1.1 : 1);
+                const double tiles_p = static_cast<double>((P + ctas * BP - 1) / (ctas * BP));
+                const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
+                                       : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
+                                                    : double((rows + bn - 1) / bn);
+                const double tile = static_cast<double>((kt + split - 1) / split) * stage;
+                const double epi = 600 + bn * 12.0;
+                const double fill = tiles_q * tiles_p * ctas * split / sm_count;
+                const double run = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) +
+                                   (split > 1 || ctas > 1 ? 1500 : 0);
+                const double mem = bytes / 3370;
+                const double t = std::max(run, mem) + 0.1 * std::min(run, mem) + 6000;
+                if (best.bn == 0 || t < best_t) {
+                    best_t = t;
+                    best.ctas = ctas;
+                    best.bn = bn;
+                    best.split = split;
+                }
+            }
+    return best;
 }
 
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
@@ -833,6 +1064,7 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.bn = t.bn;
     p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
+    p.split = t.split;
     p.q_bytes = t.bn / t.ctas * 128;
     p.stage_bytes = P_BYTES + p.q_bytes;
     p.sf_parts = 1 + (t.bn + 127) / 128;
@@ -859,26 +1091,16 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.timeout_ns = a.timeout_ns;
     p.debug_drop = a.debug_drop;
     p.group_q = 16;
-    // Upper bound of the tiles (the offsets are on the device).
-    const int64_t tiles_q = ragged_k ? int64_t{p.tiles_q} * a.groups
-                                     : (int64_t{a.rows} + t.bn - 1) / t.bn + std::min(a.groups, a.rows) - 1;
-    const int64_t units = std::max<int64_t>(1, tiles_q * p.tiles_p);
+    // A persistent grid; one cluster a tile where the contraction is split.
+    const int64_t units = max_units(ragged_k, a.rows, a.groups, a.P, a.Q, t.ctas, t.bn);
     const int64_t slots = std::max(1, (max_ctas > 0 ? std::min(max_ctas, sm_count) : sm_count) / t.ctas);
-    const int grid = static_cast<int>(t.ctas * std::min(units, slots));
-    const bool pair = t.ctas == 2;
-#define DG_RAGGED(KIND, PMN, RK)                                                                  \
-    return pair ? launch_one<KIND, 2, PMN, RK>(tmP, tmQ, p, grid, a.stream)                        \
-                : launch_one<KIND, 1, PMN, RK>(tmP, tmQ, p, grid, a.stream)
-    if (kind == kRaggedMx4) DG_RAGGED(kRaggedMx4, false, false);
-    if (kind == kRaggedTf32) {
-        if (ragged_k) DG_RAGGED(kRaggedTf32, true, true);
-        if (p_mn) DG_RAGGED(kRaggedTf32, true, false);
-        DG_RAGGED(kRaggedTf32, false, false);
-    }
-    if (ragged_k) DG_RAGGED(kRaggedBf16, true, true);
-    if (p_mn) DG_RAGGED(kRaggedBf16, true, false);
-    DG_RAGGED(kRaggedBf16, false, false);
-#undef DG_RAGGED
+    const int64_t grid = t.split > 1 ? units * t.split : t.ctas * std::min(units, slots);
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    // Stages a CTA adds up (of an average group, for a ragged contraction).
+    const int bk = ragged_bk(kind);
+    const int64_t k_len = ragged_k ? (int64_t{a.rows} + a.groups - 1) / a.groups : a.K;
+    const bool sum = a.out_bf16 == 0 && (k_len + bk - 1) / bk > int64_t{seg_stages(kind)} * t.split;
+    return dispatch(kind, t.ctas, p_mn, ragged_k, sum, Launch{tmP, tmQ, p, static_cast<int>(grid), a.stream});
 }
 
 }  // namespace dg

@@ -42,10 +42,12 @@ struct RaggedArgs {
     cudaStream_t stream = nullptr;
 };
 
-// Tile of a launch: `ctas` (1, or 2 for a pair) x 128 columns of C by bn rows.
+// Tile of a launch: `ctas` (1, or 2 for a pair) x 128 columns of C by bn rows,
+// its contraction cut over `split` CTAs (ctas = 1 and bn <= 128 only).
 struct RaggedTile {
     int ctas = 1;
     int bn = 0;
+    int split = 1;
 };
 
 // Status word of a launch whose offsets decrease or leave [0, rows].
@@ -55,8 +57,9 @@ constexpr int kRaggedMaxGroups = 4096;
 constexpr int kRaggedP = 128;    // rows of P one CTA stages
 constexpr int kRaggedBlock = 32;  // elements that share a 4-bit scale
 
-bool ragged_tile_ok(int ctas, int bn);
-RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K);
+bool ragged_tile_ok(int split, int ctas, int bn);  // split 0: none
+RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
+                            int sm_count, bool may_split);
 
 // K elements of one ring stage (128 bytes of a K-major row).
 inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : 64; }

@@ -292,13 +292,15 @@ dg::RaggedTile tile_for(const gemm_ctx *h, int kind, bool ragged_k, int64_t rows
 {
     if (h->ragged_tile) {
         dg::RaggedTile t;
-        t.ctas = h->ragged_tile / 1000;
+        t.split = std::max(1, h->ragged_tile / 10000);
+        t.ctas = h->ragged_tile / 1000 % 10;
         t.bn = h->ragged_tile % 1000;
         if (ragged_k) t.bn = t.bn == 224 ? 256 : std::max(t.bn, 128);  // whole 128-byte column chunks per CTA
         if (kind == dg::kRaggedMx4) t.bn = std::min(t.bn, 224);        // two accumulators beside the scales
         return t;
     }
-    return dg::ragged_pick_tile(kind, ragged_k, rows, static_cast<int>(groups), P, Q, K);
+    const int sms = h->max_ctas > 0 ? std::min(h->max_ctas, h->sm_count) : h->sm_count;
+    return dg::ragged_pick_tile(kind, ragged_k, rows, static_cast<int>(groups), P, Q, K, sms, h->split_k == 0);
 }
 
 dg::RaggedArgs common_args(const gemm_ctx *h, const int64_t *offsets, int64_t groups, int64_t rows, int64_t P,
@@ -325,7 +327,7 @@ std::string path_name(const char *op, int kind, const dg::RaggedTile &t, const c
 {
     const char *k = kind == dg::kRaggedMx4 ? "mx4" : kind == dg::kRaggedTf32 ? "tf32" : "bf16";
     return std::string(op) + "_" + k + (t.ctas == 2 ? "_pair" : "_") + std::to_string(128 * t.ctas) + "x" +
-           std::to_string(t.bn) + rest;
+           std::to_string(t.bn) + rest + (t.split > 1 ? "+splitk" + std::to_string(t.split) : "");
 }
 
 // A row-major operand that TMA can address: itself, or its copy in the

@@ -150,10 +150,12 @@ extern "C" {
  * 1 = never; 2 = for every FP32 problem (tests). */
 #define GEMM_OPT_SIMT_SMALL 15
 /* Tile of the grouped and 4-bit products (gemm_grouped.h, gemm_mx4.h): 0
- * (default) = chosen from the average rows of a group; else 1000 * CTAs + rows
- * with CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile of
- * 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at most
- * 224). */
+ * (default) = the least estimated time for the average group; else 1000 * CTAs
+ * + rows, CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile
+ * of 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at
+ * most 224), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
+ * 8 CTAs (CTAs 1, rows at most 128).  By default the contraction is cut where
+ * the tiles would leave SMs idle; GEMM_OPT_SPLIT_K = 1 (or more) forbids it. */
 #define GEMM_OPT_GROUPED_TILE 16
 
 typedef struct gemm_ctx *gemm_handle_t;

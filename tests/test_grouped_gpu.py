@@ -4,7 +4,9 @@ against FP64.
 Bounds, with S = sum |a b| of an element over K terms: BF16 products are exact
 in FP32 and each of the K additions loses less than 2^-23 of the partial sum,
 so |C - ref| <= (K + 2) 2^-23 S; a BF16 result is the FP32 result of the same
-call rounded once, bit for bit; TF32 keeps 11 significant bits of each operand by
+call rounded once, bit for bit, unless FP32 results are summed in segments
+(more than 12 stages of 64 elements), and then within half a unit of its eight
+significant bits, 2^-8 |C|, of a sum within that bound; TF32 keeps 11 significant bits of each operand by
 dropping the rest, less than 2^-10 each and so 2^-9 of a product, framed as
 2^-9 + 2^-20.
 """
@@ -13,7 +15,8 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-TILES = [1032, 1064, 1128, 1256, 2032, 2064, 2128, 2256]
+# CTAs and rows of a tile; 10000 S: the contraction over clusters of S CTAs
+TILES = [1032, 1064, 1128, 1256, 2032, 2064, 2128, 2256, 21032, 41064, 81032, 81128]
 
 
 @pytest.fixture(scope="module")
@@ -102,7 +105,13 @@ def test_bf16_sizes(h, sizes, KN, layout):
     A, W = draw((b[-1], K), "bf16", 1), draw((len(sizes), K, N), "bf16", 2)
     C = run_forward(h, A, W, b, layout, "bf16")
     assert_close(C, *forward_ref(A, W, b), K, "bf16")
-    assert torch.equal(run_forward(h, A, W, b, layout, "bf16", torch.bfloat16), C.bfloat16())
+    half = run_forward(h, A, W, b, layout, "bf16", torch.bfloat16)
+    if K <= 12 * 64:
+        assert torch.equal(half, C.bfloat16())
+    else:
+        ref, S = forward_ref(A, W, b)
+        t = tolerance(S, K, "bf16")
+        assert ((half.cpu().double() - ref).abs() <= t + 2.0 ** -8 * (ref.abs() + t)).all()
 
 
 @pytest.mark.parametrize("layout", ["row", "col"])
@@ -124,10 +133,10 @@ def test_every_tile(h, gm, dtype, layout, tile):
     K, N = 264, 392
     A, W = draw((b[-1], K), dtype, 5), draw((6, K, N), dtype, 6)
     assert_close(run_forward(h, A, W, b, layout, dtype), *forward_ref(A, W, b), K, dtype)
-    assert f"x{tile % 1000}" in h.last_path
+    assert f"x{tile % 1000}" in h.last_path and (f"+splitk{tile // 10000}" in h.last_path) == (tile > 9999)
 
 
-@pytest.mark.parametrize("tile", [0, 1128, 1256, 2128, 2256])
+@pytest.mark.parametrize("tile", [0, 1128, 1256, 2128, 2256, 21128, 81128])
 @pytest.mark.parametrize("dtype", ["bf16", "tf32"])
 @pytest.mark.parametrize("MN", [(1, 1), (72, 40), (256, 128), (200, 333), (129, 520)])
 def test_wgrad(h, gm, MN, dtype, tile):
@@ -160,6 +169,47 @@ def test_integers_are_exact(h, dtype):
     C = torch.empty((4, 136, 200), device="cuda")
     h.run_grouped_wgrad(A.cuda(), dY.cuda(), device_offsets(b), C, dtype)
     assert torch.equal(C.cpu().double(), wgrad_ref(A, dY, b)[0])
+
+
+@pytest.mark.parametrize("rows", [1, 7, 40, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "tf32"])
+def test_few_tiles_and_a_long_contraction_are_cut(h, gm, dtype, rows):
+    """Fewer tiles than SMs: clusters share K, unless the option forbids it."""
+    b = bounds_of([rows])
+    K, N = 4104, 200
+    A, W = draw((rows, K), dtype, 32), draw((1, K, N), dtype, 33)
+    ref = forward_ref(A, W, b)
+    cut = run_forward(h, A, W, b, "row", dtype)
+    assert "+splitk" in h.last_path
+    assert_close(cut, *ref, K, dtype)
+    if dtype == "bf16":
+        assert torch.equal(run_forward(h, A, W, b, "row", dtype, torch.bfloat16), cut.bfloat16())
+    h.set_option(gm.GEMM_OPT_SPLIT_K, 1)
+    whole = run_forward(h, A, W, b, "row", dtype)
+    assert "+splitk" not in h.last_path
+    assert_close(whole, *ref, K, dtype)
+
+
+@pytest.mark.parametrize("tile", [0, 1064, 1256, 2256])
+def test_long_sums_of_one_sign_keep_fp32_accuracy(h, gm, tile):
+    """The tensor core drops up to one unit (2^-23) of its FP32 accumulator per
+    addition; the library lets at most 48 additions pass between roundings to
+    nearest, so results of positive operands stay within 48 2^-23 of the sum at
+    any K (512 additions in one go at K = 8192)."""
+    h.set_option(gm.GEMM_OPT_GROUPED_TILE, tile)
+    gen = torch.Generator().manual_seed(34)
+    rows, K, N = 260, 8192, 256
+    A = torch.rand((rows, K), generator=gen).bfloat16()
+    W = torch.rand((1, K, N), generator=gen).bfloat16()
+    ref = forward_ref(A, W, [0, rows])[0]
+    C = run_forward(h, A, W, [0, rows], "row", "bf16").cpu().double()
+    assert float(((C - ref).abs() / ref).max()) <= 48 * 2.0 ** -23
+    g = torch.empty((1, 256, 128), device="cuda")
+    A, B = torch.rand((K, 256), generator=gen).bfloat16(), torch.rand((K, 128), generator=gen).bfloat16()
+    h.run_grouped_wgrad(A.cuda(), B.cuda(), device_offsets([0, K]), g, "bf16")
+    h.sync_status()
+    ref = A.double().T @ B.double()
+    assert float(((g[0].cpu().double() - ref).abs() / ref).max()) <= 48 * 2.0 ** -23
 
 
 def test_rows_outside_the_groups_and_padding_are_untouched(h):
@@ -301,7 +351,7 @@ def test_side_streams_and_graphs(h):
         assert_close(C, *forward_ref(A, W, b), K, "bf16")
 
 
-@pytest.mark.parametrize("tile", [1064, 2256])
+@pytest.mark.parametrize("tile", [1064, 2256, 41128])
 @pytest.mark.parametrize("op", ["forward", "wgrad"])
 def test_expired_wait_is_reported_and_the_handle_recovers(h, gm, op, tile):
     b = bounds_of([300, 200, 40])

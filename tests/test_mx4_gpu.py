@@ -182,8 +182,8 @@ def test_product(gm, h, shape):
     assert torch.equal(half, C.bfloat16())
 
 
-@pytest.mark.parametrize("tile", [1032, 1064, 1128, 1256, 2032, 2064, 2128, 2256])
-@pytest.mark.parametrize("K", [200, 2080])
+@pytest.mark.parametrize("tile", [1032, 1064, 1128, 1224, 1256, 2032, 2064, 2128, 2224, 21032, 41128, 81064])
+@pytest.mark.parametrize("K", [200, 2080, 5000])
 def test_every_tile(gm, h, tile, K):
     """Tiles enough for several accumulator hand-overs a CTA."""
     h.set_option(gm.GEMM_OPT_GROUPED_TILE, tile)
@@ -196,7 +196,7 @@ def test_every_tile(gm, h, tile, K):
     assert_close(C, a @ b.T, a.abs() @ b.abs().T, K)
 
 
-@pytest.mark.parametrize("tile", [0, 1032, 1256, 2064, 2256])
+@pytest.mark.parametrize("tile", [0, 1032, 1256, 2064, 2256, 21032, 81128])
 @pytest.mark.parametrize("sizes", [[1], [0, 3, 0, 0, 40], [300, 0, 17, 128, 257, 1], [(5 * i) % 7 for i in range(90)]],
                          ids=lambda s: f"{len(s)}groups")
 def test_grouped_product(gm, h, sizes, tile):
@@ -247,7 +247,7 @@ def test_expired_wait_is_reported_and_the_handle_recovers(gm, h):
     aq, bq, a, b = operands(gm, h, M, N, K, 13)
     C = torch.zeros((M, N), device="cuda")
     h.set_option(gm.GEMM_OPT_WAIT_TIMEOUT_NS, 20_000_000)
-    for tile in (1064, 2256):
+    for tile in (1064, 2256, 41064):
         h.set_option(gm.GEMM_OPT_GROUPED_TILE, tile)
         h.set_option(gm.GEMM_OPT_DEBUG_DROP_LOAD, 1)
         h.run_mx4(aq, bq, C)
