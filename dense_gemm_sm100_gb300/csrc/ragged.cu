@@ -177,6 +177,19 @@ struct Tile {
     int kt;   // its stages
 };
 
+// Tile r of a group's tiles_q x tiles_p: bands of group_q tile rows, column by
+// column inside a band, so that CTAs running at the same time share panels.
+__device__ __forceinline__ void tile_order(const Params &p, int r, int tiles_q, int &qb, int &pb)
+{
+    const int per = p.group_q * p.tiles_p;
+    const int band = r / per;
+    const int first = band * p.group_q;
+    const int gq = min(tiles_q - first, p.group_q);
+    const int rr = r - band * per;
+    qb = first + rr % gq;
+    pb = rr / gq;
+}
+
 template <int BK, bool RAGGED_K>
 __device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u, int krank)
 {
@@ -204,13 +217,9 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *table, int u
     group_range(p, t.g, t.lo, hi);
     t.cnt = hi - t.lo;
     if (!RAGGED_K) tiles_q = (t.cnt + p.bn - 1) / p.bn;
-    const int per = p.group_q * p.tiles_p;
-    const int grp = r / per;
-    const int first = grp * p.group_q;
-    const int gq = min(tiles_q - first, p.group_q);
-    const int rr = r - grp * per;
-    t.q0 = (first + rr % gq) * p.bn;
-    t.pb = rr / gq;
+    int qb;
+    tile_order(p, r, tiles_q, qb, t.pb);
+    t.q0 = qb * p.bn;
     t.qn = min(p.bn, (RAGGED_K ? p.Q : t.cnt) - t.q0);
     t.ks = 0;
     t.kt = ((RAGGED_K ? t.cnt : p.K) + BK - 1) / BK;
@@ -1099,7 +1108,8 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     // Stages a CTA adds up (of an average group, for a ragged contraction).
     const int bk = ragged_bk(kind);
     const int64_t k_len = ragged_k ? (int64_t{a.rows} + a.groups - 1) / a.groups : a.K;
-    const bool sum = a.out_bf16 == 0 && (k_len + bk - 1) / bk > int64_t{seg_stages(kind)} * t.split;
+    const int64_t seg = int64_t{seg_stages(kind)} * t.split;
+    const bool sum = a.out_bf16 == 0 && (k_len + bk - 1) / bk > (ragged_k ? seg * 2 / 3 : seg);  // groups differ
     return dispatch(kind, t.ctas, p_mn, ragged_k, sum, Launch{tmP, tmQ, p, static_cast<int>(grid), a.stream});
 }
 

@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
-#include <cstring>
 #include <string>
 
 #include "../../include/gemm.h"
@@ -323,11 +322,15 @@ dg::RaggedArgs common_args(const gemm_ctx *h, const int64_t *offsets, int64_t gr
     return a;
 }
 
-std::string path_name(const char *op, int kind, const dg::RaggedTile &t, const char *rest)
+// Formatted in place: these calls may take only microseconds.
+void set_path(gemm_ctx *h, const char *op, int kind, const dg::RaggedTile &t, const char *rest, bool ra, bool rb)
 {
     const char *k = kind == dg::kRaggedMx4 ? "mx4" : kind == dg::kRaggedTf32 ? "tf32" : "bf16";
-    return std::string(op) + "_" + k + (t.ctas == 2 ? "_pair" : "_") + std::to_string(128 * t.ctas) + "x" +
-           std::to_string(t.bn) + rest + (t.split > 1 ? "+splitk" + std::to_string(t.split) : "");
+    char split[16] = "", path[128];
+    if (t.split > 1) std::snprintf(split, sizeof split, "+splitk%d", t.split);
+    std::snprintf(path, sizeof path, "%s_%s%s%dx%d%s%s%s%s", op, k, t.ctas == 2 ? "_pair" : "_", 128 * t.ctas, t.bn,
+                  rest, ra ? "+repackA" : "", rb ? "+repackB" : "", split);
+    h->last_path = path;
 }
 
 // A row-major operand that TMA can address: itself, or its copy in the
@@ -394,7 +397,7 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     const cudaError_t e = dg::launch_ragged(kind, false, false, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "4-bit product launch");
     ++h->launches;
-    h->last_path = path_name(offsets ? "grouped" : "tc", kind, t, "");
+    set_path(h, offsets ? "grouped" : "tc", kind, t, "", false, false);
     return GEMM_OK;
 }
 
@@ -438,26 +441,22 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
     const dg::RaggedTile t = tile_for(h, kind, false, rows, groups, N, 0, K);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
-    std::string rest = row ? "_rowB" : "_colB";
-    bool used_ws = false;
+    Repack ra, rb;
     if (K > 0) {
-        const Repack ra = plan_repack(h, A, lda, 1, 0, rows, K, es);
-        const Repack rb = plan_repack(h, B, ldb, groups, stride_b, rows_b, cols_b, es);
-        used_ws = ra.needed || rb.needed;
-        if (used_ws && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+        ra = plan_repack(h, A, lda, 1, 0, rows, K, es);
+        rb = plan_repack(h, B, ldb, groups, stride_b, rows_b, cols_b, es);
+        if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
         uint8_t *ws = static_cast<uint8_t *>(h->ws);
         if (ra.needed) {
             if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, K, es, stream))) return rc;
             A = ws;
             lda = ra.ld;
-            rest += "+repackA";
         }
         if (rb.needed) {
             if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, groups, stride_b, rows_b, cols_b, es, stream))) return rc;
             B = ws + ra.bytes;
             ldb = rb.ld;
             stride_b = rows_b * rb.ld;
-            rest += "+repackB";
         }
         a.p_chunks = row && N % (128 / es) == 0 ? 1 : 0;
         rc = row ? encode_mn(h, &tmP, es, B, K, N, ldb, groups, stride_b, dg::kRaggedP, a.p_chunks != 0)
@@ -471,8 +470,8 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
     const cudaError_t e = dg::launch_ragged(kind, false, row, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "grouped product launch");
     ++h->launches;
-    h->last_path = path_name("grouped", kind, t, rest.c_str());
-    return used_ws ? dg::note_workspace_use(h, stream) : GEMM_OK;
+    set_path(h, "grouped", kind, t, row ? "_rowB" : "_colB", ra.needed, rb.needed);
+    return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
 }
 
 int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M, int64_t N, const int64_t *offsets,
@@ -494,25 +493,21 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, M, 0, C, ldc, c_dtype, stream);
     a.stride_c = groups > 1 ? stride_c : 0;
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
-    std::string rest = "_wgrad";
-    bool used_ws = false;
+    Repack ra, rb;
     if (rows > 0) {
-        const Repack ra = plan_repack(h, A, lda, 1, 0, rows, M, es);
-        const Repack rb = plan_repack(h, B, ldb, 1, 0, rows, N, es);
-        used_ws = ra.needed || rb.needed;
-        if (used_ws && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+        ra = plan_repack(h, A, lda, 1, 0, rows, M, es);
+        rb = plan_repack(h, B, ldb, 1, 0, rows, N, es);
+        if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
         uint8_t *ws = static_cast<uint8_t *>(h->ws);
         if (ra.needed) {
             if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, M, es, stream))) return rc;
             A = ws;
             lda = ra.ld;
-            rest += "+repackA";
         }
         if (rb.needed) {
             if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, 1, 0, rows, N, es, stream))) return rc;
             B = ws + ra.bytes;
             ldb = rb.ld;
-            rest += "+repackB";
         }
         a.p_chunks = N % (128 / es) == 0 ? 1 : 0;
         a.q_chunks = M % (128 / es) == 0 ? 1 : 0;
@@ -523,8 +518,8 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
     const cudaError_t e = dg::launch_ragged(kind, true, true, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "weight gradient launch");
     ++h->launches;
-    h->last_path = path_name("grouped", kind, t, rest.c_str());
-    return used_ws ? dg::note_workspace_use(h, stream) : GEMM_OK;
+    set_path(h, "grouped", kind, t, "_wgrad", ra.needed, rb.needed);
+    return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
 }
 
 int64_t gemm_mx4_code_pitch(int64_t K) { return K <= 0 ? 0 : round_up(round_up(K, GEMM_MX4_BLOCK) / 2, 16); }

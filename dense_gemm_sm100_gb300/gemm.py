@@ -403,19 +403,24 @@ def _matrices(t, name, device):
     return n, rows, cols, ld, (stride[0] if n > 1 else rows * ld), _type_code(t, name)
 
 
+_int64 = None
+
+
 def _offsets(t, groups, device):
-    import torch
+    global _int64
+    if _int64 is None:
+        import torch
+        _int64 = torch.int64
     _on_device(t, "offsets", device)
-    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != groups + 1 or (groups > 0 and t.stride(0) != 1):
+    if t.dtype != _int64 or t.dim() != 1 or t.shape[0] != groups + 1 or (groups > 0 and t.stride(0) != 1):
         raise ValueError(f"offsets must be a contiguous int64 tensor of {groups + 1} values")
     return t.data_ptr()
 
 
-def _operand_types(dt, **codes):
+def _operand_types(dt, a, b):
     want = GEMM_BF16 if dt == GEMM_BF16 else GEMM_F32
-    for name, code in codes.items():
-        if code != want:
-            raise ValueError(f"{name} must be {'bfloat16' if dt == GEMM_BF16 else 'float32'} for this dtype")
+    if a != want or b != want:
+        raise ValueError(f"A and B must be {'bfloat16' if dt == GEMM_BF16 else 'float32'} for this dtype")
 
 
 _current_raw_stream = None
@@ -570,7 +575,7 @@ class Gemm:
         Kb, Nb = (d1, d2) if lb == GEMM_B_ROW_MAJOR else (d2, d1)
         if Kb != K or Nb != N or rows != M:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)} ({layout_b}), C {tuple(C.shape)}")
-        _operand_types(dt, A=a_type, B=b_type)
+        _operand_types(dt, a_type, b_type)
         rc = self._lib.gemm_grouped_run(self.handle, lb, groups, M, N, K, _offsets(offsets, groups, dev), A.data_ptr(),
                                         lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt, c_type,
                                         _raw_stream(stream, dev))
@@ -591,7 +596,7 @@ class Gemm:
         groups, Mc, Nc, ldc, stride_c, c_type = _matrices(C, "C", dev)
         if rows_b != rows or Mc != M or Nc != N:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
-        _operand_types(dt, A=a_type, B=b_type)
+        _operand_types(dt, a_type, b_type)
         rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
                                           A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
                                           c_type, _raw_stream(stream, dev))
