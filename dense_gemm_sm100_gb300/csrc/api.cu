@@ -427,6 +427,7 @@ int gemm_destroy(gemm_handle_t h)
     {
         DeviceGuard guard(h->device);
         cudaDeviceSynchronize();
+        for (void *old : h->ws_retired) cudaFreeAsync(old, nullptr);
         if (h->ws) {
             cudaFreeAsync(h->ws, nullptr);  // allocated from the stream-ordered pool
             cudaStreamSynchronize(nullptr);

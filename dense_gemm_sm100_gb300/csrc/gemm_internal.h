@@ -162,8 +162,11 @@ cudaError_t launch_tile_split_reduce(const float *partials, int splits, int64_t 
                                      cudaStream_t stream);
 
 // dst[r*ldd + c] = src[r*lds + c] for r < rows, c < cols (elem_bytes 2 or 4).
+// With offsets (on the device), only rows r whose group g = r / rows_per has
+// offsets[g] < offsets[g + 1].
 cudaError_t launch_repack(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t rows,
-                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream);
+                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream,
+                          const int64_t *offsets = nullptr, int64_t rows_per = 1);
 
 // Three-part TF32 split of an FP32 operand (rows x cols at pitch lds) for the
 // FP32-accurate tensor-core mode: x = hi + lo, hi = x with its low 13

@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <string>
+#include <vector>
 
 #include "../../include/gemm.h"
 
@@ -24,6 +25,11 @@ struct gemm_ctx {
     // is released.
     cudaEvent_t ws_event = nullptr;
     bool ws_event_recorded = false;
+    // A call that used the present workspace was captured in a CUDA graph: the
+    // graph may run at any later time, so growth keeps the buffer until the
+    // handle goes.
+    bool ws_captured = false;
+    std::vector<void *> ws_retired;
     std::string last_error;
     std::string last_path;
     int64_t launches = 0;
@@ -94,7 +100,9 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
     bytes = (bytes + (size_t{2} << 20) - 1) & ~((size_t{2} << 20) - 1);
     if (h->ws_limit > 0 && bytes > h->ws_limit) bytes = need;  // stay within the limit
     cudaError_t e = cudaSuccess;
-    if (h->ws) {
+    if (h->ws && h->ws_captured) {
+        h->ws_retired.push_back(h->ws);
+    } else if (h->ws) {
         // Earlier calls (on this or another stream) may still read the old buffer.
         if (h->ws_event_recorded) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
         if (e == cudaSuccess) e = cudaFreeAsync(h->ws, stream);
@@ -103,6 +111,7 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
     h->ws = nullptr;
     h->ws_bytes = 0;
     h->ws_event_recorded = false;
+    h->ws_captured = false;
     e = cudaMallocAsync(&h->ws, bytes, stream);
     if (e != cudaSuccess) {
         h->ws = nullptr;
@@ -117,7 +126,14 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
 // `stream` is what the next growth waits for.
 inline int note_workspace_use(gemm_ctx *h, cudaStream_t stream)
 {
-    cudaError_t e = cudaEventRecord(h->ws_event, stream);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &capture);
+    if (e == cudaSuccess && capture == cudaStreamCaptureStatusActive) {
+        // an event recorded into the graph could not be waited for outside it
+        h->ws_captured = true;
+        return GEMM_OK;
+    }
+    if (e == cudaSuccess) e = cudaEventRecord(h->ws_event, stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "workspace-use event");
     h->ws_event_recorded = true;
     return GEMM_OK;

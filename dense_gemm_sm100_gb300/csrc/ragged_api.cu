@@ -353,14 +353,15 @@ Repack plan_repack(const gemm_ctx *h, const void *src, int64_t ld, int64_t group
     return r;
 }
 
+// `offsets`: skip the matrices of groups without rows.
 int run_repack(gemm_ctx *h, const Repack &r, uint8_t *dst, const void *src, int64_t ld, int64_t groups,
-               int64_t stride, int64_t rows, int64_t cols, int es, cudaStream_t stream)
+               int64_t stride, int64_t rows, int64_t cols, int es, const int64_t *offsets, cudaStream_t stream)
 {
     const bool flat = groups == 1 || stride == rows * ld;  // one matrix of groups * rows rows
     for (int64_t g = 0; g < (flat ? 1 : groups); ++g) {
         const cudaError_t e = dg::launch_repack(static_cast<const uint8_t *>(src) + g * stride * es, ld,
                                                 dst + g * rows * r.ld * es, r.ld, flat ? groups * rows : rows, cols,
-                                                es, h->sm_count, stream);
+                                                es, h->sm_count, stream, offsets ? offsets + g : nullptr, rows);
         if (e != cudaSuccess) return cuda_fail(h, e, "repack launch");
         ++h->launches;
     }
@@ -448,12 +449,13 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
         if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
         uint8_t *ws = static_cast<uint8_t *>(h->ws);
         if (ra.needed) {
-            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, K, es, stream))) return rc;
+            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, K, es, nullptr, stream))) return rc;
             A = ws;
             lda = ra.ld;
         }
         if (rb.needed) {
-            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, groups, stride_b, rows_b, cols_b, es, stream))) return rc;
+            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, groups, stride_b, rows_b, cols_b, es, offsets, stream)))
+                return rc;
             B = ws + ra.bytes;
             ldb = rb.ld;
             stride_b = rows_b * rb.ld;
@@ -500,12 +502,12 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
         if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
         uint8_t *ws = static_cast<uint8_t *>(h->ws);
         if (ra.needed) {
-            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, M, es, stream))) return rc;
+            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, M, es, nullptr, stream))) return rc;
             A = ws;
             lda = ra.ld;
         }
         if (rb.needed) {
-            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, 1, 0, rows, N, es, stream))) return rc;
+            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, 1, 0, rows, N, es, nullptr, stream))) return rc;
             B = ws + ra.bytes;
             ldb = rb.ld;
         }

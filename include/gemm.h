@@ -50,7 +50,10 @@
  * Growth is stream-ordered on the calling stream (cudaFreeAsync of the old
  * buffer after the last call that used it, then cudaMallocAsync from the
  * device's default memory pool): it neither synchronises the device nor
- * waits on the host.  gemm_destroy synchronises the device.
+ * waits on the host.  A workspace that a captured call used is kept until
+ * gemm_destroy, because its CUDA graph may run at any time (capture after a
+ * first call of the same sizes, so that nothing grows during the capture).
+ * gemm_destroy synchronises the device.
  *
  * Errors: every function returns GEMM_OK (0) or a negative GEMM_ERR_* code.
  * Argument errors are detected on the host before anything is launched.

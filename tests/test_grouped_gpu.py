@@ -351,6 +351,30 @@ def test_side_streams_and_graphs(h):
         assert_close(C, *forward_ref(A, W, b), K, "bf16")
 
 
+def test_a_captured_workspace_outlives_growth(h):
+    """Operands that are re-packed into the workspace: calls captured in a graph,
+    then eager calls whose larger workspace replaces it, then the graph again."""
+    b = bounds_of([30, 41])
+    A, W = draw((71, 77), "bf16", 35), draw((2, 77, 131), "bf16", 36)
+    A_d, W_d, o = A.cuda(), W.cuda(), device_offsets(b)
+    C = torch.zeros((71, 131), device="cuda")
+    h.run_grouped(A_d, W_d, o, C, "row", "bf16")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.run_grouped(A_d, W_d, o, C, "row", "bf16")
+    assert "+repackA+repackB" in h.last_path
+    big = draw((3000, 1001), "bf16", 37), draw((4, 1001, 999), "bf16", 38)
+    bb = bounds_of([1000, 0, 500, 1500])
+    for _ in range(2):
+        large = run_forward(h, *big, bb, "row", "bf16")
+        C.zero_()
+        graph.replay()
+        h.sync_status()
+        assert_close(C, *forward_ref(A, W, b), 77, "bf16")
+        assert_close(large, *forward_ref(*big, bb), 1001, "bf16")
+
+
 @pytest.mark.parametrize("tile", [1064, 2256, 41128])
 @pytest.mark.parametrize("op", ["forward", "wgrad"])
 def test_expired_wait_is_reported_and_the_handle_recovers(h, gm, op, tile):
