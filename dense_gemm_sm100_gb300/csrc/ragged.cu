@@ -650,18 +650,21 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 if (n <= 0 || col0 >= p.P) return;
                 const long long at = base + static_cast<long long>(unit * 16) * p.ldc;
                 if (!SUM && p.c_vec && p.out_bf16) {
-                    // words of two rows' neighbours, [row pair][column]
+                    // words of two rows' neighbours, [row pair][column], odd
+                    // pairs' 16-byte pieces swapped in twos (bank conflicts)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const __nv_bfloat162 w =
                             __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        sts_u32(stage + j * 128 + lane * 4, *reinterpret_cast<const uint32_t *>(&w));
+                        sts_u32(stage + j * 128 + ((lane * 4) ^ ((j & 1) * 16)),
+                                *reinterpret_cast<const uint32_t *>(&w));
                     }
                     __syncwarp();
                     // a lane: eight columns of two rows
                     const int piece = (lane & 3) * 8, r = (lane >> 2) * 2;
                     const uint32_t src = stage + (lane >> 2) * 128 + piece * 4;
-                    const uint4 a = lds_u4(src), b = lds_u4(src + 16);
+                    const uint32_t swap = ((lane >> 2) & 1) * 16;
+                    const uint4 a = lds_u4(src + swap), b = lds_u4(src + (16 - swap));
                     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at + r * p.ldc + piece;
                     if (col0 + piece < p.P) {
                         if (r < n)
@@ -759,9 +762,10 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         const long long ld = part == 0 ? p.lds_p : p.lds_q;
         int u = first_unit, k0 = 0, kts = 0, first = 0, limit = 0, blocks = 0;
         const uint8_t *base = nullptr;
-        // Lane l loads 16-byte piece l % 4 of rows l / 4, l / 4 + 8, ...: eight
-        // rows' 64 bytes an instruction, whole sectors.
-        const int piece = lane & 3, row8 = lane >> 2;
+        // Lane l loads 16-byte piece l / 8 of rows l % 8, l % 8 + 8, ...: eight
+        // rows' 64 bytes an instruction, whole sectors; eight lanes then store
+        // 128 contiguous bytes.
+        const int piece = lane >> 3, row8 = lane & 7;
         uint4 r[16];
         const auto tile = [&]() {
             if (u >= num_units) return;
@@ -790,27 +794,25 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             if (!mbar_wait_warp(sfree_bar + 8 * slot, ((sup >> 1) & 1u) ^ 1u, abort_flag, p.status, kWaitScaleEmpty,
                                 p.timeout_ns))
                 break;
-            // word w of the piece: stage 2 * piece + w / 2, word w % 2 of row i * 8 + row8
+            // word w of the piece: stage 2 * piece + w / 2, word w % 2
             const uint32_t stage_step = static_cast<uint32_t>(p.sf_parts * SF_PART);
             const uint32_t dst = sf_base + slot * sf_slot + part * SF_PART + 2 * piece * stage_step + row8 * 16;
             const int left = blocks - k0 * 8 - piece * 16;  // blocks of K from the piece on
             const auto keep = [&](uint32_t w, int n) {        // the first n bytes of a word
                 return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
             };
+            if (left < 16)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                uint4 x = r[i];
-                if (left < 16) {
-                    x.x = keep(x.x, left);
-                    x.y = keep(x.y, left - 4);
-                    x.z = keep(x.z, left - 8);
-                    x.w = keep(x.w, left - 12);
-                }
-                const uint32_t at = dst + (i & 3) * 128 + (i >> 2) * 4;  // rows 32 * (i / 4) + 8 * (i % 4) + row8
-                sts_u32(at, x.x);
-                sts_u32(at + 512, x.y);
-                sts_u32(at + stage_step, x.z);
-                sts_u32(at + stage_step + 512, x.w);
+                for (int i = 0; i < 16; ++i)
+                    r[i] = make_uint4(keep(r[i].x, left), keep(r[i].y, left - 4), keep(r[i].z, left - 8),
+                                      keep(r[i].w, left - 12));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // rows 8 i + row8 + (0, 32, 64, 96)
+                const uint32_t at = dst + i * 128;
+                sts_u4(at, make_uint4(r[i].x, r[i + 4].x, r[i + 8].x, r[i + 12].x));
+                sts_u4(at + 512, make_uint4(r[i].y, r[i + 4].y, r[i + 8].y, r[i + 12].y));
+                sts_u4(at + stage_step, make_uint4(r[i].z, r[i + 4].z, r[i + 8].z, r[i + 12].z));
+                sts_u4(at + stage_step + 512, make_uint4(r[i].w, r[i + 4].w, r[i + 8].w, r[i + 12].w));
             }
             k0 += SUP;
             if (k0 >= kts) {
