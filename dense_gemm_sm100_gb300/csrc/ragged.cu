@@ -1014,7 +1014,8 @@ bool ragged_tile_ok(int split, int ctas, int bn)
 // Estimated time of each tile in cycles; the least wins.  A ring stage takes
 // its four MMA instructions (measured: 128 cycles at N = 256, 64 at 128, 48 at
 // 64, 40 at 32) or the arrival of its bytes (55 a cycle and SM measured),
-// whichever is longer; a tile its stages or its epilogue (12 cycles a row); a
+// whichever is longer; a tile its stages (and for 4-bit pairs 3000 cycles: the
+// scales' hand-over between the CTAs) or its epilogue (12 cycles a row); a
 // launch the waves of tiles, one epilogue and 3 us, and at least its traffic at
 // 6.4 TB/s.  The type of C does not enter, so that a BF16 result is the FP32
 // result rounded.
@@ -1045,7 +1046,8 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
                 const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
                                        : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
                                                     : double((rows + bn - 1) / bn);
-                const double tile = static_cast<double>((kt + split - 1) / split) * stage;
+                const double tile = static_cast<double>((kt + split - 1) / split) * stage +
+                                    (kind == kRaggedMx4 && ctas > 1 ? 3000 : 0);
                 const double epi = 600 + bn * 12.0;
                 const double fill = tiles_q * tiles_p * ctas * split / sm_count;
                 const double run = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) +
