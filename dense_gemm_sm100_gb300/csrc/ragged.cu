@@ -8,7 +8,7 @@
 // group's last tile shrinks the instruction to the rows that are left, and few
 // rows per expert do not pay for 128-row tiles.  In the epilogue a warp holds
 // 32 neighbouring columns of C and walks the rows.  Where C's rows start on 16
-// bytes the warp turns 32 x 32 elements in shared memory and writes 16 bytes a
+// bytes the warp turns 16 x 32 elements in shared memory and writes 16 bytes a
 // lane; else every store instruction writes 32 neighbouring elements, at any
 // pitch and alignment.  Either way a tile ends at its group's last row, and
 // rows of the next group are never touched.
@@ -28,7 +28,8 @@
 // copies a stage's words to tensor memory (tcgen05.cp) ahead of the stage's
 // MMAs, in order with them.  Eight stages at a time because the hand-over (a
 // proxy fence, and a release at cluster scope from the odd CTA of a pair) takes
-// about 1 us: once a stage it set the pace, 395 us for 8192 x 14336 x 4096.
+// about 1 us: once a stage it set the pace, 395 us for 8192 x 14336 x 4096
+// (157 us now).
 //
 // Long FP32 sums.  The tensor core's FP32 accumulator drops the bits that do
 // not fit at every addition, an error that grows with their number (measured,
@@ -37,7 +38,7 @@
 // operands longer than 12 (8) ring stages, 48 (32) additions, the accumulator
 // therefore runs over that many stages at a time, and the epilogue warps add
 // the segments in registers, rounding to nearest (5e-7 at any K, for a tenth of
-// the rate at K = 4096).  BF16 results round by 2^-9 afterwards; sums of 4-bit
+// the rate at K = 4096).  BF16 results round by 2^-8 afterwards; sums of 4-bit
 // products have few bits and few additions (64 K elements each).
 //
 // Few tiles.  A launch with fewer tiles than SMs and a long contraction runs
@@ -77,14 +78,14 @@ constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 2 + 2 + 1;
 // Accumulators at tensor-memory columns 0 and ACC1.  For 4-bit operands the
 // scales of two stages live at SF_COL, which leaves two accumulators of 224
-// rows.  (256 rows, the accumulators sharing 48 columns that the epilogue frees
-// first: 163 us for 8192 x 14336 x 4096, 2.5 us of every tile in that hand-over.)
+// rows: 157 us for 8192 x 14336 x 4096, against 165 us with tiles of 256 rows
+// whose accumulators share 48 columns that the epilogue frees first.
 constexpr int ACC1 = 256, ACC1_MX = 224;
 constexpr int SF_COL = 448, SF_COLS = 24;  // per stage: 2 words x 4 (P) and 2 words x 8 (Q) columns
 constexpr int SUP = 8;           // ring stages whose scales are handed over together
 constexpr int SF_PART = 1024;    // a stage's words of 128 rows
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_BYTES = EPI_WARPS * 2048;  // a warp's staging: 32 x 32 BF16 or 16 x 32 FP32
+constexpr int EPI_BYTES = EPI_WARPS * 2048;  // a warp's staging: 16 x 32 FP32, or BF16 in half of it
 constexpr int WARPS = 2 + EPI_WARPS, WARPS_MX = WARPS + 3;
 constexpr int SMEM_MAX = 227 * 1024;
 
@@ -756,8 +757,10 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         // ------------------------------------------------------ block scales
         // The first: P's rows; the others: 128 rows of Q each.  Out-of-range
         // rows and blocks get scale byte 0 (their codes are zero).
-        // The loads of the next hand-over are issued before the fence of the
-        // present one, so their latencies overlap.
+        // The loads of the next hand-over are issued once the present one is
+        // announced (in front of its fence, which waits for them, they cost
+        // 166 instead of 157 us on 8192 x 14336 x 4096) and land while the
+        // warp waits for a free slot.
         const int part = warp - 2 - EPI_WARPS;
         const long long ld = part == 0 ? p.lds_p : p.lds_q;
         int u = first_unit, k0 = 0, kts = 0, first = 0, limit = 0, blocks = 0;
@@ -820,10 +823,10 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 u += unit_step;
                 tile();
             }
-            fetch();
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(sready_bar + 8 * slot);
+            fetch();
         }
     }
 
