@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "gemm_internal.h"
+#include "ptx.cuh"
 
 namespace dg {
 namespace {
@@ -33,42 +34,47 @@ namespace {
 constexpr int kRepackWords = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(256) repack_rows_kernel(const T *__restrict__ src, long long lds,
-                                                          T *__restrict__ dst, long long ldd,
-                                                          long long rows, long long cols, int pieces,
-                                                          const long long *__restrict__ offsets, long long rows_per)
+__device__ __forceinline__ void repack_piece(const RepackJob &j, long long piece, int lane)
 {
     constexpr int PER = 4 / sizeof(T);  // elements of a word
-    const int lane = threadIdx.x & 31;
-    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-    const long long total = rows * pieces;
-    for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < total; w += warps) {
-        const long long r = w / pieces;
-        if (offsets != nullptr) {
-            const long long g = r / rows_per;
-            if (offsets[g + 1] <= offsets[g]) continue;
-        }
-        const long long c0 = (w - r * pieces) * (32 * kRepackWords * PER) + lane * PER;
-        const T *s = src + r * lds + c0;
-        T *d = dst + r * ldd + c0;
-        T v[kRepackWords][PER];
+    const long long r = piece / j.pieces;
+    if (j.offsets != nullptr) {
+        const long long g = r / j.rows_per;
+        if (j.offsets[g + 1] <= j.offsets[g]) return;
+    }
+    const long long c0 = (piece - r * j.pieces) * (32 * kRepackWords * PER) + lane * PER;
+    const T *s = static_cast<const T *>(j.src) + r * j.lds + c0;
+    T *d = static_cast<T *>(j.dst) + r * j.ldd + c0;
+    T v[kRepackWords][PER];
 #pragma unroll
-        for (int i = 0; i < kRepackWords; ++i)
+    for (int i = 0; i < kRepackWords; ++i)
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-                if (c0 + i * 32 * PER + e < cols) v[i][e] = s[i * 32 * PER + e];
+        for (int e = 0; e < PER; ++e)
+            if (c0 + i * 32 * PER + e < j.cols) v[i][e] = s[i * 32 * PER + e];
 #pragma unroll
-        for (int i = 0; i < kRepackWords; ++i) {
-            const long long c = c0 + i * 32 * PER;
-            if (c + PER <= cols) {
-                uint32_t word = v[i][0];
-                if (PER == 2) word |= static_cast<uint32_t>(v[i][PER - 1]) << 16;
-                *reinterpret_cast<uint32_t *>(d + i * 32 * PER) = word;
-            } else if (c < cols) {
-                d[i * 32 * PER] = v[i][0];
-            }
+    for (int i = 0; i < kRepackWords; ++i) {
+        const long long c = c0 + i * 32 * PER;
+        if (c + PER <= j.cols) {
+            uint32_t word = v[i][0];
+            if (PER == 2) word |= static_cast<uint32_t>(v[i][PER - 1]) << 16;
+            *reinterpret_cast<uint32_t *>(d + i * 32 * PER) = word;
+        } else if (c < j.cols) {
+            d[i * 32 * PER] = v[i][0];
         }
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    repack_rows_kernel(const __grid_constant__ RepackJob a, const __grid_constant__ RepackJob b, long long warps_a,
+                       long long warps_all)
+{
+    const int lane = threadIdx.x & 31;
+    const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    griddep_wait();  // may start while the kernel before it on the stream ends
+    for (; w < warps_a; w += step) repack_piece<T>(a, w, lane);
+    for (; w < warps_all; w += step) repack_piece<T>(b, w - warps_a, lane);
 }
 
 // x split into its TF32 part and the FP32 rest.
@@ -163,24 +169,42 @@ int rows_grid(long long rows, int sm_count)
 
 }  // namespace
 
-cudaError_t launch_repack(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t rows,
-                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream, const int64_t *offsets,
-                          int64_t rows_per)
+cudaError_t launch_repack_jobs(RepackJob a, RepackJob b, int elem_bytes, int sm_count, cudaStream_t stream)
 {
-    if (rows <= 0 || cols <= 0) return cudaSuccess;
-    const long long *off = reinterpret_cast<const long long *>(offsets);
     const int64_t piece = 32 * kRepackWords * 4 / elem_bytes;  // elements of a warp's piece
-    const int64_t pieces = (cols + piece - 1) / piece;
-    const int grid = rows_grid((rows * pieces + 7) / 8, sm_count);
-    if (elem_bytes == 4)
-        repack_rows_kernel<uint32_t><<<grid, 256, 0, stream>>>(static_cast<const uint32_t *>(src), lds,
-                                                               static_cast<uint32_t *>(dst), ldd, rows, cols,
-                                                               static_cast<int>(pieces), off, rows_per);
-    else
-        repack_rows_kernel<uint16_t><<<grid, 256, 0, stream>>>(static_cast<const uint16_t *>(src), lds,
-                                                               static_cast<uint16_t *>(dst), ldd, rows, cols,
-                                                               static_cast<int>(pieces), off, rows_per);
-    return cudaGetLastError();
+    const auto warps = [&](RepackJob &j) {
+        if (j.rows <= 0 || j.cols <= 0) return int64_t{0};
+        j.pieces = static_cast<int>((j.cols + piece - 1) / piece);
+        return static_cast<int64_t>(j.rows) * j.pieces;
+    };
+    const int64_t wa = warps(a), all = wa + warps(b);
+    if (all == 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows_grid((all + 7) / 8, sm_count));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return elem_bytes == 4 ? cudaLaunchKernelEx(&cfg, repack_rows_kernel<uint32_t>, a, b, static_cast<long long>(wa),
+                                                static_cast<long long>(all))
+                           : cudaLaunchKernelEx(&cfg, repack_rows_kernel<uint16_t>, a, b, static_cast<long long>(wa),
+                                                static_cast<long long>(all));
+}
+
+cudaError_t launch_repack(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t rows,
+                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream)
+{
+    RepackJob j;
+    j.src = src;
+    j.lds = lds;
+    j.dst = dst;
+    j.ldd = ldd;
+    j.rows = rows;
+    j.cols = cols;
+    return launch_repack_jobs(j, RepackJob(), elem_bytes, sm_count, stream);
 }
 
 cudaError_t launch_split3(const float *src, int64_t lds, float *dst, int64_t ldd, int64_t rows, int64_t cols,

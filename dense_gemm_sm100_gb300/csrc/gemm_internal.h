@@ -162,11 +162,22 @@ cudaError_t launch_tile_split_reduce(const float *partials, int splits, int64_t 
                                      cudaStream_t stream);
 
 // dst[r*ldd + c] = src[r*lds + c] for r < rows, c < cols (elem_bytes 2 or 4).
-// With offsets (on the device), only rows r whose group g = r / rows_per has
-// offsets[g] < offsets[g + 1].
 cudaError_t launch_repack(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t rows,
-                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream,
-                          const int64_t *offsets = nullptr, int64_t rows_per = 1);
+                          int64_t cols, int elem_bytes, int sm_count, cudaStream_t stream);
+
+// Up to two such copies in one launch (rows 0: none).  With offsets (on the
+// device), only rows r whose group g = r / rows_per has offsets[g] <
+// offsets[g + 1].
+struct RepackJob {
+    const void *src = nullptr;
+    long long lds = 0;
+    void *dst = nullptr;
+    long long ldd = 0, rows = 0, cols = 0;
+    const long long *offsets = nullptr;
+    long long rows_per = 1;
+    int pieces = 0;  // filled in by the launch
+};
+cudaError_t launch_repack_jobs(RepackJob a, RepackJob b, int elem_bytes, int sm_count, cudaStream_t stream);
 
 // Three-part TF32 split of an FP32 operand (rows x cols at pitch lds) for the
 // FP32-accurate tensor-core mode: x = hi + lo, hi = x with its low 13

@@ -353,15 +353,38 @@ Repack plan_repack(const gemm_ctx *h, const void *src, int64_t ld, int64_t group
     return r;
 }
 
+// One matrix, or `groups` of them that follow one another, as a copy job.
 // `offsets`: skip the matrices of groups without rows.
-int run_repack(gemm_ctx *h, const Repack &r, uint8_t *dst, const void *src, int64_t ld, int64_t groups,
-               int64_t stride, int64_t rows, int64_t cols, int es, const int64_t *offsets, cudaStream_t stream)
+dg::RepackJob job_of(const Repack &r, uint8_t *dst, const void *src, int64_t ld, int64_t groups, int64_t rows,
+                     int64_t cols, const int64_t *offsets)
 {
-    const bool flat = groups == 1 || stride == rows * ld;  // one matrix of groups * rows rows
-    for (int64_t g = 0; g < (flat ? 1 : groups); ++g) {
-        const cudaError_t e = dg::launch_repack(static_cast<const uint8_t *>(src) + g * stride * es, ld,
-                                                dst + g * rows * r.ld * es, r.ld, flat ? groups * rows : rows, cols,
-                                                es, h->sm_count, stream, offsets ? offsets + g : nullptr, rows);
+    dg::RepackJob j;
+    if (!r.needed) return j;
+    j.src = src;
+    j.lds = ld;
+    j.dst = dst;
+    j.ldd = r.ld;
+    j.rows = groups * rows;
+    j.cols = cols;
+    j.offsets = reinterpret_cast<const long long *>(offsets);
+    j.rows_per = rows;
+    return j;
+}
+
+// Copies the operands that TMA cannot address into the workspace, A and B in
+// one launch; B's matrices one launch each when they do not follow one another.
+int run_repack(gemm_ctx *h, const Repack &ra, const void *A, int64_t lda, int64_t rows_a, int64_t cols_a,
+               const Repack &rb, const void *B, int64_t ldb, int64_t groups, int64_t stride_b, int64_t rows_b,
+               int64_t cols_b, const int64_t *offsets, int es, cudaStream_t stream)
+{
+    uint8_t *ws = static_cast<uint8_t *>(h->ws);
+    const bool flat = groups == 1 || stride_b == rows_b * ldb;
+    const dg::RepackJob a = job_of(ra, ws, A, lda, 1, rows_a, cols_a, nullptr);
+    for (int64_t g = 0; g < (rb.needed && !flat ? groups : 1); ++g) {
+        const dg::RepackJob b =
+            job_of(rb, ws + ra.bytes + g * rows_b * rb.ld * es, static_cast<const uint8_t *>(B) + g * stride_b * es, ldb,
+                   flat ? groups : 1, rows_b, cols_b, offsets ? offsets + g : nullptr);
+        const cudaError_t e = dg::launch_repack_jobs(g == 0 ? a : dg::RepackJob(), b, es, h->sm_count, stream);
         if (e != cudaSuccess) return cuda_fail(h, e, "repack launch");
         ++h->launches;
     }
@@ -446,17 +469,17 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
     if (K > 0) {
         ra = plan_repack(h, A, lda, 1, 0, rows, K, es);
         rb = plan_repack(h, B, ldb, groups, stride_b, rows_b, cols_b, es);
-        if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
-        uint8_t *ws = static_cast<uint8_t *>(h->ws);
+        if (ra.needed || rb.needed) {
+            if ((rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+            if ((rc = run_repack(h, ra, A, lda, rows, K, rb, B, ldb, groups, stride_b, rows_b, cols_b, offsets, es, stream)))
+                return rc;
+        }
         if (ra.needed) {
-            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, K, es, nullptr, stream))) return rc;
-            A = ws;
+            A = h->ws;
             lda = ra.ld;
         }
         if (rb.needed) {
-            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, groups, stride_b, rows_b, cols_b, es, offsets, stream)))
-                return rc;
-            B = ws + ra.bytes;
+            B = static_cast<uint8_t *>(h->ws) + ra.bytes;
             ldb = rb.ld;
             stride_b = rows_b * rb.ld;
         }
@@ -499,16 +522,16 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
     if (rows > 0) {
         ra = plan_repack(h, A, lda, 1, 0, rows, M, es);
         rb = plan_repack(h, B, ldb, 1, 0, rows, N, es);
-        if ((ra.needed || rb.needed) && (rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
-        uint8_t *ws = static_cast<uint8_t *>(h->ws);
+        if (ra.needed || rb.needed) {
+            if ((rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+            if ((rc = run_repack(h, ra, A, lda, rows, M, rb, B, ldb, 1, 0, rows, N, nullptr, es, stream))) return rc;
+        }
         if (ra.needed) {
-            if ((rc = run_repack(h, ra, ws, A, lda, 1, 0, rows, M, es, nullptr, stream))) return rc;
-            A = ws;
+            A = h->ws;
             lda = ra.ld;
         }
         if (rb.needed) {
-            if ((rc = run_repack(h, rb, ws + ra.bytes, B, ldb, 1, 0, rows, N, es, nullptr, stream))) return rc;
-            B = ws + ra.bytes;
+            B = static_cast<uint8_t *>(h->ws) + ra.bytes;
             ldb = rb.ld;
         }
         a.p_chunks = N % (128 / es) == 0 ? 1 : 0;
