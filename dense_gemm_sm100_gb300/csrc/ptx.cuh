@@ -341,6 +341,20 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
                  : "memory");
 }
 
+// Arrivals that order no memory accesses of their own: for handing tensor
+// memory back, behind tcgen05.wait and tcgen05.fence::before_thread_sync (the
+// waiter runs tcgen05.fence::after_thread_sync).  The release forms wait until
+// the thread's earlier global stores are visible.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // One lane of the (fully active) warp gets true.
 __device__ __forceinline__ bool elect_one()
 {
