@@ -36,10 +36,17 @@ struct Checker {
     }
 };
 
-int check_c(const Checker &bad, const void *C, int64_t ldc, int64_t N, int c_dtype)
+// Whether rows at this pitch span more elements (or bytes) than any memory
+// holds; below that no product of the checks and of the set-up overflows.
+bool beyond_memory(int64_t rows, int64_t ld) { return rows > 0 && ld > (int64_t{1} << 44) / rows; }
+
+constexpr const char *kBeyondMemory = "rows times pitch must stay within 2^44";
+
+int check_c(const Checker &bad, const void *C, int64_t ldc, int64_t rows, int64_t N, int c_dtype)
 {
     if (!C) return bad(GEMM_ERR_INVALID, "C is NULL");
     if (ldc < N || ldc > kMaxLd) return bad(GEMM_ERR_INVALID, "ldc must satisfy N <= ldc <= 2^36");
+    if (beyond_memory(rows, ldc)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     if (reinterpret_cast<uintptr_t>(C) % (c_dtype == GEMM_BF16 ? 2 : 4))
         return bad(GEMM_ERR_ALIGNMENT, "C is not aligned to its element size");
     return GEMM_OK;
@@ -85,13 +92,14 @@ int check_grouped(int layout_b, int64_t groups, int64_t rows, int64_t N, int64_t
     if ((rc = check_groups(bad, groups, rows, offsets))) return rc;
     if (rows == 0 || N == 0) return GEMM_OK;
     if (too_many_tiles(rows, groups, N)) return bad(GEMM_ERR_INVALID, "the product has 2^31 tiles or more");
-    if ((rc = check_c(bad, C, ldc, N, c_dtype))) return rc;
+    if ((rc = check_c(bad, C, ldc, rows, N, c_dtype))) return rc;
     if (K == 0) return GEMM_OK;
     if (!A || !B) return bad(GEMM_ERR_INVALID, "A or B is NULL");
     if (lda < K || lda > kMaxLd) return bad(GEMM_ERR_INVALID, "lda must satisfy K <= lda <= 2^36");
     const int64_t rows_b = layout_b == GEMM_B_ROW_MAJOR ? K : N, cols_b = layout_b == GEMM_B_ROW_MAJOR ? N : K;
     if (ldb < cols_b || ldb > kMaxLd)
         return bad(GEMM_ERR_INVALID, "ldb must be at least a row of B's storage and at most 2^36");
+    if (beyond_memory(rows, lda) || beyond_memory(rows_b, ldb)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     if (groups > 1 && (stride_b < (rows_b - 1) * ldb + cols_b || stride_b > kMaxStride))
         return bad(GEMM_ERR_INVALID, "stride_b must reach past a group's matrix and stay within 2^37");
     const uintptr_t es = dtype == GEMM_BF16 ? 2 : 4;
@@ -111,20 +119,22 @@ int check_wgrad(int64_t groups, int64_t rows, int64_t M, int64_t N, const int64_
     if ((rc = check_groups(bad, groups, rows, offsets))) return rc;
     if (M == 0 || N == 0) return GEMM_OK;
     if (too_many_tiles(M * groups, groups, N)) return bad(GEMM_ERR_INVALID, "the product has 2^31 tiles or more");
-    if ((rc = check_c(bad, C, ldc, N, c_dtype))) return rc;
+    if ((rc = check_c(bad, C, ldc, M, N, c_dtype))) return rc;
     if (groups > 1 && (stride_c < (M - 1) * ldc + N || stride_c > kMaxStride))
         return bad(GEMM_ERR_INVALID, "stride_c must reach past a group's matrix and stay within 2^37");
     if (rows == 0) return GEMM_OK;
     if (!A || !B) return bad(GEMM_ERR_INVALID, "A or B is NULL");
     if (lda < M || lda > kMaxLd) return bad(GEMM_ERR_INVALID, "lda must satisfy M <= lda <= 2^36");
     if (ldb < N || ldb > kMaxLd) return bad(GEMM_ERR_INVALID, "ldb must satisfy N <= ldb <= 2^36");
+    if (beyond_memory(rows, lda) || beyond_memory(rows, ldb)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     const uintptr_t es = dtype == GEMM_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(A) % es || reinterpret_cast<uintptr_t>(B) % es)
         return bad(GEMM_ERR_ALIGNMENT, "A or B is not aligned to its element size");
     return GEMM_OK;
 }
 
-int check_mx4_operand(const Checker &bad, int64_t K, const void *codes, int64_t ldq, const void *scales, int64_t lds)
+int check_mx4_operand(const Checker &bad, int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales,
+                      int64_t lds)
 {
     if (!codes || !scales) return bad(GEMM_ERR_INVALID, "codes or scales is NULL");
     const int64_t Kp = round_up(K, GEMM_MX4_BLOCK);
@@ -132,6 +142,7 @@ int check_mx4_operand(const Checker &bad, int64_t K, const void *codes, int64_t 
     if (lds < Kp / 32 || lds > kMaxLd) return bad(GEMM_ERR_INVALID, "the scale pitch must hold a row of scales");
     if (reinterpret_cast<uintptr_t>(codes) % 16 || reinterpret_cast<uintptr_t>(scales) % 16 || ldq % 16 || lds % 16)
         return bad(GEMM_ERR_ALIGNMENT, "codes, scales and their pitches must be multiples of 16 bytes");
+    if (beyond_memory(rows, ldq) || beyond_memory(rows, lds)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     return GEMM_OK;
 }
 
@@ -150,14 +161,15 @@ int check_mx4(int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t 
         return bad(GEMM_ERR_INVALID, "M must be in 0..2^31 - 1025");
     }
     if (rows == 0 || N == 0) return GEMM_OK;
-    if (grouped && K > 0 && N * bq >= (int64_t{1} << 40))
-        return bad(GEMM_ERR_INVALID, "a group's matrix must span less than 2^40 bytes");
     if (groups * N > kMaxDim) return bad(GEMM_ERR_INVALID, "groups * N must be below 2^31 - 1024");
     if (too_many_tiles(rows, groups, N)) return bad(GEMM_ERR_INVALID, "the product has 2^31 tiles or more");
-    if ((rc = check_c(bad, C, ldc, N, c_dtype))) return rc;
+    if ((rc = check_c(bad, C, ldc, rows, N, c_dtype))) return rc;
     if (K == 0) return GEMM_OK;
-    if ((rc = check_mx4_operand(bad, K, ac, aq, as, al))) return rc;
-    return check_mx4_operand(bad, K, bc, bq, bs, bl);
+    if ((rc = check_mx4_operand(bad, rows, K, ac, aq, as, al))) return rc;
+    if ((rc = check_mx4_operand(bad, groups * N, K, bc, bq, bs, bl))) return rc;
+    if (groups > 1 && N * bq >= (int64_t{1} << 40))
+        return bad(GEMM_ERR_INVALID, "a group's matrix must span less than 2^40 bytes");
+    return GEMM_OK;
 }
 
 int check_quantise(int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld, int64_t stride,
@@ -176,11 +188,12 @@ int check_quantise(int layout, int64_t batch, int64_t rows, int64_t K, const voi
     const bool k_rows = layout == GEMM_B_ROW_MAJOR;
     const int64_t src_rows = k_rows ? K : rows, src_cols = k_rows ? rows : K;
     if (ld < src_cols || ld > kMaxLd) return bad(GEMM_ERR_INVALID, "ld must be at least a row of src and at most 2^36");
+    if (beyond_memory(src_rows, ld)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     if (batch > 1 && (stride < (src_rows - 1) * ld + src_cols || stride > kMaxStride))
         return bad(GEMM_ERR_INVALID, "stride must reach past a matrix and stay within 2^37");
     if (reinterpret_cast<uintptr_t>(src) % (src_dtype == GEMM_BF16 ? 2 : 4))
         return bad(GEMM_ERR_ALIGNMENT, "src is not aligned to its element size");
-    return check_mx4_operand(bad, K, codes, ldq, scales, lds);
+    return check_mx4_operand(bad, batch * rows, K, codes, ldq, scales, lds);
 }
 
 int check_dequantise(int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales, int64_t lds,
@@ -194,9 +207,10 @@ int check_dequantise(int64_t rows, int64_t K, const void *codes, int64_t ldq, co
     if (rows == 0 || K == 0) return GEMM_OK;
     if (!dst) return bad(GEMM_ERR_INVALID, "dst is NULL");
     if (ldd < K || ldd > kMaxLd) return bad(GEMM_ERR_INVALID, "ldd must satisfy K <= ldd <= 2^36");
+    if (beyond_memory(rows, ldd)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     if (reinterpret_cast<uintptr_t>(dst) % (dst_dtype == GEMM_BF16 ? 2 : 4))
         return bad(GEMM_ERR_ALIGNMENT, "dst is not aligned to its element size");
-    return check_mx4_operand(bad, K, codes, ldq, scales, lds);
+    return check_mx4_operand(bad, rows, K, codes, ldq, scales, lds);
 }
 
 // ------------------------------------------------------------- tensor maps

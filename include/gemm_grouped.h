@@ -33,7 +33,8 @@
  * GEMM_F32 or GEMM_BF16.  A, B must be aligned to their element size, C to
  * its own.  Operands whose address, pitch or group stride is not a multiple
  * of 16 bytes are first re-packed into the handle's workspace.  At most
- * GEMM_GROUPED_MAX_GROUPS groups.  Handles, streams, asynchrony, errors and
+ * GEMM_GROUPED_MAX_GROUPS groups; the rows of a matrix times its pitch stay
+ * within 2^44 elements and a group stride within 2^37.  Handles, streams, asynchrony, errors and
  * in-kernel time limits are those of gemm_run; results are bit-identical from
  * call to call.
  */

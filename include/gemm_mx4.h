@@ -37,7 +37,8 @@
  *                      group g is multiplied by rows g*N .. g*N + N - 1 of B.
  *
  * Handles, streams, asynchrony, errors and in-kernel time limits are those of
- * gemm_run.  No call here uses workspace.
+ * gemm_run.  No call here uses workspace.  The rows of a matrix times a pitch
+ * stay within 2^44, and a group's codes below 2^40 bytes.
  */
 #ifndef DENSE_GEMM_SM100_GB300_GEMM_MX4_H
 #define DENSE_GEMM_SM100_GB300_GEMM_MX4_H

@@ -82,6 +82,9 @@ GROUPED = dict(layout=0, groups=3, rows=8, N=4, K=6, offsets=P, A=P, lda=6, B=P,
     ({"N": 0, "B": 0, "C": 0}, 0),
     ({"K": 0, "A": 0, "B": 0}, 0),
     ({"rows": 1 << 31}, -1),
+    ({"rows": 1 << 30, "lda": 1 << 36}, -1),             # rows times pitch past any memory
+    ({"K": 1 << 30, "lda": 1 << 30, "ldb": 1 << 36, "stride_b": 1 << 37}, -1),
+    ({"rows": 1 << 30, "ldc": 1 << 36}, -1),
     ({"rows": (1 << 31) - 2048, "N": (1 << 31) - 2048, "ldc": 1 << 31, "ldb": 1 << 31, "stride_b": 1 << 36}, -1),
 ])
 def test_grouped_arguments(g, change, code):
@@ -108,6 +111,7 @@ WGRAD = dict(groups=3, rows=8, M=4, N=6, offsets=P, A=P, lda=4, B=P, ldb=6, C=P,
     ({"C": P + 1, "c_dtype": 2}, -2),
     ({"rows": 0, "A": 0, "B": 0}, 0),        # every C is zero
     ({"M": 0, "C": 0}, 0),
+    ({"M": 1 << 30, "lda": 1 << 30, "ldc": 1 << 36, "stride_c": 1 << 37}, -1),
 ])
 def test_wgrad_arguments(g, change, code):
     assert g.gemm_grouped_wgrad_validate(*{**WGRAD, **change}.values()) == code
@@ -134,6 +138,7 @@ MX4 = dict(groups=2, rows=4, N=5, K=40, offsets=P, ac=P, aq=32, as_=P, al=16, bc
     ({"K": 0, "ac": 0, "bc": 0}, 0),
     ({"rows": 0, "C": 0}, 0),
     ({"groups": 4096, "N": 1 << 20, "ldc": 1 << 20}, -1),
+    ({"N": 1 << 20, "ldc": 1 << 20, "bq": 1 << 30}, -1),
 ])
 def test_mx4_arguments(g, change, code):
     assert g.gemm_mx4_validate(*{**MX4, **change}.values()) == code
@@ -155,6 +160,7 @@ QUANT = dict(layout=1, batch=1, rows=4, K=40, src=P, ld=40, stride=0, dtype=2, c
     ({"ldq": 16}, -1),
     ({"scales": P + 1}, -2),
     ({"rows": 0, "src": 0}, 0),
+    ({"rows": 1 << 30, "ld": 1 << 36}, -1),
 ])
 def test_quantise_arguments(g, change, code):
     assert g.gemm_mx4_quantise_validate(*{**QUANT, **change}.values()) == code
