@@ -461,7 +461,7 @@ int gemm_grouped_wgrad_validate(int64_t groups, int64_t rows, int64_t M, int64_t
 int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows, int64_t N, int64_t K,
                      const int64_t *offsets, const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
                      void *C, int64_t ldc, int dtype, int c_dtype, cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     int rc = check_grouped(layout_b, groups, rows, N, K, offsets, A, lda, B, ldb, stride_b, C, ldc, dtype, c_dtype,
@@ -511,12 +511,14 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
     ++h->launches;
     set_path(h, "grouped", kind, t, row ? "_rowB" : "_colB", ra.needed, rb.needed);
     return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M, int64_t N, const int64_t *offsets,
                        const void *A, int64_t lda, const void *B, int64_t ldb, void *C, int64_t ldc, int64_t stride_c,
                        int dtype, int c_dtype, cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     int rc = check_wgrad(groups, rows, M, N, offsets, A, lda, B, ldb, C, ldc, stride_c, dtype, c_dtype, &why);
@@ -559,6 +561,8 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
     ++h->launches;
     set_path(h, "grouped", kind, t, "_wgrad", ra.needed, rb.needed);
     return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 int64_t gemm_mx4_code_pitch(int64_t K) { return K <= 0 ? 0 : round_up(round_up(K, GEMM_MX4_BLOCK) / 2, 16); }
@@ -589,7 +593,7 @@ int gemm_mx4_validate(int64_t groups, int64_t rows, int64_t N, int64_t K, const 
 int gemm_mx4_quantise(gemm_handle_t h, int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
                       int64_t stride, int src_dtype, void *codes, int64_t ldq, void *scales, int64_t lds,
                       cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     const int rc = check_quantise(layout, batch, rows, K, src, ld, stride, src_dtype, codes, ldq, scales, lds, &why);
@@ -607,11 +611,13 @@ int gemm_mx4_quantise(gemm_handle_t h, int layout, int64_t batch, int64_t rows, 
     ++h->launches;
     h->last_path = layout == GEMM_B_ROW_MAJOR ? "mx4_quantise_rowB" : "mx4_quantise_colB";
     return GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 int gemm_mx4_dequantise(gemm_handle_t h, int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales,
                         int64_t lds, void *dst, int64_t ldd, int dst_dtype, cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     const int rc = check_dequantise(rows, K, codes, ldq, scales, lds, dst, ldd, dst_dtype, &why);
@@ -629,12 +635,14 @@ int gemm_mx4_dequantise(gemm_handle_t h, int64_t rows, int64_t K, const void *co
     ++h->launches;
     h->last_path = "mx4_dequantise";
     return GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 int gemm_mx4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *a_codes, int64_t a_ldq,
                  const void *a_scales, int64_t a_lds, const void *b_codes, int64_t b_ldq, const void *b_scales,
                  int64_t b_lds, void *C, int64_t ldc, int c_dtype, cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     const int rc = check_mx4(1, M, N, K, nullptr, a_codes, a_ldq, a_scales, a_lds, b_codes, b_ldq, b_scales, b_lds, C,
@@ -642,13 +650,15 @@ int gemm_mx4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *a
     if (rc) return fail(h, rc, why);
     return run_mx4(h, 1, M, N, K, nullptr, a_codes, a_ldq, a_scales, a_lds, b_codes, b_ldq, b_scales, b_lds, C, ldc,
                    c_dtype, stream);
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 int gemm_mx4_grouped_run(gemm_handle_t h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets,
                          const void *a_codes, int64_t a_ldq, const void *a_scales, int64_t a_lds, const void *b_codes,
                          int64_t b_ldq, const void *b_scales, int64_t b_lds, void *C, int64_t ldc, int c_dtype,
                          cudaStream_t stream)
-{
+try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
     const int rc = check_mx4(groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, a_lds, b_codes, b_ldq, b_scales,
@@ -656,6 +666,8 @@ int gemm_mx4_grouped_run(gemm_handle_t h, int64_t groups, int64_t rows, int64_t 
     if (rc) return fail(h, rc, why);
     return run_mx4(h, groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, a_lds, b_codes, b_ldq, b_scales, b_lds, C,
                    ldc, c_dtype, stream);
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
 
 }  // extern "C"
