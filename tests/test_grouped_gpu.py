@@ -212,6 +212,23 @@ def test_long_sums_of_one_sign_keep_fp32_accuracy(h, gm, tile):
     assert float(((g[0].cpu().double() - ref).abs() / ref).max()) <= 48 * 2.0 ** -23
 
 
+@pytest.mark.parametrize("tile", [1128, 2256])
+@pytest.mark.parametrize("dtype", ["bf16", "tf32"])
+def test_a_long_group_among_short_ones_is_summed_as_alone(h, gm, dtype, tile):
+    """The length at which a weight gradient is summed in segments is the
+    group's own: its bits do not depend on how long the others are."""
+    h.set_option(gm.GEMM_OPT_GROUPED_TILE, tile)
+    sizes = [3] * 31 + [2100]
+    b = bounds_of(sizes)
+    A, B = draw((b[-1], 136), dtype, 21).cuda(), draw((b[-1], 264), dtype, 22).cuda()
+    C = torch.empty((len(sizes), 136, 264), device="cuda")
+    h.run_grouped_wgrad(A, B, device_offsets(b), C, dtype)
+    alone = torch.empty((1, 136, 264), device="cuda")
+    h.run_grouped_wgrad(A[b[-2]:], B[b[-2]:], device_offsets([0, sizes[-1]]), alone, dtype)
+    h.sync_status()
+    assert torch.equal(C[-1], alone[0])
+
+
 def test_rows_outside_the_groups_and_padding_are_untouched(h):
     b = bounds_of([20, 0, 45], start=7)
     rows, K, N = 90, 72, 100
