@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             // The accumulator is in registers: hand it back to the MMA warp.
             // Relaxed, because a release would wait for the stores to C of the
             // columns before (weight gradient of 16 experts of 4096 x 2048:
-            // 150 us, now 125 to 138).
+            // 150 us against 125 to 138, both without segments).
             const auto release = [&]() {
                 const uint32_t bar = tempty_bar + 8 * (acc_it & 1u);
                 tc_fence_before_sync();
