@@ -3,7 +3,7 @@ grouped product on the library's kernels.
 
 ``group_rows`` turns a router's choices into the row order and offsets that the
 grouped products read (both stay on the device); ``grouped_matmul`` is
-``Gemm.run_grouped`` with its two gradients.
+``Gemm.run_grouped`` with its two gradients, differentiable any number of times.
 """
 from __future__ import annotations
 
@@ -32,10 +32,22 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
     return t if ok else t.contiguous()
 
 
+def _product(A, B, offsets, layout, dtype, out_dtype, handle):
+    # dense copies are taken out here, where autograd sees them
+    return _GroupedMatmul.apply(_dense_rows(A), _dense_rows(B), offsets, layout, dtype, out_dtype, handle)
+
+
+def _outer(A, B, offsets, dtype, out_dtype, handle):
+    return _GroupedOuter.apply(_dense_rows(A), _dense_rows(B), offsets, dtype, out_dtype, handle)
+
+
 class _GroupedMatmul(torch.autograd.Function):
+    """C[r] = A[r] · B[g], linear in A and in B.  Both gradients are grouped
+    products again, taken through differentiable functions, so gradients of any
+    order come out of the same two kernels."""
+
     @staticmethod
     def forward(ctx, A, B, offsets, layout, dtype, out_dtype, handle):
-        A, B = _dense_rows(A), _dense_rows(B)
         ctx.save_for_backward(A, B, offsets)
         ctx.config = (layout, dtype, handle)
         N = B.shape[2] if layout == _g.GEMM_B_ROW_MAJOR else B.shape[1]
@@ -50,13 +62,35 @@ class _GroupedMatmul(torch.autograd.Function):
         dC = _dense_rows(dC.to(A.dtype))
         dA = dB = None
         if ctx.needs_input_grad[0]:
-            dA = torch.zeros_like(A, memory_format=torch.contiguous_format)
-            handle.run_grouped(dC, B, offsets, dA, _g.GEMM_B_COL_MAJOR if row else _g.GEMM_B_ROW_MAJOR, dtype)
+            flipped = _g.GEMM_B_COL_MAJOR if row else _g.GEMM_B_ROW_MAJOR
+            dA = _product(dC, B, offsets, flipped, dtype, A.dtype, handle)
         if ctx.needs_input_grad[1]:
-            dB = torch.empty_like(B, memory_format=torch.contiguous_format)
             left, right = (A, dC) if row else (dC, A)
-            handle.run_grouped_wgrad(left, right, offsets, dB, dtype)
+            dB = _outer(left, right, offsets, dtype, B.dtype, handle)
         return dA, dB, None, None, None, None, None
+
+
+class _GroupedOuter(torch.autograd.Function):
+    """C[g] = A_g^T · B_g, the weight gradient, linear in A and in B."""
+
+    @staticmethod
+    def forward(ctx, A, B, offsets, dtype, out_dtype, handle):
+        ctx.save_for_backward(A, B, offsets)
+        ctx.config = (dtype, handle)
+        C = torch.empty((offsets.shape[0] - 1, A.shape[1], B.shape[1]), dtype=out_dtype, device=A.device)
+        return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
+
+    @staticmethod
+    def backward(ctx, dC):
+        A, B, offsets = ctx.saved_tensors
+        dtype, handle = ctx.config
+        dC = _dense_rows(dC.to(A.dtype))
+        dA = dB = None
+        if ctx.needs_input_grad[0]:
+            dA = _product(B, dC, offsets, _g.GEMM_B_COL_MAJOR, dtype, A.dtype, handle)
+        if ctx.needs_input_grad[1]:
+            dB = _product(A, dC, offsets, _g.GEMM_B_ROW_MAJOR, dtype, B.dtype, handle)
+        return dA, dB, None, None, None, None
 
 
 def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gemm | None = None):
@@ -66,10 +100,11 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
     (groups, N, K) with ``layout_b="col"``; offsets (groups + 1,) int64 on the
     device.  C has A's dtype unless ``out_dtype`` says otherwise (float32 for
     bfloat16 operands); rows of no group are zero.  The gradients have their
-    operand's dtype, and dC enters the backward products in A's."""
+    operand's dtype, and dC enters the backward products in A's.  They are
+    differentiable themselves (``create_graph=True``)."""
     layout = _g.LAYOUTS.get(layout_b, layout_b)
     dtype = _g.GEMM_BF16 if A.dtype == torch.bfloat16 else _g.GEMM_TF32
     if A.device.type != "cuda":
         raise ValueError(f"A is on {A.device}: the grouped products run on a CUDA device")
-    return _GroupedMatmul.apply(A, B, offsets, layout, dtype, out_dtype or A.dtype,
-                                handle or _g._default_handle(A.device.index or 0))
+    return _product(A, B, offsets, layout, dtype, out_dtype or A.dtype,
+                    handle or _g._default_handle(A.device.index or 0))

@@ -1,0 +1,57 @@
+"""``experts.grouped_matmul`` on the GPU beyond its first gradients."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dense_gemm_sm100_gb300 import build, gemm
+    build.build()
+    return gemm
+
+
+def offsets_of(sizes, start=0):
+    b = [start]
+    for s in sizes:
+        b.append(b[-1] + s)
+    return torch.tensor(b, dtype=torch.int64, device="cuda")
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_second_order_gradients_are_the_formulas(gm, dtype, layout):
+    """With gA = dC B^T and gB = A^T dC, the gradient of sum(gA U) + sum(gB V) is
+    dC V^T in A, U^T dC in B and U B + A V in dC.  Small integers make every
+    sum exact (at most 4 * 72 * 4 in FP32), so each is its value in 64 bits
+    rounded once to the operand's type."""
+    from dense_gemm_sm100_gb300.experts import grouped_matmul
+    gen = torch.Generator().manual_seed(51)
+    sizes, K, N = [40, 0, 70, 1], 72, 48
+    rows = sum(sizes) + 5
+
+    def ints(*shape):
+        return torch.randint(-2, 3, shape, generator=gen).to(dtype).cuda()
+
+    A, W, dC, U, V = ints(rows, K), ints(4, K, N), ints(rows, N), ints(rows, K), ints(4, K, N)
+    lay = (lambda t: t) if layout == "row" else (lambda t: t.transpose(1, 2).contiguous())
+    o = offsets_of(sizes, 2)
+    a, w, d = A.clone().requires_grad_(), lay(W).requires_grad_(), dC.clone().requires_grad_()
+    gA, gB = torch.autograd.grad(grouped_matmul(a, w, o, layout), (a, w), d, create_graph=True)
+    got = torch.autograd.grad((gA * U).sum() + (gB * lay(V)).sum(), (a, w, d))
+    b = o.tolist()
+    A, W, dC, U, V = (t.double() for t in (A, W, dC, U, V))
+    dA = torch.zeros(rows, K, dtype=torch.float64, device="cuda")
+    first, second = torch.zeros(2, rows, N, dtype=torch.float64, device="cuda")
+    dW = torch.zeros_like(W)
+    for g in range(4):
+        s = slice(b[g], b[g + 1])
+        dA[s] = dC[s] @ V[g].T
+        dW[g] = U[s].T @ dC[s]
+        first[s], second[s] = U[s] @ W[g], A[s] @ V[g]
+    assert torch.equal(got[0], dA.to(dtype))
+    assert torch.equal(got[1], lay(dW).to(dtype))
+    assert torch.equal(got[2], first.to(dtype) + second.to(dtype))
