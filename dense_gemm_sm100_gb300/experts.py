@@ -77,7 +77,8 @@ class _GroupedOuter(torch.autograd.Function):
     def forward(ctx, A, B, offsets, dtype, out_dtype, handle):
         ctx.save_for_backward(A, B, offsets)
         ctx.config = (dtype, handle)
-        C = torch.empty((offsets.shape[0] - 1, A.shape[1], B.shape[1]), dtype=out_dtype, device=A.device)
+        # every element is written below, unless the call is refused or a wait expires
+        C = torch.full((offsets.shape[0] - 1, A.shape[1], B.shape[1]), float("nan"), dtype=out_dtype, device=A.device)
         return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
 
     @staticmethod
@@ -101,7 +102,12 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
     device.  C has A's dtype unless ``out_dtype`` says otherwise (float32 for
     bfloat16 operands); rows of no group are zero.  The gradients have their
     operand's dtype, and dC enters the backward products in A's.  They are
-    differentiable themselves (``create_graph=True``)."""
+    differentiable themselves (``create_graph=True``).
+
+    Offsets that decrease or leave [0, rows] are found on the device: the output
+    and dA are then zero, dB is NaN, and the handle's ``sync_status`` raises.
+    The same call reports an expired wait inside a kernel, which leaves parts of
+    a result at those values."""
     layout = _g.LAYOUTS.get(layout_b, layout_b)
     dtype = _g.GEMM_BF16 if A.dtype == torch.bfloat16 else _g.GEMM_TF32
     if A.device.type != "cuda":

@@ -90,3 +90,15 @@ def test_a_gradient_penalty_of_operands_that_are_copied():
         got.append(torch.autograd.grad(sum(x.pow(2).sum() for x in grads), (view, wide)))
     for x, ref in zip(*got):
         torch.testing.assert_close(x, ref, rtol=1e-10, atol=1e-10)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_a_refused_call_leaves_no_unwritten_memory(layout):
+    """Where the kernels compute nothing, the output and dA are zero and dB is
+    NaN everywhere, whatever the allocator hands out."""
+    A, B, b = operands(layout)
+    handle = StandIn()
+    handle.refuse = True
+    y = product(A, B, torch.tensor(b), layout, handle)
+    y.sum().backward()
+    assert (y == 0).all() and (A.grad == 0).all() and torch.isnan(B.grad).all()

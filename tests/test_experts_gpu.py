@@ -55,3 +55,24 @@ def test_second_order_gradients_are_the_formulas(gm, dtype, layout):
     assert torch.equal(got[0], dA.to(dtype))
     assert torch.equal(got[1], lay(dW).to(dtype))
     assert torch.equal(got[2], first.to(dtype) + second.to(dtype))
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("bad", [[0, 5, 3, 8], [0, 2, 3, 9]])
+def test_refused_offsets_give_defined_results_and_are_reported(gm, bad, layout):
+    from dense_gemm_sm100_gb300.experts import grouped_matmul
+    a = torch.ones((8, 64), device="cuda").bfloat16().requires_grad_()
+    w = torch.ones((3, 64, 64), device="cuda").bfloat16().requires_grad_()
+    with gm.Gemm(0) as h:
+        y = grouped_matmul(a, w, torch.tensor(bad, device="cuda"), layout, handle=h)
+        y.sum().backward()
+        assert (y == 0).all() and (a.grad == 0).all() and torch.isnan(w.grad).all()
+        with pytest.raises(gm.GemmError) as e:
+            h.sync_status()
+        assert e.value.code == gm.GEMM_ERR_INVALID
+        a.grad = w.grad = None
+        y = grouped_matmul(a, w, torch.tensor([0, 2, 3, 8], device="cuda"), layout, handle=h)
+        y.sum().backward()
+        h.sync_status()
+        assert (y == 64).all() and (a.grad == 64).all()
+        assert (w.grad == torch.tensor([2, 1, 5], device="cuda").view(3, 1, 1)).all()
