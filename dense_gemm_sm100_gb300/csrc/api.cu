@@ -427,11 +427,9 @@ int gemm_destroy(gemm_handle_t h)
     {
         DeviceGuard guard(h->device);
         cudaDeviceSynchronize();
-        for (void *old : h->ws_retired) cudaFreeAsync(old, nullptr);
-        if (h->ws) {
-            cudaFreeAsync(h->ws, nullptr);  // allocated from the stream-ordered pool
-            cudaStreamSynchronize(nullptr);
-        }
+        // cudaFree takes blocks of the stream-ordered pool and of cudaMalloc (captures)
+        for (void *old : h->ws_retired) cudaFree(old);
+        if (h->ws) cudaFree(h->ws);
         if (h->d_status) cudaFree(h->d_status);
         if (h->ws_event) cudaEventDestroy(h->ws_event);
         if (h->copy_in) cudaStreamDestroy(h->copy_in);

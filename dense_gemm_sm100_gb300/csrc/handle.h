@@ -9,6 +9,7 @@
 
 #include <cstdint>
 #include <cstdio>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -27,7 +28,8 @@ struct gemm_ctx {
     bool ws_event_recorded = false;
     // A call that used the present workspace was captured in a CUDA graph: the
     // graph may run at any later time, so growth keeps the buffer until the
-    // handle goes.
+    // handle goes.  So it does with a buffer that is outgrown during a capture,
+    // which has no place in the graph for its release.
     bool ws_captured = false;
     std::vector<void *> ws_retired;
     std::string last_error;
@@ -85,7 +87,10 @@ inline bool tma_ready(const void *p, int64_t ld, int es)
 // Grows the workspace in stream order on `stream`: the stream first waits
 // for the last call that used the old buffer, then frees it and allocates
 // the new one from the device's stream-ordered pool.  Nothing waits on the
-// host, and work the caller queued on other streams is not held up.
+// host, and work the caller queued on other streams is not held up.  While
+// `stream` is being captured the new buffer is allocated outside the graph
+// (memory that a graph's node allocates is there only while the graph runs,
+// and later calls on the handle would use its address all the same).
 inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
 {
     if (need <= h->ws_bytes) return GEMM_OK;
@@ -99,9 +104,16 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
     size_t bytes = need > grow ? need : grow;
     bytes = (bytes + (size_t{2} << 20) - 1) & ~((size_t{2} << 20) - 1);
     if (h->ws_limit > 0 && bytes > h->ws_limit) bytes = need;  // stay within the limit
-    cudaError_t e = cudaSuccess;
-    if (h->ws && h->ws_captured) {
-        h->ws_retired.push_back(h->ws);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &capture);
+    if (e != cudaSuccess) return cuda_fail(h, e, "growth of the workspace");
+    const bool capturing = capture != cudaStreamCaptureStatusNone;
+    if (h->ws && (capturing || h->ws_captured)) {
+        try {
+            h->ws_retired.push_back(h->ws);
+        } catch (const std::bad_alloc &) {
+            return GEMM_ERR_NOMEM;
+        }
     } else if (h->ws) {
         // Earlier calls (on this or another stream) may still read the old buffer.
         if (h->ws_event_recorded) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
@@ -111,12 +123,22 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
     h->ws = nullptr;
     h->ws_bytes = 0;
     h->ws_event_recorded = false;
-    h->ws_captured = false;
-    e = cudaMallocAsync(&h->ws, bytes, stream);
+    h->ws_captured = capturing;
+    if (capturing) {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // of this thread, for the one call
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) {
+            e = cudaMalloc(&h->ws, bytes);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+        }
+    } else {
+        e = cudaMallocAsync(&h->ws, bytes, stream);
+    }
     if (e != cudaSuccess) {
         h->ws = nullptr;
+        h->ws_captured = false;
         cudaGetLastError();
-        return fail(h, GEMM_ERR_NOMEM, std::string("workspace cudaMallocAsync: ") + cudaGetErrorString(e));
+        return fail(h, GEMM_ERR_NOMEM, std::string("workspace allocation: ") + cudaGetErrorString(e));
     }
     h->ws_bytes = bytes;
     return GEMM_OK;

@@ -51,8 +51,9 @@
  * buffer after the last call that used it, then cudaMallocAsync from the
  * device's default memory pool): it neither synchronises the device nor
  * waits on the host.  A workspace that a captured call used is kept until
- * gemm_destroy, because its CUDA graph may run at any time (capture after a
- * first call of the same sizes, so that nothing grows during the capture).
+ * gemm_destroy, because its CUDA graph may run at any time; growth during a
+ * capture allocates outside the graph (cudaMalloc) and keeps the old buffer
+ * as well (a first call of the same sizes before the capture avoids that).
  * gemm_destroy synchronises the device.
  *
  * Errors: every function returns GEMM_OK (0) or a negative GEMM_ERR_* code.
