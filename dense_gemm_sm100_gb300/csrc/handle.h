@@ -22,10 +22,11 @@ struct gemm_ctx {
     void *ws = nullptr;
     size_t ws_bytes = 0;
     // Recorded on the caller's stream after every call that used the
-    // workspace; growth waits on it (stream-ordered) before the old buffer
-    // is released.
+    // workspace.  Calls on another stream wait on it, and growth does before
+    // the old buffer is released (both in stream order).
     cudaEvent_t ws_event = nullptr;
     bool ws_event_recorded = false;
+    unsigned long long ws_stream = 0;  // id of the stream it was recorded on
     // A call that used the present workspace was captured in a CUDA graph: the
     // graph may run at any later time, so growth keeps the buffer until the
     // handle goes.  So it does with a buffer that is outgrown during a capture,
@@ -84,16 +85,47 @@ inline bool tma_ready(const void *p, int64_t ld, int es)
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
 }
 
-// Grows the workspace in stream order on `stream`: the stream first waits
-// for the last call that used the old buffer, then frees it and allocates
-// the new one from the device's stream-ordered pool.  Nothing waits on the
-// host, and work the caller queued on other streams is not held up.  While
-// `stream` is being captured the new buffer is allocated outside the graph
-// (memory that a graph's node allocates is there only while the graph runs,
-// and later calls on the handle would use its address all the same).
+// The end of the work queued on `stream` so far is what the workspace's next
+// user waits for.
+inline cudaError_t record_workspace_event(gemm_ctx *h, cudaStream_t stream)
+{
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamGetId(stream, &id);
+    if (e == cudaSuccess) e = cudaEventRecord(h->ws_event, stream);
+    if (e == cudaSuccess) {
+        h->ws_stream = id;
+        h->ws_event_recorded = true;
+    }
+    return e;
+}
+
+// Before a call's first use of a workspace that is large enough: calls on
+// different streams take turns.  (A capture cannot wait for work outside its
+// graph; its launches are the caller's to order.)
+inline int order_workspace(gemm_ctx *h, cudaStream_t stream)
+{
+    if (!h->ws_event_recorded) return GEMM_OK;
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamGetId(stream, &id);
+    if (e == cudaSuccess && id == h->ws_stream) return GEMM_OK;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (e == cudaSuccess) e = cudaStreamIsCapturing(stream, &capture);
+    if (e == cudaSuccess && capture == cudaStreamCaptureStatusNone) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
+    return e == cudaSuccess ? GEMM_OK : cuda_fail(h, e, "ordering the workspace's uses");
+}
+
+// Makes `need` bytes of workspace usable on `stream`.
+//
+// Growth is in stream order: the stream first waits for the last call that
+// used the old buffer, then frees it and allocates the new one from the
+// device's stream-ordered pool.  Nothing waits on the host, and work the caller
+// queued on other streams is not held up.  While `stream` is being captured the
+// new buffer is allocated outside the graph (memory that a graph's node
+// allocates is there only while the graph runs, and later calls on the handle
+// would use its address all the same).
 inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
 {
-    if (need <= h->ws_bytes) return GEMM_OK;
+    if (need <= h->ws_bytes) return order_workspace(h, stream);
     if (h->ws_limit > 0 && need > h->ws_limit) {
         char msg[160];
         std::snprintf(msg, sizeof msg, "workspace of %zu bytes needed, limit %zu (GEMM_OPT_WORKSPACE_LIMIT)", need,
@@ -141,11 +173,13 @@ inline int ensure_workspace(gemm_ctx *h, size_t need, cudaStream_t stream)
         return fail(h, GEMM_ERR_NOMEM, std::string("workspace allocation: ") + cudaGetErrorString(e));
     }
     h->ws_bytes = bytes;
+    // cudaMalloc's memory is there for every stream at once
+    if (!capturing && (e = record_workspace_event(h, stream)) != cudaSuccess)
+        return cuda_fail(h, e, "workspace-use event");
     return GEMM_OK;
 }
 
-// After a call whose launches read or write the workspace: its end on
-// `stream` is what the next growth waits for.
+// After a call whose launches read or write the workspace.
 inline int note_workspace_use(gemm_ctx *h, cudaStream_t stream)
 {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
@@ -155,10 +189,8 @@ inline int note_workspace_use(gemm_ctx *h, cudaStream_t stream)
         h->ws_captured = true;
         return GEMM_OK;
     }
-    if (e == cudaSuccess) e = cudaEventRecord(h->ws_event, stream);
-    if (e != cudaSuccess) return cuda_fail(h, e, "workspace-use event");
-    h->ws_event_recorded = true;
-    return GEMM_OK;
+    if (e == cudaSuccess) e = record_workspace_event(h, stream);
+    return e == cudaSuccess ? GEMM_OK : cuda_fail(h, e, "workspace-use event");
 }
 
 inline int encode_2d(gemm_ctx *h, CUtensorMap *map, int es, const void *base, int64_t inner,

@@ -45,8 +45,10 @@
  * demand (used to re-pack operands whose address or leading dimension is not
  * a multiple of 16 bytes, for the K-slice partial products of small FP32
  * problems, and by gemm_run_host).  Calls on one handle must be
- * issued from one host thread at a time and be ordered on the GPU (one
- * stream, or streams the caller orders), because they share the workspace.
+ * issued from one host thread at a time.  Calls on different streams that use
+ * the workspace take turns on the GPU (the later one's stream waits for the
+ * earlier call); the caller orders CUDA graphs of captured calls against each
+ * other and against the handle's other calls.
  * Growth is stream-ordered on the calling stream (cudaFreeAsync of the old
  * buffer after the last call that used it, then cudaMallocAsync from the
  * device's default memory pool): it neither synchronises the device nor

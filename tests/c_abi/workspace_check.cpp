@@ -169,6 +169,35 @@ void no_memory_in_capture()
     check(use(&h, MB, s) == GEMM_OK && async_blocks.count(h.ws) == 1, "and usable");
 }
 
+// Calls on two streams that the caller does not order share the workspace.
+void two_streams()
+{
+    gemm_ctx h;
+    Stream a, b;
+    check(use(&h, MB, a) == GEMM_OK, "a call on the first stream");
+    calls.clear();
+    check(use(&h, MB, a) == GEMM_OK && count("wait") == 0, "calls on one stream are in order by themselves");
+    calls.clear();
+    check(use(&h, MB, b) == GEMM_OK && count("wait") == 1, "a call on another stream waits for the last use");
+    check(calls.front() == "wait", "before it touches the workspace");
+    calls.clear();
+    check(use(&h, MB, a) == GEMM_OK && count("wait") == 1, "and back");
+    a.capturing = b.capturing = true;
+    calls.clear();
+    check(use(&h, MB, b) == GEMM_OK && count("wait") == 0, "a capture cannot wait for work outside the graph");
+}
+
+// Nothing but the allocation itself happened on the stream that grew the
+// workspace (the call failed after it).
+void allocated_on_another_stream()
+{
+    gemm_ctx h;
+    Stream a, b;
+    check(dg::ensure_workspace(&h, MB, handle_of(a)) == GEMM_OK, "growth on the first stream");
+    calls.clear();
+    check(use(&h, MB, b) == GEMM_OK && count("wait") == 1, "the other stream waits for the allocation");
+}
+
 }  // namespace
 
 int main(int argc, char **argv)
@@ -180,6 +209,10 @@ int main(int argc, char **argv)
         eager_then_growth_in_capture();
     else if (name == "no_memory_in_capture")
         no_memory_in_capture();
+    else if (name == "two_streams")
+        two_streams();
+    else if (name == "allocated_on_another_stream")
+        allocated_on_another_stream();
     else
         check(false, "unknown scenario");
     return checks_failed == 0 ? 0 : 1;

@@ -23,7 +23,8 @@ def program(tmp_path_factory):
     return out
 
 
-@pytest.mark.parametrize("scenario", ["growth_in_capture", "eager_then_growth_in_capture", "no_memory_in_capture"])
+@pytest.mark.parametrize("scenario", ["growth_in_capture", "eager_then_growth_in_capture", "no_memory_in_capture",
+                                      "two_streams", "allocated_on_another_stream"])
 def test_workspace(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout + r.stderr

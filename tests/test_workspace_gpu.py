@@ -80,3 +80,17 @@ def test_the_workspace_grows_while_a_call_is_captured(h, grouped):
         small.run(h)
         h.sync_status()
         assert small.right() and large.right()
+
+
+@pytest.mark.parametrize("grouped", [False, True], ids=["dense", "grouped"])
+def test_calls_on_streams_that_nothing_orders(h, grouped):
+    calls = [Call(grouped, 1501 + 100 * i, 77, 999, 10 + i) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(12):
+            calls[i % 4].run(h, streams[i % 3])
+        for s in streams:
+            h.sync_status(s)
+        assert all(c.right() for c in calls)
+        torch.cuda.synchronize()
