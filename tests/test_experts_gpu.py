@@ -43,9 +43,9 @@ def test_second_order_gradients_are_the_formulas(gm, dtype, layout):
     gA, gB = torch.autograd.grad(grouped_matmul(a, w, o, layout), (a, w), d, create_graph=True)
     got = torch.autograd.grad((gA * U).sum() + (gB * lay(V)).sum(), (a, w, d))
     b = o.tolist()
-    A, W, dC, U, V = (t.double() for t in (A, W, dC, U, V))
+    A, W, dC, U, V = (t.detach().double() for t in (A, W, dC, U, V))
     dA = torch.zeros(rows, K, dtype=torch.float64, device="cuda")
-    first, second = torch.zeros(2, rows, N, dtype=torch.float64, device="cuda")
+    first, second = (torch.zeros(rows, N, dtype=torch.float64, device="cuda") for _ in range(2))
     dW = torch.zeros_like(W)
     for g in range(4):
         s = slice(b[g], b[g + 1])
