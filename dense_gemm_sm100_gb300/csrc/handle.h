@@ -105,12 +105,12 @@ inline cudaError_t record_workspace_event(gemm_ctx *h, cudaStream_t stream)
 inline int order_workspace(gemm_ctx *h, cudaStream_t stream)
 {
     if (!h->ws_event_recorded) return GEMM_OK;
-    unsigned long long id = 0;
-    cudaError_t e = cudaStreamGetId(stream, &id);
-    if (e == cudaSuccess && id == h->ws_stream) return GEMM_OK;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (e == cudaSuccess) e = cudaStreamIsCapturing(stream, &capture);
-    if (e == cudaSuccess && capture == cudaStreamCaptureStatusNone) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
+    cudaError_t e = cudaStreamIsCapturing(stream, &capture);
+    if (e == cudaSuccess && capture != cudaStreamCaptureStatusNone) return GEMM_OK;
+    unsigned long long id = 0;  // not to be had from a stream that is being captured
+    if (e == cudaSuccess) e = cudaStreamGetId(stream, &id);
+    if (e == cudaSuccess && id != h->ws_stream) e = cudaStreamWaitEvent(stream, h->ws_event, 0);
     return e == cudaSuccess ? GEMM_OK : cuda_fail(h, e, "ordering the workspace's uses");
 }
 

@@ -58,6 +58,7 @@ cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus *out)
 
 cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long *id)
 {
+    if (of(s)->capturing) return cudaErrorStreamCaptureUnsupported;
     *id = reinterpret_cast<uintptr_t>(s);
     return cudaSuccess;
 }
