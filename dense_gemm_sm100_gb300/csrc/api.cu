@@ -21,12 +21,10 @@ PFN_cuTensorMapEncodeTiled_v12000 dg::g_encode = nullptr;
 using dg::cuda_fail;
 using dg::DeviceGuard;
 using dg::encode_2d;
-using dg::ensure_workspace;
 using dg::fail;
 using dg::g_encode;
 using dg::kMaxDim;
 using dg::kMaxLd;
-using dg::note_workspace_use;
 using dg::round_up;
 using dg::tma_ready;
 
@@ -463,13 +461,10 @@ int gemm_run(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K, con
     if (rc) return fail(h, rc, why);
     DeviceGuard guard(h->device);
     const PackPlan pp = plan_pack(h, layout_b, M, N, K, A, lda, B, ldb, dtype);
-    if (pp.total()) {
-        rc = ensure_workspace(h, pp.total(), stream);
-        if (rc) return rc;
-    }
+    dg::WorkspaceUse ws(h, stream);
+    if (pp.total() && (rc = ws.acquire(pp.total()))) return rc;
     rc = run_device(h, layout_b, M, N, K, A, lda, B, ldb, C, ldc, dtype, stream, pp, 0);
-    if (rc == GEMM_OK && pp.total()) rc = note_workspace_use(h, stream);
-    return rc;
+    return rc ? rc : ws.done();
 }
 
 namespace {
@@ -648,7 +643,8 @@ int gemm_run_host(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K
     for (int64_t mi : {block_m(0), block_m(hb.pm - 1)})
         for (int64_t nj : {block_n(0), block_n(hb.pn - 1), N})
             extra = std::max(extra, plan_pack(h, layout_b, mi, nj, K, nullptr, lda_d, nullptr, ldb_d, dtype).total());
-    rc = ensure_workspace(h, staged + extra, stream);
+    dg::WorkspaceUse use(h, stream);
+    rc = use.acquire(staged + extra);
     if (rc) return rc;
     uint8_t *ws = static_cast<uint8_t *>(h->ws);
     uint8_t *A_d = ws, *B_d = ws + a_bytes;
@@ -723,7 +719,7 @@ int gemm_run_host(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K
     e = cudaEventRecord(h->ev_done, h->copy_out);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, h->ev_done, 0);  // the call ends on `stream`
     if (e != cudaSuccess) return cuda_fail(h, e, "host-copy pipeline completion");
-    if ((rc = note_workspace_use(h, stream))) return rc;
+    if ((rc = use.done())) return rc;
     h->last_path = "host+" + path;
     if (block > 1) h->last_path += "+blocks" + std::to_string(hb.pm) + "x" + std::to_string(hb.pn);  // launches: (pm-1)*pn+1
     return GEMM_OK;

@@ -193,6 +193,42 @@ inline int note_workspace_use(gemm_ctx *h, cudaStream_t stream)
     return e == cudaSuccess ? GEMM_OK : cuda_fail(h, e, "workspace-use event");
 }
 
+// One call's use of the workspace.  Its end is recorded however the call
+// leaves: a launch that fails, or an exception, may follow launches that
+// already work on the buffer.
+class WorkspaceUse {
+  public:
+    WorkspaceUse(gemm_ctx *h, cudaStream_t stream) : h_(h), stream_(stream) {}
+    ~WorkspaceUse()
+    {
+        try {
+            done();
+        } catch (...) {
+        }
+    }
+    WorkspaceUse(const WorkspaceUse &) = delete;
+    WorkspaceUse &operator=(const WorkspaceUse &) = delete;
+
+    int acquire(size_t need)
+    {
+        const int rc = ensure_workspace(h_, need, stream_);
+        held_ = rc == GEMM_OK;
+        return rc;
+    }
+
+    int done()
+    {
+        if (!held_) return GEMM_OK;
+        held_ = false;
+        return note_workspace_use(h_, stream_);
+    }
+
+  private:
+    gemm_ctx *h_;
+    cudaStream_t stream_;
+    bool held_ = false;
+};
+
 inline int encode_2d(gemm_ctx *h, CUtensorMap *map, int es, const void *base, int64_t inner,
               int64_t outer, int64_t ld, int box_inner, int box_outer,
               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)

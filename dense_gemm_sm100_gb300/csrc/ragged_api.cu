@@ -479,12 +479,13 @@ try {
     const dg::RaggedTile t = tile_for(h, kind, false, rows, groups, N, 0, K);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
+    dg::WorkspaceUse ws(h, stream);
     Repack ra, rb;
     if (K > 0) {
         ra = plan_repack(h, A, lda, 1, 0, rows, K, es);
         rb = plan_repack(h, B, ldb, groups, stride_b, rows_b, cols_b, es);
         if (ra.needed || rb.needed) {
-            if ((rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+            if ((rc = ws.acquire(ra.bytes + rb.bytes))) return rc;
             if ((rc = run_repack(h, ra, A, lda, rows, K, rb, B, ldb, groups, stride_b, rows_b, cols_b, offsets, es, stream)))
                 return rc;
         }
@@ -510,7 +511,7 @@ try {
     if (e != cudaSuccess) return cuda_fail(h, e, "grouped product launch");
     ++h->launches;
     set_path(h, "grouped", kind, t, row ? "_rowB" : "_colB", ra.needed, rb.needed);
-    return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
+    return ws.done();
 } catch (...) {
     return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }
@@ -534,12 +535,13 @@ try {
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, M, 0, C, ldc, c_dtype, stream);
     a.stride_c = groups > 1 ? stride_c : 0;
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
+    dg::WorkspaceUse ws(h, stream);
     Repack ra, rb;
     if (rows > 0) {
         ra = plan_repack(h, A, lda, 1, 0, rows, M, es);
         rb = plan_repack(h, B, ldb, 1, 0, rows, N, es);
         if (ra.needed || rb.needed) {
-            if ((rc = dg::ensure_workspace(h, ra.bytes + rb.bytes, stream))) return rc;
+            if ((rc = ws.acquire(ra.bytes + rb.bytes))) return rc;
             if ((rc = run_repack(h, ra, A, lda, rows, M, rb, B, ldb, 1, 0, rows, N, nullptr, es, stream))) return rc;
         }
         if (ra.needed) {
@@ -560,7 +562,7 @@ try {
     if (e != cudaSuccess) return cuda_fail(h, e, "weight gradient launch");
     ++h->launches;
     set_path(h, "grouped", kind, t, "_wgrad", ra.needed, rb.needed);
-    return ra.needed || rb.needed ? dg::note_workspace_use(h, stream) : GEMM_OK;
+    return ws.done();
 } catch (...) {
     return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }

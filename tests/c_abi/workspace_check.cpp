@@ -199,6 +199,31 @@ void allocated_on_another_stream()
     check(use(&h, MB, b) == GEMM_OK && count("wait") == 1, "the other stream waits for the allocation");
 }
 
+// A call that fails behind a launch that works on the buffer.
+void failed_call()
+{
+    gemm_ctx h;
+    Stream a, b;
+    {
+        dg::WorkspaceUse u(&h, handle_of(a));
+        check(u.acquire(MB) == GEMM_OK, "acquired");
+        calls.clear();
+    }
+    check(count("record") == 1, "the end of what it launched is recorded");
+    {
+        dg::WorkspaceUse u(&h, handle_of(b));
+        check(u.acquire(64 * MB) == GEMM_OK && calls[1] == "wait" && calls[2] == "freeAsync", "and growth waits for it");
+        calls.clear();
+        check(u.done() == GEMM_OK && count("record") == 1, "a call that succeeds records its end");
+    }
+    check(count("record") == 1, "once");
+    {
+        dg::WorkspaceUse u(&h, handle_of(a));
+        calls.clear();
+    }
+    check(calls.empty(), "a call that uses no workspace records nothing");
+}
+
 }  // namespace
 
 int main(int argc, char **argv)
@@ -214,6 +239,8 @@ int main(int argc, char **argv)
         two_streams();
     else if (name == "allocated_on_another_stream")
         allocated_on_another_stream();
+    else if (name == "failed_call")
+        failed_call();
     else
         check(false, "unknown scenario");
     return checks_failed == 0 ? 0 : 1;

@@ -24,7 +24,7 @@ def program(tmp_path_factory):
 
 
 @pytest.mark.parametrize("scenario", ["growth_in_capture", "eager_then_growth_in_capture", "no_memory_in_capture",
-                                      "two_streams", "allocated_on_another_stream"])
+                                      "two_streams", "allocated_on_another_stream", "failed_call"])
 def test_workspace(program, scenario):
     r = subprocess.run([program, scenario], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout + r.stderr
