@@ -9,4 +9,5 @@ used by the benchmark.
 """
 from . import build, inputs, roofline  # noqa: F401
 from .gemm import (GEMM_B_COL_MAJOR, GEMM_B_ROW_MAJOR, GEMM_BF16, GEMM_F32,  # noqa: F401
-                   GEMM_TF32, Gemm, GemmError, GemmLibraryMissing, Mx4, matmul, mx4_empty)
+                   GEMM_TF32, Gemm, GemmError, GemmLibraryMissing, Mx4, default_handle, matmul,
+                   mx4_empty)

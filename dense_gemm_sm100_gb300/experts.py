@@ -105,12 +105,16 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
     differentiable themselves (``create_graph=True``).
 
     Offsets that decrease or leave [0, rows] are found on the device: the output
-    and dA are then zero, dB is NaN, and the handle's ``sync_status`` raises.
+    and dA are then zero, dB is NaN, and the handle's ``sync_status`` raises
+    (``gemm.default_handle().sync_status()`` where no ``handle`` is given).
     The same call reports an expired wait inside a kernel, which leaves parts of
-    a result at those values."""
+    a result at those values.
+
+    All calls run on torch's current stream; threads and streams may share a
+    handle, the default one included."""
     layout = _g.LAYOUTS.get(layout_b, layout_b)
     dtype = _g.GEMM_BF16 if A.dtype == torch.bfloat16 else _g.GEMM_TF32
     if A.device.type != "cuda":
         raise ValueError(f"A is on {A.device}: the grouped products run on a CUDA device")
     return _product(A, B, offsets, layout, dtype, out_dtype or A.dtype,
-                    handle or _g._default_handle(A.device.index or 0))
+                    handle or _g.default_handle(A.device.index or 0))

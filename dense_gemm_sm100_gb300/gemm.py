@@ -488,13 +488,15 @@ class Gemm:
     row-major, B is (K, N) for ``layout_b="row"`` or (N, K) for ``"col"``
     (each row holding one column of the logical B), C is (M, N).  Rows may be
     padded (any stride(0) >= columns, stride(1) == 1).  The call is queued on
-    ``stream`` (default: torch's current stream) and returns at once.
+    ``stream`` (default: torch's current stream) and returns at once.  Calls of
+    several host threads take turns.
     """
 
     def __init__(self, device: int = 0):
         self.device = device
         self.handle = gemm_create(device)
         self._lib = load_library()
+        self._turn = threading.Lock()  # the library wants one thread at a time on a handle
 
     def close(self):
         if self.handle:
@@ -518,7 +520,8 @@ class Gemm:
             raise GemmError(rc, gemm_last_error_string(self.handle))
 
     def set_option(self, option: int, value: int):
-        self._check(gemm_set_option(self.handle, option, int(value)))
+        with self._turn:
+            self._check(gemm_set_option(self.handle, option, int(value)))
 
     @staticmethod
     def _dims(A, B, layout_b):
@@ -543,8 +546,9 @@ class Gemm:
         M, N, K = self._dims(A, B, lb)
         if tuple(C.shape) != (M, N):
             raise ValueError(f"C has shape {tuple(C.shape)}, expected {(M, N)}")
-        self._check(gemm_run(self.handle, lb, M, N, K, A.data_ptr(), self._ld(A), B.data_ptr(),
-                             self._ld(B), C.data_ptr(), self._ld(C), dt, _stream_handle(stream)))
+        with self._turn:
+            self._check(gemm_run(self.handle, lb, M, N, K, A.data_ptr(), self._ld(A), B.data_ptr(),
+                                 self._ld(B), C.data_ptr(), self._ld(C), dt, _stream_handle(stream)))
         return C
 
     def run_host(self, A, B, C, layout_b="row", dtype="f32", stream=None):
@@ -553,9 +557,10 @@ class Gemm:
         lb = LAYOUTS.get(layout_b, layout_b)
         dt = DTYPES.get(dtype, dtype)
         M, N, K = self._dims(A, B, lb)
-        self._check(gemm_run_host(self.handle, lb, M, N, K, A.data_ptr(), self._ld(A),
-                                  B.data_ptr(), self._ld(B), C.data_ptr(), self._ld(C), dt,
-                                  _stream_handle(stream)))
+        with self._turn:
+            self._check(gemm_run_host(self.handle, lb, M, N, K, A.data_ptr(), self._ld(A),
+                                      B.data_ptr(), self._ld(B), C.data_ptr(), self._ld(C), dt,
+                                      _stream_handle(stream)))
         return C
 
     def run_grouped(self, A, B, offsets, C, layout_b="row", dtype="bf16", stream=None):
@@ -576,11 +581,12 @@ class Gemm:
         if Kb != K or Nb != N or rows != M:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)} ({layout_b}), C {tuple(C.shape)}")
         _operand_types(dt, a_type, b_type)
-        rc = self._lib.gemm_grouped_run(self.handle, lb, groups, M, N, K, _offsets(offsets, groups, dev), A.data_ptr(),
-                                        lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt, c_type,
-                                        _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_grouped_run(self.handle, lb, groups, M, N, K, _offsets(offsets, groups, dev),
+                                            A.data_ptr(), lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt,
+                                            c_type, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return C
 
     def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None):
@@ -597,11 +603,12 @@ class Gemm:
         if rows_b != rows or Mc != M or Nc != N:
             raise ValueError(f"shapes differ: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
         _operand_types(dt, a_type, b_type)
-        rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
-                                          A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
-                                          c_type, _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
+                                              A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
+                                              c_type, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return C
 
     def mx4_quantise(self, src, out: Mx4, layout="col", stream=None):
@@ -620,10 +627,11 @@ class Gemm:
         rows, K = (d1, d2) if lb == GEMM_B_COL_MAJOR else (d2, d1)
         if out.rows != batch * rows or out.K != K:
             raise ValueError(f"out holds {out.rows} x {out.K}, src has {batch} x {rows} x {K}")
-        rc = self._lib.gemm_mx4_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride, s_type,
-                                         *out._args(dev), _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_mx4_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride, s_type,
+                                             *out._args(dev), _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return out
 
     def mx4_dequantise(self, q: Mx4, out, stream=None):
@@ -632,10 +640,11 @@ class Gemm:
         rows, K, ld, o_type = _matrix(out, "out", dev)
         if rows != q.rows or K != q.K:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(q.rows, q.K)}")
-        rc = self._lib.gemm_mx4_dequantise(self.handle, rows, K, *q._args(dev), out.data_ptr(), ld, o_type,
-                                           _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_mx4_dequantise(self.handle, rows, K, *q._args(dev), out.data_ptr(), ld, o_type,
+                                               _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return out
 
     def run_mx4(self, A: Mx4, B: Mx4, C, stream=None):
@@ -645,10 +654,11 @@ class Gemm:
         M, N, ldc, c_type = _matrix(C, "C", dev)
         if A.K != B.K or M != A.rows or N != B.rows:
             raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K}, C {tuple(C.shape)}")
-        rc = self._lib.gemm_mx4_run(self.handle, M, N, A.K, *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
-                                    _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_mx4_run(self.handle, M, N, A.K, *A._args(dev), *B._args(dev), C.data_ptr(), ldc,
+                                        c_type, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return C
 
     def run_mx4_grouped(self, A: Mx4, B: Mx4, offsets, C, stream=None):
@@ -660,16 +670,27 @@ class Gemm:
         if A.K != B.K or M != A.rows or B.rows != groups * N:
             raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K} for {groups} groups, "
                              f"C {tuple(C.shape)}")
-        rc = self._lib.gemm_mx4_grouped_run(self.handle, groups, M, N, A.K, _offsets(offsets, groups, dev),
-                                            *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
-                                            _raw_stream(stream, dev))
-        if rc:
-            self._check(rc)
+        with self._turn:
+            rc = self._lib.gemm_mx4_grouped_run(self.handle, groups, M, N, A.K, _offsets(offsets, groups, dev),
+                                                *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
+                                                _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
         return C
 
     def sync_status(self, stream=None):
-        """Wait for ``stream`` and raise GemmError if an in-kernel wait expired."""
-        self._check(gemm_sync_status(self.handle, _stream_handle(stream)))
+        """Wait for ``stream`` and raise GemmError if an in-kernel wait expired or
+        a call's group offsets were refused."""
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream()
+        if hasattr(stream, "synchronize"):
+            try:
+                stream.synchronize()  # other threads' calls need not wait with this one
+            except RuntimeError:
+                pass  # the library reports it
+        with self._turn:
+            self._check(gemm_sync_status(self.handle, _stream_handle(stream)))
 
     @property
     def last_path(self) -> str:
@@ -687,18 +708,24 @@ def matmul(A, B, layout_b="row", dtype="f32", out=None, stream=None, handle: Gem
     M, N, _ = Gemm._dims(A, B, lb)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    g = handle or _default_handle(A.device.index or 0)
+    g = handle or default_handle(A.device.index or 0)
     return g.run(A, B, out, lb, dtype, stream)
 
 
 _handles: dict[int, Gemm] = {}
+_handles_lock = threading.Lock()
 
 
-def _default_handle(device: int) -> Gemm:
-    with _lock:
+def default_handle(device: int | None = None) -> Gemm:
+    """The handle of ``matmul`` and ``experts.grouped_matmul`` calls that name
+    none, one per device (default: torch's current device).  All threads and
+    streams share it; its ``sync_status`` reports what such calls found wrong on
+    the GPU."""
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    with _handles_lock:
         h = _handles.get(device)
-    if h is None:
-        h = Gemm(device)
-        with _lock:
-            _handles[device] = h
+        if h is None:
+            h = _handles[device] = Gemm(device)
     return h

@@ -76,3 +76,42 @@ def test_refused_offsets_give_defined_results_and_are_reported(gm, bad, layout):
         h.sync_status()
         assert (y == 64).all() and (a.grad == 64).all()
         assert (w.grad == torch.tensor([2, 1, 5], device="cuda").view(3, 1, 1)).all()
+
+
+def test_streams_and_threads_share_the_default_handle(gm):
+    """Operands with odd pitches go through the handle's workspace; small
+    integers make forward and backward exact (sums of at most 4 * 300 in FP32
+    before the rounding to the operand's type)."""
+    import threading
+    from dense_gemm_sm100_gb300.experts import grouped_matmul
+    sizes, K, N = [300, 0, 211], 77, 131
+    o = offsets_of(sizes)
+
+    def work(seed, results):
+        gen = torch.Generator().manual_seed(seed)
+        ints = lambda *s: torch.randint(-2, 3, s, generator=gen).bfloat16().cuda()
+        stream = torch.cuda.Stream()
+        ok = True
+        for _ in range(6):
+            A, W, dC = ints(sum(sizes), K), ints(3, K, N), ints(sum(sizes), N)
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                a, w = A.clone().requires_grad_(), W.clone().requires_grad_()
+                y = grouped_matmul(a, w, o, "row", torch.float32)
+                y.backward(dC.float())
+                stream.synchronize()
+            ref = torch.cat([A[:300].float() @ W[0].float(), A[300:].float() @ W[2].float()])
+            dA = torch.cat([dC[:300].float() @ W[0].float().T, dC[300:].float() @ W[2].float().T])
+            dW = torch.stack([A[:300].float().T @ dC[:300].float(), torch.zeros(K, N, device="cuda"),
+                              A[300:].float().T @ dC[300:].float()])
+            ok = ok and torch.equal(y, ref) and torch.equal(a.grad, dA.bfloat16()) and torch.equal(w.grad, dW.bfloat16())
+        results.append(ok)
+
+    results = []
+    threads = [threading.Thread(target=work, args=(60 + i, results)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    gm.default_handle().sync_status()
+    assert results == [True] * 3
