@@ -19,6 +19,8 @@ def group_rows(expert: torch.Tensor, groups: int):
     if expert.dim() != 1:
         raise ValueError("expert must be 1-D")
     sorted_expert, order = torch.sort(expert, stable=True)
+    if not expert.dtype.is_floating_point and torch.iinfo(expert.dtype).max < groups:
+        sorted_expert = sorted_expert.long()  # 256 does not fit into a uint8 of 256 experts
     edges = torch.arange(groups + 1, device=expert.device, dtype=sorted_expert.dtype)
     return order, torch.searchsorted(sorted_expert, edges)
 

@@ -102,3 +102,13 @@ def test_a_refused_call_leaves_no_unwritten_memory(layout):
     y = product(A, B, torch.tensor(b), layout, handle)
     y.sum().backward()
     assert (y == 0).all() and (A.grad == 0).all() and torch.isnan(B.grad).all()
+
+
+@pytest.mark.parametrize("dtype,groups", [(torch.uint8, 255), (torch.uint8, 256), (torch.int8, 127), (torch.int8, 128),
+                                          (torch.int8, 300), (torch.int16, 4096), (torch.int32, 256)])
+def test_group_rows_of_narrow_indices(dtype, groups):
+    """The count of groups need not fit into the indices' type."""
+    expert = torch.tensor([3, 0, 120, 3, 126, 1]).to(dtype)
+    order, offsets = experts.group_rows(expert, groups)
+    assert order.tolist() == [1, 5, 0, 3, 2, 4]
+    assert offsets.tolist() == [int((expert.long() < g).sum()) for g in range(groups)] + [6] and offsets.dtype == torch.int64
