@@ -459,7 +459,7 @@ class Mx4:
             raise ValueError("codes and scales must have the same rows and device")
         self.codes, self.scales, self.K = codes, scales, int(K)
         self.rows = codes.shape[0]
-        self._pitches = [max(t.stride(0), t.shape[1]) if self.rows > 1 else t.shape[1] for t in (codes, scales)]
+        self._pitches = [t.stride(0) if self.rows > 1 else t.shape[1] for t in (codes, scales)]
         if self.rows > 1 and (codes.stride(0) < blocks * 16 or scales.stride(0) < blocks):
             raise ValueError("the rows of codes or scales overlap")
         self._device = codes.get_device() if codes.is_cuda else None

@@ -211,3 +211,19 @@ def test_grouped_matmul_needs_a_gpu_tensor():
     from dense_gemm_sm100_gb300.experts import grouped_matmul
     with pytest.raises(ValueError):
         grouped_matmul(torch.zeros(2, 3), torch.zeros(1, 3, 4), torch.tensor([0, 2]))
+
+
+def test_mx4_rows_closer_together_than_their_columns(g):
+    """Rows of 32 bytes of codes 32 bytes apart, seen as 64 columns: the pitch is
+    the distance of the rows, or reads run past the end of the storage."""
+    codes = torch.zeros(4 * 32 + 32, dtype=torch.uint8).as_strided((4, 64), (32, 1))
+    scales = torch.zeros(4 * 16 + 16, dtype=torch.uint8).as_strided((4, 32), (16, 1))
+    q = g.Mx4(codes, scales, 64)
+    q._device = 0
+    assert q._args(0)[1::2] == (32, 16)
+    one = g.Mx4(codes[:1], scales[:1], 64)  # one row has no distance: the columns that it shows
+    one._device = 0
+    assert one._args(0)[1::2] == (64, 32)
+    wide = g.Mx4(torch.zeros(4, 64, dtype=torch.uint8)[:, :32], torch.zeros(4, 48, dtype=torch.uint8)[:, :16], 64)
+    wide._device = 0
+    assert wide._args(0)[1::2] == (64, 48)
