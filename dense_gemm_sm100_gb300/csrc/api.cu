@@ -404,7 +404,6 @@ int gemm_create(gemm_handle_t *out, int device)
     cudaError_t e = g_encode ? cudaSuccess : cudaErrorNotSupported;
     if (e == cudaSuccess) e = dg::prepare_simt();
     if (e == cudaSuccess) e = dg::prepare_tc();
-    if (e == cudaSuccess) e = dg::prepare_ragged();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_status, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(h->d_status, 0, sizeof(int));
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&h->ws_event, cudaEventDisableTiming);

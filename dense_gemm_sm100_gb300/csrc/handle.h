@@ -50,6 +50,7 @@ struct gemm_ctx {
     int tc_cluster = 3;   // tensor-core mode: 1 one CTA per tile, 3 pair MMA
     int tc_tma_store = 1; // tensor-core epilogue writes C with TMA stores when C allows it
     int tc_slices = 0;    // pair MMA: K slices per ring stage (0: library's choice)
+    bool ragged_ready = false;  // prepare_ragged has run for this handle
     int ragged_tile = 0;  // grouped and 4-bit products: 0 chosen, else 10000 * split + 1000 * CTAs + rows of a tile
     int debug_drop = 0;   // test hook (GEMM_OPT_DEBUG_DROP_LOAD)
     // gemm_run_host pipeline: copy streams and events (created on first use)

@@ -67,6 +67,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "ptx.cuh"
 #include "ragged.h"
@@ -977,8 +978,10 @@ int64_t max_units(bool ragged_k, int64_t rows, int64_t groups, int64_t P, int64_
 }
 
 // Clusters of 2, 4 and 8 CTAs that run at the same time (the SMs of a cluster
-// share a GPC, so fewer than SMs / size); filled in by prepare_ragged.
+// share a GPC, so fewer than SMs / size); filled in by the first prepare_ragged
+// and not changed after that.
 int g_clusters[3] = {};
+std::mutex g_prepare;
 
 int max_clusters(int split) { return g_clusters[split == 2 ? 0 : split == 4 ? 1 : 2]; }
 
@@ -1002,6 +1005,7 @@ cudaError_t query_clusters(int split, int *out)
 
 cudaError_t prepare_ragged()
 {
+    const std::lock_guard<std::mutex> lock(g_prepare);
     cudaError_t e = cudaSuccess;
     for (int kind : {kRaggedBf16, kRaggedTf32, kRaggedMx4})
         for (int ctas = 1; ctas <= 2; ++ctas)
@@ -1009,7 +1013,7 @@ cudaError_t prepare_ragged()
                 for (bool sum : {false, true})
                     if (e == cudaSuccess) e = dispatch(kind, ctas, form > 0, form == 2, sum, SetAttrs());
     for (int i = 0; i < 3; ++i)
-        if (e == cudaSuccess) e = query_clusters(2 << i, &g_clusters[i]);
+        if (e == cudaSuccess && g_clusters[i] == 0) e = query_clusters(2 << i, &g_clusters[i]);
     return e;
 }
 

@@ -64,6 +64,9 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
 // K elements of one ring stage (128 bytes of a K-major row).
 inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : 64; }
 
+// Sets the kernels' attributes on the current device: once per handle, before
+// its first product (1.5 ms for the first handle of a process, whose creation
+// it would hold up for callers who never use these kernels).
 cudaError_t prepare_ragged();
 // tmP / tmQ: the operand views of ragged_api.cu.
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,

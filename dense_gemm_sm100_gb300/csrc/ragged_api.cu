@@ -300,6 +300,22 @@ int encode_k_major(gemm_ctx *h, CUtensorMap *map, CUtensorMapDataType type, int 
     return encode(h, map, type, grouped ? 3 : 2, reinterpret_cast<uintptr_t>(base), dims, st, box, swizzle, what);
 }
 
+// The handle's first grouped or 4-bit product prepares the kernels; the call
+// may be captured, and loading them is no part of the graph.
+int prepare(gemm_ctx *h)
+{
+    if (h->ragged_ready) return GEMM_OK;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) {
+        e = dg::prepare_ragged();
+        cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+    if (e != cudaSuccess) return cuda_fail(h, e, "preparing the grouped kernels");
+    h->ragged_ready = true;
+    return GEMM_OK;
+}
+
 dg::RaggedTile tile_for(const gemm_ctx *h, int kind, bool ragged_k, int64_t rows, int64_t groups, int64_t P,
                         int64_t Q, int64_t K)
 {
@@ -414,6 +430,8 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
         return GEMM_OK;
     }
     dg::DeviceGuard guard(h->device);
+    int rc = prepare(h);
+    if (rc) return rc;
     const int kind = dg::kRaggedMx4;
     const dg::RaggedTile t = tile_for(h, kind, false, rows, groups, N, 0, K);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
@@ -422,7 +440,7 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
         const int64_t Kp = round_up(K, GEMM_MX4_BLOCK);
         const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-        int rc = encode_k_major(h, &tmP, u8, 1, bc, Kp / 2, N, bq, groups, N * bq, 128, dg::kRaggedP, sw, true,
+        rc = encode_k_major(h, &tmP, u8, 1, bc, Kp / 2, N, bq, groups, N * bq, 128, dg::kRaggedP, sw, true,
                                 "the codes of B");
         if (!rc) rc = encode_k_major(h, &tmQ, u8, 1, ac, Kp / 2, rows, aq, 1, 0, 128, t.bn / t.ctas, sw, false,
                                      "the codes of A");
@@ -472,6 +490,7 @@ try {
         return GEMM_OK;
     }
     dg::DeviceGuard guard(h->device);
+    if ((rc = prepare(h))) return rc;
     const int es = dtype == GEMM_BF16 ? 2 : 4;
     const int kind = dtype == GEMM_BF16 ? dg::kRaggedBf16 : dg::kRaggedTf32;
     const bool row = layout_b == GEMM_B_ROW_MAJOR;
@@ -529,6 +548,7 @@ try {
         return GEMM_OK;
     }
     dg::DeviceGuard guard(h->device);
+    if ((rc = prepare(h))) return rc;
     const int es = dtype == GEMM_BF16 ? 2 : 4;
     const int kind = dtype == GEMM_BF16 ? dg::kRaggedBf16 : dg::kRaggedTf32;
     const dg::RaggedTile t = tile_for(h, kind, true, rows, groups, N, M, 0);
