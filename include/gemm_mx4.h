@@ -32,7 +32,12 @@
  *                      as float or BF16 (exact in both).
  * gemm_mx4_run         C[i*ldc + j] = sum_k a(i, k) * b(j, k), i < M, j < N:
  *                      both operands quantised along K.  FP32 sums; C float or
- *                      BF16 (c_dtype GEMM_F32 or GEMM_BF16).
+ *                      BF16 (c_dtype GEMM_F32 or GEMM_BF16).  The tensor core
+ *                      truncates at every addition of 64 products: sums are
+ *                      exact while they fit 24 bits (block scales of a row
+ *                      within a factor of 16: up to K = 16384 as measured);
+ *                      scales spread over 2^16 cost 1.0e-6 of the result's
+ *                      norm at K = 4096 and 4.5e-6 at K = 16384.
  * gemm_mx4_grouped_run The same over row groups (see gemm_grouped.h): row r of
  *                      group g is multiplied by rows g*N .. g*N + N - 1 of B.
  *
