@@ -35,12 +35,31 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
 
 
 def _product(A, B, offsets, layout, dtype, out_dtype, handle):
-    # dense copies are taken out here, where autograd sees them
-    return _GroupedMatmul.apply(_dense_rows(A), _dense_rows(B), offsets, layout, dtype, out_dtype, handle)
+    """A[r] · B[g], differentiable where autograd records (in a backward pass:
+    with ``create_graph``; else the call skips autograd's bookkeeping, 20 to 30 us
+    on the host)."""
+    A, B = _dense_rows(A), _dense_rows(B)  # copies are taken out here, where autograd sees them
+    f = _GroupedMatmul.apply if torch.is_grad_enabled() else _run_product
+    return f(A, B, offsets, layout, dtype, out_dtype, handle)
 
 
 def _outer(A, B, offsets, dtype, out_dtype, handle):
-    return _GroupedOuter.apply(_dense_rows(A), _dense_rows(B), offsets, dtype, out_dtype, handle)
+    """A_g^T · B_g, likewise."""
+    A, B = _dense_rows(A), _dense_rows(B)
+    f = _GroupedOuter.apply if torch.is_grad_enabled() else _run_outer
+    return f(A, B, offsets, dtype, out_dtype, handle)
+
+
+def _run_product(A, B, offsets, layout, dtype, out_dtype, handle):
+    N = B.shape[2] if layout == _g.GEMM_B_ROW_MAJOR else B.shape[1]
+    C = torch.zeros((A.shape[0], N), dtype=out_dtype, device=A.device)  # rows of no group give zeros
+    return handle.run_grouped(A, B, offsets, C, layout, dtype)
+
+
+def _run_outer(A, B, offsets, dtype, out_dtype, handle):
+    # every element is written below, unless the call is refused or a wait expires
+    C = torch.full((offsets.shape[0] - 1, A.shape[1], B.shape[1]), float("nan"), dtype=out_dtype, device=A.device)
+    return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
 
 
 class _GroupedMatmul(torch.autograd.Function):
@@ -52,9 +71,7 @@ class _GroupedMatmul(torch.autograd.Function):
     def forward(ctx, A, B, offsets, layout, dtype, out_dtype, handle):
         ctx.save_for_backward(A, B, offsets)
         ctx.config = (layout, dtype, handle)
-        N = B.shape[2] if layout == _g.GEMM_B_ROW_MAJOR else B.shape[1]
-        C = torch.zeros((A.shape[0], N), dtype=out_dtype, device=A.device)  # rows of no group give zeros
-        return handle.run_grouped(A, B, offsets, C, layout, dtype)
+        return _run_product(A, B, offsets, layout, dtype, out_dtype, handle)
 
     @staticmethod
     def backward(ctx, dC):
@@ -79,9 +96,7 @@ class _GroupedOuter(torch.autograd.Function):
     def forward(ctx, A, B, offsets, dtype, out_dtype, handle):
         ctx.save_for_backward(A, B, offsets)
         ctx.config = (dtype, handle)
-        # every element is written below, unless the call is refused or a wait expires
-        C = torch.full((offsets.shape[0] - 1, A.shape[1], B.shape[1]), float("nan"), dtype=out_dtype, device=A.device)
-        return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
+        return _run_outer(A, B, offsets, dtype, out_dtype, handle)
 
     @staticmethod
     def backward(ctx, dC):
