@@ -333,13 +333,6 @@ __device__ __forceinline__ float4 lds_cluster_f4(uint32_t cluster_addr)
     return v;
 }
 
-__device__ __forceinline__ uint32_t lds_cluster_u32(uint32_t cluster_addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
 // Arrive on an mbarrier given by a shared::cluster address (any CTA of the
 // cluster), release at cluster scope.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)

@@ -58,9 +58,7 @@
 // beside the barrier set-up) and finds the group of tile u by bisection.
 // Offsets that decrease or leave [0, rows] are reported in the status word and
 // the launch computes nothing; reads of the offsets are clamped all the same,
-// so no tile reads or writes outside the operands.  On request the epilogue
-// warps then write NaN to a weight gradient, and after an expired wait to the
-// tiles that are left: loops of their own, so that the main one stays as it is.
+// so no tile reads or writes outside the operands.
 //
 // Ragged contraction.  The k rows of a group start anywhere and end inside a
 // stage.  Both operands are read through a view {column, y < BK, z} whose y
@@ -108,7 +106,6 @@ struct Params {
     long long ldc, stride_c;
     int out_bf16, p_chunks, q_chunks;
     int c_vec;  // 1: C is written in pieces of 16 bytes
-    int nan_on_error;
     // 4-bit operands: scale bytes of P (groups of P rows) and Q, blocks of K
     const uint8_t *scale_p, *scale_q;
     long long lds_p, lds_q;
@@ -615,8 +612,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 2048;
         uint32_t acc_it = 0;
         bool ok = true;
-        int u = first_unit;
-        for (; u < num_units; u += unit_step) {
+        for (int u = first_unit; ok && u < num_units; u += unit_step) {
             const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
             const int col0 = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32;  // the warp's first column
             const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
@@ -768,23 +764,6 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             }
             __syncwarp();
         }
-        if (!MX && p.nan_on_error) {
-            // What is left: nothing, the tiles from an expired wait on, or every
-            // tile of a weight gradient whose offsets are refused.
-            const int all = RAGGED_K ? p.groups * p.tiles_p * p.tiles_q : num_units;
-            for (; u < all; u += unit_step) {
-                const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
-                const int col = (t.pb * CG + static_cast<int>(rank)) * BP + q * 32 + lane;
-                const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
-                for (int r = half * 32; r < t.qn && col < p.P; r += (r & 31) == 31 ? 33 : 1) {
-                    const long long at = (RAGGED_K ? t.g * p.stride_c : 0) + (first_row + r) * p.ldc + col;
-                    if (p.out_bf16)
-                        static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
-                    else
-                        static_cast<float *>(p.C)[at] = __int_as_float(0x7fffffff);
-                }
-            }
-        }
     } else if (MX && p.K > 0 && (warp - 2 - EPI_WARPS - 1) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
         // The first: P's rows; the others: 128 rows of Q each.  Out-of-range
@@ -868,17 +847,12 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         __syncwarp();
         cluster_sync();
         if (first_unit < num_units) {
-            float start = 0.0f;  // NaN where a wait of any CTA expired and that is asked for
-            if (!MX && p.nan_on_error)
-                for (int r = 0; r < p.split; ++r)
-                    if (lds_cluster_u32(mapa_shared(smem_addr(const_cast<int *>(abort_flag)), r)) != 0)
-                        start = __int_as_float(0x7fffffff);
             const Tile t = tile_at<BK, RAGGED_K>(p, table, first_unit, krank);
             const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
             const int piece = (threadIdx.x & 31) * 4;
             const int col = t.pb * BP + piece;
             for (int j = krank + p.split * warp; j < t.qn && col < p.P; j += p.split * (THREADS / 32)) {
-                float4 x = make_float4(start, start, start, start);
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int r = 0; r < p.split; ++r) {
                     const float4 y = lds_cluster_f4(mapa_shared(sbase + j * 512 + piece * 4, r));
                     x.x += y.x;
@@ -1132,7 +1106,6 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.ldc = a.ldc;
     p.stride_c = a.stride_c;
     p.out_bf16 = a.out_bf16;
-    p.nan_on_error = a.nan_on_error;
     // 16-byte pieces of C: aligned rows that hold whole pieces
     const int eo = a.out_bf16 ? 2 : 4;
     p.c_vec = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && (a.ldc * eo) % 16 == 0 && (a.stride_c * eo) % 16 == 0 &&

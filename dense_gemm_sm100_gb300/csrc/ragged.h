@@ -31,7 +31,6 @@ struct RaggedArgs {
     int64_t ldc = 0;
     int64_t stride_c = 0;  // ragged_k: elements from one group's C to the next
     int out_bf16 = 0;
-    int nan_on_error = 0;  // C's unwritten elements become NaN (not for kRaggedMx4)
     int p_chunks = 0;  // MN-major P: tmP is the view in 128-byte column chunks
     int q_chunks = 0;  // the same for Q (ragged_k)
     // kRaggedMx4: scale bytes of B (rows of P, groups one after another) and A

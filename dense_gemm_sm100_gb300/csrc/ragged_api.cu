@@ -72,14 +72,6 @@ int check_types(const Checker &bad, int dtype, int c_dtype)
     return GEMM_OK;
 }
 
-// Takes GEMM_GROUPED_NAN_ON_ERROR off a c_dtype argument.
-bool take_nan_flag(int &c_dtype)
-{
-    const bool nan = (c_dtype & GEMM_GROUPED_NAN_ON_ERROR) != 0;
-    c_dtype &= ~GEMM_GROUPED_NAN_ON_ERROR;
-    return nan;
-}
-
 // Tiles are counted in 32 bits on the device; `rows_of_c` rows cut into tiles
 // of at least 32, plus one per group.
 bool too_many_tiles(int64_t rows_of_c, int64_t groups, int64_t cols)
@@ -473,7 +465,6 @@ int gemm_grouped_validate(int layout_b, int64_t groups, int64_t rows, int64_t N,
                           const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b, const void *C,
                           int64_t ldc, int dtype, int c_dtype)
 {
-    take_nan_flag(c_dtype);
     return check_grouped(layout_b, groups, rows, N, K, offsets, A, lda, B, ldb, stride_b, C, ldc, dtype, c_dtype,
                          nullptr);
 }
@@ -482,7 +473,6 @@ int gemm_grouped_wgrad_validate(int64_t groups, int64_t rows, int64_t M, int64_t
                                 const void *A, int64_t lda, const void *B, int64_t ldb, const void *C, int64_t ldc,
                                 int64_t stride_c, int dtype, int c_dtype)
 {
-    take_nan_flag(c_dtype);
     return check_wgrad(groups, rows, M, N, offsets, A, lda, B, ldb, C, ldc, stride_c, dtype, c_dtype, nullptr);
 }
 
@@ -492,7 +482,6 @@ int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows
 try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
-    const bool nan_on_error = take_nan_flag(c_dtype);
     int rc = check_grouped(layout_b, groups, rows, N, K, offsets, A, lda, B, ldb, stride_b, C, ldc, dtype, c_dtype,
                            &why);
     if (rc) return fail(h, rc, why);
@@ -508,7 +497,6 @@ try {
     const int64_t rows_b = row ? K : N, cols_b = row ? N : K;
     const dg::RaggedTile t = tile_for(h, kind, false, rows, groups, N, 0, K);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
-    a.nan_on_error = nan_on_error;
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
     dg::WorkspaceUse ws(h, stream);
     Repack ra, rb;
@@ -553,7 +541,6 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
 try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
-    const bool nan_on_error = take_nan_flag(c_dtype);
     int rc = check_wgrad(groups, rows, M, N, offsets, A, lda, B, ldb, C, ldc, stride_c, dtype, c_dtype, &why);
     if (rc) return fail(h, rc, why);
     if (M == 0 || N == 0) {
@@ -567,7 +554,6 @@ try {
     const dg::RaggedTile t = tile_for(h, kind, true, rows, groups, N, M, 0);
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, M, 0, C, ldc, c_dtype, stream);
     a.stride_c = groups > 1 ? stride_c : 0;
-    a.nan_on_error = nan_on_error;
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
     dg::WorkspaceUse ws(h, stream);
     Repack ra, rb;

@@ -53,12 +53,13 @@ def _outer(A, B, offsets, dtype, out_dtype, handle):
 def _run_product(A, B, offsets, layout, dtype, out_dtype, handle):
     N = B.shape[2] if layout == _g.GEMM_B_ROW_MAJOR else B.shape[1]
     C = torch.zeros((A.shape[0], N), dtype=out_dtype, device=A.device)  # rows of no group give zeros
-    return handle.run_grouped(A, B, offsets, C, layout, dtype, nan_on_error=True)
+    return handle.run_grouped(A, B, offsets, C, layout, dtype)
 
 
 def _run_outer(A, B, offsets, dtype, out_dtype, handle):
-    C = torch.empty((offsets.shape[0] - 1, A.shape[1], B.shape[1]), dtype=out_dtype, device=A.device)
-    return handle.run_grouped_wgrad(A, B, offsets, C, dtype, nan_on_error=True)
+    # every element is written below, unless the call is refused or a wait expires
+    C = torch.full((offsets.shape[0] - 1, A.shape[1], B.shape[1]), float("nan"), dtype=out_dtype, device=A.device)
+    return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
 
 
 class _GroupedMatmul(torch.autograd.Function):
@@ -123,8 +124,8 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
     Offsets that decrease or leave [0, rows] are found on the device: the output
     and dA are then zero, dB is NaN, and the handle's ``sync_status`` raises
     (``gemm.default_handle().sync_status()`` where no ``handle`` is given).
-    The same call reports an expired wait inside a kernel; the parts of a result
-    that it cut short are NaN.
+    The same call reports an expired wait inside a kernel, which leaves parts of
+    a result at those values.
 
     All calls run on torch's current stream; threads and streams may share a
     handle, the default one included."""

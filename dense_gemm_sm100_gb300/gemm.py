@@ -55,7 +55,6 @@ GEMM_OPT_SIMT_SMALL = 15
 GEMM_OPT_GROUPED_TILE = 16
 
 GEMM_GROUPED_MAX_GROUPS = 4096
-GEMM_GROUPED_NAN_ON_ERROR = 0x100
 GEMM_MX4_BLOCK = 32
 
 DTYPES = {"f32": GEMM_F32, "tf32": GEMM_TF32, "bf16": GEMM_BF16, "f32x3": GEMM_F32_3XTF32}
@@ -564,15 +563,14 @@ class Gemm:
                                       _stream_handle(stream)))
         return C
 
-    def run_grouped(self, A, B, offsets, C, layout_b="row", dtype="bf16", stream=None, nan_on_error=False):
+    def run_grouped(self, A, B, offsets, C, layout_b="row", dtype="bf16", stream=None):
         """C[r] = A[r] · B[g] for the rows r of every group g.
 
         A is (rows, K) with the rows sorted by group, ``offsets`` (groups + 1,)
         int64 on the device, B (groups, K, N) for ``layout_b="row"`` or
         (groups, N, K) for ``"col"``, C (rows, N) float32 or bfloat16.  Rows
         outside [offsets[0], offsets[-1]) keep what C held.  ``dtype`` is
-        "bf16" or "tf32".  ``nan_on_error``: tiles that an expired wait cuts
-        short are NaN instead of what C held."""
+        "bf16" or "tf32"."""
         lb = LAYOUTS.get(layout_b, layout_b)
         dt = DTYPES.get(dtype, dtype)
         dev = self.device
@@ -586,20 +584,17 @@ class Gemm:
         with self._turn:
             rc = self._lib.gemm_grouped_run(self.handle, lb, groups, M, N, K, _offsets(offsets, groups, dev),
                                             A.data_ptr(), lda, B.data_ptr(), ldb, stride_b, C.data_ptr(), ldc, dt,
-                                            c_type | (GEMM_GROUPED_NAN_ON_ERROR if nan_on_error else 0),
-                                            _raw_stream(stream, dev))
+                                            c_type, _raw_stream(stream, dev))
             if rc:
                 self._check(rc)
         return C
 
-    def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None, nan_on_error=False):
+    def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None):
         """C[g] = A_g^T · B_g over the rows of group g (zeros where it has none).
 
         A is (rows, M), B (rows, N), C (groups, M, N) float32 or bfloat16: the
         gradient of a row-major weight with A the input and B the output's
-        gradient, of a column-major weight with the two exchanged.
-        ``nan_on_error``: C is NaN where refused offsets or an expired wait
-        leave it unwritten, instead of what it held."""
+        gradient, of a column-major weight with the two exchanged."""
         dt = DTYPES.get(dtype, dtype)
         dev = self.device
         rows, M, lda, a_type = _matrix(A, "A", dev)
@@ -611,8 +606,7 @@ class Gemm:
         with self._turn:
             rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
                                               A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
-                                              c_type | (GEMM_GROUPED_NAN_ON_ERROR if nan_on_error else 0),
-                                              _raw_stream(stream, dev))
+                                              c_type, _raw_stream(stream, dev))
             if rc:
                 self._check(rc)
         return C

@@ -49,13 +49,6 @@ extern "C" {
 
 #define GEMM_GROUPED_MAX_GROUPS 4096
 
-/* Or-ed to c_dtype: what the call leaves unwritten is NaN.  That is all of C
- * where gemm_grouped_wgrad refuses its offsets, and for both calls the tiles
- * that an expired wait inside the kernel cut short (else they keep what C
- * held).  gemm_grouped_run with refused offsets writes nothing all the same:
- * no rows are its own. */
-#define GEMM_GROUPED_NAN_ON_ERROR 0x100
-
 int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows, int64_t N, int64_t K,
                      const int64_t *offsets, const void *A, int64_t lda, const void *B, int64_t ldb,
                      int64_t stride_b, void *C, int64_t ldc, int dtype, int c_dtype, cudaStream_t stream);
