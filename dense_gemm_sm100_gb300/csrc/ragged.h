@@ -72,6 +72,10 @@ cudaError_t prepare_ragged();
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
                           const CUtensorMap &tmQ, const RaggedArgs &a, int sm_count, int max_ctas);
 
+// Behind a weight gradient (its arguments `a`): NaN to all of C where the
+// offsets were refused or the status word holds an expired wait.
+cudaError_t launch_nan_on_error(const RaggedArgs &a, int sm_count);
+
 // Quantises `batch` matrices of `rows` x K elements (BF16 or FP32) to E2M1
 // codes and E8M0 scales, batch * rows output rows.  k_rows: element (r, k) is
 // src[k * ld + r] instead of src[r * ld + k].

@@ -72,6 +72,14 @@ int check_types(const Checker &bad, int dtype, int c_dtype)
     return GEMM_OK;
 }
 
+// Takes GEMM_GROUPED_NAN_ON_ERROR off a c_dtype argument.
+bool take_nan_flag(int &c_dtype)
+{
+    const bool nan = (c_dtype & GEMM_GROUPED_NAN_ON_ERROR) != 0;
+    c_dtype &= ~GEMM_GROUPED_NAN_ON_ERROR;
+    return nan;
+}
+
 // Tiles are counted in 32 bits on the device; `rows_of_c` rows cut into tiles
 // of at least 32, plus one per group.
 bool too_many_tiles(int64_t rows_of_c, int64_t groups, int64_t cols)
@@ -473,6 +481,7 @@ int gemm_grouped_wgrad_validate(int64_t groups, int64_t rows, int64_t M, int64_t
                                 const void *A, int64_t lda, const void *B, int64_t ldb, const void *C, int64_t ldc,
                                 int64_t stride_c, int dtype, int c_dtype)
 {
+    take_nan_flag(c_dtype);
     return check_wgrad(groups, rows, M, N, offsets, A, lda, B, ldb, C, ldc, stride_c, dtype, c_dtype, nullptr);
 }
 
@@ -541,6 +550,7 @@ int gemm_grouped_wgrad(gemm_handle_t h, int64_t groups, int64_t rows, int64_t M,
 try {
     if (!h) return GEMM_ERR_INVALID;
     std::string why;
+    const bool nan_on_error = take_nan_flag(c_dtype);
     int rc = check_wgrad(groups, rows, M, N, offsets, A, lda, B, ldb, C, ldc, stride_c, dtype, c_dtype, &why);
     if (rc) return fail(h, rc, why);
     if (M == 0 || N == 0) {
@@ -578,9 +588,13 @@ try {
         if (!rc) rc = encode_ragged_k(h, &tmQ, es, A, rows, M, lda, t.bn / t.ctas, a.q_chunks != 0);
         if (rc) return rc;
     }
-    const cudaError_t e = dg::launch_ragged(kind, true, true, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
+    cudaError_t e = dg::launch_ragged(kind, true, true, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "weight gradient launch");
     ++h->launches;
+    if (nan_on_error) {
+        if ((e = dg::launch_nan_on_error(a, h->sm_count)) != cudaSuccess) return cuda_fail(h, e, "NaN launch");
+        ++h->launches;
+    }
     set_path(h, "grouped", kind, t, "_wgrad", ra.needed, rb.needed);
     return ws.done();
 } catch (...) {

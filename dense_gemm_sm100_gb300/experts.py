@@ -28,6 +28,8 @@ def group_rows(expert: torch.Tensor, groups: int):
 def _dense_rows(t: torch.Tensor) -> torch.Tensor:
     """t, or a copy when its rows overlap or are not unit-stride (an expanded
     gradient, a transposed view)."""
+    if t.is_contiguous():
+        return t
     ok = t.shape[-1] <= 1 or t.stride(-1) == 1
     for d in range(t.dim() - 1):
         ok = ok and (t.shape[d] <= 1 or t.stride(d) >= t.stride(d + 1) * t.shape[d + 1])
@@ -35,17 +37,20 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
 
 
 def _product(A, B, offsets, layout, dtype, out_dtype, handle):
+    # copies are taken out here, where autograd sees them
+    return _dense_product(_dense_rows(A), _dense_rows(B), offsets, layout, dtype, out_dtype, handle)
+
+
+def _dense_product(A, B, offsets, layout, dtype, out_dtype, handle):
     """A[r] · B[g], differentiable where autograd records (in a backward pass:
     with ``create_graph``; else the call skips autograd's bookkeeping, 20 to 30 us
     on the host)."""
-    A, B = _dense_rows(A), _dense_rows(B)  # copies are taken out here, where autograd sees them
     f = _GroupedMatmul.apply if torch.is_grad_enabled() else _run_product
     return f(A, B, offsets, layout, dtype, out_dtype, handle)
 
 
-def _outer(A, B, offsets, dtype, out_dtype, handle):
+def _dense_outer(A, B, offsets, dtype, out_dtype, handle):
     """A_g^T · B_g, likewise."""
-    A, B = _dense_rows(A), _dense_rows(B)
     f = _GroupedOuter.apply if torch.is_grad_enabled() else _run_outer
     return f(A, B, offsets, dtype, out_dtype, handle)
 
@@ -57,9 +62,8 @@ def _run_product(A, B, offsets, layout, dtype, out_dtype, handle):
 
 
 def _run_outer(A, B, offsets, dtype, out_dtype, handle):
-    # every element is written below, unless the call is refused or a wait expires
-    C = torch.full((offsets.shape[0] - 1, A.shape[1], B.shape[1]), float("nan"), dtype=out_dtype, device=A.device)
-    return handle.run_grouped_wgrad(A, B, offsets, C, dtype)
+    C = torch.empty((offsets.shape[0] - 1, A.shape[1], B.shape[1]), dtype=out_dtype, device=A.device)
+    return handle.run_grouped_wgrad(A, B, offsets, C, dtype, nan_on_error=True)
 
 
 class _GroupedMatmul(torch.autograd.Function):
@@ -82,10 +86,10 @@ class _GroupedMatmul(torch.autograd.Function):
         dA = dB = None
         if ctx.needs_input_grad[0]:
             flipped = _g.GEMM_B_COL_MAJOR if row else _g.GEMM_B_ROW_MAJOR
-            dA = _product(dC, B, offsets, flipped, dtype, A.dtype, handle)
+            dA = _dense_product(dC, B, offsets, flipped, dtype, A.dtype, handle)
         if ctx.needs_input_grad[1]:
             left, right = (A, dC) if row else (dC, A)
-            dB = _outer(left, right, offsets, dtype, B.dtype, handle)
+            dB = _dense_outer(left, right, offsets, dtype, B.dtype, handle)
         return dA, dB, None, None, None, None, None
 
 
@@ -105,9 +109,9 @@ class _GroupedOuter(torch.autograd.Function):
         dC = _dense_rows(dC.to(A.dtype))
         dA = dB = None
         if ctx.needs_input_grad[0]:
-            dA = _product(B, dC, offsets, _g.GEMM_B_COL_MAJOR, dtype, A.dtype, handle)
+            dA = _dense_product(B, dC, offsets, _g.GEMM_B_COL_MAJOR, dtype, A.dtype, handle)
         if ctx.needs_input_grad[1]:
-            dB = _product(A, dC, offsets, _g.GEMM_B_ROW_MAJOR, dtype, B.dtype, handle)
+            dB = _dense_product(A, dC, offsets, _g.GEMM_B_ROW_MAJOR, dtype, B.dtype, handle)
         return dA, dB, None, None, None, None
 
 
@@ -125,7 +129,7 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
     and dA are then zero, dB is NaN, and the handle's ``sync_status`` raises
     (``gemm.default_handle().sync_status()`` where no ``handle`` is given).
     The same call reports an expired wait inside a kernel, which leaves parts of
-    a result at those values.
+    the output and dA at zero and makes dB NaN until it has been reported.
 
     All calls run on torch's current stream; threads and streams may share a
     handle, the default one included."""

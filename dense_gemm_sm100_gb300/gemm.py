@@ -55,6 +55,7 @@ GEMM_OPT_SIMT_SMALL = 15
 GEMM_OPT_GROUPED_TILE = 16
 
 GEMM_GROUPED_MAX_GROUPS = 4096
+GEMM_GROUPED_NAN_ON_ERROR = 0x100
 GEMM_MX4_BLOCK = 32
 
 DTYPES = {"f32": GEMM_F32, "tf32": GEMM_TF32, "bf16": GEMM_BF16, "f32x3": GEMM_F32_3XTF32}
@@ -589,12 +590,14 @@ class Gemm:
                 self._check(rc)
         return C
 
-    def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None):
+    def run_grouped_wgrad(self, A, B, offsets, C, dtype="bf16", stream=None, nan_on_error=False):
         """C[g] = A_g^T · B_g over the rows of group g (zeros where it has none).
 
         A is (rows, M), B (rows, N), C (groups, M, N) float32 or bfloat16: the
         gradient of a row-major weight with A the input and B the output's
-        gradient, of a column-major weight with the two exchanged."""
+        gradient, of a column-major weight with the two exchanged.
+        ``nan_on_error``: C is NaN where the offsets are refused (else it keeps
+        what it held), and while an expired wait of the handle is unreported."""
         dt = DTYPES.get(dtype, dtype)
         dev = self.device
         rows, M, lda, a_type = _matrix(A, "A", dev)
@@ -606,7 +609,8 @@ class Gemm:
         with self._turn:
             rc = self._lib.gemm_grouped_wgrad(self.handle, groups, rows, M, N, _offsets(offsets, groups, dev),
                                               A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, stride_c, dt,
-                                              c_type, _raw_stream(stream, dev))
+                                              c_type | (GEMM_GROUPED_NAN_ON_ERROR if nan_on_error else 0),
+                                              _raw_stream(stream, dev))
             if rc:
                 self._check(rc)
         return C

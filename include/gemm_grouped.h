@@ -49,6 +49,12 @@ extern "C" {
 
 #define GEMM_GROUPED_MAX_GROUPS 4096
 
+/* Or-ed to gemm_grouped_wgrad's c_dtype: all of C becomes NaN where the offsets
+ * are refused (without the flag C keeps what it held), and while an expired
+ * wait of any call on the handle has not been reported by gemm_sync_status (C
+ * may be incomplete). */
+#define GEMM_GROUPED_NAN_ON_ERROR 0x100
+
 int gemm_grouped_run(gemm_handle_t h, int layout_b, int64_t groups, int64_t rows, int64_t N, int64_t K,
                      const int64_t *offsets, const void *A, int64_t lda, const void *B, int64_t ldb,
                      int64_t stride_b, void *C, int64_t ldc, int dtype, int c_dtype, cudaStream_t stream);

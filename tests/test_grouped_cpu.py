@@ -227,3 +227,13 @@ def test_mx4_rows_closer_together_than_their_columns(g):
     wide = g.Mx4(torch.zeros(4, 64, dtype=torch.uint8)[:, :32], torch.zeros(4, 48, dtype=torch.uint8)[:, :16], 64)
     wide._device = 0
     assert wide._args(0)[1::2] == (64, 48)
+
+
+def test_the_nan_flag_is_taken_with_a_weight_gradients_type(g):
+    for c_dtype in (g.GEMM_F32, g.GEMM_BF16):
+        flagged = {"c_dtype": c_dtype | g.GEMM_GROUPED_NAN_ON_ERROR}
+        assert g.gemm_grouped_wgrad_validate(*{**WGRAD, **flagged}.values()) == 0
+        assert g.gemm_grouped_validate(*{**GROUPED, **flagged}.values()) == -1
+        assert g.gemm_mx4_validate(*{**MX4, **flagged}.values()) == -1
+    assert g.gemm_grouped_wgrad_validate(*{**WGRAD, "c_dtype": 1 | g.GEMM_GROUPED_NAN_ON_ERROR}.values()) == -1
+    assert g.gemm_grouped_wgrad_validate(*{**WGRAD, "dtype": 1, "c_dtype": 2 | g.GEMM_GROUPED_NAN_ON_ERROR}.values()) == -1
