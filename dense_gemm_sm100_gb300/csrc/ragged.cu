@@ -41,12 +41,14 @@
 // the rate at K = 4096).  A weight gradient takes this form where all its rows
 // together are that long, since one group may hold them all: 16 skewed groups
 // of 512 rows on average come to 5.6e-7 instead of 6.4e-7 to 1.2e-6, for 247
-// instead of 231 us with the input gradient.  BF16 results round by 2^-8
-// afterwards.  Sums of 4-bit products are not cut: an addition covers 64 K
-// elements, and where the block scales of a row lie within a factor of 16 the
-// sums need no more than 24 bits (measured: exact up to K = 16384).  Scales
-// that spread over 2^16 lose as much per addition as above: 1.0e-6 of the
-// result's norm at K = 4096, 4.5e-6 at 16384, 1.9e-5 at 65536.
+// instead of 231 us with the input gradient.  The sums are 128 registers a
+// thread beside the segment being added, of the 168 that ten warps leave: 20 to
+// 28 bytes are spilled.  BF16 results round by 2^-8 afterwards.  Sums of 4-bit
+// products are not cut: an addition covers 64 K elements, and where the block
+// scales of a row lie within a factor of 16 the sums need no more than 24 bits
+// (measured: exact up to K = 16384).  Scales that spread over 2^16 lose as much
+// per addition as above: 1.0e-6 of the result's norm at K = 4096, 4.5e-6 at
+// 16384, 1.9e-5 at 65536.
 //
 // Few tiles.  A launch with fewer tiles than SMs and a long contraction runs
 // each tile on a cluster of 2, 4 or 8 CTAs, each with its own range of K.  The
@@ -1063,7 +1065,10 @@ bool ragged_tile_ok(int split, int ctas, int bn)
 // scales' hand-over between the CTAs) or its epilogue (12 cycles a row); a
 // launch the waves of tiles, one epilogue and 3 us, and at least its traffic at
 // 6.4 TB/s.  The type of C does not enter, so that a BF16 result is the FP32
-// result rounded.
+// result rounded where that is not summed in segments.  The number of TMA boxes
+// of a stage does not enter either (one, or one per 128-byte chunk where a width
+// is no multiple of the chunk): 13 + 10 us for the TF32 gradients of 2011 rows and
+// 13 experts of 1020 x 520, which take 24 + 27.
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
                             int sm_count, bool may_split)
 {
