@@ -539,6 +539,8 @@ class Gemm:
     def _ld(t):
         if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
             raise ValueError("operands must be 2-D with unit stride along rows")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError("the rows of an operand overlap")
         return max(t.stride(0), t.shape[1], 1)
 
     def run(self, A, B, C, layout_b="row", dtype="f32", stream=None):

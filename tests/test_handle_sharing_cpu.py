@@ -109,3 +109,20 @@ def test_threads_get_one_default_handle(monkeypatch):
     in_threads(4, lambda: got.append(g.default_handle(0)))
     assert made == [0] and len(set(map(id, got))) == 1
     assert g.default_handle(0) is got[0] and g.default_handle(1) is not got[0]
+
+
+def test_dense_operands_whose_rows_overlap_are_refused(shared):
+    """An expanded operand would be read at the pitch of its columns, past the
+    end of its storage."""
+    h, busy = shared
+    a, b, c = torch.zeros(4, 8), torch.zeros(8, 4), torch.zeros(4, 4)
+    row = torch.zeros(1, 8)
+    for args in ((row.expand(4, 8), b, c), (a, torch.zeros(1, 4).expand(8, 4), c), (a, b, torch.zeros(1, 4).expand(4, 4)),
+                 (torch.zeros(32).as_strided((4, 8), (4, 1)), b, c)):
+        for run in (h.run, h.run_host):
+            with pytest.raises(ValueError):
+                run(*args, stream=0)
+    assert busy.calls == 0
+    h.run(row.expand(1, 8), b, c[:1], stream=0)
+    h.run(torch.zeros(4, 16)[:, :8], b, c, stream=0)
+    assert busy.calls == 2
