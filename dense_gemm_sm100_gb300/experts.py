@@ -1,9 +1,11 @@
-"""Expert products for torch models: row grouping and a differentiable
+"""Expert products for torch models: routing, row grouping and a differentiable
 grouped product on the library's kernels.
 
-``group_rows`` turns a router's choices into the row order and offsets that the
-grouped products read (both stay on the device); ``grouped_matmul`` is
-``Gemm.run_grouped`` with its two gradients, differentiable any number of times.
+``route`` takes a router's logits to the chosen experts, their weights
+(differentiable in the logits) and the row order and offsets that the grouped
+products read, all on the device; ``group_rows`` makes the latter two from
+choices made elsewhere; ``grouped_matmul`` is ``Gemm.run_grouped`` with its two
+gradients, differentiable any number of times.
 """
 from __future__ import annotations
 
@@ -139,3 +141,63 @@ def grouped_matmul(A, B, offsets, layout_b="row", out_dtype=None, handle: _g.Gem
         raise ValueError(f"A is on {A.device}: the grouped products run on a CUDA device")
     return _product(A, B, offsets, layout, dtype, out_dtype or A.dtype,
                     handle or _g.default_handle(A.device.index or 0))
+
+
+def _weights_of(logits, expert, scoring, renormalise, scale):
+    """The weights of given choices as torch operations, for gradients of gradients."""
+    chosen, x = expert >= 0, logits.float()
+    index = expert.clamp(min=0)
+    if scoring == "sigmoid":
+        score = torch.sigmoid(torch.gather(x, 1, index)).masked_fill(~chosen, 0.0)
+        if renormalise:
+            score = score / (score.sum(-1, keepdim=True) + 1e-20)
+    elif renormalise:
+        # a finite stand-in where there is no choice: 0 * nan would stay in the gradient
+        score = torch.softmax(torch.gather(x, 1, index).masked_fill(~chosen, -1e30), -1).masked_fill(~chosen, 0.0)
+    else:
+        x = x.masked_fill(~chosen.any(-1, keepdim=True), 0.0)
+        score = torch.gather(torch.softmax(x, -1), 1, index).masked_fill(~chosen, 0.0)
+    return scale * score
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, scoring, bias, groups, top_groups, renormalise, scale, handle):
+        out = _g.routing_empty(logits.shape[0], logits.shape[1], k, logits.device)
+        handle.route(logits, out, scoring, bias, groups, top_groups, renormalise, scale)
+        ctx.save_for_backward(logits, out.expert)
+        ctx.config = (scoring, renormalise, scale, handle)
+        ctx.mark_non_differentiable(out.expert, out.order, out.offsets)
+        return tuple(out)
+
+    @staticmethod
+    def backward(ctx, dweights, *_):
+        logits, expert = ctx.saved_tensors
+        scoring, renormalise, scale, handle = ctx.config
+        if torch.is_grad_enabled():  # create_graph
+            w = _weights_of(logits, expert, scoring, renormalise, scale)
+            dlogits, = torch.autograd.grad(w, logits, dweights, create_graph=True)
+        else:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+            handle.route_grad(logits, expert, dweights.contiguous(), dlogits, scoring, renormalise, scale)
+        return (dlogits,) + (None,) * 8
+
+
+def route(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, renormalise=True, scale=1.0,
+          handle: _g.Gemm | None = None) -> _g.Routing:
+    """The k experts of every row of ``logits`` (tokens, experts), their weights,
+    and the rows token * k + choice sorted by expert: ``Gemm.route`` with
+    ``weights`` differentiable in the logits (any number of times; the choices
+    are constants, and so is ``bias``).
+
+    With ``r = route(logits, k)`` and ``rows = x[r.order // k]``, expert g's rows
+    are ``rows[r.offsets[g]:r.offsets[g + 1]]``, as ``grouped_matmul`` takes them.
+    Logits of minus infinity are never chosen; choices that are not there
+    (``expert`` -1, weight 0) come first in ``order``, in no expert's rows."""
+    if logits.device.type != "cuda":
+        raise ValueError(f"logits are on {logits.device}: the router runs on a CUDA device")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    h = handle or _g.default_handle(logits.device.index or 0)
+    return _g.Routing(*_Route.apply(_dense_rows(logits), k, scoring, None if bias is None else bias.detach(), groups,
+                                    top_groups, renormalise, scale, h))

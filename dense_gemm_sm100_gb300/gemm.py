@@ -6,11 +6,11 @@ The functions ``gemm_create``, ``gemm_run``, ``gemm_run_host``,
 ``gemm_last_path``, ``gemm_launch_count``, ``gemm_version``,
 ``gemm_run_noalloc``, ``gemm_ladder_run``, ``gemm_ladder_name``,
 ``gemm_peak_fma_run`` and ``gemm_peak_mma_run``, and those of
-include/gemm_grouped.h and include/gemm_mx4.h, take and return the same
-plain values as their C counterparts (pointers as ints; the FLOP-count
-out-parameter of the peak calls is returned as a second value).  ``Gemm``
-wraps a handle for torch tensors; ``Mx4`` holds a matrix in microscaled 4-bit
-floating point.  Every GEMM step runs in the library's CUDA
+include/gemm_grouped.h, include/gemm_mx4.h and include/gemm_route.h, take and
+return the same plain values as their C counterparts (pointers as ints; the
+FLOP-count out-parameter of the peak calls is returned as a second value).
+``Gemm`` wraps a handle for torch tensors; ``Mx4`` holds a matrix in microscaled
+4-bit floating point, ``Routing`` the choices of a router.  Every GEMM step runs in the library's CUDA
 kernels; there is no other code path, and calling anything here without the
 built library raises ``GemmLibraryMissing``.
 """
@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 from . import build as _build
 
@@ -57,6 +58,12 @@ GEMM_OPT_GROUPED_TILE = 16
 GEMM_GROUPED_MAX_GROUPS = 4096
 GEMM_GROUPED_NAN_ON_ERROR = 0x100
 GEMM_MX4_BLOCK = 32
+
+GEMM_ROUTE_MAX_EXPERTS = 1024
+GEMM_ROUTE_MAX_K = 31
+GEMM_ROUTE_MAX_GROUPS = 32
+GEMM_ROUTE_SIGMOID = 1
+GEMM_ROUTE_RENORMALISE = 2
 
 DTYPES = {"f32": GEMM_F32, "tf32": GEMM_TF32, "bf16": GEMM_BF16, "f32x3": GEMM_F32_3XTF32}
 LAYOUTS = {"row": GEMM_B_ROW_MAJOR, "col": GEMM_B_COL_MAJOR}
@@ -132,6 +139,15 @@ def load_library():
             "gemm_mx4_quantise_validate": (quantise, ci),
             "gemm_mx4_dequantise_validate": (dequantise, ci),
             "gemm_mx4_validate": (mx4_grouped, ci),
+        })
+        cf = ctypes.c_float
+        route = [i64, i64, i64, vp, i64, ci, vp, i64, i64, ci, cf, vp, vp, vp, vp]
+        route_grad = [i64, i64, i64, vp, i64, ci, vp, vp, ci, cf, vp, i64]
+        sig.update({
+            "gemm_route": ([vp, *route, vp], ci),
+            "gemm_route_grad": ([vp, *route_grad, vp], ci),
+            "gemm_route_validate": (route, ci),
+            "gemm_route_grad_validate": (route_grad, ci),
         })
         for name, (argtypes, restype) in sig.items():
             fn = getattr(lib, name)
@@ -267,6 +283,24 @@ def gemm_mx4_dequantise_validate(*args) -> int:
 
 def gemm_mx4_validate(*args) -> int:
     return load_library().gemm_mx4_validate(*args)
+
+
+# include/gemm_route.h, argument for argument.
+
+def gemm_route(*args) -> int:
+    return load_library().gemm_route(*args)
+
+
+def gemm_route_grad(*args) -> int:
+    return load_library().gemm_route_grad(*args)
+
+
+def gemm_route_validate(*args) -> int:
+    return load_library().gemm_route_validate(*args)
+
+
+def gemm_route_grad_validate(*args) -> int:
+    return load_library().gemm_route_grad_validate(*args)
 
 
 GEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -482,6 +516,47 @@ def mx4_empty(rows: int, K: int, device="cuda") -> Mx4:
                torch.empty((rows, gemm_mx4_scale_pitch(K)), dtype=torch.uint8, device=device), K)
 
 
+class Routing(NamedTuple):
+    """A router's choices: ``weights`` (tokens, k) float32 and ``expert``
+    (tokens, k) int64, -1 where there is none; ``order`` (tokens * k,) int64, the
+    rows token * k + choice sorted by expert, and ``offsets`` (experts + 1,)
+    int64, the experts' bounds in it."""
+
+    weights: Any
+    expert: Any
+    order: Any
+    offsets: Any
+
+
+def routing_empty(tokens: int, experts: int, k: int, device="cuda") -> Routing:
+    """Uninitialised ``Routing`` storage."""
+    import torch
+    ints = lambda *shape: torch.empty(shape, dtype=torch.int64, device=device)
+    return Routing(torch.empty((tokens, k), dtype=torch.float32, device=device), ints(tokens, k), ints(tokens * k),
+                   ints(experts + 1))
+
+
+_plain_types = None
+
+
+def _plain(t, name, shape, kind, device):
+    """The address of a contiguous tensor of the given shape; kind "int64" or "float32"."""
+    global _plain_types
+    if _plain_types is None:
+        import torch
+        _plain_types = {"int64": torch.int64, "float32": torch.float32}
+    _on_device(t, name, device)
+    if t.dtype != _plain_types[kind] or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {kind} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _route_flags(scoring, renormalise):
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', not {scoring!r}")
+    return (GEMM_ROUTE_SIGMOID if scoring == "sigmoid" else 0) | (GEMM_ROUTE_RENORMALISE if renormalise else 0)
+
+
 class Gemm:
     """A library handle used with torch tensors.
 
@@ -616,6 +691,56 @@ class Gemm:
             if rc:
                 self._check(rc)
         return C
+
+    def route(self, logits, out: Routing, scoring="softmax", bias=None, groups=1, top_groups=1, renormalise=True,
+              scale=1.0, stream=None):
+        """Every token's k experts and their weights, and the rows sorted by
+        expert, into ``out`` (k is the width of ``out.expert``).
+
+        logits is (tokens, experts) float32 or bfloat16; ``bias`` (experts,)
+        float32 is added to the scores for the choice alone; of ``groups``
+        equal groups of neighbouring experts the ``top_groups`` best by the sum
+        of their two best experts stay open.  Weights are the scores
+        ("softmax" or "sigmoid"), renormalised over the choices or not, times
+        ``scale``.  Logits of minus infinity are never chosen."""
+        dev = self.device
+        T, E, ld, l_type = _matrix(logits, "logits", dev)
+        if out.expert.dim() != 2:
+            raise ValueError("out.expert must be 2-D")
+        k = out.expert.shape[1]
+        flags = _route_flags(scoring, renormalise)
+        weights = _plain(out.weights, "out.weights", (T, k), "float32", dev)
+        expert = _plain(out.expert, "out.expert", (T, k), "int64", dev)
+        order = _plain(out.order, "out.order", (T * k,), "int64", dev)
+        offsets = _plain(out.offsets, "out.offsets", (E + 1,), "int64", dev)
+        b = None if bias is None else _plain(bias, "bias", (E,), "float32", dev)
+        with self._turn:
+            rc = self._lib.gemm_route(self.handle, T, E, k, logits.data_ptr(), ld, l_type, b, groups, top_groups, flags,
+                                      scale, weights, expert, order, offsets, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return out
+
+    def route_grad(self, logits, expert, dweights, dlogits, scoring="softmax", renormalise=True, scale=1.0, stream=None):
+        """The gradient of the logits for ``dweights`` (tokens, k), with the
+        choices ``expert`` of ``route`` held fixed."""
+        dev = self.device
+        T, E, ld, l_type = _matrix(logits, "logits", dev)
+        rows, cols, ldd, d_type = _matrix(dlogits, "dlogits", dev)
+        if (rows, cols, d_type) != (T, E, l_type):
+            raise ValueError("dlogits must have the shape and type of logits")
+        if expert.dim() != 2:
+            raise ValueError("expert must be 2-D")
+        k = expert.shape[1]
+        flags = _route_flags(scoring, renormalise)
+        e = _plain(expert, "expert", (T, k), "int64", dev)
+        d = _plain(dweights, "dweights", (T, k), "float32", dev)
+        with self._turn:
+            rc = self._lib.gemm_route_grad(self.handle, T, E, k, logits.data_ptr(), ld, l_type, e, d, flags, scale,
+                                           dlogits.data_ptr(), ldd, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return dlogits
 
     def mx4_quantise(self, src, out: Mx4, layout="col", stream=None):
         """Quantise ``src`` (float32 or bfloat16) along K into ``out``.
