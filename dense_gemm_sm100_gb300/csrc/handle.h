@@ -251,12 +251,16 @@ inline int encode_2d(gemm_ctx *h, CUtensorMap *map, int es, const void *base, in
     return GEMM_OK;
 }
 
+// The handle's device for the length of a call.  Set even where it is the
+// thread's already: a thread that has made no CUDA call yet (one of an autograd
+// engine's, say) reports device 0 without a context, and tensor maps cannot be
+// encoded without one.
 class DeviceGuard {
   public:
     explicit DeviceGuard(int dev)
     {
         if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        if (prev_ != dev) cudaSetDevice(dev);
+        cudaSetDevice(dev);
     }
     ~DeviceGuard()
     {
