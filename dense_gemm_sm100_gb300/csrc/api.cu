@@ -817,6 +817,11 @@ int gemm_set_option(gemm_handle_t h, int option, int64_t value)
             break;
         h->ragged_tile = static_cast<int>(value);
         return GEMM_OK;
+    case GEMM_OPT_ORTHO_TILE:
+        if (value != 0 && value / 1000 != 1 && value / 1000 != 2) break;
+        if (value != 0 && value % 1000 != 32 && value % 1000 != 64 && value % 1000 != 128 && value % 1000 != 256) break;
+        h->ortho_tile = static_cast<int>(value);
+        return GEMM_OK;
     default:
         return fail(h, GEMM_ERR_INVALID, "unknown option");
     }

@@ -51,7 +51,9 @@ struct gemm_ctx {
     int tc_tma_store = 1; // tensor-core epilogue writes C with TMA stores when C allows it
     int tc_slices = 0;    // pair MMA: K slices per ring stage (0: library's choice)
     bool ragged_ready = false;  // prepare_ragged has run for this handle
+    bool i8_ready = false;      // prepare_ragged_i8 has
     int ragged_tile = 0;  // grouped and 4-bit products: 0 chosen, else 10000 * split + 1000 * CTAs + rows of a tile
+    int ortho_tile = 0;   // orthogonalisation's products: 0 chosen, else 1000 * CTAs + columns of a tile
     int debug_drop = 0;   // test hook (GEMM_OPT_DEBUG_DROP_LOAD)
     // gemm_run_host pipeline: copy streams and events (created on first use)
     cudaStream_t copy_in = nullptr, copy_out = nullptr;
@@ -249,6 +251,28 @@ inline int encode_2d(gemm_ctx *h, CUtensorMap *map, int es, const void *base, in
         return fail(h, GEMM_ERR_CUDA, msg);
     }
     return GEMM_OK;
+}
+
+// A tiled map of any rank: extents in elements, strides in bytes.
+inline int encode(gemm_ctx *h, CUtensorMap *map, CUtensorMapDataType type, int rank, uintptr_t base,
+                  const int64_t *dims, const int64_t *strides, const int *box, CUtensorMapSwizzle swizzle,
+                  const char *what)
+{
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        es[i] = 1;
+        if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]);
+    }
+    const CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), reinterpret_cast<void *>(base), d, st, b,
+                                    es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GEMM_OK;
+    char msg[128];
+    std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), what);
+    return fail(h, GEMM_ERR_CUDA, msg);
 }
 
 // The handle's device for the length of a call.  Set even where it is the

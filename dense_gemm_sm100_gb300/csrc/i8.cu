@@ -1,0 +1,453 @@
+// 8-bit integers with one FP32 scale a row: s = max|x| / 127 rounded to FP32,
+// codes x / s rounded to the nearest integer, ties to even, within -127 .. 127.
+// The quotient is taken as if in infinite precision: x * (1 / s) in FP32 is off
+// by 1.5e-5 at most, and where that leaves the rounding open (4e-5 on either
+// side of a half) the exact remainder x - c * s decides.  A row of zeros has scale
+// 0; one that holds an infinity or a NaN has scale NaN; both have codes 0.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "ragged.h"
+
+namespace dg {
+namespace {
+
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Eight elements of a row as they are loaded (vec: 16-byte loads are allowed;
+// past the row's end zeros), and widened.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *s, int n, bool vec)
+    {
+        if (vec && n >= 8) {
+            a = *reinterpret_cast<const float4 *>(s);
+            b = *(reinterpret_cast<const float4 *>(s) + 1);
+        } else {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? s[i] : 0.0f;
+            a = make_float4(v[0], v[1], v[2], v[3]);
+            b = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    __device__ __forceinline__ void widen(float (&v)[8]) const
+    {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *s, int n, bool vec)
+    {
+        if (vec && n >= 8) {
+            a = *reinterpret_cast<const uint4 *>(s);
+        } else {
+            const uint16_t *t = reinterpret_cast<const uint16_t *>(s);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = (2 * i < n ? uint32_t{t[2 * i]} : 0u) | (2 * i + 1 < n ? uint32_t{t[2 * i + 1]} << 16 : 0u);
+            a = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __device__ __forceinline__ void widen(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+// The scale of a row from the largest magnitude's bits (NaN > infinity > finite
+// as integers).
+__device__ __forceinline__ float scale_of(uint32_t amax_bits)
+{
+    return amax_bits >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
+}
+
+// Codes of values by a row's scale.
+struct Coder {
+    float scale, inverse;
+    bool none, small;
+    __device__ __forceinline__ explicit Coder(float s) : scale(s)
+    {
+        none = !(s > 0.0f);
+        small = s < 1e-30f;  // no FP32 reciprocal to rely on
+        inverse = none || small ? 0.0f : 1.0f / s;
+    }
+    // Where the estimate leaves the rounding open.  The remainder is exact: a
+    // multiple of half a unit of the scale's last place, and little more than
+    // half the scale.
+    __device__ __forceinline__ int settle(float x) const
+    {
+        if (small) return static_cast<int>(fmin(fmax(rint(static_cast<double>(x) / scale), -127.0), 127.0));
+        float c = rintf(x * inverse);
+        const float d = fmaf(-c, scale, x), twice = 2.0f * fabsf(d);
+        if (twice > scale || (twice == scale && (static_cast<int>(c) & 1))) c += copysignf(1.0f, d);
+        return static_cast<int>(c);
+    }
+    // Eight codes.  Adding 1.5 * 2^23 rounds to an integer and leaves it in the
+    // low bits; |x| <= 127 s keeps it within -127 .. 127.
+    __device__ __forceinline__ uint2 operator()(const float (&v)[8]) const
+    {
+        if (none) return make_uint2(0u, 0u);
+        constexpr float ROUND = 12582912.0f;
+        uint32_t w[8];
+        float far = small ? 1.0f : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = fmaf(v[i], inverse, ROUND);
+            far = fmaxf(far, fabsf(fmaf(v[i], inverse, -(t - ROUND))));
+            w[i] = __float_as_uint(t);
+        }
+        if (far > 0.49996f)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = static_cast<uint32_t>(settle(v[i]));
+        const auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+        };
+        return make_uint2(four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7]));
+    }
+};
+
+__device__ __forceinline__ void store8(int8_t *dst, uint2 c, int n)
+{
+    if (n >= 8) {
+        *reinterpret_cast<uint2 *>(dst) = c;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) dst[i] = static_cast<int8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    }
+}
+
+// TPR threads a row, U pieces of eight elements a thread kept in registers
+// between the maximum and the codes (U = 0: the row is read again).
+template <typename T, int TPR, int U>
+__global__ void __launch_bounds__(THREADS)
+    quantise_kernel(const T *src, long long ld, long long stride, long long rows, long long all, int K, bool vec,
+                    int8_t *codes, long long ldq, float *scales)
+{
+    __shared__ uint32_t part[THREADS / 32];
+    constexpr int ROWS = THREADS / TPR;
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int pieces = (K + 7) / 8;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (long long r0 = static_cast<long long>(blockIdx.x) * ROWS; r0 < all; r0 += static_cast<long long>(gridDim.x) * ROWS) {
+        const long long r = r0 + sub;
+        const bool there = r < all;
+        const long long b = there ? r / rows : 0;
+        const T *row = src + (there ? b * stride + (r - b * rows) * ld : 0);
+        Raw<T> kept[U > 0 ? U : 1];
+        uint32_t amax = 0;
+        const auto top = [&](const Raw<T> &raw) {
+            float v[8];
+            raw.widen(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+        };
+        if (U > 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = (u * TPR + t) * 8;
+                kept[u].load(row + k, there ? K - k : 0, vec);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) top(kept[u]);
+        } else if (there) {
+            for (int i = t; i < pieces; i += TPR) {
+                kept[0].load(row + i * 8, K - i * 8, vec);
+                top(kept[0]);
+            }
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        if (TPR > 32) {
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < TPR / 32; ++w) amax = max(amax, part[w]);
+            __syncthreads();  // part is written again for the next row
+        }
+        const Coder q(scale_of(amax));
+        if (there && t == 0) scales[r] = q.scale;
+        int8_t *out = codes + r * ldq;
+        const auto put = [&](const Raw<T> &raw, int k) {
+            float v[8];
+            raw.widen(v);
+            store8(out + k, q(v), K - k);
+        };
+        if (U > 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = (u * TPR + t) * 8;
+                if (there && k < K) put(kept[u], k);
+            }
+        } else if (there) {
+            for (int i = t; i < pieces; i += TPR) {
+                kept[0].load(row + i * 8, K - i * 8, vec);
+                put(kept[0], i * 8);
+            }
+        }
+    }
+}
+
+// Row-major weights: element (r, k) at src[k * ld + r].  A CTA takes 32 rows of
+// the output: the maxima of its 32 columns, then 128 values of K at a time
+// through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(THREADS)
+    quantise_turn_kernel(const T *src, long long ld, long long stride, int rows, int K, int8_t *codes, long long ldq,
+                         float *scales)
+{
+    constexpr int W = THREADS / 32;
+    __shared__ uint32_t part[W][32];
+    __shared__ __align__(16) int8_t tile[32][128 + 16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int blocks = (rows + 31) / 32;
+    const long long b = blockIdx.x / blocks;
+    const int r0 = static_cast<int>(blockIdx.x - b * blocks) * 32, r = r0 + lane;
+    const T *col = src + b * stride + r;
+    uint32_t amax = 0;
+    if (r < rows)
+#pragma unroll 8
+        for (int k = warp; k < K; k += W)
+            amax = max(amax, __float_as_uint(to_f32(col[static_cast<long long>(k) * ld])) & 0x7fffffffu);
+    part[warp][lane] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) amax = max(amax, part[w][lane]);
+    const Coder q(scale_of(amax));
+    const long long first = b * rows + r0;
+    if (warp == 0 && r < rows) scales[first + lane] = q.scale;
+    const int out_row = threadIdx.x >> 3, piece = (threadIdx.x & 7) * 16;
+    for (int k0 = 0; k0 < K; k0 += 128) {
+#pragma unroll
+        for (int j = warp * 8; j < 128; j += W * 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = r < rows && k0 + j + i < K ? to_f32(col[static_cast<long long>(k0 + j + i) * ld]) : 0.0f;
+            *reinterpret_cast<uint2 *>(&tile[lane][j]) = q(v);
+        }
+        __syncthreads();
+        if (r0 + out_row < rows) {
+            int8_t *dst = codes + (first + out_row) * ldq + k0 + piece;
+            const int n = K - k0 - piece;
+            const uint4 v = *reinterpret_cast<const uint4 *>(&tile[out_row][piece]);
+            if (n >= 16) {
+                *reinterpret_cast<uint4 *>(dst) = v;
+            } else {
+                store8(dst, make_uint2(v.x, v.y), n);
+                store8(dst + 8, make_uint2(v.z, v.w), n - 8);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ void put8(float *dst, const float (&v)[8], int n, bool vec)
+{
+    if (vec && n >= 8) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        *(reinterpret_cast<float4 *>(dst) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) dst[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void put8(__nv_bfloat16 *dst, const float (&v)[8], int n, bool vec)
+{
+    if (vec && n >= 8) {
+        const __nv_bfloat162 w[4] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3]),
+                                     __floats2bfloat162_rn(v[4], v[5]), __floats2bfloat162_rn(v[6], v[7])};
+        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// A warp takes 256 elements of a row.
+template <typename T>
+__global__ void __launch_bounds__(THREADS)
+    dequantise_kernel(long long rows, int K, const int8_t *codes, long long ldq, const float *scales, T *dst,
+                      long long ldd, bool vec)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int chunks = (K + 255) / 256, lane = threadIdx.x & 31;
+    const long long all = rows * chunks;
+    for (long long w = blockIdx.x * (THREADS / 32LL) + (threadIdx.x >> 5); w < all; w += gridDim.x * (THREADS / 32LL)) {
+        const long long r = w / chunks;
+        const int k = static_cast<int>(w - r * chunks) * 256 + lane * 8, n = K - k;
+        if (n <= 0) continue;
+        const float s = scales[r];
+        float v[8];
+        if (n >= 8) {
+            const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * ldq + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)))) * s;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? static_cast<float>(codes[r * ldq + k + i]) * s : 0.0f;
+        }
+        put8(dst + r * ldd + k, v, n, vec);
+    }
+}
+
+// A warp takes WIDEN x 512 codes of a row, 16 a lane at a time.  Rows are read
+// up to the end of their last 16 bytes, which the pitch holds, and written so.
+constexpr int WIDEN = 4;
+struct WidenJob {
+    const int8_t *src;
+    long long ld, rows;
+    __half *dst;
+    const long long *offsets;
+    long long rows_per;
+};
+
+__global__ void __launch_bounds__(THREADS) widen_kernel(const WidenJob a, const WidenJob b, int K)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int pieces = (K + 15) / 16, chunks = (pieces + 32 * WIDEN - 1) / (32 * WIDEN), lane = threadIdx.x & 31;
+    const long long pitch = pieces * 16LL, all = (a.rows + b.rows) * chunks;
+    for (long long w = blockIdx.x * (THREADS / 32LL) + (threadIdx.x >> 5); w < all; w += gridDim.x * (THREADS / 32LL)) {
+        const long long row = w / chunks;
+        const int p0 = static_cast<int>(w - row * chunks) * 32 * WIDEN + lane;
+        const bool second = row >= a.rows;
+        const WidenJob &j = second ? b : a;
+        const long long r = second ? row - a.rows : row;
+        if (j.offsets != nullptr) {
+            const long long g = r / j.rows_per;
+            if (j.offsets[g] >= j.offsets[g + 1]) continue;
+        }
+        const uint4 *src = reinterpret_cast<const uint4 *>(j.src + r * j.ld);
+        uint4 *dst = reinterpret_cast<uint4 *>(j.dst + r * pitch);
+        uint4 c[WIDEN];
+#pragma unroll
+        for (int i = 0; i < WIDEN; ++i)
+            if (p0 + i * 32 < pieces) c[i] = src[p0 + i * 32];
+#pragma unroll
+        for (int i = 0; i < WIDEN; ++i)
+            if (p0 + i * 32 < pieces) {
+                uint4 lo, hi;
+                i8_to_f16(c[i], lo, hi);
+                dst[2 * (p0 + i * 32)] = lo;
+                dst[2 * (p0 + i * 32) + 1] = hi;
+            }
+    }
+}
+
+int grid_for(long long units, int per_cta, int per_sm, int sm_count)
+{
+    return static_cast<int>(std::max(1LL, std::min<long long>((units + per_cta - 1) / per_cta, int64_t{per_sm} * sm_count)));
+}
+
+template <typename T, int TPR, int U>
+cudaError_t launch_quantise(const void *src, int64_t ld, int64_t stride, int64_t batch, int64_t rows, int64_t K,
+                            int8_t *codes, int64_t ldq, float *scales, int sm_count, cudaStream_t stream)
+{
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (ld * sizeof(T)) % 16 == 0 &&
+                     (stride * sizeof(T)) % 16 == 0;
+    const cudaError_t e = kernel_ready<quantise_kernel<T, TPR, U>>(0);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(quantise_kernel<T, TPR, U>, grid_for(batch * rows, THREADS / TPR, 8, sm_count), THREADS, 0, stream,
+                      1, static_cast<const T *>(src), static_cast<long long>(ld), static_cast<long long>(stride),
+                      static_cast<long long>(rows), static_cast<long long>(batch * rows), static_cast<int>(K), vec, codes,
+                      static_cast<long long>(ldq), scales);
+}
+
+template <typename T>
+cudaError_t launch_quantise_for(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
+                                int64_t stride, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                                cudaStream_t stream)
+{
+    if (k_rows) {
+        const int64_t grid = batch * ((rows + 31) / 32);
+        const cudaError_t e = kernel_ready<quantise_turn_kernel<T>>(0);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(quantise_turn_kernel<T>, static_cast<int>(grid), THREADS, 0, stream, 1,
+                          static_cast<const T *>(src), static_cast<long long>(ld), static_cast<long long>(stride),
+                          static_cast<int>(rows), static_cast<int>(K), codes, static_cast<long long>(ldq), scales);
+    }
+    const auto run = [&](auto f) { return f(src, ld, stride, batch, rows, K, codes, ldq, scales, sm_count, stream); };
+    if (K <= 256) return run(launch_quantise<T, 32, 1>);
+    if (K <= 1024) return run(launch_quantise<T, 32, 4>);
+    if (K <= 4096) return run(launch_quantise<T, 256, 2>);
+    if (K <= 16384) return run(launch_quantise<T, 256, 8>);
+    return run(launch_quantise<T, 256, 0>);
+}
+
+}  // namespace
+
+cudaError_t launch_i8_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
+                               int64_t stride, bool src_bf16, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                               cudaStream_t stream)
+{
+    return src_bf16 ? launch_quantise_for<__nv_bfloat16>(k_rows, batch, rows, K, src, ld, stride, codes, ldq, scales,
+                                                         sm_count, stream)
+                    : launch_quantise_for<float>(k_rows, batch, rows, K, src, ld, stride, codes, ldq, scales, sm_count,
+                                                 stream);
+}
+
+cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
+                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, cudaStream_t stream)
+{
+    const int es = dst_bf16 ? 2 : 4;
+    const bool vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && (ldd * es) % 16 == 0;
+    const int grid = grid_for(rows * ((K + 255) / 256), THREADS / 32, 8, sm_count);
+    cudaError_t e;
+    if (dst_bf16) {
+        e = kernel_ready<dequantise_kernel<__nv_bfloat16>>(0);
+        return e != cudaSuccess ? e
+                                : launch_pdl(dequantise_kernel<__nv_bfloat16>, grid, THREADS, 0, stream, 1,
+                                             static_cast<long long>(rows), static_cast<int>(K), codes,
+                                             static_cast<long long>(ldq), scales, static_cast<__nv_bfloat16 *>(dst),
+                                             static_cast<long long>(ldd), vec);
+    }
+    e = kernel_ready<dequantise_kernel<float>>(0);
+    return e != cudaSuccess ? e
+                            : launch_pdl(dequantise_kernel<float>, grid, THREADS, 0, stream, 1,
+                                         static_cast<long long>(rows), static_cast<int>(K), codes,
+                                         static_cast<long long>(ldq), scales, static_cast<float *>(dst),
+                                         static_cast<long long>(ldd), vec);
+}
+
+cudaError_t launch_i8_widen(const int8_t *a, int64_t lda, int64_t rows_a, const int8_t *b, int64_t ldb, int64_t rows_b,
+                            int64_t K, void *a16, void *b16, const int64_t *offsets, int64_t rows_per, int sm_count,
+                            cudaStream_t stream)
+{
+    WidenJob ja = {a, lda, rows_a, static_cast<__half *>(a16), nullptr, 1};
+    WidenJob jb = {b, ldb, rows_b, static_cast<__half *>(b16), reinterpret_cast<const long long *>(offsets), rows_per};
+    const int64_t chunks = (K + 512 * WIDEN - 1) / (512 * WIDEN);
+    const cudaError_t e = kernel_ready<widen_kernel>(0);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(widen_kernel, grid_for((rows_a + rows_b) * chunks, THREADS / 32, 8, sm_count), THREADS, 0, stream,
+                      1, ja, jb, static_cast<int>(K));
+}
+
+}  // namespace dg

@@ -1,4 +1,4 @@
-// Launch helpers of the router, the 8-bit products and the orthogonalised
+// Launch helpers of the router, the 8-bit conversions and the orthogonalised
 // update: programmatic stream serialisation, and kernels loaded before use.
 #pragma once
 

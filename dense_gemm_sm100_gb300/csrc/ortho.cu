@@ -1,0 +1,926 @@
+// Newton-Schulz steps X <- a X + (b A + c A A) X, A = X X^T, on the tensor cores.
+//
+// Three products a step, each with its epilogue: A = X X^T; B = b A + c A A;
+// X' = a X + B X.  A and B are symmetric: only tiles on and below the diagonal
+// are computed, and what lies below is written twice.
+//
+// Numbers.  The products' operands are FP16 (11 bits; BF16's 8 would cost a
+// relative 1e-2 to 4e-2 of the result), scaled by powers of two so that FP16's
+// range fits: X by 2^12, A by 2^11, B by 2^10.  A step multiplies what is small
+// in X by a = 3.4, five steps by 485, so it matters where roundings fall
+// (simulated in FP64, of the result's norm, gradients with a few strong
+// directions and noise / plain noise): all operands rounded to FP16 3.5e-3 /
+// 1.3e-3; the term a X taken from X in two FP16 numbers, its rest beside the
+// value, 3e-4 / 1.5e-3; the diagonals of A and B, their largest elements, kept
+// out of the products and applied in FP32 in the epilogues as well 2.7e-4 /
+// 7e-4; BF16's rounding of the result is 1.7e-3.  With E the part of A off the
+// diagonal and d the diagonal, A A = E E + (d_i + d_j) E + d^2.  FP32 results
+// take both FP16 numbers of every operand: three products (the fourth is below
+// 2^-22 of the first), and sums cut into segments that are added to nearest.
+//
+// The norm.  X is stored as Y = G 2^e with the norm of Y in [1, 2): exact for
+// BF16 and FP32 alike, the rest of 1 / (|G| + eps) enters A's and X's first
+// epilogues.  Where eps outweighs |G| the result is tiny; its power of two
+// stays out of Y until the result is written.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "launch.h"
+#include "ortho.h"
+#include "ptx.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int BP = 128;               // rows of P one CTA stages
+constexpr int BK = 64;                // K elements of a ring stage
+constexpr int P_BYTES = BP * 128;
+constexpr int MAX_STAGES = 12;
+constexpr int TMEM_COLS = 512;
+constexpr int ACC1 = 256;             // the second accumulator's column
+constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 1;
+constexpr int EPI_WARPS = 8;
+constexpr int WARPS = 2 + EPI_WARPS;
+constexpr int THREADS = 32 * WARPS;
+constexpr int SMEM_MAX = 227 * 1024;
+constexpr int SEG = 4;                // ring stages of a segment of a two-term sum
+constexpr float SCALE_A = 2048.0f, SCALE_B = 1024.0f;
+constexpr int SCALE_X_LOG = 12;
+
+// factors of a matrix, see below
+enum Factor : int { kFactorA0 = 0, kFactorA, kFactorX0, kFactorOut, kFactorUp0, kFactorUp1 };
+constexpr int FACTORS = ORTHO_FACTORS;
+
+struct Params {
+    int m, n, ldm, ldn, batch;
+    int mode, bn, tiles_i, tiles, stages, stage_bytes, q_bytes, kt;
+    int first, last, has_rest;
+    float ca, cb, cc;
+    const __half *x[2];  // planes of X as read
+    __half *x_out[2];
+    __half *a[2], *b[2];
+    float *da, *db;
+    const float *factors;
+    void *o;
+    long long ldo, stride_o;
+    int turned, o_bf16, o_vec;
+    int *status;
+    unsigned long long timeout_ns;
+    int debug_drop;
+};
+
+struct Tile {
+    int b, i0, j0;  // matrix, first row (of the CTA pair), first column
+    bool mirror;    // wholly below the diagonal
+    bool some;      // it has columns
+};
+
+// Symmetric products (r = rows of a tile / its columns): block row I holds the
+// r (I + 1) tiles up to the diagonal; block columns past m are empty.
+template <int CG, bool SYM>
+__device__ __forceinline__ Tile tile_at(const Params &p, int u)
+{
+    constexpr int BM = CG * BP;
+    Tile t;
+    t.b = u / p.tiles;
+    const int k = u - t.b * p.tiles;
+    int I, J;
+    if (SYM) {
+        const int r = max(1, BM / p.bn);
+        I = static_cast<int>((sqrtf(8.0f * static_cast<float>(k) / static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (r * (I * (I + 1) / 2) > k) --I;
+        while (r * ((I + 1) * (I + 2) / 2) <= k) ++I;
+        J = k - r * (I * (I + 1) / 2);
+        t.mirror = J / r < I;
+    } else {
+        J = k / p.tiles_i;
+        I = k - J * p.tiles_i;
+        t.mirror = false;
+    }
+    t.i0 = I * BM;
+    t.j0 = J * p.bn;
+    t.some = t.j0 < (SYM ? p.m : p.n);
+    return t;
+}
+
+__device__ __forceinline__ uint32_t pack(__half a, __half b)
+{
+    return static_cast<uint32_t>(__half_as_ushort(a)) | static_cast<uint32_t>(__half_as_ushort(b)) << 16;
+}
+
+__device__ __forceinline__ void load16(const __half *src, float (&v)[16])
+{
+    const uint4 w[2] = {*reinterpret_cast<const uint4 *>(src), *(reinterpret_cast<const uint4 *>(src) + 1)};
+    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void store16(__half *dst, const __half (&v)[16])
+{
+    reinterpret_cast<uint4 *>(dst)[0] =
+        make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+    reinterpret_cast<uint4 *>(dst)[1] =
+        make_uint4(pack(v[8], v[9]), pack(v[10], v[11]), pack(v[12], v[13]), pack(v[14], v[15]));
+}
+
+// SPLIT: operands of two FP16 numbers.  XSTEP: X' = a X + B X, Q = X with its
+// rows as K; else A or B, symmetric, P and Q the same matrix along K.
+template <int CG, bool SPLIT, bool XSTEP>
+__global__ void __launch_bounds__(THREADS, 1)
+    ortho_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
+                 const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1, const Params p)
+{
+    constexpr int PLANES = SPLIT ? 2 : 1;
+    // FP16 operands, FP32 accumulator; Q MN-major for X
+    constexpr uint32_t IDESC = (1u << 4) | ((XSTEP ? 1u : 0u) << 16) | (static_cast<uint32_t>((CG * BP) >> 4) << 24);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
+    const uint32_t sbase = raw_addr + pad;
+    const uint32_t bars = sbase + static_cast<uint32_t>(p.stages * p.stage_bytes);
+    const uint32_t full_bar = bars;                         // [stages], used in the even CTA
+    const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;   // [stages]
+    const uint32_t tfull_bar = empty_bar + 8 * MAX_STAGES;  // [2]
+    const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
+    const uint32_t drain_bar = tempty_bar + 16;
+    uint8_t *tail = smem_raw + pad + p.stages * p.stage_bytes + NUM_BARS * 8;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int first_unit = blockIdx.x / CG, unit_step = gridDim.x / CG;
+    const int num_units = p.tiles * p.batch;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full_bar + 8 * s, 1);
+            mbar_init(empty_bar + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar + 8 * b, 1);
+            mbar_init(tempty_bar + 8 * b, EPI_WARPS * CG);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmP0);
+        tma_prefetch_desc(&tmQ0);
+    }
+    if (warp == 1) {
+        const uint32_t slot = smem_addr(const_cast<uint32_t *>(tmem_slot));
+        if (CG == 2) {
+            tmem_alloc_pair(slot, TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(slot, TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before_sync();
+    if (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const int q_cta = p.bn / CG;
+            const uint32_t tx = static_cast<uint32_t>(CG * PLANES * (P_BYTES + p.q_bytes));
+            uint32_t it = 0, s = 0, ph = 0;
+            bool ok = true;
+            for (int u = first_unit; ok && u < num_units; u += unit_step) {
+                const Tile t = tile_at<CG, !XSTEP>(p, u);
+                if (!t.some) continue;
+                const int pi = t.i0 + static_cast<int>(rank) * BP;
+                const int qj = t.j0 + static_cast<int>(rank) * q_cta;
+                for (int kt = 0; kt < p.kt; ++kt, ++it) {
+                    if (!mbar_wait(empty_bar + 8 * s, ph ^ 1u, abort_flag, p.status, kWaitProducerEmpty,
+                                   p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb_local = full_bar + 8 * s;
+                    const uint32_t fb = CG == 2 ? mapa_shared(fb_local, 0) : fb_local;
+                    const uint32_t st = sbase + s * p.stage_bytes;
+                    if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                    if (++s == static_cast<uint32_t>(p.stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (p.debug_drop && blockIdx.x == 0 && it == 0) continue;  // bytes that never come
+#pragma unroll
+                    for (int pl = 0; pl < PLANES; ++pl) {
+                        const CUtensorMap *mp = pl ? &tmP1 : &tmP0, *mq = pl ? &tmQ1 : &tmQ0;
+                        const uint32_t p_st = st + pl * P_BYTES, q_st = st + PLANES * P_BYTES + pl * p.q_bytes;
+                        if (CG == 2)
+                            tma_load_3d_pair(p_st, mp, fb, kt * BK, pi, t.b);
+                        else
+                            tma_load_3d(p_st, mp, fb, kt * BK, pi, t.b);
+                        if (XSTEP) {  // chunks of 64 columns by 64 rows of K
+                            if (CG == 2)
+                                tma_load_4d_pair(q_st, mq, fb, 0, kt * BK, qj / 64, t.b);
+                            else
+                                tma_load_4d(q_st, mq, fb, 0, kt * BK, qj / 64, t.b);
+                        } else {
+                            if (CG == 2)
+                                tma_load_3d_pair(q_st, mq, fb, kt * BK, qj, t.b);
+                            else
+                                tma_load_3d(q_st, mq, fb, kt * BK, qj, t.b);
+                        }
+                    }
+                }
+            }
+            // Stages issued last, oldest first: (s, ph) is the next one.
+            const uint32_t n = min(it, static_cast<uint32_t>(p.stages));
+            uint32_t ds = s >= n ? s - n : s + p.stages - n;
+            uint32_t dph = s >= n ? ph : ph ^ 1u;
+            for (uint32_t i = 0; i < n; ++i) {
+                int dummy = 0;
+                if (ok) {
+                    // every release must have landed before shared memory goes away
+                    mbar_wait(empty_bar + 8 * ds, dph, abort_flag, p.status, kWaitDrain, p.timeout_ns);
+                } else if (leader) {
+                    // after an abort: leave no copy in flight
+                    mbar_wait(full_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+                }
+                if (++ds == static_cast<uint32_t>(p.stages)) {
+                    ds = 0;
+                    dph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer (even CTA)
+        if (leader) {
+            const uint32_t idesc = IDESC | (static_cast<uint32_t>(p.bn >> 3) << 17);
+            uint32_t s = 0, ph = 0, acc_it = 0;
+            bool ok = true, issued = false;
+            for (int u = first_unit; ok && u < num_units; u += unit_step) {
+                if (!tile_at<CG, !XSTEP>(p, u).some) continue;
+                for (int seg0 = 0; seg0 < p.kt; seg0 += SPLIT ? SEG : p.kt, ++acc_it) {
+                    const int seg1 = SPLIT ? min(p.kt, seg0 + SEG) : p.kt;
+                    const uint32_t abuf = acc_it & 1u;
+                    if (!mbar_wait_warp(tempty_bar + 8 * abuf, ((acc_it >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                                        kWaitMmaTmemEmpty, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d_tmem = tmem_base + abuf * ACC1;
+                    for (int kt = seg0; kt < seg1; ++kt) {
+                        if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t p_st = sbase + s * p.stage_bytes, q_st = p_st + PLANES * P_BYTES;
+                        if (elect_one()) {
+                            // value x value, then value x rest and rest x value
+#pragma unroll
+                            for (int term = 0; term < (SPLIT ? 3 : 1); ++term) {
+                                const uint32_t pa = p_st + (term == 2 ? P_BYTES : 0);
+                                const uint32_t qa = q_st + (term == 1 ? p.q_bytes : 0);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    const uint64_t pd = smem_desc(pa + kk * 32, 16, 1024, kLayoutSw128);
+                                    const uint64_t qd = XSTEP ? smem_desc(qa + kk * 16 * 128, BK * 128, 1024, kLayoutSw128)
+                                                              : smem_desc(qa + kk * 32, 16, 1024, kLayoutSw128);
+                                    const uint32_t acc = kt > seg0 || kk > 0 || term > 0 ? 1u : 0u;
+                                    if (CG == 2)
+                                        tc_mma_f16_pair(d_tmem, pd, qd, idesc, acc);
+                                    else
+                                        tc_mma_f16(d_tmem, pd, qd, idesc, acc);
+                                }
+                            }
+                            if (CG == 2)
+                                tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
+                            else
+                                tc_commit(empty_bar + 8 * s);
+                        }
+                        __syncwarp();
+                        issued = true;
+                        if (++s == static_cast<uint32_t>(p.stages)) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (CG == 2)
+                            tc_commit_pair_multicast(tfull_bar + 8 * abuf, 0x3);
+                        else
+                            tc_commit(tfull_bar + 8 * abuf);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && issued && lane == 0) {
+                // Let every MMA already issued finish before TMEM is freed.
+                if (CG == 2)
+                    tc_commit_pair_multicast(drain_bar, 0x1);
+                else
+                    tc_commit(drain_bar);
+                int dummy = 0;
+                mbar_wait(drain_bar, 0, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+            }
+        }
+    } else {
+        // ------------------------------------------------------ epilogue
+        // A lane holds a row of the result, 16 neighbouring columns at a time.
+        const int q = warp & 3;            // tensor-memory lane quarter
+        const int half = (warp - 2) >> 2;  // 0: even chunks of 32 columns, 1: odd ones
+        const int mine = (p.bn / 32 + 1 - half) / 2;
+        const auto unit_of = [&](int k) { return 4 * (k >> 1) + 2 * half + (k & 1); };
+        uint32_t acc_it = 0;
+        bool ok = true;
+        for (int u = first_unit; ok && u < num_units; u += unit_step) {
+            const Tile t = tile_at<CG, !XSTEP>(p, u);
+            if (!t.some) continue;
+            const int i = t.i0 + static_cast<int>(rank) * BP + q * 32 + lane;
+            const bool in = i < p.m;
+            const long long mat = t.b;
+            const float *f = p.factors + mat * FACTORS;
+            float diag = 0.0f, scale = 0.0f;
+            if (XSTEP) {
+                if (in) diag = p.ca + p.db[mat * p.ldm + i];
+                scale = 1.0f / SCALE_B;
+            } else if (p.mode == kOrthoA) {
+                scale = f[p.first ? kFactorA0 : kFactorA];
+            } else {
+                if (in) diag = p.da[mat * p.ldm + i];
+                scale = 1.0f / (SCALE_A * SCALE_A);
+            }
+            const float post = !XSTEP ? 1.0f : (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
+            const long long row_m = (mat * p.m + i) * p.ldm, row_n = (mat * p.m + i) * p.ldn;
+
+            const auto await = [&]() {
+                const uint32_t abuf = acc_it & 1u;
+                ok = mbar_wait_warp(tfull_bar + 8 * abuf, (acc_it >> 1) & 1u, abort_flag, p.status, kWaitEpiTmemFull,
+                                    p.timeout_ns);
+                tc_fence_after_sync();
+                return ok;
+            };
+            const auto release = [&]() {  // relaxed: see ragged.cu
+                const uint32_t bar = tempty_bar + 8 * (acc_it & 1u);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive_relaxed(bar);
+                    else
+                        mbar_arrive_cluster_relaxed(mapa_shared(bar, 0));
+                }
+                ++acc_it;
+            };
+            const auto load = [&](int unit, uint32_t(&v)[16]) {
+                tmem_load_16cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc_it & 1u) * ACC1 + unit * 16, v);
+            };
+            // Symmetric results: row i, and column i where the tile is mirrored.
+            const auto put_symmetric = [&](__half *const(&planes)[2], int j, float (&v)[16], float up) {
+                __half hi[16], lo[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float s = v[c] * up;
+                    hi[c] = __float2half_rn(s);
+                    if (SPLIT) lo[c] = __float2half_rn(s - __half2float(hi[c]));
+                }
+                if (in) {
+                    store16(planes[0] + row_m + j, hi);
+                    if (SPLIT) store16(planes[1] + row_m + j, lo);
+                    if (t.mirror) {
+                        __half *col = planes[0] + (mat * p.m + j) * p.ldm + i;
+                        __half *col1 = planes[1] + (mat * p.m + j) * p.ldm + i;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (j + c < p.m) {
+                                col[static_cast<long long>(c) * p.ldm] = hi[c];
+                                if (SPLIT) col1[static_cast<long long>(c) * p.ldm] = lo[c];
+                            }
+                    }
+                }
+            };
+            const auto finish = [&](int unit, const uint32_t(&acc)[16]) {
+                const int j = t.j0 + unit * 16;
+                if (j >= (XSTEP ? p.n : p.m)) return;
+                float v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(acc[c]) * scale;
+                if (!XSTEP && p.mode == kOrthoA) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (j + c == i) {
+                            if (in) p.da[mat * p.ldm + i] = v[c];
+                            v[c] = 0.0f;
+                        }
+                    put_symmetric(p.a, j, v, SCALE_A);
+                } else if (!XSTEP) {
+                    float e[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) e[c] = 0.0f;
+                    if (in) {
+                        load16(p.a[0] + row_m + j, e);
+                        if (SPLIT) {
+                            float r[16];
+                            load16(p.a[1] + row_m + j, r);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) e[c] += r[c];
+                        }
+                    }
+                    const float4 *dj = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        const float4 d4 = dj[c4];
+                        const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                        for (int c1 = 0; c1 < 4; ++c1) {
+                            const int c = c4 * 4 + c1;
+                            if (j + c == i) {
+                                if (in) p.db[mat * p.ldm + i] = p.cb * diag + p.cc * fmaf(diag, diag, v[c]);
+                                v[c] = 0.0f;
+                            } else {
+                                const float a = e[c] * (1.0f / SCALE_A);
+                                v[c] = p.cb * a + p.cc * fmaf(diag + d[c1], a, v[c]);
+                            }
+                        }
+                    }
+                    put_symmetric(p.b, j, v, SCALE_B);
+                } else if (in) {
+                    float x[16];
+                    load16(p.x[0] + row_n + j, x);
+                    if (p.has_rest) {
+                        float r[16];
+                        load16(p.x[1] + row_n + j, r);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x[c] += r[c];
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = fmaf(diag, x[c], v[c]) * post;
+                    if (!p.last) {
+                        __half hi[16], lo[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            hi[c] = __float2half_rn(v[c]);
+                            lo[c] = __float2half_rn(v[c] - __half2float(hi[c]));
+                        }
+                        store16(p.x_out[0] + row_n + j, hi);
+                        store16(p.x_out[1] + row_n + j, lo);
+                    } else if (p.turned) {
+                        const long long at = mat * p.stride_o + j * p.ldo + i;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (j + c < p.n) {
+                                if (p.o_bf16)
+                                    static_cast<__nv_bfloat16 *>(p.o)[at + c * p.ldo] = __float2bfloat16_rn(v[c]);
+                                else
+                                    static_cast<float *>(p.o)[at + c * p.ldo] = v[c];
+                            }
+                    } else {
+                        const long long at = mat * p.stride_o + i * p.ldo + j;
+                        if (p.o_vec && j + 16 <= p.n) {
+                            if (p.o_bf16) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+                                    w[c] = *reinterpret_cast<const uint32_t *>(&b);
+                                }
+                                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at);
+                                out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            } else {
+                                float4 *out = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    out[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (j + c < p.n) {
+                                    if (p.o_bf16)
+                                        static_cast<__nv_bfloat16 *>(p.o)[at + c] = __float2bfloat16_rn(v[c]);
+                                    else
+                                        static_cast<float *>(p.o)[at + c] = v[c];
+                                }
+                        }
+                    }
+                }
+            };
+            if (SPLIT) {
+                uint32_t sum[8][16];
+                for (int seg0 = 0; seg0 < p.kt; seg0 += SEG) {
+                    if (!await()) break;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= 2 * mine) break;
+                        if (seg0 == 0) {
+                            load(unit_of(k), sum[k]);
+                        } else {
+                            uint32_t v[16];
+                            load(unit_of(k), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                sum[k][c] = __float_as_uint(__uint_as_float(sum[k][c]) + __uint_as_float(v[c]));
+                        }
+                    }
+                    tmem_wait_ld();
+                    release();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < 2 * mine) finish(unit_of(k), sum[k]);
+            } else {
+                if (!await()) break;
+                uint32_t v[2][16];
+#pragma unroll 1
+                for (int k = 0; k == 0 || k < 2 * mine; k += 2) {
+                    if (k < 2 * mine) {
+                        load(unit_of(k), v[0]);
+                        load(unit_of(k + 1), v[1]);
+                        tmem_wait_ld();
+                    }
+                    if (k + 2 >= 2 * mine) release();
+                    if (k < 2 * mine) {
+                        finish(unit_of(k), v[0]);
+                        finish(unit_of(k + 1), v[1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncwarp();
+    if (CG == 2)
+        cluster_sync();  // no CTA leaves while its peer may still target its shared memory
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if (CG == 2)
+            tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------ norm and start
+
+constexpr int NORM_THREADS = 256;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// From the norm of a matrix: the factors of its products and the power of two
+// of X (two factors, whose product may leave FP32's range).
+__device__ void write_factors(double norm, double eps, float *f)
+{
+    // |G| 2^e in [1, 2); 1 / ((|G| + eps) 2^e) = rest 2^-down, down > 0 only where eps outweighs |G|
+    int e = 0, down = 0;
+    double rest = 1.0;
+    if (!(norm < INFINITY)) {
+        rest = __longlong_as_double(0x7fffffffffffffffLL);  // NaN
+    } else if (norm > 0.0) {
+        int top;
+        frexp(norm, &top);
+        e = 1 - top;
+        rest = 1.0 / ldexp(norm + eps, e);
+        if (rest < 0.25) {
+            int low;
+            rest = 2.0 * frexp(rest, &low);
+            down = 1 - low;
+        }
+    }
+    // X may grow by the steps' factors where A is too small to hold it back
+    const int storage = SCALE_X_LOG - min(down, 9), up = e + storage, up0 = max(-126, min(126, up));
+    const double s2 = ldexp(1.0, -2 * storage - 2 * down);
+    f[kFactorA0] = static_cast<float>(s2 * rest * rest);
+    f[kFactorA] = static_cast<float>(s2);
+    f[kFactorX0] = static_cast<float>(rest);
+    f[kFactorOut] = static_cast<float>(ldexp(1.0, -storage - down));
+    f[kFactorUp0] = ldexpf(1.0f, up0);
+    f[kFactorUp1] = ldexpf(1.0f, max(-126, min(126, up - up0)));
+}
+
+// Sums of squares of the rows of a part of a matrix.  A thread adds in FP32, the
+// threads in FP64.  Where squares would leave FP32 (largest magnitude above 2^50
+// or below 2^-40) the part is summed again, scaled by a power of two.  A matrix
+// of one part has its factors written here.
+template <typename T>
+__global__ void __launch_bounds__(NORM_THREADS)
+    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, float eps,
+                double *parts, float *factors)
+{
+    __shared__ double sums[NORM_THREADS / 32];
+    __shared__ float tops[NORM_THREADS / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long b = blockIdx.x / num_parts;
+    const int part = static_cast<int>(blockIdx.x - b * num_parts);
+    const int per = (rows + num_parts - 1) / num_parts;
+    const int r0 = min(rows, part * per), r1 = min(rows, r0 + per);
+    const T *base = g + b * stride;
+    float scale = 1.0f;
+    for (int pass = 0;; ++pass) {
+        float top = 0.0f;
+        double total = 0.0;
+        for (int r = r0 + warp; r < r1; r += NORM_THREADS / 32) {
+            const T *row = base + r * ldg;
+            for (int c0 = 0; c0 < cols; c0 += 32 * 64) {  // 64 additions in FP32 at a time
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const int c1 = min(cols, c0 + 32 * 64);
+#pragma unroll 4
+                for (int c = c0 + lane; c < c1; c += 128) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + 32 * k < c1) {
+                            const float x = to_f32(row[c + 32 * k]) * scale;
+                            top = fmaxf(top, fabsf(x));
+                            s[k] = fmaf(x, x, s[k]);
+                        }
+                }
+                total += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, d);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        }
+        if (lane == 0) {
+            sums[warp] = total;
+            tops[warp] = top;
+        }
+        __syncthreads();
+        total = 0.0;
+        top = 0.0f;
+        for (int w = 0; w < NORM_THREADS / 32; ++w) {
+            total += sums[w];
+            top = fmaxf(top, tops[w]);
+        }
+        __syncthreads();
+        const bool again = pass == 0 && top > 0.0f && top < INFINITY && (top > 0x1p50f || top < 0x1p-40f);
+        if (!again) {
+            total /= static_cast<double>(scale) * scale;
+            if (threadIdx.x == 0 && num_parts == 1) write_factors(sqrt(total), eps, factors + b * FACTORS);
+            if (threadIdx.x == 0 && num_parts > 1) parts[b * num_parts + part] = total;
+            return;
+        }
+        int e;
+        frexpf(top, &e);
+        scale = ldexpf(1.0f, max(-126, min(126, -e)));
+    }
+}
+
+__global__ void factors_kernel(const double *parts, int num_parts, float eps, float *factors)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long b = blockIdx.x;
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < num_parts; k += 32) sum += parts[b * num_parts + k];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (threadIdx.x == 0) write_factors(sqrt(sum), eps, factors + b * FACTORS);
+}
+
+// X in two FP16 numbers from G, turned where rows > cols.  A CTA takes 64 x 64
+// elements.
+template <typename T>
+__global__ void __launch_bounds__(NORM_THREADS)
+    start_kernel(const T *g, long long ldg, long long stride, int turned, int m, int n, int ldn, int tiles_j, int tiles,
+                 __half *x0, __half *x1, const float *factors)
+{
+    __shared__ float tile[64][65];
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long b = blockIdx.x / tiles;
+    const int t = static_cast<int>(blockIdx.x - b * tiles);
+    const int i0 = t / tiles_j * 64, j0 = t % tiles_j * 64;
+    const float s0 = factors[b * FACTORS + kFactorUp0], s1 = factors[b * FACTORS + kFactorUp1];
+    const T *base = g + b * stride;
+    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+#pragma unroll
+    for (int k = r; k < 64; k += NORM_THREADS / 64) {
+        float v = 0.0f;
+        if (turned) {
+            if (j0 + k < n && i0 + c < m) v = to_f32(base[(j0 + k) * ldg + i0 + c]);
+            tile[c][k] = v * s0 * s1;
+        } else {
+            if (i0 + k < m && j0 + c < n) v = to_f32(base[(i0 + k) * ldg + j0 + c]);
+            tile[k][c] = v * s0 * s1;
+        }
+    }
+    __syncthreads();
+    const int c2 = (threadIdx.x & 31) * 2;
+#pragma unroll
+    for (int k = threadIdx.x >> 5; k < 64; k += NORM_THREADS / 32)
+        if (i0 + k < m) {
+            const float a = tile[k][c2], z = tile[k][c2 + 1];
+            const __half h0 = __float2half_rn(a), h1 = __float2half_rn(z);
+            const long long at = (b * m + i0 + k) * ldn + j0 + c2;
+            *reinterpret_cast<uint32_t *>(x0 + at) = pack(h0, h1);
+            if (x1)
+                *reinterpret_cast<uint32_t *>(x1 + at) =
+                    pack(__float2half_rn(a - __half2float(h0)), __float2half_rn(z - __half2float(h1)));
+        }
+}
+
+template <int CG, bool SPLIT, bool XSTEP>
+cudaError_t launch_one(const CUtensorMap (&maps)[4], const Params &p, int grid, cudaStream_t stream)
+{
+    return launch_pdl(ortho_kernel<CG, SPLIT, XSTEP>, grid, THREADS, SMEM_MAX, stream, CG, maps[0], maps[1], maps[2],
+                      maps[3], p);
+}
+
+int64_t product_tiles(int step, int ctas, int bn, int64_t m, int64_t n)
+{
+    const int64_t bm = ctas * BP, ti = (m + bm - 1) / bm;
+    if (step == kOrthoX) return ti * ((n + bn - 1) / bn);
+    return std::max<int64_t>(1, bm / bn) * (ti * (ti + 1) / 2);
+}
+
+}  // namespace
+
+size_t ortho_bytes(int64_t m, int64_t n, bool split)
+{
+    const int64_t ldm = (m + 63) / 64 * 64, ldn = (n + 63) / 64 * 64;
+    const int64_t planes = split ? 2 : 1;
+    return static_cast<size_t>(4 * m * ldn * 2 + 2 * planes * m * ldm * 2 + 2 * ldm * 4 + ORTHO_PARTS * 8 + ORTHO_FACTORS * 4);
+}
+
+void ortho_layout(OrthoBuffers &o, uint8_t *base, bool split)
+{
+    const size_t xs = static_cast<size_t>(o.batch) * o.m * o.ldn * 2, as = static_cast<size_t>(o.batch) * o.m * o.ldm * 2;
+    const auto take = [&](size_t bytes) {  // whole 256 bytes
+        uint8_t *at = base;
+        base += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    for (auto &x : o.x)
+        for (auto &plane : x) plane = take(xs);
+    for (int pl = 0; pl < (split ? 2 : 1); ++pl) {
+        o.a[pl] = take(as);
+        o.b[pl] = take(as);
+    }
+    o.da = reinterpret_cast<float *>(take(static_cast<size_t>(o.batch) * o.ldm * 4));
+    o.db = reinterpret_cast<float *>(take(static_cast<size_t>(o.batch) * o.ldm * 4));
+    o.parts = reinterpret_cast<double *>(take(static_cast<size_t>(o.batch) * ORTHO_PARTS * 8));
+    o.factors = reinterpret_cast<float *>(take(static_cast<size_t>(o.batch) * ORTHO_FACTORS * 4));
+}
+
+cudaError_t prepare_ortho()
+{
+    cudaError_t e = kernel_ready<norm_kernel<float>>(0);
+    if (e == cudaSuccess) e = kernel_ready<norm_kernel<__nv_bfloat16>>(0);
+    if (e == cudaSuccess) e = kernel_ready<factors_kernel>(0);
+    if (e == cudaSuccess) e = kernel_ready<start_kernel<float>>(0);
+    if (e == cudaSuccess) e = kernel_ready<start_kernel<__nv_bfloat16>>(0);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, false, false>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, false, true>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, true, false>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, true, true>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, false, false>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, false, true>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, true, false>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, true, true>>(SMEM_MAX);
+    return e;
+}
+
+cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, cudaStream_t stream,
+                               int *launches)
+{
+    // one part up to 16384 elements: a launch less for small matrices
+    const int64_t size = int64_t{u.rows} * u.cols;
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ORTHO_PARTS, size / 16384)));
+    const __nv_bfloat16 *gb = static_cast<const __nv_bfloat16 *>(u.g);
+    const float *gf = static_cast<const float *>(u.g);
+    cudaError_t e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb,
+                                        u.ldg, u.stride_g, u.rows, u.cols, parts, u.eps, w.parts, w.factors)
+                           : launch_pdl(norm_kernel<float>, parts * w.batch, NORM_THREADS, 0, stream, 1, gf, u.ldg,
+                                        u.stride_g, u.rows, u.cols, parts, u.eps, w.parts, w.factors);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if (parts > 1) {
+        const double *sums = w.parts;
+        e = launch_pdl(factors_kernel, w.batch, 32, 0, stream, 1, sums, parts, u.eps, w.factors);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    const int tiles_j = (w.n + 63) / 64, tiles = (w.m + 63) / 64 * tiles_j;
+    const int grid = tiles * w.batch, turned = u.rows > u.cols;
+    __half *x0 = reinterpret_cast<__half *>(w.x[0][0]), *x1 = split ? reinterpret_cast<__half *>(w.x[0][1]) : nullptr;
+    const float *factors = w.factors;
+    e = u.bf16 ? launch_pdl(start_kernel<__nv_bfloat16>, grid, NORM_THREADS, 0, stream, 1, gb, u.ldg, u.stride_g,
+                            turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, factors)
+               : launch_pdl(start_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, turned, w.m,
+                            w.n, w.ldn, tiles_j, tiles, x0, x1, factors);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+// Estimated cycles of each tile, the least wins: a stage takes its MMA
+// instructions (bn / 2 cycles each from 64 columns on) or the arrival of its
+// bytes (55 a cycle), a tile its stages or its epilogue, a launch its waves.
+OrthoTile ortho_pick_tile(int step, bool split, int64_t batch, int64_t m, int64_t n, int sm_count)
+{
+    const int64_t kt = ((step == kOrthoA ? n : m) + BK - 1) / BK;
+    OrthoTile best;
+    double best_t = 0;
+    for (int ctas = 1; ctas <= 2; ++ctas)
+        for (int bn : {32, 64, 128, 256}) {
+            if (step != kOrthoX && ctas * BP % bn) continue;      // columns of tiles within their rows' blocks
+            if (step == kOrthoX && bn / ctas < 64) continue;      // whole 128-byte column chunks a CTA
+            const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
+            const int planes = split ? 2 : 1;
+            const double stage = std::max(4 * mma * (split ? 3 : 1), planes * (P_BYTES + bn / ctas * 128) / 55.0);
+            const double tile = static_cast<double>(kt) * stage, epi = 600 + bn * (step == kOrthoX ? 16.0 : 20.0);
+            const double fill = static_cast<double>(batch * product_tiles(step, ctas, bn, m, n) * ctas) / sm_count;
+            const double t = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) + (ctas > 1 ? 1500 : 0);
+            if (best_t == 0 || t < best_t) {
+                best_t = t;
+                best.ctas = ctas;
+                best.bn = bn;
+            }
+        }
+    return best;
+}
+
+cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, const OrthoProduct &r,
+                                 const CUtensorMap (&maps)[4], int sm_count, int max_ctas)
+{
+    const int planes = r.split ? 2 : 1, cg = r.tile.ctas;
+    Params p;
+    p.m = w.m;
+    p.n = w.n;
+    p.ldm = w.ldm;
+    p.ldn = w.ldn;
+    p.batch = w.batch;
+    p.mode = r.step;
+    p.bn = r.tile.bn;
+    p.tiles_i = (w.m + cg * BP - 1) / (cg * BP);
+    const int64_t tiles = product_tiles(r.step, cg, r.tile.bn, w.m, w.n);
+    if (tiles * w.batch > INT_MAX / 2) return cudaErrorInvalidValue;
+    p.tiles = static_cast<int>(tiles);
+    p.q_bytes = r.tile.bn / cg * 128;
+    p.stage_bytes = planes * (P_BYTES + p.q_bytes);
+    p.stages = std::min(MAX_STAGES, (SMEM_MAX - 1024 - NUM_BARS * 8 - 16) / p.stage_bytes);
+    p.kt = ((r.step == kOrthoA ? w.n : w.m) + BK - 1) / BK;
+    p.first = r.first;
+    p.last = r.last;
+    p.has_rest = r.split || !r.first;  // BF16 input is exact in FP16
+    p.ca = r.ca;
+    p.cb = r.cb;
+    p.cc = r.cc;
+    for (int pl = 0; pl < 2; ++pl) {
+        p.x[pl] = reinterpret_cast<const __half *>(w.x[r.from][pl]);
+        p.x_out[pl] = reinterpret_cast<__half *>(w.x[r.from ^ 1][pl]);
+        p.a[pl] = reinterpret_cast<__half *>(w.a[pl]);
+        p.b[pl] = reinterpret_cast<__half *>(w.b[pl]);
+    }
+    p.da = w.da;
+    p.db = w.db;
+    p.factors = w.factors;
+    p.o = u.o;
+    p.ldo = u.ldo;
+    p.stride_o = u.stride_o;
+    p.turned = u.rows > u.cols;
+    p.o_bf16 = u.bf16;
+    const int es = u.bf16 ? 2 : 4;
+    p.o_vec = reinterpret_cast<uintptr_t>(u.o) % 16 == 0 && (u.ldo * es) % 16 == 0 && (u.stride_o * es) % 16 == 0;
+    p.status = r.status;
+    p.timeout_ns = r.timeout_ns;
+    p.debug_drop = r.debug_drop;
+    const int64_t slots = std::max(1, (max_ctas > 0 ? std::min(max_ctas, sm_count) : sm_count) / cg);
+    const int grid = static_cast<int>(cg * std::min<int64_t>(tiles * w.batch, slots));
+    const bool x = r.step == kOrthoX;
+    if (cg == 2) {
+        if (r.split) return x ? launch_one<2, true, true>(maps, p, grid, r.stream) : launch_one<2, true, false>(maps, p, grid, r.stream);
+        return x ? launch_one<2, false, true>(maps, p, grid, r.stream) : launch_one<2, false, false>(maps, p, grid, r.stream);
+    }
+    if (r.split) return x ? launch_one<1, true, true>(maps, p, grid, r.stream) : launch_one<1, true, false>(maps, p, grid, r.stream);
+    return x ? launch_one<1, false, true>(maps, p, grid, r.stream) : launch_one<1, false, false>(maps, p, grid, r.stream);
+}
+
+}  // namespace dg

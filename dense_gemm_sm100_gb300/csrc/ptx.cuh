@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 namespace dg {
 
@@ -19,6 +20,7 @@ enum WaitSite : int {
     kWaitDrain = 6,
     kWaitScaleEmpty = 7,
     kWaitMmaScale = 8,
+    kWaitConvFull = 9,
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
@@ -586,6 +588,19 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&v)[1
 __device__ __forceinline__ void tmem_wait_ld()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// 16 integers of 8 bits to FP16, in order: the byte with its sign bit flipped, put
+// below the exponent of 1024, reads 1152 more than the value.
+__device__ __forceinline__ void i8_to_f16(uint4 b, uint4 &lo, uint4 &hi)
+{
+    const auto two = [](uint32_t w, uint32_t sel) {
+        const uint32_t biased = __byte_perm(w ^ 0x80808080u, 0x64646464u, sel);  // 1024 + 128 + x
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&biased), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    lo = make_uint4(two(b.x, 0x4140), two(b.x, 0x4342), two(b.y, 0x4140), two(b.y, 0x4342));
+    hi = make_uint4(two(b.z, 0x4140), two(b.z, 0x4342), two(b.w, 0x4140), two(b.w, 0x4342));
 }
 
 // Shared-memory matrix descriptor (tcgen05): start address, leading- and

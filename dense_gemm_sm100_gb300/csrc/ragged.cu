@@ -1,6 +1,7 @@
 // Grouped tensor-core products for sm_103a (tcgen05.mma): C_g = A_g · B_g over
 // ragged row groups, C_g = A_g^T · B_g over ragged contractions, with BF16,
-// TF32 or microscaled 4-bit (E2M1 x E8M0) operands and FP32 accumulation.
+// TF32, microscaled 4-bit (E2M1 x E8M0) or 8-bit integer operands and FP32
+// accumulation.
 //
 // Orientation.  The MMA's M side (128 tensor-memory lanes per CTA) carries the
 // index that runs along a row of C ("P", the columns of C), its N side the
@@ -18,7 +19,19 @@
 // overlaps the next tile's main loop; two warps a scheduler, because one warp
 // issues every fourth cycle at best: 4.6 us for a 128 x 256 tile with four
 // warps, which set the pace below K = 4096); for 4-bit operands warps 10-12
-// regroup the block scales.
+// regroup the block scales; for 8-bit operands warps 10-17 convert them.
+//
+// 8-bit integers.  The tensor cores of this GPU multiply FP16 far faster than
+// integers, and every value of -128 .. 127 is an FP16 number, every product and
+// every sum of 1024 products an FP32 number: the accumulator holds the integer
+// sum exactly as long as it fits 24 bits (at any K up to 1024; FP32 results add
+// segments of 768).  TMA fetches the bytes; a converter warp turns 16 bytes a
+// lane into 16 FP16 values (the byte with its sign bit flipped, put below the
+// exponent of 1024, is 1152 more than the value), writes them in the swizzled
+// layout of the MMA, and hands the stage on.  Eight warps in two teams, each
+// with every other stage of the ring (an even number of stages).  kRaggedI8Wide finds its operands in FP16 (a product
+// with many rows converts once, not once a tile, and runs on CTA pairs).  In the
+// epilogue a lane multiplies by its column's scale and each row's.
 //
 // Block scales.  A row's scales are contiguous bytes; the tensor core wants,
 // for 128 rows and 128 elements of K, one 4-byte word per row, row i in lane
@@ -86,6 +99,7 @@ constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 2 + 2 + 1;
+constexpr int NUM_BARS_I8 = NUM_BARS + MAX_STAGES;
 // Accumulators at tensor-memory columns 0 and ACC1.  For 4-bit operands the
 // scales of two stages live at SF_COL, which leaves two accumulators of 224
 // rows: 157 us for 8192 x 14336 x 4096, against 165 us with tiles of 256 rows
@@ -97,6 +111,9 @@ constexpr int SF_PART = 1024;    // a stage's words of 128 rows
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_BYTES = EPI_WARPS * 2048;  // a warp's staging: 16 x 32 FP32, or BF16 in half of it
 constexpr int WARPS = 2 + EPI_WARPS, WARPS_MX = WARPS + 3;
+constexpr int CONV_TEAMS = 2, CONV_WARPS = 4;  // converter warps of a team
+constexpr int WARPS_I8 = WARPS + CONV_TEAMS * CONV_WARPS;
+constexpr int P_RAW = BP * 64;  // 128 rows of P x 64 bytes of K, as fetched
 constexpr int SMEM_MAX = 227 * 1024;
 
 struct Params {
@@ -112,6 +129,7 @@ struct Params {
     const uint8_t *scale_p, *scale_q;
     long long lds_p, lds_q;
     int blocks;
+    const float *row_scale_p, *row_scale_q;  // 8-bit operands
     int *status;
     unsigned long long timeout_ns;
     int debug_drop;
@@ -252,18 +270,26 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
     return RAGGED_K ? p.bn : (t.qn + G - 1) / G * G;
 }
 
+__host__ __device__ constexpr bool is_i8(int kind) { return kind == kRaggedI8 || kind == kRaggedI8Wide; }
+__host__ __device__ constexpr int warps_of(int kind) { return kind == kRaggedMx4 ? WARPS_MX : kind == kRaggedI8 ? WARPS_I8 : WARPS; }
+__host__ __device__ constexpr int bar_bytes(int kind) { return 8 * (kind == kRaggedI8 ? NUM_BARS_I8 : NUM_BARS); }
+// Behind the barriers: the tensor-memory address, the abort flag, a sum a warp.
+constexpr int tail_bytes(int kind) { return 16 + (kind == kRaggedI8 ? 80 : 64); }
+
 // Stages of a segment of a long FP32 sum.
 __host__ __device__ constexpr int seg_stages(int kind) { return kind == kRaggedTf32 ? 8 : 12; }
 
 // SUM: long FP32 sums (see above).
 template <int KIND, int CG, bool P_MN, bool RAGGED_K, bool SUM>
-__global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 1)
+__global__ void __launch_bounds__(32 * warps_of(KIND), 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
+    constexpr bool I8 = is_i8(KIND), CONV = KIND == kRaggedI8;
     constexpr int SEG = seg_stages(KIND);
-    constexpr int THREADS = 32 * (MX ? WARPS_MX : WARPS);
-    constexpr int ES = KIND == kRaggedBf16 ? 2 : 4;                 // bytes an element (not for 4-bit)
+    constexpr int THREADS = 32 * warps_of(KIND);
+    constexpr int ES = KIND == kRaggedBf16 || I8 ? 2 : 4;           // bytes an element as multiplied (not for 4-bit)
+    constexpr int SUM_UNITS = CONV ? 4 : 8;                         // 16-row units of a tile that a warp adds up
     constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
     constexpr int K_STEPS = 4;                                      // MMA instructions of a stage, 32 bytes of K each
     constexpr int CHUNK = 128 / ES;                                 // MN-major: elements of a 128-byte row
@@ -274,7 +300,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     // Instruction descriptor without N.  BF16 / TF32: FP32 accumulator, operand
     // formats, major-ness; 4-bit: E2M1 formats and E8M0 scales (the scale ids
     // are added per instruction).
-    constexpr uint32_t FMT = KIND == kRaggedBf16 ? 1u : 2u;
+    constexpr uint32_t FMT = I8 ? 0u : KIND == kRaggedBf16 ? 1u : 2u;
     constexpr uint32_t IDESC = MX ? (1u << 7) | (1u << 10) | (1u << 23) | (static_cast<uint32_t>((CG * BP) >> 4) << 24)
                                   : (1u << 4) | (FMT << 7) | (FMT << 10) | ((P_MN ? 1u : 0u) << 15) |
                                         ((Q_MN ? 1u : 0u) << 16) | (static_cast<uint32_t>((CG * BP) >> 4) << 24);
@@ -297,7 +323,8 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
     const uint32_t sready_bar = tempty_bar + 16;            // [2], scale slot filled, used in the even CTA
     const uint32_t sfree_bar = sready_bar + 16;             // [2], scale slot read
     const uint32_t drain_bar = sfree_bar + 16;
-    uint8_t *tail = smem + ring + 2 * sf_slot + EPI_BYTES + p.table_bytes + NUM_BARS * 8;
+    const uint32_t conv_bar = drain_bar + 8;                // [stages], stage converted (kRaggedI8 only)
+    uint8_t *tail = smem + ring + 2 * sf_slot + EPI_BYTES + p.table_bytes + bar_bytes(KIND);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
     int *warp_sum = reinterpret_cast<int *>(tail + 16);
@@ -317,6 +344,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar + 8 * s, 1);
             mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
+            if (CONV) mbar_init(conv_bar + 8 * s, CONV_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
@@ -361,7 +389,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             const int q_cta = p.bn / CG;  // rows of Q this CTA stages
-            const uint32_t tx = static_cast<uint32_t>(CG * (P_BYTES + p.q_bytes));
+            const uint32_t tx = static_cast<uint32_t>(CONV ? P_RAW + p.q_bytes / 2 : CG * (P_BYTES + p.q_bytes));
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
@@ -419,6 +447,12 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                         continue;
                     }
                     const int kx = (t.ks + kt) * (MX ? 128 : BK);  // 4-bit views count bytes
+                    if (CONV) {  // the bytes lie behind the stage's converted operands
+                        const uint32_t raw = q_st + p.q_bytes;
+                        tma_load_3d(raw, &tmP, fb, kx, p0, t.g);
+                        tma_load_2d(raw + P_RAW, &tmQ, fb, kx, qx);
+                        continue;
+                    }
                     if (P_MN) {
                         if (p.p_chunks) {
                             if (CG == 2)
@@ -483,7 +517,8 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                     tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + abuf * acc1;
                     for (int kt = seg0; kt < seg1; ++kt, ++it) {
-                        if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
+                        if (!mbar_wait_warp((CONV ? conv_bar : full_bar) + 8 * s, ph, abort_flag, p.status, kWaitMmaFull,
+                                            p.timeout_ns)) {
                             ok = false;
                             break;
                         }
@@ -534,7 +569,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                                         tc_mma_mx4_pair(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
                                     else
                                         tc_mma_mx4(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
-                                } else if (KIND == kRaggedBf16) {
+                                } else if (KIND == kRaggedBf16 || I8) {
                                     if (CG == 2)
                                         tc_mma_f16_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
                                     else
@@ -620,6 +655,8 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             const long long first_row = RAGGED_K ? t.q0 : static_cast<long long>(t.lo) + t.q0;
             const long long base = (RAGGED_K ? t.g * p.stride_c : 0) + first_row * p.ldc + col0;
             const int chunks = (t.qn + 31) / 32;
+            float col_scale = 0.0f;
+            if (I8 && p.K > 0 && col0 + lane < p.P) col_scale = p.row_scale_p[static_cast<long long>(t.g) * p.P + col0 + lane];
             const auto await = [&]() {
                 const uint32_t abuf = acc_it & 1u;
                 ok = mbar_wait_warp(tfull_bar + 8 * abuf, (acc_it >> 1) & 1u, abort_flag, p.status, kWaitEpiTmemFull,
@@ -653,7 +690,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 }
             };
             // 16 rows of C from unit * 16 on, the warp's 32 columns.
-            const auto store = [&](int unit, const uint32_t(&v)[16]) {
+            const auto store = [&](int unit, uint32_t(&v)[16]) {
                 if (CG == 1 && p.split > 1) {
                     // this CTA's part of the sum, [row][128 columns], where the ring was
 #pragma unroll
@@ -662,6 +699,14 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 }
                 const int n = t.qn - unit * 16;  // rows left
                 if (n <= 0 || col0 >= p.P) return;
+                if (I8 && p.K > 0) {
+                    const float row_scale =
+                        (lane & 15) < n ? p.row_scale_q[first_row + unit * 16 + (lane & 15)] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __float_as_uint(__uint_as_float(v[j]) * __shfl_sync(0xffffffffu, row_scale, j) *
+                                               col_scale);
+                }
                 const long long at = base + static_cast<long long>(unit * 16) * p.ldc;
                 if (!SUM && p.c_vec && p.out_bf16) {
                     // words of two rows' neighbours, [row pair][column], odd
@@ -723,11 +768,11 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
             const int mine = (chunks + 1 - half) / 2;
             const auto unit_of = [&](int k) { return 4 * (k >> 1) + 2 * half + (k & 1); };
             if (SUM) {
-                uint32_t sum[8][16];
+                uint32_t sum[SUM_UNITS][16];
                 for (int seg0 = 0; seg0 == 0 || seg0 < t.kt; seg0 += SEG) {
                     if (!await()) break;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < SUM_UNITS; ++k) {
                         if (k >= 2 * mine) break;
                         if (seg0 == 0) {
                             load(unit_of(k), sum[k]);
@@ -745,7 +790,7 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < SUM_UNITS; ++k)
                     if (k < 2 * mine) store(unit_of(k), sum[k]);
             } else {
                 if (!await()) break;
@@ -765,6 +810,45 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                 }
             }
             __syncwarp();
+        }
+    } else if (CONV) {
+        // ------------------------------------------------------ conversion
+        // Item i of a stage: 16 bytes of K of row i / 4 of P, then of Q; they
+        // lie behind one another.  A quarter of a warp stores two rows' even (or
+        // odd) 16-byte pieces, which the swizzle spreads over all banks.
+        const int team = (warp - WARPS) / CONV_WARPS;
+        const int first = threadIdx.x - 32 * (WARPS + team * CONV_WARPS);
+        uint32_t it = 0, s = 0, ph = 0;
+        bool ok = true;
+        for (int u = first_unit; ok && u < num_units; u += unit_step) {
+            const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
+            const int items = 4 * (BP + mma_n<CG, RAGGED_K>(p, t));
+            for (int kt = 0; kt < t.kt; ++kt, ++it) {
+                if (it % CONV_TEAMS == static_cast<uint32_t>(team)) {
+                    if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitConvFull, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t p_st = sbase + s * p.stage_bytes;
+                    const uint32_t raw = p_st + P_BYTES + p.q_bytes;
+#pragma unroll 4
+                    for (int i = first; i < items; i += 32 * CONV_WARPS) {
+                        uint4 lo, hi;
+                        i8_to_f16(lds_u4(raw + i * 16), lo, hi);
+                        const uint32_t row = i >> 2, piece = (i & 3) * 2;
+                        const uint32_t at = p_st + row * 128;  // Q's rows follow P's
+                        sts_u4(at + ((piece ^ (row & 7)) * 16), lo);
+                        sts_u4(at + (((piece + 1) ^ (row & 7)) * 16), hi);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(conv_bar + 8 * s);
+                }
+                if (++s == static_cast<uint32_t>(p.stages)) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
         }
     } else if (MX && p.K > 0 && (warp - 2 - EPI_WARPS - 1) * 128 < p.bn) {
         // ------------------------------------------------------ block scales
@@ -863,6 +947,15 @@ __global__ void __launch_bounds__(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS), 
                     x.w += y.w;
                 }
                 const long long at = (RAGGED_K ? t.g * p.stride_c : 0) + (first_row + j) * p.ldc + col;
+                if (I8 && p.K > 0) {
+                    const float rs = p.row_scale_q[first_row + j];
+                    const float *cs = p.row_scale_p + static_cast<long long>(t.g) * p.P + col;
+                    const int left = p.P - col;
+                    x.x = x.x * rs * cs[0];
+                    if (left > 1) x.y = x.y * rs * cs[1];
+                    if (left > 2) x.z = x.z * rs * cs[2];
+                    if (left > 3) x.w = x.w * rs * cs[3];
+                }
                 const float v[4] = {x.x, x.y, x.z, x.w};
                 if (p.out_bf16) {
                     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.C) + at;
@@ -945,7 +1038,7 @@ cudaError_t launch_one(const CUtensorMap &tmP, const CUtensorMap &tmQ, const Par
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(32 * (KIND == kRaggedMx4 ? WARPS_MX : WARPS));
+    cfg.blockDim = dim3(32 * warps_of(KIND));
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -975,6 +1068,12 @@ cudaError_t dispatch(int kind, int ctas, bool p_mn, bool ragged_k, bool sum, con
     if (kind == kRaggedMx4)
         return ctas == 2 ? op.template apply<kRaggedMx4, 2, false, false, false>()
                          : op.template apply<kRaggedMx4, 1, false, false, false>();
+    if (kind == kRaggedI8)
+        return sum ? op.template apply<kRaggedI8, 1, false, false, true>()
+                   : op.template apply<kRaggedI8, 1, false, false, false>();
+    if (kind == kRaggedI8Wide)
+        return sum ? op.template apply<kRaggedI8Wide, 2, false, false, true>()
+                   : op.template apply<kRaggedI8Wide, 2, false, false, false>();
     if (kind == kRaggedTf32)
         return ctas == 2 ? dispatch_form<kRaggedTf32, 2>(p_mn, ragged_k, sum, op)
                          : dispatch_form<kRaggedTf32, 1>(p_mn, ragged_k, sum, op);
@@ -1051,6 +1150,15 @@ cudaError_t prepare_ragged()
     return e;
 }
 
+cudaError_t prepare_ragged_i8()
+{
+    cudaError_t e = prepare_ragged();  // the clusters that run at the same time
+    for (int kind : {kRaggedI8, kRaggedI8Wide})
+        for (bool sum : {false, true})
+            if (e == cudaSuccess) e = dispatch(kind, 1, false, false, sum, SetAttrs());
+    return e;
+}
+
 bool ragged_tile_ok(int split, int ctas, int bn)
 {
     if (!(bn == 32 || bn == 64 || bn == 128 || bn == 224 || bn == 256)) return false;
@@ -1070,9 +1178,10 @@ bool ragged_tile_ok(int split, int ctas, int bn)
 // is no multiple of the chunk): 13 + 10 us for the TF32 gradients of 2011 rows and
 // 13 experts of 1020 x 520, which take 24 + 27.
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
-                            int sm_count, bool may_split)
+                            int sm_count, bool may_split, double *cycles)
 {
-    const double es = kind == kRaggedMx4 ? 17.0 / 32 : kind == kRaggedTf32 ? 4 : 2, eo = ragged_k ? 4 : 2;
+    const double es = kind == kRaggedMx4 ? 17.0 / 32 : kind == kRaggedTf32 ? 4 : kind == kRaggedI8 ? 1 : 2;
+    const double eo = ragged_k ? 4 : 2;
     const double busy = static_cast<double>(std::max<int64_t>(1, std::min<int64_t>(groups, rows)));
     const double per_group = static_cast<double>(rows) / busy;
     const int bk = ragged_bk(kind);
@@ -1086,12 +1195,16 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
         for (int bn : {32, 64, 128, kind == kRaggedMx4 ? ACC1_MX : 256})
             for (int split = 1; split <= 8; split *= 2) {
                 if (ragged_k && bn < 128) continue;  // whole 128-byte column chunks per CTA
+                if (kind == kRaggedI8 && (ctas > 1 || bn > 128)) continue;
+                if (kind == kRaggedI8Wide && ctas < 2) continue;
                 const int64_t units = max_units(ragged_k, rows, groups, P, Q, ctas, bn);
                 if (split > 1 && (!may_split || ctas > 1 || bn > 128 || units > max_clusters(split) || units * split > sm_count ||
                                   kt < 4 * split))
                     continue;
                 const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
-                const double stage = std::max(4 * mma, (P_BYTES + bn / ctas * 128) / 55.0) * (kind == kRaggedMx4 ? 1.1 : 1);
+                const double arrival = (P_BYTES + bn / ctas * 128) / 55.0 * (kind == kRaggedI8 ? 0.5 : 1);
+                const double convert = kind == kRaggedI8 ? (bn == 32 ? 650 : 870) : 0;
+                const double stage = std::max({4 * mma, arrival, convert}) * (kind == kRaggedMx4 ? 1.1 : 1);
                 const double tiles_p = static_cast<double>((P + ctas * BP - 1) / (ctas * BP));
                 const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
                                        : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
@@ -1111,6 +1224,7 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
                     best.split = split;
                 }
             }
+    if (cycles) *cycles = best_t;
     return best;
 }
 
@@ -1129,12 +1243,15 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
     p.split = t.split;
     p.q_bytes = t.bn / t.ctas * 128;
-    p.stage_bytes = P_BYTES + p.q_bytes;
+    p.stage_bytes = P_BYTES + p.q_bytes + (kind == kRaggedI8 ? P_RAW + p.q_bytes / 2 : 0);
     p.sf_parts = 1 + (t.bn + 127) / 128;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
     const int sf_bytes = kind == kRaggedMx4 ? 2 * SUP * p.sf_parts * SF_PART : 0;
-    const int fixed = 1024 + sf_bytes + EPI_BYTES + p.table_bytes + NUM_BARS * 8 + 16 + 64;
+    const int fixed = 1024 + sf_bytes + EPI_BYTES + p.table_bytes + bar_bytes(kind) + tail_bytes(kind);
     p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);
+    // A team of converter warps keeps to its own ring stages: it sees all of their
+    // phases, and none of the others'.
+    if (kind == kRaggedI8) p.stages -= p.stages % CONV_TEAMS;
     p.C = a.C;
     p.ldc = a.ldc;
     p.stride_c = a.stride_c;
@@ -1150,6 +1267,8 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.lds_p = a.lds_p;
     p.lds_q = a.lds_q;
     p.blocks = (a.K + kRaggedBlock - 1) / kRaggedBlock;
+    p.row_scale_p = a.row_scale_p;
+    p.row_scale_q = a.row_scale_q;
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
     p.debug_drop = a.debug_drop;

@@ -9,8 +9,11 @@
 
 namespace dg {
 
-// Operand kinds of the grouped kernel.
-enum RaggedKind : int { kRaggedBf16 = 0, kRaggedTf32 = 1, kRaggedMx4 = 2 };
+// Operand kinds of the grouped kernel.  8-bit integers are multiplied as FP16,
+// in which they are exact: kRaggedI8 converts both operands on their way through
+// shared memory (one CTA a tile), kRaggedI8Wide takes operands converted before
+// (CTA pairs).
+enum RaggedKind : int { kRaggedBf16 = 0, kRaggedTf32 = 1, kRaggedMx4 = 2, kRaggedI8 = 3, kRaggedI8Wide = 4 };
 
 // The kernel computes, for every group g, D[p][q] = sum_k P_g[p][k] Q_g[q][k]
 // and stores D[p][q] at C[row(q) * ldc + p]: P is the operand whose index runs
@@ -36,6 +39,8 @@ struct RaggedArgs {
     // kRaggedMx4: scale bytes of B (rows of P, groups one after another) and A
     const uint8_t *scale_p = nullptr, *scale_q = nullptr;
     int64_t lds_p = 0, lds_q = 0;
+    // 8-bit kinds: a scale for every row of B (groups one after another) and of A
+    const float *row_scale_p = nullptr, *row_scale_q = nullptr;
     int *status = nullptr;
     uint64_t timeout_ns = 0;
     int debug_drop = 0;
@@ -58,16 +63,18 @@ constexpr int kRaggedP = 128;    // rows of P one CTA stages
 constexpr int kRaggedBlock = 32;  // elements that share a 4-bit scale
 
 bool ragged_tile_ok(int split, int ctas, int bn);  // split 0: none
+// cycles (may be null): the estimated time that the choice is made by
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
-                            int sm_count, bool may_split);
+                            int sm_count, bool may_split, double *cycles = nullptr);
 
-// K elements of one ring stage (128 bytes of a K-major row).
+// K elements of one ring stage (128 bytes of a K-major row as it is multiplied).
 inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : 64; }
 
 // Sets the kernels' attributes on the current device: once per handle, before
 // its first product (1.5 ms for the first handle of a process, whose creation
 // it would hold up for callers who never use these kernels).
 cudaError_t prepare_ragged();
+cudaError_t prepare_ragged_i8();  // the same for 8-bit operands
 // tmP / tmQ: the operand views of ragged_api.cu.
 cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &t, const CUtensorMap &tmP,
                           const CUtensorMap &tmQ, const RaggedArgs &a, int sm_count, int max_ctas);
@@ -82,6 +89,17 @@ cudaError_t launch_nan_on_error(const RaggedArgs &a, int sm_count);
 cudaError_t launch_mx4_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
                                 int64_t stride, bool src_bf16, uint8_t *codes, int64_t ldq, uint8_t *scales,
                                 int64_t lds, int sm_count, cudaStream_t stream);
+// 8-bit integers (i8.cu): batch * rows output rows of codes, one scale a row.
+cudaError_t launch_i8_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
+                               int64_t stride, bool src_bf16, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                               cudaStream_t stream);
+cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
+                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, cudaStream_t stream);
+// rows_a rows of A's codes and rows_b of B's as FP16, at pitches of K rounded up
+// to 16; with offsets only B's rows of groups (rows_per each) that own rows.
+cudaError_t launch_i8_widen(const int8_t *a, int64_t lda, int64_t rows_a, const int8_t *b, int64_t ldb, int64_t rows_b,
+                            int64_t K, void *a16, void *b16, const int64_t *offsets, int64_t rows_per, int sm_count,
+                            cudaStream_t stream);
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
                                   int64_t lds, void *dst, int64_t ldd, bool dst_bf16, int sm_count,
                                   cudaStream_t stream);

@@ -1,5 +1,6 @@
-// The C ABI of include/gemm_grouped.h and include/gemm_mx4.h: argument checks,
-// re-packing of operands TMA cannot address, tensor-map encoding and dispatch.
+// The C ABI of include/gemm_grouped.h, include/gemm_mx4.h and include/gemm_i8.h:
+// argument checks, re-packing of operands TMA cannot address, tensor-map
+// encoding and dispatch.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -10,12 +11,14 @@
 
 #include "../../include/gemm.h"
 #include "../../include/gemm_grouped.h"
+#include "../../include/gemm_i8.h"
 #include "../../include/gemm_mx4.h"
 #include "gemm_internal.h"
 #include "handle.h"
 #include "ragged.h"
 
 using dg::cuda_fail;
+using dg::encode;
 using dg::fail;
 using dg::kMaxDim;
 using dg::kMaxLd;
@@ -180,10 +183,11 @@ int check_mx4(int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t 
     return GEMM_OK;
 }
 
+// The source of a quantisation; `codes` checks what it is written to.
+template <typename Codes>
 int check_quantise(int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld, int64_t stride,
-                   int src_dtype, const void *codes, int64_t ldq, const void *scales, int64_t lds, std::string *why)
+                   int src_dtype, const Checker &bad, const Codes &codes)
 {
-    const Checker bad{why};
     if (layout != GEMM_B_ROW_MAJOR && layout != GEMM_B_COL_MAJOR)
         return bad(GEMM_ERR_INVALID, "layout must be GEMM_B_ROW_MAJOR or GEMM_B_COL_MAJOR");
     if (src_dtype != GEMM_F32 && src_dtype != GEMM_BF16)
@@ -201,13 +205,22 @@ int check_quantise(int layout, int64_t batch, int64_t rows, int64_t K, const voi
         return bad(GEMM_ERR_INVALID, "stride must reach past a matrix and stay within 2^37");
     if (reinterpret_cast<uintptr_t>(src) % (src_dtype == GEMM_BF16 ? 2 : 4))
         return bad(GEMM_ERR_ALIGNMENT, "src is not aligned to its element size");
-    return check_mx4_operand(bad, batch * rows, K, codes, ldq, scales, lds);
+    return codes();
 }
 
-int check_dequantise(int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales, int64_t lds,
-                     const void *dst, int64_t ldd, int dst_dtype, std::string *why)
+int check_quantise(int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld, int64_t stride,
+                   int src_dtype, const void *codes, int64_t ldq, const void *scales, int64_t lds, std::string *why)
 {
     const Checker bad{why};
+    return check_quantise(layout, batch, rows, K, src, ld, stride, src_dtype, bad,
+                          [&] { return check_mx4_operand(bad, batch * rows, K, codes, ldq, scales, lds); });
+}
+
+// The destination of a dequantisation, then what it is made from.
+template <typename Codes>
+int check_dequantise(int64_t rows, int64_t K, const void *dst, int64_t ldd, int dst_dtype, const Checker &bad,
+                     const Codes &codes)
+{
     if (dst_dtype != GEMM_F32 && dst_dtype != GEMM_BF16)
         return bad(GEMM_ERR_INVALID, "dst_dtype must be GEMM_F32 or GEMM_BF16");
     if (rows < 0 || K < 0 || rows > kMaxDim || K > kMaxDim)
@@ -218,30 +231,54 @@ int check_dequantise(int64_t rows, int64_t K, const void *codes, int64_t ldq, co
     if (beyond_memory(rows, ldd)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
     if (reinterpret_cast<uintptr_t>(dst) % (dst_dtype == GEMM_BF16 ? 2 : 4))
         return bad(GEMM_ERR_ALIGNMENT, "dst is not aligned to its element size");
-    return check_mx4_operand(bad, rows, K, codes, ldq, scales, lds);
+    return codes();
+}
+
+int check_dequantise(int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales, int64_t lds,
+                     const void *dst, int64_t ldd, int dst_dtype, std::string *why)
+{
+    const Checker bad{why};
+    return check_dequantise(rows, K, dst, ldd, dst_dtype, bad,
+                            [&] { return check_mx4_operand(bad, rows, K, codes, ldq, scales, lds); });
+}
+
+int check_i8_operand(const Checker &bad, int64_t rows, int64_t K, const void *codes, int64_t ldq, const void *scales)
+{
+    if (!codes || !scales) return bad(GEMM_ERR_INVALID, "codes or scales is NULL");
+    if (ldq < K || ldq > kMaxLd) return bad(GEMM_ERR_INVALID, "the code pitch must hold a row of codes");
+    if (reinterpret_cast<uintptr_t>(codes) % 16 || ldq % 16 || reinterpret_cast<uintptr_t>(scales) % 4)
+        return bad(GEMM_ERR_ALIGNMENT, "codes and their pitch must be multiples of 16 bytes, scales of 4");
+    if (beyond_memory(rows, ldq)) return bad(GEMM_ERR_INVALID, kBeyondMemory);
+    return GEMM_OK;
+}
+
+int check_i8(int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const void *ac, int64_t aq,
+             const void *as, const void *bc, int64_t bq, const void *bs, const void *C, int64_t ldc, int c_dtype,
+             bool grouped, std::string *why)
+{
+    const Checker bad{why};
+    int rc;
+    if (c_dtype != GEMM_F32 && c_dtype != GEMM_BF16)
+        return bad(GEMM_ERR_INVALID, "c_dtype must be GEMM_F32 or GEMM_BF16");
+    if (N < 0 || K < 0 || N > kMaxDim || K > kMaxDim) return bad(GEMM_ERR_INVALID, "N and K must be in 0..2^31 - 1025");
+    if (grouped) {
+        if ((rc = check_groups(bad, groups, rows, offsets))) return rc;
+    } else if (rows < 0 || rows > kMaxDim) {
+        return bad(GEMM_ERR_INVALID, "M must be in 0..2^31 - 1025");
+    }
+    if (rows == 0 || N == 0) return GEMM_OK;
+    if (groups * N > kMaxDim) return bad(GEMM_ERR_INVALID, "groups * N must be below 2^31 - 1024");
+    if (too_many_tiles(rows, groups, N)) return bad(GEMM_ERR_INVALID, "the product has 2^31 tiles or more");
+    if ((rc = check_c(bad, C, ldc, rows, N, c_dtype))) return rc;
+    if (K == 0) return GEMM_OK;
+    if ((rc = check_i8_operand(bad, rows, K, ac, aq, as))) return rc;
+    if ((rc = check_i8_operand(bad, groups * N, K, bc, bq, bs))) return rc;
+    if (groups > 1 && N * bq >= (int64_t{1} << 40))
+        return bad(GEMM_ERR_INVALID, "a group's matrix must span less than 2^40 bytes");
+    return GEMM_OK;
 }
 
 // ------------------------------------------------------------- tensor maps
-
-int encode(gemm_ctx *h, CUtensorMap *map, CUtensorMapDataType type, int rank, uintptr_t base, const int64_t *dims,
-           const int64_t *strides, const int *box, CUtensorMapSwizzle swizzle, const char *what)
-{
-    cuuint64_t d[5], st[4];
-    cuuint32_t b[5], es[5];
-    for (int i = 0; i < rank; ++i) {
-        d[i] = static_cast<cuuint64_t>(dims[i]);
-        b[i] = static_cast<cuuint32_t>(box[i]);
-        es[i] = 1;
-        if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]);
-    }
-    const CUresult r = dg::g_encode(map, type, static_cast<cuuint32_t>(rank), reinterpret_cast<void *>(base), d, st, b,
-                                    es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r == CUDA_SUCCESS) return GEMM_OK;
-    char msg[128];
-    std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), what);
-    return fail(h, GEMM_ERR_CUDA, msg);
-}
 
 CUtensorMapDataType float_type(int es)
 {
@@ -308,21 +345,25 @@ int encode_k_major(gemm_ctx *h, CUtensorMap *map, CUtensorMapDataType type, int 
     return encode(h, map, type, grouped ? 3 : 2, reinterpret_cast<uintptr_t>(base), dims, st, box, swizzle, what);
 }
 
-// The handle's first grouped or 4-bit product prepares the kernels; the call
-// may be captured, and loading them is no part of the graph.
-int prepare(gemm_ctx *h)
+// The handle's first grouped or 4-bit product prepares the kernels, its first
+// 8-bit one those for that; the call may be captured, and loading them is no part
+// of the graph.
+int prepare(gemm_ctx *h, bool i8 = false)
 {
-    if (h->ragged_ready) return GEMM_OK;
+    bool &ready = i8 ? h->i8_ready : h->ragged_ready;
+    if (ready) return GEMM_OK;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e == cudaSuccess) {
-        e = dg::prepare_ragged();
+        e = i8 ? dg::prepare_ragged_i8() : dg::prepare_ragged();
         cudaThreadExchangeStreamCaptureMode(&mode);
     }
     if (e != cudaSuccess) return cuda_fail(h, e, "preparing the grouped kernels");
-    h->ragged_ready = true;
+    ready = true;
     return GEMM_OK;
 }
+
+int usable_sms(const gemm_ctx *h) { return h->max_ctas > 0 ? std::min(h->max_ctas, h->sm_count) : h->sm_count; }
 
 dg::RaggedTile tile_for(const gemm_ctx *h, int kind, bool ragged_k, int64_t rows, int64_t groups, int64_t P,
                         int64_t Q, int64_t K)
@@ -336,8 +377,7 @@ dg::RaggedTile tile_for(const gemm_ctx *h, int kind, bool ragged_k, int64_t rows
         if (kind == dg::kRaggedMx4) t.bn = std::min(t.bn, 224);        // two accumulators beside the scales
         return t;
     }
-    const int sms = h->max_ctas > 0 ? std::min(h->max_ctas, h->sm_count) : h->sm_count;
-    return dg::ragged_pick_tile(kind, ragged_k, rows, static_cast<int>(groups), P, Q, K, sms, h->split_k == 0);
+    return dg::ragged_pick_tile(kind, ragged_k, rows, static_cast<int>(groups), P, Q, K, usable_sms(h), h->split_k == 0);
 }
 
 dg::RaggedArgs common_args(const gemm_ctx *h, const int64_t *offsets, int64_t groups, int64_t rows, int64_t P,
@@ -363,7 +403,10 @@ dg::RaggedArgs common_args(const gemm_ctx *h, const int64_t *offsets, int64_t gr
 // Formatted in place: these calls may take only microseconds.
 void set_path(gemm_ctx *h, const char *op, int kind, const dg::RaggedTile &t, const char *rest, bool ra, bool rb)
 {
-    const char *k = kind == dg::kRaggedMx4 ? "mx4" : kind == dg::kRaggedTf32 ? "tf32" : "bf16";
+    const char *k = kind == dg::kRaggedMx4    ? "mx4"
+                    : kind == dg::kRaggedTf32 ? "tf32"
+                    : kind == dg::kRaggedBf16 ? "bf16"
+                                              : "i8";
     char split[16] = "", path[128];
     if (t.split > 1) std::snprintf(split, sizeof split, "+splitk%d", t.split);
     std::snprintf(path, sizeof path, "%s_%s%s%dx%d%s%s%s%s", op, k, t.ctas == 2 ? "_pair" : "_", 128 * t.ctas, t.bn,
@@ -463,6 +506,79 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     ++h->launches;
     set_path(h, offsets ? "grouped" : "tc", kind, t, "", false, false);
     return GEMM_OK;
+}
+
+// Converting the operands first (2 bytes written and read for each one read)
+// costs a launch of its own and its traffic, and the product then reads 16-bit
+// operands; converting inside the product costs every tile that reads them.  The
+// estimates of both decide (cycles of 1.9 GHz, 3370 bytes each), as the tile's.
+dg::RaggedTile i8_tile(const gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, int *kind)
+{
+    dg::RaggedTile t;
+    if (h->ragged_tile) {
+        t = tile_for(h, dg::kRaggedI8, false, rows, groups, N, 0, K);
+        *kind = t.ctas == 2 ? dg::kRaggedI8Wide : dg::kRaggedI8;
+        if (t.ctas == 1) t.bn = std::min(t.bn, 128);
+        return t;
+    }
+    const int g = static_cast<int>(groups);
+    double narrow = 0, wide = 0;
+    t = dg::ragged_pick_tile(dg::kRaggedI8, false, rows, g, N, 0, K, usable_sms(h), h->split_k == 0, &narrow);
+    const dg::RaggedTile w =
+        dg::ragged_pick_tile(dg::kRaggedI8Wide, false, rows, g, N, 0, K, usable_sms(h), false, &wide);
+    const double busy = static_cast<double>(std::min(groups, rows));
+    wide += (static_cast<double>(rows) + busy * N) * K * 3 / 3370 + 5000;
+    *kind = wide < narrow ? dg::kRaggedI8Wide : dg::kRaggedI8;
+    return wide < narrow ? w : t;
+}
+
+int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const int8_t *ac,
+           int64_t aq, const float *as, const int8_t *bc, int64_t bq, const float *bs, void *C, int64_t ldc,
+           int c_dtype, cudaStream_t stream)
+{
+    if (rows == 0 || N == 0) {
+        h->last_path = "noop";
+        return GEMM_OK;
+    }
+    dg::DeviceGuard guard(h->device);
+    int rc = prepare(h, true);
+    if (rc) return rc;
+    int kind;
+    const dg::RaggedTile t = i8_tile(h, groups, rows, N, K, &kind);
+    dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
+    a.row_scale_p = bs;
+    a.row_scale_q = as;
+    alignas(64) CUtensorMap tmP = {}, tmQ = {};
+    dg::WorkspaceUse ws(h, stream);
+    const bool wide = kind == dg::kRaggedI8Wide;
+    if (K > 0 && wide) {
+        const int64_t ld = round_up(K, 16), a_bytes = round_up(rows * ld * 2, 256);
+        if ((rc = ws.acquire(static_cast<size_t>(a_bytes + groups * N * ld * 2)))) return rc;
+        uint8_t *a16 = static_cast<uint8_t *>(h->ws), *b16 = a16 + a_bytes;
+        const cudaError_t e = dg::launch_i8_widen(ac, aq, rows, bc, bq, groups * N, K, a16, b16, offsets, N, h->sm_count,
+                                                  stream);
+        if (e != cudaSuccess) return cuda_fail(h, e, "conversion launch");
+        ++h->launches;
+        rc = encode_k_major(h, &tmP, float_type(2), 2, b16, K, N, ld, groups, N * ld, 64, dg::kRaggedP,
+                            CU_TENSOR_MAP_SWIZZLE_128B, true, "B in 16 bits");
+        if (!rc)
+            rc = encode_k_major(h, &tmQ, float_type(2), 2, a16, K, rows, ld, 1, 0, 64, t.bn / t.ctas,
+                                CU_TENSOR_MAP_SWIZZLE_128B, false, "A in 16 bits");
+        if (rc) return rc;
+    } else if (K > 0) {
+        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        rc = encode_k_major(h, &tmP, u8, 1, bc, K, N, bq, groups, N * bq, 64, dg::kRaggedP, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            true, "the codes of B");
+        if (!rc)
+            rc = encode_k_major(h, &tmQ, u8, 1, ac, K, rows, aq, 1, 0, 64, t.bn, CU_TENSOR_MAP_SWIZZLE_NONE, false,
+                                "the codes of A");
+        if (rc) return rc;
+    }
+    const cudaError_t e = dg::launch_ragged(kind, false, false, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
+    if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
+    ++h->launches;
+    set_path(h, offsets ? "grouped" : "tc", kind, t, wide ? "_widened" : "", false, false);
+    return ws.done();
 }
 
 }  // namespace
@@ -702,6 +818,110 @@ try {
     if (rc) return fail(h, rc, why);
     return run_mx4(h, groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, a_lds, b_codes, b_ldq, b_scales, b_lds, C,
                    ldc, c_dtype, stream);
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
+}
+
+int64_t gemm_i8_code_pitch(int64_t K) { return K <= 0 ? 0 : round_up(K, 16); }
+
+int gemm_i8_quantise_validate(int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
+                              int64_t stride, int src_dtype, const int8_t *codes, int64_t ldq, const float *scales)
+{
+    const Checker bad{nullptr};
+    return check_quantise(layout, batch, rows, K, src, ld, stride, src_dtype, bad,
+                          [&] { return check_i8_operand(bad, batch * rows, K, codes, ldq, scales); });
+}
+
+int gemm_i8_dequantise_validate(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
+                                const void *dst, int64_t ldd, int dst_dtype)
+{
+    const Checker bad{nullptr};
+    return check_dequantise(rows, K, dst, ldd, dst_dtype, bad,
+                            [&] { return check_i8_operand(bad, rows, K, codes, ldq, scales); });
+}
+
+int gemm_i8_validate(int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets,
+                     const int8_t *a_codes, int64_t a_ldq, const float *a_scales, const int8_t *b_codes,
+                     int64_t b_ldq, const float *b_scales, const void *C, int64_t ldc, int c_dtype)
+{
+    return check_i8(groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, b_codes, b_ldq, b_scales, C, ldc, c_dtype,
+                    !(groups == 1 && offsets == nullptr), nullptr);
+}
+
+int gemm_i8_quantise(gemm_handle_t h, int layout, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
+                     int64_t stride, int src_dtype, int8_t *codes, int64_t ldq, float *scales, cudaStream_t stream)
+try {
+    if (!h) return GEMM_ERR_INVALID;
+    std::string why;
+    const Checker bad{&why};
+    const int rc = check_quantise(layout, batch, rows, K, src, ld, stride, src_dtype, bad,
+                                  [&] { return check_i8_operand(bad, batch * rows, K, codes, ldq, scales); });
+    if (rc) return fail(h, rc, why);
+    if (batch == 0 || rows == 0 || K == 0) {
+        h->last_path = "noop";
+        return GEMM_OK;
+    }
+    dg::DeviceGuard guard(h->device);
+    const cudaError_t e = dg::launch_i8_quantise(layout == GEMM_B_ROW_MAJOR, batch, rows, K, src, ld,
+                                                 batch > 1 ? stride : 0, src_dtype == GEMM_BF16, codes, ldq, scales,
+                                                 h->sm_count, stream);
+    if (e != cudaSuccess) return cuda_fail(h, e, "quantisation launch");
+    ++h->launches;
+    h->last_path = layout == GEMM_B_ROW_MAJOR ? "i8_quantise_rowB" : "i8_quantise_colB";
+    return GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
+}
+
+int gemm_i8_dequantise(gemm_handle_t h, int64_t rows, int64_t K, const int8_t *codes, int64_t ldq,
+                       const float *scales, void *dst, int64_t ldd, int dst_dtype, cudaStream_t stream)
+try {
+    if (!h) return GEMM_ERR_INVALID;
+    std::string why;
+    const Checker bad{&why};
+    const int rc = check_dequantise(rows, K, dst, ldd, dst_dtype, bad,
+                                    [&] { return check_i8_operand(bad, rows, K, codes, ldq, scales); });
+    if (rc) return fail(h, rc, why);
+    if (rows == 0 || K == 0) {
+        h->last_path = "noop";
+        return GEMM_OK;
+    }
+    dg::DeviceGuard guard(h->device);
+    const cudaError_t e =
+        dg::launch_i8_dequantise(rows, K, codes, ldq, scales, dst, ldd, dst_dtype == GEMM_BF16, h->sm_count, stream);
+    if (e != cudaSuccess) return cuda_fail(h, e, "dequantisation launch");
+    ++h->launches;
+    h->last_path = "i8_dequantise";
+    return GEMM_OK;
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
+}
+
+int gemm_i8_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const int8_t *a_codes, int64_t a_ldq,
+                const float *a_scales, const int8_t *b_codes, int64_t b_ldq, const float *b_scales, void *C,
+                int64_t ldc, int c_dtype, cudaStream_t stream)
+try {
+    if (!h) return GEMM_ERR_INVALID;
+    std::string why;
+    const int rc = check_i8(1, M, N, K, nullptr, a_codes, a_ldq, a_scales, b_codes, b_ldq, b_scales, C, ldc, c_dtype,
+                            false, &why);
+    if (rc) return fail(h, rc, why);
+    return run_i8(h, 1, M, N, K, nullptr, a_codes, a_ldq, a_scales, b_codes, b_ldq, b_scales, C, ldc, c_dtype, stream);
+} catch (...) {
+    return GEMM_ERR_NOMEM;  // no exception leaves a C entry
+}
+
+int gemm_i8_grouped_run(gemm_handle_t h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets,
+                        const int8_t *a_codes, int64_t a_ldq, const float *a_scales, const int8_t *b_codes,
+                        int64_t b_ldq, const float *b_scales, void *C, int64_t ldc, int c_dtype, cudaStream_t stream)
+try {
+    if (!h) return GEMM_ERR_INVALID;
+    std::string why;
+    const int rc = check_i8(groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, b_codes, b_ldq, b_scales, C, ldc,
+                            c_dtype, true, &why);
+    if (rc) return fail(h, rc, why);
+    return run_i8(h, groups, rows, N, K, offsets, a_codes, a_ldq, a_scales, b_codes, b_ldq, b_scales, C, ldc, c_dtype,
+                  stream);
 } catch (...) {
     return GEMM_ERR_NOMEM;  // no exception leaves a C entry
 }

@@ -6,11 +6,12 @@ The functions ``gemm_create``, ``gemm_run``, ``gemm_run_host``,
 ``gemm_last_path``, ``gemm_launch_count``, ``gemm_version``,
 ``gemm_run_noalloc``, ``gemm_ladder_run``, ``gemm_ladder_name``,
 ``gemm_peak_fma_run`` and ``gemm_peak_mma_run``, and those of
-include/gemm_grouped.h, include/gemm_mx4.h and include/gemm_route.h, take and
-return the same plain values as their C counterparts (pointers as ints; the
-FLOP-count out-parameter of the peak calls is returned as a second value).
-``Gemm`` wraps a handle for torch tensors; ``Mx4`` holds a matrix in microscaled
-4-bit floating point, ``Routing`` the choices of a router.  Every GEMM step runs in the library's CUDA
+include/gemm_grouped.h, include/gemm_mx4.h, include/gemm_i8.h,
+include/gemm_route.h and include/gemm_ortho.h, take and return the same plain
+values as their C counterparts (pointers as ints; the FLOP-count out-parameter
+of the peak calls is returned as a second value).  ``Gemm`` wraps a handle for torch tensors;
+``Mx4`` holds a matrix in microscaled 4-bit floating point, ``I8`` one in 8-bit
+integers, ``Routing`` the choices of a router.  Every GEMM step runs in the library's CUDA
 kernels; there is no other code path, and calling anything here without the
 built library raises ``GemmLibraryMissing``.
 """
@@ -54,6 +55,7 @@ GEMM_OPT_TC_STAGE_SLICES = 13
 GEMM_OPT_STREAM_K = 14
 GEMM_OPT_SIMT_SMALL = 15
 GEMM_OPT_GROUPED_TILE = 16
+GEMM_OPT_ORTHO_TILE = 17
 
 GEMM_GROUPED_MAX_GROUPS = 4096
 GEMM_GROUPED_NAN_ON_ERROR = 0x100
@@ -64,6 +66,8 @@ GEMM_ROUTE_MAX_K = 31
 GEMM_ROUTE_MAX_GROUPS = 32
 GEMM_ROUTE_SIGMOID = 1
 GEMM_ROUTE_RENORMALISE = 2
+
+GEMM_ORTHO_MAX_STEPS = 32
 
 DTYPES = {"f32": GEMM_F32, "tf32": GEMM_TF32, "bf16": GEMM_BF16, "f32x3": GEMM_F32_3XTF32}
 LAYOUTS = {"row": GEMM_B_ROW_MAJOR, "col": GEMM_B_COL_MAJOR}
@@ -140,6 +144,20 @@ def load_library():
             "gemm_mx4_dequantise_validate": (dequantise, ci),
             "gemm_mx4_validate": (mx4_grouped, ci),
         })
+        i8_quantise = [ci, i64, i64, i64, vp, i64, i64, ci, vp, i64, vp]
+        i8_dequantise = [i64, i64, vp, i64, vp, vp, i64, ci]
+        i8 = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, ci]
+        i8_grouped = [i64, i64, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp, i64, ci]
+        sig.update({
+            "gemm_i8_code_pitch": ([i64], i64),
+            "gemm_i8_quantise": ([vp, *i8_quantise, vp], ci),
+            "gemm_i8_dequantise": ([vp, *i8_dequantise, vp], ci),
+            "gemm_i8_run": ([vp, *i8, vp], ci),
+            "gemm_i8_grouped_run": ([vp, *i8_grouped, vp], ci),
+            "gemm_i8_quantise_validate": (i8_quantise, ci),
+            "gemm_i8_dequantise_validate": (i8_dequantise, ci),
+            "gemm_i8_validate": (i8_grouped, ci),
+        })
         cf = ctypes.c_float
         route = [i64, i64, i64, vp, i64, ci, vp, i64, i64, ci, cf, vp, vp, vp, vp]
         route_grad = [i64, i64, i64, vp, i64, ci, vp, vp, ci, cf, vp, i64]
@@ -148,6 +166,11 @@ def load_library():
             "gemm_route_grad": ([vp, *route_grad, vp], ci),
             "gemm_route_validate": (route, ci),
             "gemm_route_grad_validate": (route_grad, ci),
+        })
+        ortho = [i64, i64, i64, vp, i64, i64, vp, i64, i64, ci, ci, vp, cf]
+        sig.update({
+            "gemm_orthogonalise": ([vp, *ortho, vp], ci),
+            "gemm_orthogonalise_validate": (ortho, ci),
         })
         for name, (argtypes, restype) in sig.items():
             fn = getattr(lib, name)
@@ -285,7 +308,40 @@ def gemm_mx4_validate(*args) -> int:
     return load_library().gemm_mx4_validate(*args)
 
 
-# include/gemm_route.h, argument for argument.
+# include/gemm_i8.h, include/gemm_route.h and include/gemm_ortho.h, argument for
+# argument.
+
+def gemm_i8_code_pitch(K) -> int:
+    return load_library().gemm_i8_code_pitch(K)
+
+
+def gemm_i8_quantise(*args) -> int:
+    return load_library().gemm_i8_quantise(*args)
+
+
+def gemm_i8_dequantise(*args) -> int:
+    return load_library().gemm_i8_dequantise(*args)
+
+
+def gemm_i8_run(*args) -> int:
+    return load_library().gemm_i8_run(*args)
+
+
+def gemm_i8_grouped_run(*args) -> int:
+    return load_library().gemm_i8_grouped_run(*args)
+
+
+def gemm_i8_quantise_validate(*args) -> int:
+    return load_library().gemm_i8_quantise_validate(*args)
+
+
+def gemm_i8_dequantise_validate(*args) -> int:
+    return load_library().gemm_i8_dequantise_validate(*args)
+
+
+def gemm_i8_validate(*args) -> int:
+    return load_library().gemm_i8_validate(*args)
+
 
 def gemm_route(*args) -> int:
     return load_library().gemm_route(*args)
@@ -301,6 +357,14 @@ def gemm_route_validate(*args) -> int:
 
 def gemm_route_grad_validate(*args) -> int:
     return load_library().gemm_route_grad_validate(*args)
+
+
+def gemm_orthogonalise(*args) -> int:
+    return load_library().gemm_orthogonalise(*args)
+
+
+def gemm_orthogonalise_validate(*args) -> int:
+    return load_library().gemm_orthogonalise_validate(*args)
 
 
 GEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -516,6 +580,47 @@ def mx4_empty(rows: int, K: int, device="cuda") -> Mx4:
                torch.empty((rows, gemm_mx4_scale_pitch(K)), dtype=torch.uint8, device=device), K)
 
 
+class I8:
+    """A matrix of rows x K elements in 8-bit integers with a scale a row.
+
+    ``codes`` is (rows, pitch) int8, rows and pitch multiples of 16 bytes
+    (``i8_empty`` makes them so), ``scales`` (rows,) float32.  The expert matrices
+    of a grouped product follow one another along the rows."""
+
+    def __init__(self, codes, scales, K: int):
+        import torch
+        if codes.dtype != torch.int8 or codes.dim() != 2:
+            raise ValueError("codes must be a 2-D int8 tensor")
+        if codes.shape[1] < K or (codes.shape[1] > 1 and codes.stride(1) != 1):
+            raise ValueError(f"codes must hold {K} bytes of each row, next to one another")
+        if scales.dtype != torch.float32 or scales.dim() != 1 or not scales.is_contiguous():
+            raise ValueError("scales must be a contiguous 1-D float32 tensor")
+        if codes.shape[0] != scales.shape[0] or codes.device != scales.device:
+            raise ValueError("codes and scales must have the same rows and device")
+        self.codes, self.scales, self.K = codes, scales, int(K)
+        self.rows = codes.shape[0]
+        self._pitch = codes.stride(0) if self.rows > 1 else codes.shape[1]
+        if self._pitch < K:
+            raise ValueError("the rows of codes overlap")
+        self._device = codes.get_device() if codes.is_cuda else None
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _args(self, device):
+        if self._device != device:
+            raise ValueError(f"an 8-bit operand is on {self.device}, the handle on cuda:{device}")
+        return self.codes.data_ptr(), self._pitch, self.scales.data_ptr()
+
+
+def i8_empty(rows: int, K: int, device="cuda") -> I8:
+    """Uninitialised ``I8`` storage for rows x K elements."""
+    import torch
+    return I8(torch.empty((rows, gemm_i8_code_pitch(K)), dtype=torch.int8, device=device),
+              torch.empty(rows, dtype=torch.float32, device=device), K)
+
+
 class Routing(NamedTuple):
     """A router's choices: ``weights`` (tokens, k) float32 and ``expert``
     (tokens, k) int64, -1 where there is none; ``order`` (tokens * k,) int64, the
@@ -555,6 +660,16 @@ def _route_flags(scoring, renormalise):
     if scoring not in ("softmax", "sigmoid"):
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', not {scoring!r}")
     return (GEMM_ROUTE_SIGMOID if scoring == "sigmoid" else 0) | (GEMM_ROUTE_RENORMALISE if renormalise else 0)
+
+
+def _step_table(steps, coefficients):
+    """The C table of 3 * steps coefficients."""
+    if steps < 1 or steps > GEMM_ORTHO_MAX_STEPS:
+        raise ValueError(f"steps must be in 1..{GEMM_ORTHO_MAX_STEPS}")
+    rows = coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients must be three numbers, or three for every step")
+    return (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
 
 
 class Gemm:
@@ -742,6 +857,32 @@ class Gemm:
                 self._check(rc)
         return dlogits
 
+    def orthogonalise(self, G, out, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, stream=None):
+        """The orthogonal factor of ``G``, or of every matrix of a batch, by
+        Newton-Schulz steps, into ``out`` (which may be ``G``).
+
+        X = G / (|G| + eps), then X <- a X + (b A + c A A) X with A = X X^T, or
+        X^T X where that is smaller.  ``coefficients`` is (a, b, c), or one such
+        triple a step.  float32 or bfloat16, out of G's type."""
+        dev = self.device
+        if G.dim() == 3:
+            batch, rows, cols, ldg, sg, g_type = _matrices(G, "G", dev)
+            got = _matrices(out, "out", dev)
+        else:
+            rows, cols, ldg, g_type = _matrix(G, "G", dev)
+            batch, sg = 1, 0
+            r, c, ld, o_type = _matrix(out, "out", dev)
+            got = (1, r, c, ld, 0, o_type)
+        if (got[0], got[1], got[2], got[5]) != (batch, rows, cols, g_type):
+            raise ValueError("out must have the shape and type of G")
+        table = _step_table(steps, coefficients)
+        with self._turn:
+            rc = self._lib.gemm_orthogonalise(self.handle, batch, rows, cols, G.data_ptr(), ldg, sg, out.data_ptr(),
+                                              got[3], got[4], g_type, steps, table, eps, _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return out
+
     def mx4_quantise(self, src, out: Mx4, layout="col", stream=None):
         """Quantise ``src`` (float32 or bfloat16) along K into ``out``.
 
@@ -809,6 +950,71 @@ class Gemm:
                 self._check(rc)
         return C
 
+    def i8_quantise(self, src, out: I8, layout="col", stream=None):
+        """Quantise ``src`` (float32 or bfloat16) along K into ``out``, one scale a
+        row; ``src`` and ``layout`` as in ``mx4_quantise``."""
+        lb = LAYOUTS.get(layout, layout)
+        dev = self.device
+        if src.dim() == 3:
+            batch, d1, d2, ld, stride, s_type = _matrices(src, "src", dev)
+        else:
+            d1, d2, ld, s_type = _matrix(src, "src", dev)
+            batch, stride = 1, 0
+        rows, K = (d1, d2) if lb == GEMM_B_COL_MAJOR else (d2, d1)
+        if out.rows != batch * rows or out.K != K:
+            raise ValueError(f"out holds {out.rows} x {out.K}, src has {batch} x {rows} x {K}")
+        with self._turn:
+            rc = self._lib.gemm_i8_quantise(self.handle, lb, batch, rows, K, src.data_ptr(), ld, stride, s_type,
+                                            *out._args(dev), _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return out
+
+    def i8_dequantise(self, q: I8, out, stream=None):
+        """The values ``q`` stands for, code * scale, as float32 or bfloat16."""
+        dev = self.device
+        rows, K, ld, o_type = _matrix(out, "out", dev)
+        if rows != q.rows or K != q.K:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(q.rows, q.K)}")
+        with self._turn:
+            rc = self._lib.gemm_i8_dequantise(self.handle, rows, K, *q._args(dev), out.data_ptr(), ld, o_type,
+                                              _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return out
+
+    def run_i8(self, A: I8, B: I8, C, stream=None):
+        """C = A · B^T of two 8-bit matrices (M x K and N x K), each sum of the
+        codes' products times its row's and its column's scale; C float32 or
+        bfloat16."""
+        dev = self.device
+        M, N, ldc, c_type = _matrix(C, "C", dev)
+        if A.K != B.K or M != A.rows or N != B.rows:
+            raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K}, C {tuple(C.shape)}")
+        with self._turn:
+            rc = self._lib.gemm_i8_run(self.handle, M, N, A.K, *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
+                                       _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return C
+
+    def run_i8_grouped(self, A: I8, B: I8, offsets, C, stream=None):
+        """``run_grouped`` of 8-bit operands: B holds the experts' N x K matrices
+        one after another, N = C's columns."""
+        dev = self.device
+        M, N, ldc, c_type = _matrix(C, "C", dev)
+        groups = offsets.shape[0] - 1
+        if A.K != B.K or M != A.rows or B.rows != groups * N:
+            raise ValueError(f"shapes differ: A {A.rows} x {A.K}, B {B.rows} x {B.K} for {groups} groups, "
+                             f"C {tuple(C.shape)}")
+        with self._turn:
+            rc = self._lib.gemm_i8_grouped_run(self.handle, groups, M, N, A.K, _offsets(offsets, groups, dev),
+                                               *A._args(dev), *B._args(dev), C.data_ptr(), ldc, c_type,
+                                               _raw_stream(stream, dev))
+            if rc:
+                self._check(rc)
+        return C
+
     def sync_status(self, stream=None):
         """Wait for ``stream`` and raise GemmError if an in-kernel wait expired or
         a call's group offsets were refused."""
@@ -841,6 +1047,18 @@ def matmul(A, B, layout_b="row", dtype="f32", out=None, stream=None, handle: Gem
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     g = handle or default_handle(A.device.index or 0)
     return g.run(A, B, out, lb, dtype, stream)
+
+
+def orthogonalise(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, stream=None,
+                  handle: Gemm | None = None):
+    """Allocate ``out`` (as G) if needed and return ``Gemm.orthogonalise``'s result."""
+    import torch
+    if G.device.type != "cuda":
+        raise ValueError(f"G is on {G.device}: the products run on a CUDA device")
+    if out is None:
+        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    g = handle or default_handle(G.device.index or 0)
+    return g.orthogonalise(G, out, steps, coefficients, eps, stream)
 
 
 _handles: dict[int, Gemm] = {}

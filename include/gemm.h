@@ -155,14 +155,20 @@ extern "C" {
  * when GEMM_OPT_SIMT_CONFIG, GEMM_OPT_MAX_CTAS and GEMM_OPT_SPLIT_K are 0;
  * 1 = never; 2 = for every FP32 problem (tests). */
 #define GEMM_OPT_SIMT_SMALL 15
-/* Tile of the grouped and 4-bit products (gemm_grouped.h, gemm_mx4.h): 0
+/* Tile of the grouped, 4-bit and 8-bit products (gemm_grouped.h, gemm_mx4.h,
+ * gemm_i8.h): 0
  * (default) = the least estimated time for the average group; else 1000 * CTAs
  * + rows, CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile
  * of 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at
- * most 224), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
+ * most 224, 8-bit products of one CTA at most 128 and convert their operands on
+ * the way, of a pair before), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
  * 8 CTAs (CTAs 1, rows at most 128).  By default the contraction is cut where
  * the tiles would leave SMs idle; GEMM_OPT_SPLIT_K = 1 (or more) forbids it. */
 #define GEMM_OPT_GROUPED_TILE 16
+/* Tile of the products of gemm_ortho.h: 0 (default) = the least estimated time
+ * of each; else 1000 * CTAs + columns, CTAs 1 or 2 and columns 32, 64, 128 or 256
+ * per tile of 128 * CTAs rows (as far as a product takes them). */
+#define GEMM_OPT_ORTHO_TILE 17
 
 typedef struct gemm_ctx *gemm_handle_t;
 
