@@ -218,6 +218,21 @@ def test_close_sums_are_decided_in_64_bits(gm, h, scoring):
         assert torch.equal(r.expert.cpu(), e)
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_neighbouring_logits_keep_their_order(gm, h, sign):
+    """FP32 logits one unit in the last place apart, and equal ones."""
+    gen = torch.Generator().manual_seed(23)
+    for E in (24, 96, 250, 700):
+        steps = torch.stack([torch.randperm(E, generator=gen) for _ in range(70)])
+        x = sign * (1.0 + (steps // 2).float() * 2.0 ** -23)
+        for k, groups, top in ((8, 1, 1), (3, 2, 1), (8, 2, 2)):
+            r = fresh(gm, 70, E, k)
+            h.route(x.cuda(), r, "sigmoid", None, groups, top)
+            if groups == 1 or top == groups:
+                assert torch.equal(r.expert.cpu(), definition(x, k, "sigmoid")[1])
+            check_sorted(r, E)
+
+
 def test_odd_values(gm, h):
     """NaN, infinities, far logits, biases that exclude or force an expert."""
     x = torch.randn((12, 40), generator=torch.Generator().manual_seed(9))
