@@ -45,6 +45,7 @@ constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 256;             // the second accumulator's column
 constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 1;
 constexpr int EPI_WARPS = 8;
+constexpr int EPI_BYTES = EPI_WARPS * 4096;  // a warp's 32 x 32 values
 constexpr int WARPS = 2 + EPI_WARPS;
 constexpr int THREADS = 32 * WARPS;
 constexpr int SMEM_MAX = 227 * 1024;
@@ -113,24 +114,42 @@ __device__ __forceinline__ uint32_t pack(__half a, __half b)
     return static_cast<uint32_t>(__half_as_ushort(a)) | static_cast<uint32_t>(__half_as_ushort(b)) << 16;
 }
 
-__device__ __forceinline__ void load16(const __half *src, float (&v)[16])
+// Eight FP16 numbers added to v.
+__device__ __forceinline__ void add8(uint4 w, float (&v)[8])
 {
-    const uint4 w[2] = {*reinterpret_cast<const uint4 *>(src), *(reinterpret_cast<const uint4 *>(src) + 1)};
-    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[2 * i] += f.x;
+        v[2 * i + 1] += f.y;
     }
 }
 
-__device__ __forceinline__ void store16(__half *dst, const __half (&v)[16])
+// Eight values in FP16, and what that leaves of them.
+__device__ __forceinline__ uint4 round8(const float (&v)[8], float (&rest)[8])
 {
-    reinterpret_cast<uint4 *>(dst)[0] =
-        make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
-    reinterpret_cast<uint4 *>(dst)[1] =
-        make_uint4(pack(v[8], v[9]), pack(v[10], v[11]), pack(v[12], v[13]), pack(v[14], v[15]));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        const float2 f = __half22float2(h);
+        rest[2 * i] = v[2 * i] - f.x;
+        rest[2 * i + 1] = v[2 * i + 1] - f.y;
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 round8(const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // SPLIT: operands of two FP16 numbers.  XSTEP: X' = a X + B X, Q = X with its
@@ -147,13 +166,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
     const uint32_t sbase = raw_addr + pad;
-    const uint32_t bars = sbase + static_cast<uint32_t>(p.stages * p.stage_bytes);
+    const uint32_t epi_base = sbase + static_cast<uint32_t>(p.stages * p.stage_bytes);
+    const uint32_t bars = epi_base + EPI_BYTES;
     const uint32_t full_bar = bars;                         // [stages], used in the even CTA
     const uint32_t empty_bar = full_bar + 8 * MAX_STAGES;   // [stages]
     const uint32_t tfull_bar = empty_bar + 8 * MAX_STAGES;  // [2]
     const uint32_t tempty_bar = tfull_bar + 16;             // [2], used in the even CTA
     const uint32_t drain_bar = tempty_bar + 16;
-    uint8_t *tail = smem_raw + pad + p.stages * p.stage_bytes + NUM_BARS * 8;
+    uint8_t *tail = smem_raw + pad + p.stages * p.stage_bytes + EPI_BYTES + NUM_BARS * 8;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
 
@@ -343,32 +363,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         // ------------------------------------------------------ epilogue
-        // A lane holds a row of the result, 16 neighbouring columns at a time.
+        // A warp turns 32 x 32 sums in shared memory so that a lane holds 8
+        // neighbouring columns of rows lane / 4, + 8, + 16, + 24: loads and stores
+        // of 16 bytes a lane touch 8 lines an instruction.  (With a row a lane
+        // they touched 32, and the line look-ups set the pace: X of 16 matrices of
+        // 4096 x 2048 500 us, B 150 us.)
         const int q = warp & 3;            // tensor-memory lane quarter
         const int half = (warp - 2) >> 2;  // 0: even chunks of 32 columns, 1: odd ones
         const int mine = (p.bn / 32 + 1 - half) / 2;
-        const auto unit_of = [&](int k) { return 4 * (k >> 1) + 2 * half + (k & 1); };
+        const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 4096;
+        const int sub = lane >> 2, piece = lane & 3;
+        // 16 bytes c of row r: bank conflicts are spread over the rows
+        const auto at = [&](int r, int c) { return stage + r * 128 + ((c ^ (r & 7)) * 16); };
         uint32_t acc_it = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
             const Tile t = tile_at<CG, !XSTEP>(p, u);
             if (!t.some) continue;
-            const int i = t.i0 + static_cast<int>(rank) * BP + q * 32 + lane;
-            const bool in = i < p.m;
+            const int i0 = t.i0 + static_cast<int>(rank) * BP + q * 32;  // the warp's first row
             const long long mat = t.b;
             const float *f = p.factors + mat * FACTORS;
-            float diag = 0.0f, scale = 0.0f;
-            if (XSTEP) {
-                if (in) diag = p.ca + p.db[mat * p.ldm + i];
-                scale = 1.0f / SCALE_B;
-            } else if (p.mode == kOrthoA) {
-                scale = f[p.first ? kFactorA0 : kFactorA];
-            } else {
-                if (in) diag = p.da[mat * p.ldm + i];
-                scale = 1.0f / (SCALE_A * SCALE_A);
+            float diag[4], scale = 0.0f;  // of rows i0 + sub, + 8, ...
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + sub + 8 * k;
+                diag[k] = i >= p.m ? 0.0f
+                          : XSTEP  ? p.ca + p.db[mat * p.ldm + i]
+                          : p.mode == kOrthoB ? p.da[mat * p.ldm + i]
+                                              : 0.0f;
             }
+            if (XSTEP)
+                scale = 1.0f / SCALE_B;
+            else if (p.mode == kOrthoA)
+                scale = f[p.first ? kFactorA0 : kFactorA];
+            else
+                scale = 1.0f / (SCALE_A * SCALE_A);
             const float post = !XSTEP ? 1.0f : (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
-            const long long row_m = (mat * p.m + i) * p.ldm, row_n = (mat * p.m + i) * p.ldn;
+            const int width = XSTEP ? p.n : p.m, ld = XSTEP ? p.ldn : p.ldm;
+            const long long rows = mat * p.m;
 
             const auto await = [&]() {
                 const uint32_t abuf = acc_it & 1u;
@@ -392,136 +424,172 @@ __global__ void __launch_bounds__(THREADS, 1)
             const auto load = [&](int unit, uint32_t(&v)[16]) {
                 tmem_load_16cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc_it & 1u) * ACC1 + unit * 16, v);
             };
-            // Symmetric results: row i, and column i where the tile is mirrored.
-            const auto put_symmetric = [&](__half *const(&planes)[2], int j, float (&v)[16], float up) {
-                __half hi[16], lo[16];
+            // Chunk k of this warp: columns from column(k) on.
+            const auto column = [&](int k) { return t.j0 + (2 * k + half) * 32; };
+            const auto turn = [&](const uint32_t(&lo)[16], const uint32_t(&hi)[16]) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const float s = v[c] * up;
-                    hi[c] = __float2half_rn(s);
-                    if (SPLIT) lo[c] = __float2half_rn(s - __half2float(hi[c]));
+                for (int c = 0; c < 4; ++c) {
+                    sts_u4(at(lane, c), make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]));
+                    sts_u4(at(lane, c + 4), make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]));
                 }
-                if (in) {
-                    store16(planes[0] + row_m + j, hi);
-                    if (SPLIT) store16(planes[1] + row_m + j, lo);
-                    if (t.mirror) {
-                        __half *col = planes[0] + (mat * p.m + j) * p.ldm + i;
-                        __half *col1 = planes[1] + (mat * p.m + j) * p.ldm + i;
+                __syncwarp();
+            };
+            // The operands that the epilogue adds: X, or A where B is made.
+            uint4 extra[2][4];
+            const bool reads = XSTEP || p.mode == kOrthoB;
+            const bool two = SPLIT || (XSTEP && p.has_rest);
+            const auto fetch = [&](int k) {
+                if (!reads) return;
+                const int j = column(k) + piece * 8;
+                const __half *const *planes = XSTEP ? p.x : p.a;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            if (j + c < p.m) {
-                                col[static_cast<long long>(c) * p.ldm] = hi[c];
-                                if (SPLIT) col1[static_cast<long long>(c) * p.ldm] = lo[c];
-                            }
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i0 + sub + 8 * r;
+                    const bool in = i < p.m && j < width;
+                    const long long o = (rows + i) * ld + j;
+                    extra[0][r] = in ? *reinterpret_cast<const uint4 *>(planes[0] + o) : make_uint4(0u, 0u, 0u, 0u);
+                    if (two) extra[1][r] = in ? *reinterpret_cast<const uint4 *>(planes[1] + o) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
-            const auto finish = [&](int unit, const uint32_t(&acc)[16]) {
-                const int j = t.j0 + unit * 16;
-                if (j >= (XSTEP ? p.n : p.m)) return;
-                float v[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(acc[c]) * scale;
-                if (!XSTEP && p.mode == kOrthoA) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (j + c == i) {
-                            if (in) p.da[mat * p.ldm + i] = v[c];
-                            v[c] = 0.0f;
-                        }
-                    put_symmetric(p.a, j, v, SCALE_A);
-                } else if (!XSTEP) {
-                    float e[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) e[c] = 0.0f;
-                    if (in) {
-                        load16(p.a[0] + row_m + j, e);
-                        if (SPLIT) {
-                            float r[16];
-                            load16(p.a[1] + row_m + j, r);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) e[c] += r[c];
-                        }
+            const bool back = XSTEP ? p.last && p.turned : t.mirror;  // results are needed column by column
+            const auto finish = [&](int k) {
+                const int jc = column(k), j = jc + piece * 8;
+                if (jc < width) {
+                    float dj[8];
+                    if (!XSTEP && p.mode == kOrthoB && j < width) {
+                        const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
+                        const float4 d0 = d[0], d1 = d[1];
+                        dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
+                        dj[4] = d1.x, dj[5] = d1.y, dj[6] = d1.z, dj[7] = d1.w;
                     }
-                    const float4 *dj = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        const float4 d4 = dj[c4];
-                        const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = sub + 8 * r, i = i0 + row;
+                        if (i >= p.m || j >= width) continue;
+                        const uint4 a0 = lds_u4(at(row, 2 * piece)), a1 = lds_u4(at(row, 2 * piece + 1));
+                        const uint32_t w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                        float v[8];
 #pragma unroll
-                        for (int c1 = 0; c1 < 4; ++c1) {
-                            const int c = c4 * 4 + c1;
-                            if (j + c == i) {
-                                if (in) p.db[mat * p.ldm + i] = p.cb * diag + p.cc * fmaf(diag, diag, v[c]);
-                                v[c] = 0.0f;
+                        for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(w[c]) * scale;
+                        const long long o = (rows + i) * ld + j;
+                        if (!XSTEP) {
+                            const float up = p.mode == kOrthoA ? SCALE_A : SCALE_B;
+                            if (p.mode == kOrthoA) {
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (j + c == i) {
+                                        p.da[mat * p.ldm + i] = v[c];
+                                        v[c] = 0.0f;
+                                    }
                             } else {
-                                const float a = e[c] * (1.0f / SCALE_A);
-                                v[c] = p.cb * a + p.cc * fmaf(diag + d[c1], a, v[c]);
-                            }
-                        }
-                    }
-                    put_symmetric(p.b, j, v, SCALE_B);
-                } else if (in) {
-                    float x[16];
-                    load16(p.x[0] + row_n + j, x);
-                    if (p.has_rest) {
-                        float r[16];
-                        load16(p.x[1] + row_n + j, r);
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) x[c] += r[c];
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) v[c] = fmaf(diag, x[c], v[c]) * post;
-                    if (!p.last) {
-                        __half hi[16], lo[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            hi[c] = __float2half_rn(v[c]);
-                            lo[c] = __float2half_rn(v[c] - __half2float(hi[c]));
-                        }
-                        store16(p.x_out[0] + row_n + j, hi);
-                        store16(p.x_out[1] + row_n + j, lo);
-                    } else if (p.turned) {
-                        const long long at = mat * p.stride_o + j * p.ldo + i;
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            if (j + c < p.n) {
-                                if (p.o_bf16)
-                                    static_cast<__nv_bfloat16 *>(p.o)[at + c * p.ldo] = __float2bfloat16_rn(v[c]);
-                                else
-                                    static_cast<float *>(p.o)[at + c * p.ldo] = v[c];
-                            }
-                    } else {
-                        const long long at = mat * p.stride_o + i * p.ldo + j;
-                        if (p.o_vec && j + 16 <= p.n) {
-                            if (p.o_bf16) {
-                                uint32_t w[8];
+                                float e[8] = {};
+                                add8(extra[0][r], e);
+                                if (SPLIT) add8(extra[1][r], e);
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) {
-                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-                                    w[c] = *reinterpret_cast<const uint32_t *>(&b);
+                                    const float a = e[c] * (1.0f / SCALE_A);
+                                    if (j + c == i) {
+                                        p.db[mat * p.ldm + i] = p.cb * diag[r] + p.cc * fmaf(diag[r], diag[r], v[c]);
+                                        v[c] = 0.0f;
+                                    } else {
+                                        v[c] = p.cb * a + p.cc * fmaf(diag[r] + dj[c], a, v[c]);
+                                    }
                                 }
-                                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at);
-                                out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                            } else {
-                                float4 *out = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at);
+                            }
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    out[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                            for (int c = 0; c < 8; ++c) v[c] *= up;
+                            __half *const *planes = p.mode == kOrthoA ? p.a : p.b;
+                            if (SPLIT) {
+                                float rest[8];
+                                *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v, rest);
+                                *reinterpret_cast<uint4 *>(planes[1] + o) = round8(rest);
+                            } else {
+                                *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v);
                             }
                         } else {
+                            float x[8] = {};
+                            add8(extra[0][r], x);
+                            if (two) add8(extra[1][r], x);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                if (j + c < p.n) {
-                                    if (p.o_bf16)
-                                        static_cast<__nv_bfloat16 *>(p.o)[at + c] = __float2bfloat16_rn(v[c]);
-                                    else
-                                        static_cast<float *>(p.o)[at + c] = v[c];
+                            for (int c = 0; c < 8; ++c) v[c] = fmaf(diag[r], x[c], v[c]) * post;
+                            if (!p.last) {
+                                float rest[8];
+                                *reinterpret_cast<uint4 *>(p.x_out[0] + o) = round8(v, rest);
+                                *reinterpret_cast<uint4 *>(p.x_out[1] + o) = round8(rest);
+                            } else if (!p.turned) {
+                                const long long to = mat * p.stride_o + i * p.ldo + j;
+                                if (p.o_bf16) {
+                                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + to;
+                                    if (p.o_vec && j + 8 <= p.n) {
+                                        uint32_t y[4];
+#pragma unroll
+                                        for (int c = 0; c < 4; ++c) {
+                                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+                                            y[c] = *reinterpret_cast<const uint32_t *>(&b);
+                                        }
+                                        *reinterpret_cast<uint4 *>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+                                    } else {
+#pragma unroll
+                                        for (int c = 0; c < 8; ++c)
+                                            if (j + c < p.n) out[c] = __float2bfloat16_rn(v[c]);
+                                    }
+                                } else {
+                                    float *out = static_cast<float *>(p.o) + to;
+                                    if (p.o_vec && j + 8 <= p.n) {
+                                        *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+                                        *(reinterpret_cast<float4 *>(out) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+                                    } else {
+#pragma unroll
+                                        for (int c = 0; c < 8; ++c)
+                                            if (j + c < p.n) out[c] = v[c];
+                                    }
                                 }
+                            }
+                        }
+                        if (back) {
+                            sts_f4(at(row, 2 * piece), make_float4(v[0], v[1], v[2], v[3]));
+                            sts_f4(at(row, 2 * piece + 1), make_float4(v[4], v[5], v[6], v[7]));
+                        }
+                    }
+                    if (back) {
+                        __syncwarp();
+                        const auto value = [&](int r, int c) {
+                            float x;
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at(r, c >> 2) + (c & 3) * 4) : "memory");
+                            return x;
+                        };
+                        if (!XSTEP) {
+                            // column jc + c of the result is row jc + c of the mirrored half:
+                            // two rows of the tile a lane, two columns at a time
+                            __half *const *planes = p.mode == kOrthoA ? p.a : p.b;
+                            const int r = (lane & 15) * 2;
+#pragma unroll 4
+                            for (int c = lane >> 4; c < 32; c += 2) {
+                                if (jc + c >= p.m || i0 + r >= p.m) continue;
+                                const float v0 = value(r, c), v1 = value(r + 1, c);
+                                const long long to = (rows + jc + c) * p.ldm + i0 + r;
+                                const __half2 h = __floats2half2_rn(v0, v1);
+                                *reinterpret_cast<__half2 *>(planes[0] + to) = h;
+                                if (SPLIT) {
+                                    const float2 b = __half22float2(h);
+                                    *reinterpret_cast<__half2 *>(planes[1] + to) = __floats2half2_rn(v0 - b.x, v1 - b.y);
+                                }
+                            }
+                        } else if (i0 + lane < p.m) {
+                            const long long to = mat * p.stride_o + jc * p.ldo + i0 + lane;
+#pragma unroll 4
+                            for (int c = 0; c < 32; ++c) {
+                                if (jc + c >= p.n) break;
+                                const float v = value(lane, c);
+                                if (p.o_bf16)
+                                    static_cast<__nv_bfloat16 *>(p.o)[to + c * p.ldo] = __float2bfloat16_rn(v);
+                                else
+                                    static_cast<float *>(p.o)[to + c * p.ldo] = v;
+                            }
                         }
                     }
                 }
+                __syncwarp();
             };
             if (SPLIT) {
                 uint32_t sum[8][16];
@@ -530,11 +598,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         if (k >= 2 * mine) break;
+                        const int unit = 4 * (k >> 1) + 2 * half + (k & 1);
                         if (seg0 == 0) {
-                            load(unit_of(k), sum[k]);
+                            load(unit, sum[k]);
                         } else {
                             uint32_t v[16];
-                            load(unit_of(k), v);
+                            load(unit, v);
                             tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
@@ -545,23 +614,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                     release();
                 }
                 if (!ok) break;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < 2 * mine) finish(unit_of(k), sum[k]);
+                // one body for all chunks: unrolled, it spills
+#pragma unroll 1
+                for (int k = 0; k < mine; ++k) {
+                    if (k == 0) turn(sum[0], sum[1]);
+                    if (k == 1) turn(sum[2], sum[3]);
+                    if (k == 2) turn(sum[4], sum[5]);
+                    if (k == 3) turn(sum[6], sum[7]);
+                    fetch(k);
+                    finish(k);
+                }
             } else {
+                fetch(0);
                 if (!await()) break;
                 uint32_t v[2][16];
 #pragma unroll 1
-                for (int k = 0; k == 0 || k < 2 * mine; k += 2) {
-                    if (k < 2 * mine) {
-                        load(unit_of(k), v[0]);
-                        load(unit_of(k + 1), v[1]);
+                for (int k = 0; k == 0 || k < mine; ++k) {
+                    if (k < mine) {
+                        load(4 * k + 2 * half, v[0]);
+                        load(4 * k + 2 * half + 1, v[1]);
                         tmem_wait_ld();
                     }
-                    if (k + 2 >= 2 * mine) release();
-                    if (k < 2 * mine) {
-                        finish(unit_of(k), v[0]);
-                        finish(unit_of(k + 1), v[1]);
+                    if (k + 1 >= mine) release();
+                    if (k < mine) {
+                        turn(v[0], v[1]);
+                        finish(k);
+                        if (k + 1 < mine) fetch(k + 1);
                     }
                 }
             }
@@ -811,9 +889,9 @@ cudaError_t prepare_ortho()
 cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, cudaStream_t stream,
                                int *launches)
 {
-    // one part up to 16384 elements: a launch less for small matrices
+    // one part below 8192 elements: a launch less
     const int64_t size = int64_t{u.rows} * u.cols;
-    const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ORTHO_PARTS, size / 16384)));
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ORTHO_PARTS, size / 4096)));
     const __nv_bfloat16 *gb = static_cast<const __nv_bfloat16 *>(u.g);
     const float *gf = static_cast<const float *>(u.g);
     cudaError_t e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb,
@@ -855,7 +933,7 @@ OrthoTile ortho_pick_tile(int step, bool split, int64_t batch, int64_t m, int64_
             const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
             const int planes = split ? 2 : 1;
             const double stage = std::max(4 * mma * (split ? 3 : 1), planes * (P_BYTES + bn / ctas * 128) / 55.0);
-            const double tile = static_cast<double>(kt) * stage, epi = 600 + bn * (step == kOrthoX ? 16.0 : 20.0);
+            const double tile = static_cast<double>(kt) * stage, epi = 600 + bn * (step == kOrthoA ? 10.0 : 14.0);
             const double fill = static_cast<double>(batch * product_tiles(step, ctas, bn, m, n) * ctas) / sm_count;
             const double t = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) + (ctas > 1 ? 1500 : 0);
             if (best_t == 0 || t < best_t) {
@@ -885,7 +963,7 @@ cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, 
     p.tiles = static_cast<int>(tiles);
     p.q_bytes = r.tile.bn / cg * 128;
     p.stage_bytes = planes * (P_BYTES + p.q_bytes);
-    p.stages = std::min(MAX_STAGES, (SMEM_MAX - 1024 - NUM_BARS * 8 - 16) / p.stage_bytes);
+    p.stages = std::min(MAX_STAGES, (SMEM_MAX - 1024 - EPI_BYTES - NUM_BARS * 8 - 16) / p.stage_bytes);
     p.kt = ((r.step == kOrthoA ? w.n : w.m) + BK - 1) / BK;
     p.first = r.first;
     p.last = r.last;
