@@ -109,11 +109,6 @@ __device__ __forceinline__ Tile tile_at(const Params &p, int u)
     return t;
 }
 
-__device__ __forceinline__ uint32_t pack(__half a, __half b)
-{
-    return static_cast<uint32_t>(__half_as_ushort(a)) | static_cast<uint32_t>(__half_as_ushort(b)) << 16;
-}
-
 // Eight FP16 numbers added to v.
 __device__ __forceinline__ void add8(uint4 w, float (&v)[8])
 {
@@ -154,7 +149,9 @@ __device__ __forceinline__ uint4 round8(const float (&v)[8])
 
 // SPLIT: operands of two FP16 numbers.  XSTEP: X' = a X + B X, Q = X with its
 // rows as K; else A or B, symmetric, P and Q the same matrix along K.
-template <int CG, bool SPLIT, bool XSTEP>
+// UNITS: 16-column units of a tile that a warp adds up (SPLIT; 8 for tiles of more
+// than 128 columns, whose sums take 128 registers a thread and leave some spilled).
+template <int CG, bool SPLIT, bool XSTEP, int UNITS>
 __global__ void __launch_bounds__(THREADS, 1)
     ortho_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                  const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1, const Params p)
@@ -383,22 +380,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int i0 = t.i0 + static_cast<int>(rank) * BP + q * 32;  // the warp's first row
             const long long mat = t.b;
             const float *f = p.factors + mat * FACTORS;
-            float diag[4], scale = 0.0f;  // of rows i0 + sub, + 8, ...
+            // With the powers of two of what is read and written in the constants, a
+            // value is acc * scale (A), + e * (row + column) (B; e an element of A,
+            // row and column from the diagonal), or + x * row (X).
+            float scale, row_c[4], column_c = 0.0f;  // rows i0 + sub, + 8, ...
+            if (XSTEP) {
+                const float post = (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
+                scale = post / SCALE_B;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = i0 + sub + 8 * k;
-                diag[k] = i >= p.m ? 0.0f
-                          : XSTEP  ? p.ca + p.db[mat * p.ldm + i]
-                          : p.mode == kOrthoB ? p.da[mat * p.ldm + i]
-                                              : 0.0f;
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i0 + sub + 8 * r;
+                    row_c[r] = i < p.m ? (p.ca + p.db[mat * p.ldm + i]) * post : 0.0f;
+                }
+            } else if (p.mode == kOrthoA) {
+                scale = f[p.first ? kFactorA0 : kFactorA] * SCALE_A;
+            } else {
+                scale = p.cc * (SCALE_B / (SCALE_A * SCALE_A));
+                column_c = p.cc * (SCALE_B / SCALE_A);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i0 + sub + 8 * r;
+                    row_c[r] = i < p.m ? fmaf(p.cc, p.da[mat * p.ldm + i], p.cb) * (SCALE_B / SCALE_A) : 0.0f;
+                }
             }
-            if (XSTEP)
-                scale = 1.0f / SCALE_B;
-            else if (p.mode == kOrthoA)
-                scale = f[p.first ? kFactorA0 : kFactorA];
-            else
-                scale = 1.0f / (SCALE_A * SCALE_A);
-            const float post = !XSTEP ? 1.0f : (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
             const int width = XSTEP ? p.n : p.m, ld = XSTEP ? p.ldn : p.ldm;
             const long long rows = mat * p.m;
 
@@ -441,163 +445,165 @@ __global__ void __launch_bounds__(THREADS, 1)
             const auto fetch = [&](int k) {
                 if (!reads) return;
                 const int j = column(k) + piece * 8;
-                const __half *const *planes = XSTEP ? p.x : p.a;
+                const __half *const *from = XSTEP ? p.x : p.a;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = i0 + sub + 8 * r;
                     const bool in = i < p.m && j < width;
                     const long long o = (rows + i) * ld + j;
-                    extra[0][r] = in ? *reinterpret_cast<const uint4 *>(planes[0] + o) : make_uint4(0u, 0u, 0u, 0u);
-                    if (two) extra[1][r] = in ? *reinterpret_cast<const uint4 *>(planes[1] + o) : make_uint4(0u, 0u, 0u, 0u);
+                    extra[0][r] = in ? *reinterpret_cast<const uint4 *>(from[0] + o) : make_uint4(0u, 0u, 0u, 0u);
+                    if (two) extra[1][r] = in ? *reinterpret_cast<const uint4 *>(from[1] + o) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
             const bool back = XSTEP ? p.last && p.turned : t.mirror;  // results are needed column by column
+            __half *const *planes = XSTEP ? p.x_out : p.mode == kOrthoA ? p.a : p.b;
             const auto finish = [&](int k) {
                 const int jc = column(k), j = jc + piece * 8;
-                if (jc < width) {
-                    float dj[8];
-                    if (!XSTEP && p.mode == kOrthoB && j < width) {
-                        const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
-                        const float4 d0 = d[0], d1 = d[1];
-                        dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
-                        dj[4] = d1.x, dj[5] = d1.y, dj[6] = d1.z, dj[7] = d1.w;
+                if (jc >= width) {
+                    __syncwarp();
+                    return;
+                }
+                float dj[8];
+                if (!XSTEP && p.mode == kOrthoB && j < width) {
+                    const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
+                    const float4 d0 = d[0], d1 = d[1];
+                    dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
+                    dj[4] = d1.x, dj[5] = d1.y, dj[6] = d1.z, dj[7] = d1.w;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) dj[c] *= column_c;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = sub + 8 * r, i = i0 + row;
+                    if (i >= p.m || j >= width) continue;
+                    const float4 a0 = lds_f4(at(row, 2 * piece)), a1 = lds_f4(at(row, 2 * piece + 1));
+                    float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, e[8] = {};
+                    if (reads) {
+                        add8(extra[0][r], e);
+                        if (two) add8(extra[1][r], e);
                     }
+                    if (!XSTEP && i >= j && i < j + 8) {
+                        // the diagonal, kept in FP32 and out of the matrix
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = sub + 8 * r, i = i0 + row;
-                        if (i >= p.m || j >= width) continue;
-                        const uint4 a0 = lds_u4(at(row, 2 * piece)), a1 = lds_u4(at(row, 2 * piece + 1));
-                        const uint32_t w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-                        float v[8];
+                        for (int c = 0; c < 8; ++c)
+                            if (j + c == i) {
+                                if (p.mode == kOrthoA) {
+                                    p.da[mat * p.ldm + i] = v[c] * scale * (1.0f / SCALE_A);
+                                } else {
+                                    const float d = p.da[mat * p.ldm + i];
+                                    p.db[mat * p.ldm + i] =
+                                        p.cb * d + p.cc * fmaf(d, d, v[c] * (1.0f / (SCALE_A * SCALE_A)));
+                                }
+                                v[c] = e[c] = 0.0f;
+                            }
+                    }
+                    const float rc = reads ? row_c[r] : 0.0f;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(w[c]) * scale;
-                        const long long o = (rows + i) * ld + j;
-                        if (!XSTEP) {
-                            const float up = p.mode == kOrthoA ? SCALE_A : SCALE_B;
-                            if (p.mode == kOrthoA) {
+                    for (int c = 0; c < 8; ++c) {
+                        v[c] *= scale;
+                        if (XSTEP)
+                            v[c] = fmaf(e[c], rc, v[c]);
+                        else if (p.mode == kOrthoB)
+                            v[c] = fmaf(e[c], rc + dj[c], v[c]);
+                    }
+                    const long long o = (rows + i) * ld + j;
+                    if (!XSTEP || !p.last) {
+                        if (SPLIT || XSTEP) {
+                            float rest[8];
+                            *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v, rest);
+                            *reinterpret_cast<uint4 *>(planes[1] + o) = round8(rest);
+                        } else {
+                            *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v);
+                        }
+                    } else if (!p.turned) {
+                        const long long to = mat * p.stride_o + i * p.ldo + j;
+                        if (p.o_bf16) {
+                            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + to;
+                            if (p.o_vec && j + 8 <= p.n) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+                                    y[c] = *reinterpret_cast<const uint32_t *>(&b);
+                                }
+                                *reinterpret_cast<uint4 *>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+                            } else {
 #pragma unroll
                                 for (int c = 0; c < 8; ++c)
-                                    if (j + c == i) {
-                                        p.da[mat * p.ldm + i] = v[c];
-                                        v[c] = 0.0f;
-                                    }
-                            } else {
-                                float e[8] = {};
-                                add8(extra[0][r], e);
-                                if (SPLIT) add8(extra[1][r], e);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const float a = e[c] * (1.0f / SCALE_A);
-                                    if (j + c == i) {
-                                        p.db[mat * p.ldm + i] = p.cb * diag[r] + p.cc * fmaf(diag[r], diag[r], v[c]);
-                                        v[c] = 0.0f;
-                                    } else {
-                                        v[c] = p.cb * a + p.cc * fmaf(diag[r] + dj[c], a, v[c]);
-                                    }
-                                }
-                            }
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] *= up;
-                            __half *const *planes = p.mode == kOrthoA ? p.a : p.b;
-                            if (SPLIT) {
-                                float rest[8];
-                                *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v, rest);
-                                *reinterpret_cast<uint4 *>(planes[1] + o) = round8(rest);
-                            } else {
-                                *reinterpret_cast<uint4 *>(planes[0] + o) = round8(v);
+                                    if (j + c < p.n) out[c] = __float2bfloat16_rn(v[c]);
                             }
                         } else {
-                            float x[8] = {};
-                            add8(extra[0][r], x);
-                            if (two) add8(extra[1][r], x);
+                            float *out = static_cast<float *>(p.o) + to;
+                            if (p.o_vec && j + 8 <= p.n) {
+                                *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+                                *(reinterpret_cast<float4 *>(out) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+                            } else {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] = fmaf(diag[r], x[c], v[c]) * post;
-                            if (!p.last) {
-                                float rest[8];
-                                *reinterpret_cast<uint4 *>(p.x_out[0] + o) = round8(v, rest);
-                                *reinterpret_cast<uint4 *>(p.x_out[1] + o) = round8(rest);
-                            } else if (!p.turned) {
-                                const long long to = mat * p.stride_o + i * p.ldo + j;
-                                if (p.o_bf16) {
-                                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.o) + to;
-                                    if (p.o_vec && j + 8 <= p.n) {
-                                        uint32_t y[4];
-#pragma unroll
-                                        for (int c = 0; c < 4; ++c) {
-                                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-                                            y[c] = *reinterpret_cast<const uint32_t *>(&b);
-                                        }
-                                        *reinterpret_cast<uint4 *>(out) = make_uint4(y[0], y[1], y[2], y[3]);
-                                    } else {
-#pragma unroll
-                                        for (int c = 0; c < 8; ++c)
-                                            if (j + c < p.n) out[c] = __float2bfloat16_rn(v[c]);
-                                    }
-                                } else {
-                                    float *out = static_cast<float *>(p.o) + to;
-                                    if (p.o_vec && j + 8 <= p.n) {
-                                        *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
-                                        *(reinterpret_cast<float4 *>(out) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-                                    } else {
-#pragma unroll
-                                        for (int c = 0; c < 8; ++c)
-                                            if (j + c < p.n) out[c] = v[c];
-                                    }
-                                }
+                                for (int c = 0; c < 8; ++c)
+                                    if (j + c < p.n) out[c] = v[c];
                             }
-                        }
-                        if (back) {
-                            sts_f4(at(row, 2 * piece), make_float4(v[0], v[1], v[2], v[3]));
-                            sts_f4(at(row, 2 * piece + 1), make_float4(v[4], v[5], v[6], v[7]));
                         }
                     }
                     if (back) {
-                        __syncwarp();
-                        const auto value = [&](int r, int c) {
-                            float x;
-                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at(r, c >> 2) + (c & 3) * 4) : "memory");
-                            return x;
-                        };
-                        if (!XSTEP) {
-                            // column jc + c of the result is row jc + c of the mirrored half:
-                            // two rows of the tile a lane, two columns at a time
-                            __half *const *planes = p.mode == kOrthoA ? p.a : p.b;
-                            const int r = (lane & 15) * 2;
-#pragma unroll 4
-                            for (int c = lane >> 4; c < 32; c += 2) {
-                                if (jc + c >= p.m || i0 + r >= p.m) continue;
-                                const float v0 = value(r, c), v1 = value(r + 1, c);
-                                const long long to = (rows + jc + c) * p.ldm + i0 + r;
-                                const __half2 h = __floats2half2_rn(v0, v1);
-                                *reinterpret_cast<__half2 *>(planes[0] + to) = h;
+                        sts_f4(at(row, 2 * piece), make_float4(v[0], v[1], v[2], v[3]));
+                        sts_f4(at(row, 2 * piece + 1), make_float4(v[4], v[5], v[6], v[7]));
+                    }
+                }
+                __syncwarp();
+                if (!back) return;
+                if (!XSTEP) {
+                    // Column c of the result is row jc + c of the mirrored half: rows r and
+                    // r + 1 of the tile a lane, columns 2 n and 2 n + 1 an instruction.
+                    const int r = (lane & 15) * 2, h = lane >> 4;
+                    const uint32_t base = stage + r * 128 + h * 4;
+                    __half *to = planes[0] + (rows + jc + h) * p.ldm + i0 + r;
+                    const long long step = 2LL * p.ldm, rest = SPLIT ? planes[1] - planes[0] : 0;
+                    const bool in = i0 + r < p.m;
+                    const int left = p.m - jc - h;
+#pragma unroll
+                    for (int n = 0; n < 16; n += 4) {
+                        float v0[4], v1[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t c = ((n + x) >> 1) ^ (r & 7), low = ((n + x) & 1) * 8;
+                            v0[x] = lds_f1(base + c * 16 + low);
+                            v1[x] = lds_f1(base + 128 + (c ^ 1) * 16 + low);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            if (in && 2 * (n + x) < left) {
+                                const __half2 b = __floats2half2_rn(v0[x], v1[x]);
+                                *reinterpret_cast<__half2 *>(to) = b;
                                 if (SPLIT) {
-                                    const float2 b = __half22float2(h);
-                                    *reinterpret_cast<__half2 *>(planes[1] + to) = __floats2half2_rn(v0 - b.x, v1 - b.y);
+                                    const float2 w = __half22float2(b);
+                                    *reinterpret_cast<__half2 *>(to + rest) = __floats2half2_rn(v0[x] - w.x, v1[x] - w.y);
                                 }
                             }
-                        } else if (i0 + lane < p.m) {
-                            const long long to = mat * p.stride_o + jc * p.ldo + i0 + lane;
-#pragma unroll 4
-                            for (int c = 0; c < 32; ++c) {
-                                if (jc + c >= p.n) break;
-                                const float v = value(lane, c);
-                                if (p.o_bf16)
-                                    static_cast<__nv_bfloat16 *>(p.o)[to + c * p.ldo] = __float2bfloat16_rn(v);
-                                else
-                                    static_cast<float *>(p.o)[to + c * p.ldo] = v;
-                            }
+                            to += step;
                         }
+                    }
+                } else if (i0 + lane < p.m) {
+                    const long long to = mat * p.stride_o + jc * p.ldo + i0 + lane;
+#pragma unroll 8
+                    for (int c = 0; c < 32; ++c) {
+                        if (jc + c >= p.n) break;
+                        const float v = lds_f1(at(lane, c >> 2) + (c & 3) * 4);
+                        if (p.o_bf16)
+                            static_cast<__nv_bfloat16 *>(p.o)[to + c * p.ldo] = __float2bfloat16_rn(v);
+                        else
+                            static_cast<float *>(p.o)[to + c * p.ldo] = v;
                     }
                 }
                 __syncwarp();
             };
             if (SPLIT) {
-                uint32_t sum[8][16];
+                uint32_t sum[UNITS][16];
                 for (int seg0 = 0; seg0 < p.kt; seg0 += SEG) {
+                    if (UNITS == 4 && seg0 + SEG >= p.kt) fetch(0);
                     if (!await()) break;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (k >= 2 * mine) break;
+                    for (int k = 0; k < UNITS; ++k) {
+                        if (k >= 2 * mine) continue;
                         const int unit = 4 * (k >> 1) + 2 * half + (k & 1);
                         if (seg0 == 0) {
                             load(unit, sum[k]);
@@ -617,12 +623,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // one body for all chunks: unrolled, it spills
 #pragma unroll 1
                 for (int k = 0; k < mine; ++k) {
-                    if (k == 0) turn(sum[0], sum[1]);
-                    if (k == 1) turn(sum[2], sum[3]);
-                    if (k == 2) turn(sum[4], sum[5]);
-                    if (k == 3) turn(sum[6], sum[7]);
-                    fetch(k);
+#pragma unroll
+                    for (int n = 0; n < UNITS / 2; ++n)
+                        if (k == n) turn(sum[2 * n], sum[2 * n + 1]);
+                    if (UNITS > 4) fetch(k);
                     finish(k);
+                    if (UNITS == 4 && k + 1 < mine) fetch(k + 1);
                 }
             } else {
                 fetch(0);
@@ -669,6 +675,23 @@ constexpr int NORM_THREADS = 256;
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// 16 bytes of a row.
+__device__ __forceinline__ void load_vec(const float *src, float (&x)[4])
+{
+    const float4 v = *reinterpret_cast<const float4 *>(src);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_vec(const __nv_bfloat16 *src, float (&x)[8])
+{
+    const uint4 v = *reinterpret_cast<const uint4 *>(src);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
 // From the norm of a matrix: the factors of its products and the power of two
 // of X (two factors, whose product may leave FP32's range).
 __device__ void write_factors(double norm, double eps, float *f)
@@ -706,9 +729,10 @@ __device__ void write_factors(double norm, double eps, float *f)
 // of one part has its factors written here.
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
-    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, float eps,
+    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, float eps, bool vec,
                 double *parts, float *factors)
 {
+    constexpr int N = 16 / sizeof(T);
     __shared__ double sums[NORM_THREADS / 32];
     __shared__ float tops[NORM_THREADS / 32];
     griddep_wait();
@@ -728,15 +752,24 @@ __global__ void __launch_bounds__(NORM_THREADS)
             for (int c0 = 0; c0 < cols; c0 += 32 * 64) {  // 64 additions in FP32 at a time
                 float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const int c1 = min(cols, c0 + 32 * 64);
+                const auto add = [&](float x, int k) {
+                    x *= scale;
+                    top = fmaxf(top, fabsf(x));
+                    s[k & 3] = fmaf(x, x, s[k & 3]);
+                };
+                int c = c0 + lane * N;
+                if (vec) {
 #pragma unroll 4
-                for (int c = c0 + lane; c < c1; c += 128) {
+                    for (; c + N <= c1; c += 32 * N) {
+                        float x[N];
+                        load_vec(row + c, x);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c + 32 * k < c1) {
-                            const float x = to_f32(row[c + 32 * k]) * scale;
-                            top = fmaxf(top, fabsf(x));
-                            s[k] = fmaf(x, x, s[k]);
-                        }
+                        for (int k = 0; k < N; ++k) add(x[k], k);
+                    }
+                    for (int k = 0; k < N && c + k < c1; ++k) add(to_f32(row[c + k]), k);
+                } else {
+#pragma unroll 8
+                    for (c = c0 + lane; c < c1; c += 32) add(to_f32(row[c]), 0);
                 }
                 total += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
             }
@@ -787,8 +820,8 @@ __global__ void factors_kernel(const double *parts, int num_parts, float eps, fl
 // elements.
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
-    start_kernel(const T *g, long long ldg, long long stride, int turned, int m, int n, int ldn, int tiles_j, int tiles,
-                 __half *x0, __half *x1, const float *factors)
+    start_kernel(const T *g, long long ldg, long long stride, bool vec, int turned, int m, int n, int ldn, int tiles_j,
+                 int tiles, __half *x0, __half *x1, const float *factors)
 {
     __shared__ float tile[64][65];
     griddep_wait();
@@ -797,38 +830,50 @@ __global__ void __launch_bounds__(NORM_THREADS)
     const int t = static_cast<int>(blockIdx.x - b * tiles);
     const int i0 = t / tiles_j * 64, j0 = t % tiles_j * 64;
     const float s0 = factors[b * FACTORS + kFactorUp0], s1 = factors[b * FACTORS + kFactorUp1];
+    constexpr int N = 16 / sizeof(T);
     const T *base = g + b * stride;
-    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+    // tile[a][c]: row a of G's part (64 x 64), turned on the way out
+    const int ga = turned ? j0 : i0, gc = turned ? i0 : j0, rows = turned ? n : m, cols = turned ? m : n;
+    if (vec) {
 #pragma unroll
-    for (int k = r; k < 64; k += NORM_THREADS / 64) {
-        float v = 0.0f;
-        if (turned) {
-            if (j0 + k < n && i0 + c < m) v = to_f32(base[(j0 + k) * ldg + i0 + c]);
-            tile[c][k] = v * s0 * s1;
-        } else {
-            if (i0 + k < m && j0 + c < n) v = to_f32(base[(i0 + k) * ldg + j0 + c]);
-            tile[k][c] = v * s0 * s1;
+        for (int k = threadIdx.x; k < 64 * 64 / N; k += NORM_THREADS) {
+            const int a = k / (64 / N), c = k % (64 / N) * N;
+            float x[N];
+            if (ga + a < rows && gc + c + N <= cols) {
+                load_vec(base + (ga + a) * ldg + gc + c, x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    x[i] = ga + a < rows && gc + c + i < cols ? to_f32(base[(ga + a) * ldg + gc + c + i]) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) tile[a][c + i] = x[i] * s0 * s1;
+        }
+    } else {
+#pragma unroll 4
+        for (int k = threadIdx.x; k < 64 * 64; k += NORM_THREADS) {
+            const int a = k >> 6, c = k & 63;
+            tile[a][c] = (ga + a < rows && gc + c < cols ? to_f32(base[(ga + a) * ldg + gc + c]) : 0.0f) * s0 * s1;
         }
     }
     __syncthreads();
-    const int c2 = (threadIdx.x & 31) * 2;
 #pragma unroll
-    for (int k = threadIdx.x >> 5; k < 64; k += NORM_THREADS / 32)
-        if (i0 + k < m) {
-            const float a = tile[k][c2], z = tile[k][c2 + 1];
-            const __half h0 = __float2half_rn(a), h1 = __float2half_rn(z);
-            const long long at = (b * m + i0 + k) * ldn + j0 + c2;
-            *reinterpret_cast<uint32_t *>(x0 + at) = pack(h0, h1);
-            if (x1)
-                *reinterpret_cast<uint32_t *>(x1 + at) =
-                    pack(__float2half_rn(a - __half2float(h0)), __float2half_rn(z - __half2float(h1)));
-        }
+    for (int k = threadIdx.x; k < 64 * 8; k += NORM_THREADS) {
+        const int r = k >> 3, c = (k & 7) * 8;  // 16 bytes of X
+        if (i0 + r >= m) continue;
+        float v[8], rest[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = turned ? tile[c + i][r] : tile[r][c + i];
+        const long long at = (b * m + i0 + r) * ldn + j0 + c;
+        *reinterpret_cast<uint4 *>(x0 + at) = round8(v, rest);
+        if (x1) *reinterpret_cast<uint4 *>(x1 + at) = round8(rest);
+    }
 }
 
-template <int CG, bool SPLIT, bool XSTEP>
+template <int CG, bool SPLIT, bool XSTEP, int UNITS>
 cudaError_t launch_one(const CUtensorMap (&maps)[4], const Params &p, int grid, cudaStream_t stream)
 {
-    return launch_pdl(ortho_kernel<CG, SPLIT, XSTEP>, grid, THREADS, SMEM_MAX, stream, CG, maps[0], maps[1], maps[2],
+    return launch_pdl(ortho_kernel<CG, SPLIT, XSTEP, UNITS>, grid, THREADS, SMEM_MAX, stream, CG, maps[0], maps[1], maps[2],
                       maps[3], p);
 }
 
@@ -868,6 +913,32 @@ void ortho_layout(OrthoBuffers &o, uint8_t *base, bool split)
     o.factors = reinterpret_cast<float *>(take(static_cast<size_t>(o.batch) * ORTHO_FACTORS * 4));
 }
 
+template <int CG>
+static cudaError_t ready_for()
+{
+    cudaError_t e = kernel_ready<ortho_kernel<CG, false, false, 8>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, true, 8>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, false, 4>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, true, 4>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, false, 8>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, true, 8>>(SMEM_MAX);
+    return e;
+}
+
+template <int CG>
+static cudaError_t launch_for(bool split, bool x, int bn, const CUtensorMap (&maps)[4], const Params &p, int grid,
+                              cudaStream_t stream)
+{
+    if (!split)
+        return x ? launch_one<CG, false, true, 8>(maps, p, grid, stream)
+                 : launch_one<CG, false, false, 8>(maps, p, grid, stream);
+    if (bn <= 128)
+        return x ? launch_one<CG, true, true, 4>(maps, p, grid, stream)
+                 : launch_one<CG, true, false, 4>(maps, p, grid, stream);
+    return x ? launch_one<CG, true, true, 8>(maps, p, grid, stream)
+             : launch_one<CG, true, false, 8>(maps, p, grid, stream);
+}
+
 cudaError_t prepare_ortho()
 {
     cudaError_t e = kernel_ready<norm_kernel<float>>(0);
@@ -875,14 +946,8 @@ cudaError_t prepare_ortho()
     if (e == cudaSuccess) e = kernel_ready<factors_kernel>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<float>>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<__nv_bfloat16>>(0);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, false, false>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, false, true>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, true, false>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<1, true, true>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, false, false>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, false, true>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, true, false>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<2, true, true>>(SMEM_MAX);
+    if (e == cudaSuccess) e = ready_for<1>();
+    if (e == cudaSuccess) e = ready_for<2>();
     return e;
 }
 
@@ -892,12 +957,14 @@ cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bo
     // one part below 8192 elements: a launch less
     const int64_t size = int64_t{u.rows} * u.cols;
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ORTHO_PARTS, size / 4096)));
+    const int es = u.bf16 ? 2 : 4;
+    const bool vec = reinterpret_cast<uintptr_t>(u.g) % 16 == 0 && (u.ldg * es) % 16 == 0 && (u.stride_g * es) % 16 == 0;
     const __nv_bfloat16 *gb = static_cast<const __nv_bfloat16 *>(u.g);
     const float *gf = static_cast<const float *>(u.g);
     cudaError_t e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb,
-                                        u.ldg, u.stride_g, u.rows, u.cols, parts, u.eps, w.parts, w.factors)
+                                        u.ldg, u.stride_g, u.rows, u.cols, parts, u.eps, vec, w.parts, w.factors)
                            : launch_pdl(norm_kernel<float>, parts * w.batch, NORM_THREADS, 0, stream, 1, gf, u.ldg,
-                                        u.stride_g, u.rows, u.cols, parts, u.eps, w.parts, w.factors);
+                                        u.stride_g, u.rows, u.cols, parts, u.eps, vec, w.parts, w.factors);
     if (e != cudaSuccess) return e;
     ++*launches;
     if (parts > 1) {
@@ -911,8 +978,8 @@ cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bo
     __half *x0 = reinterpret_cast<__half *>(w.x[0][0]), *x1 = split ? reinterpret_cast<__half *>(w.x[0][1]) : nullptr;
     const float *factors = w.factors;
     e = u.bf16 ? launch_pdl(start_kernel<__nv_bfloat16>, grid, NORM_THREADS, 0, stream, 1, gb, u.ldg, u.stride_g,
-                            turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, factors)
-               : launch_pdl(start_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, turned, w.m,
+                            vec, turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, factors)
+               : launch_pdl(start_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, vec, turned, w.m,
                             w.n, w.ldn, tiles_j, tiles, x0, x1, factors);
     if (e == cudaSuccess) ++*launches;
     return e;
@@ -933,7 +1000,8 @@ OrthoTile ortho_pick_tile(int step, bool split, int64_t batch, int64_t m, int64_
             const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
             const int planes = split ? 2 : 1;
             const double stage = std::max(4 * mma * (split ? 3 : 1), planes * (P_BYTES + bn / ctas * 128) / 55.0);
-            const double tile = static_cast<double>(kt) * stage, epi = 600 + bn * (step == kOrthoA ? 10.0 : 14.0);
+            const double tile = static_cast<double>(kt) * stage, epi =
+                600 + bn * (step == kOrthoA ? 10.0 : 14.0) * (split ? bn > 128 ? 4 : 1.5 : 1);
             const double fill = static_cast<double>(batch * product_tiles(step, ctas, bn, m, n) * ctas) / sm_count;
             const double t = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) + (ctas > 1 ? 1500 : 0);
             if (best_t == 0 || t < best_t) {
@@ -993,12 +1061,8 @@ cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, 
     const int64_t slots = std::max(1, (max_ctas > 0 ? std::min(max_ctas, sm_count) : sm_count) / cg);
     const int grid = static_cast<int>(cg * std::min<int64_t>(tiles * w.batch, slots));
     const bool x = r.step == kOrthoX;
-    if (cg == 2) {
-        if (r.split) return x ? launch_one<2, true, true>(maps, p, grid, r.stream) : launch_one<2, true, false>(maps, p, grid, r.stream);
-        return x ? launch_one<2, false, true>(maps, p, grid, r.stream) : launch_one<2, false, false>(maps, p, grid, r.stream);
-    }
-    if (r.split) return x ? launch_one<1, true, true>(maps, p, grid, r.stream) : launch_one<1, true, false>(maps, p, grid, r.stream);
-    return x ? launch_one<1, false, true>(maps, p, grid, r.stream) : launch_one<1, false, false>(maps, p, grid, r.stream);
+    return cg == 2 ? launch_for<2>(r.split, x, r.tile.bn, maps, p, grid, r.stream)
+                   : launch_for<1>(r.split, x, r.tile.bn, maps, p, grid, r.stream);
 }
 
 }  // namespace dg

@@ -159,6 +159,13 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float lds_f1(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void sts_f4(uint32_t addr, float4 v)
 {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
