@@ -321,43 +321,30 @@ __global__ void __launch_bounds__(THREADS)
 // A warp takes WIDEN x 512 codes of a row, 16 a lane at a time.  Rows are read
 // up to the end of their last 16 bytes, which the pitch holds, and written so.
 constexpr int WIDEN = 4;
-struct WidenJob {
-    const int8_t *src;
-    long long ld, rows;
-    __half *dst;
-    const long long *offsets;
-    long long rows_per;
-};
 
-__global__ void __launch_bounds__(THREADS) widen_kernel(const WidenJob a, const WidenJob b, int K)
+__global__ void __launch_bounds__(THREADS)
+    widen_kernel(const int8_t *src, long long ld, long long rows, int K, __half *dst)
 {
     griddep_wait();
     griddep_launch_dependents();
     const int pieces = (K + 15) / 16, chunks = (pieces + 32 * WIDEN - 1) / (32 * WIDEN), lane = threadIdx.x & 31;
-    const long long pitch = pieces * 16LL, all = (a.rows + b.rows) * chunks;
+    const long long pitch = pieces * 16LL, all = rows * chunks;
     for (long long w = blockIdx.x * (THREADS / 32LL) + (threadIdx.x >> 5); w < all; w += gridDim.x * (THREADS / 32LL)) {
         const long long row = w / chunks;
         const int p0 = static_cast<int>(w - row * chunks) * 32 * WIDEN + lane;
-        const bool second = row >= a.rows;
-        const WidenJob &j = second ? b : a;
-        const long long r = second ? row - a.rows : row;
-        if (j.offsets != nullptr) {
-            const long long g = r / j.rows_per;
-            if (j.offsets[g] >= j.offsets[g + 1]) continue;
-        }
-        const uint4 *src = reinterpret_cast<const uint4 *>(j.src + r * j.ld);
-        uint4 *dst = reinterpret_cast<uint4 *>(j.dst + r * pitch);
+        const uint4 *from = reinterpret_cast<const uint4 *>(src + row * ld);
+        uint4 *to = reinterpret_cast<uint4 *>(dst + row * pitch);
         uint4 c[WIDEN];
 #pragma unroll
         for (int i = 0; i < WIDEN; ++i)
-            if (p0 + i * 32 < pieces) c[i] = src[p0 + i * 32];
+            if (p0 + i * 32 < pieces) c[i] = from[p0 + i * 32];
 #pragma unroll
         for (int i = 0; i < WIDEN; ++i)
             if (p0 + i * 32 < pieces) {
                 uint4 lo, hi;
                 i8_to_f16(c[i], lo, hi);
-                dst[2 * (p0 + i * 32)] = lo;
-                dst[2 * (p0 + i * 32) + 1] = hi;
+                to[2 * (p0 + i * 32)] = lo;
+                to[2 * (p0 + i * 32) + 1] = hi;
             }
     }
 }
@@ -437,17 +424,15 @@ cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, i
                                          static_cast<long long>(ldd), vec);
 }
 
-cudaError_t launch_i8_widen(const int8_t *a, int64_t lda, int64_t rows_a, const int8_t *b, int64_t ldb, int64_t rows_b,
-                            int64_t K, void *a16, void *b16, const int64_t *offsets, int64_t rows_per, int sm_count,
+cudaError_t launch_i8_widen(const int8_t *src, int64_t ld, int64_t rows, int64_t K, void *dst, int sm_count,
                             cudaStream_t stream)
 {
-    WidenJob ja = {a, lda, rows_a, static_cast<__half *>(a16), nullptr, 1};
-    WidenJob jb = {b, ldb, rows_b, static_cast<__half *>(b16), reinterpret_cast<const long long *>(offsets), rows_per};
     const int64_t chunks = (K + 512 * WIDEN - 1) / (512 * WIDEN);
     const cudaError_t e = kernel_ready<widen_kernel>(0);
     if (e != cudaSuccess) return e;
-    return launch_pdl(widen_kernel, grid_for((rows_a + rows_b) * chunks, THREADS / 32, 8, sm_count), THREADS, 0, stream,
-                      1, ja, jb, static_cast<int>(K));
+    return launch_pdl(widen_kernel, grid_for(rows * chunks, THREADS / 32, 8, sm_count), THREADS, 0, stream, 1, src,
+                      static_cast<long long>(ld), static_cast<long long>(rows), static_cast<int>(K),
+                      static_cast<__half *>(dst));
 }
 
 }  // namespace dg

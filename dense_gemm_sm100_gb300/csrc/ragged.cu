@@ -25,13 +25,16 @@
 // integers, and every value of -128 .. 127 is an FP16 number, every product and
 // every sum of 1024 products an FP32 number: the accumulator holds the integer
 // sum exactly as long as it fits 24 bits (at any K up to 1024; FP32 results add
-// segments of 768).  TMA fetches the bytes; a converter warp turns 16 bytes a
-// lane into 16 FP16 values (the byte with its sign bit flipped, put below the
-// exponent of 1024, is 1152 more than the value), writes them in the swizzled
-// layout of the MMA, and hands the stage on.  Eight warps in two teams, each
-// with every other stage of the ring (an even number of stages).  kRaggedI8Wide finds its operands in FP16 (a product
-// with many rows converts once, not once a tile, and runs on CTA pairs).  In the
-// epilogue a lane multiplies by its column's scale and each row's.
+// segments of 768).  Q, the activations, is converted in memory before (2 bytes an
+// element, small beside the weights).  P, the weights, arrives as bytes, 128 of K a
+// stage: TMA goes row by row, and boxes 64 bytes wide took 0.4 us for 8 KB, which
+// set the pace (14336 x 4096 weights and 4 rows: 27 us, of which the bytes take 9).
+// A converter thread takes 64 bytes of a row from shared memory, turns them into
+// FP16 pairs (the byte with its sign bit flipped, put below the exponent of 1024,
+// is 1152 more than the value) and writes them to tensor memory, from where the MMA
+// takes its M operand; shared memory sees P once as bytes and never as FP16, and no
+// fence to the async proxy is needed.  Eight warps, four for each half of a stage.
+// In the epilogue a lane multiplies by its column's scale and each row's.
 //
 // Block scales.  A row's scales are contiguous bytes; the tensor core wants,
 // for 128 rows and 128 elements of K, one 4-byte word per row, row i in lane
@@ -99,7 +102,8 @@ constexpr int P_BYTES = BP * 128;  // 128 rows of P x 128 bytes of K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARS = 2 * MAX_STAGES + 2 + 2 + 2 + 2 + 1;
-constexpr int NUM_BARS_I8 = NUM_BARS + MAX_STAGES;
+constexpr int SLOT_COLS = 64, MAX_SLOTS = 4;  // 8-bit operands: stages of P in tensor memory
+constexpr int NUM_BARS_I8 = NUM_BARS + MAX_STAGES + 2 * MAX_SLOTS;
 // Accumulators at tensor-memory columns 0 and ACC1.  For 4-bit operands the
 // scales of two stages live at SF_COL, which leaves two accumulators of 224
 // rows: 157 us for 8192 x 14336 x 4096, against 165 us with tiles of 256 rows
@@ -111,9 +115,11 @@ constexpr int SF_PART = 1024;    // a stage's words of 128 rows
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_BYTES = EPI_WARPS * 2048;  // a warp's staging: 16 x 32 FP32, or BF16 in half of it
 constexpr int WARPS = 2 + EPI_WARPS, WARPS_MX = WARPS + 3;
-constexpr int CONV_TEAMS = 2, CONV_WARPS = 4;  // converter warps of a team
-constexpr int WARPS_I8 = WARPS + CONV_TEAMS * CONV_WARPS;
-constexpr int P_RAW = BP * 64;  // 128 rows of P x 64 bytes of K, as fetched
+constexpr int CONV_WARPS = 8;  // 8-bit operands: converter warps
+constexpr int WARPS_I8 = WARPS + CONV_WARPS;
+// Two accumulators of 192 rows leave two slots of P (pairs only: a CTA alone would
+// stage 24 KB of Q); FP32 sums in segments take 128, whose sums fit the registers.
+constexpr int I8_MOST_BN = 192;
 constexpr int SMEM_MAX = 227 * 1024;
 
 struct Params {
@@ -130,6 +136,7 @@ struct Params {
     long long lds_p, lds_q;
     int blocks;
     const float *row_scale_p, *row_scale_q;  // 8-bit operands
+    int acc1, slots;  // their second accumulator's column (P's slots follow it), slots
     int *status;
     unsigned long long timeout_ns;
     int debug_drop;
@@ -270,14 +277,13 @@ __device__ __forceinline__ int mma_n(const Params &p, const Tile &t)
     return RAGGED_K ? p.bn : (t.qn + G - 1) / G * G;
 }
 
-__host__ __device__ constexpr bool is_i8(int kind) { return kind == kRaggedI8 || kind == kRaggedI8Wide; }
 __host__ __device__ constexpr int warps_of(int kind) { return kind == kRaggedMx4 ? WARPS_MX : kind == kRaggedI8 ? WARPS_I8 : WARPS; }
 __host__ __device__ constexpr int bar_bytes(int kind) { return 8 * (kind == kRaggedI8 ? NUM_BARS_I8 : NUM_BARS); }
 // Behind the barriers: the tensor-memory address, the abort flag, a sum a warp.
 constexpr int tail_bytes(int kind) { return 16 + (kind == kRaggedI8 ? 80 : 64); }
 
 // Stages of a segment of a long FP32 sum.
-__host__ __device__ constexpr int seg_stages(int kind) { return kind == kRaggedTf32 ? 8 : 12; }
+__host__ __device__ constexpr int seg_stages(int kind) { return kind == kRaggedTf32 ? 8 : kind == kRaggedI8 ? 6 : 12; }
 
 // SUM: long FP32 sums (see above).
 template <int KIND, int CG, bool P_MN, bool RAGGED_K, bool SUM>
@@ -285,13 +291,13 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
     ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p)
 {
     constexpr bool MX = KIND == kRaggedMx4;
-    constexpr bool I8 = is_i8(KIND), CONV = KIND == kRaggedI8;
+    constexpr bool I8 = KIND == kRaggedI8;
     constexpr int SEG = seg_stages(KIND);
     constexpr int THREADS = 32 * warps_of(KIND);
     constexpr int ES = KIND == kRaggedBf16 || I8 ? 2 : 4;           // bytes an element as multiplied (not for 4-bit)
-    constexpr int SUM_UNITS = CONV ? 4 : 8;                         // 16-row units of a tile that a warp adds up
-    constexpr int BK = MX ? 256 : 128 / ES;                         // K elements of a stage
-    constexpr int K_STEPS = 4;                                      // MMA instructions of a stage, 32 bytes of K each
+    constexpr int SUM_UNITS = I8 ? 4 : 8;                           // 16-row units of a tile that a warp adds up
+    constexpr int BK = MX ? 256 : I8 ? 128 : 128 / ES;              // K elements of a stage
+    constexpr int K_STEPS = I8 ? 8 : 4;                             // MMA instructions of a stage, 32 bytes of K each
     constexpr int CHUNK = 128 / ES;                                 // MN-major: elements of a 128-byte row
     constexpr int BOX_BYTES = BK * 128;                             // MN-major: one chunk of a stage
     constexpr uint32_t MN_LAYOUT = ES == 2 ? kLayoutSw128 : kLayoutSw128Atom32;
@@ -323,7 +329,10 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
     const uint32_t sready_bar = tempty_bar + 16;            // [2], scale slot filled, used in the even CTA
     const uint32_t sfree_bar = sready_bar + 16;             // [2], scale slot read
     const uint32_t drain_bar = sfree_bar + 16;
-    const uint32_t conv_bar = drain_bar + 8;                // [stages], stage converted (kRaggedI8 only)
+    // kRaggedI8 only
+    const uint32_t raw_bar = drain_bar + 8;               // [stages], P's bytes have arrived
+    const uint32_t conv_bar = raw_bar + 8 * MAX_STAGES;   // [slots], slot converted, used in the even CTA
+    const uint32_t slot_bar = conv_bar + 8 * MAX_SLOTS;   // [slots], slot read
     uint8_t *tail = smem + ring + 2 * sf_slot + EPI_BYTES + p.table_bytes + bar_bytes(KIND);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
@@ -338,14 +347,19 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
     const int per_unit = CG == 1 ? p.split : CG;
     const int first_unit = blockIdx.x / per_unit;
     const int unit_step = gridDim.x / per_unit;
-    const int acc1 = MX ? ACC1_MX : ACC1;
+    const int acc1 = I8 ? p.acc1 : MX ? ACC1_MX : ACC1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar + 8 * s, 1);
             mbar_init(empty_bar + 8 * s, 1);  // the MMA issuer's commit
-            if (CONV) mbar_init(conv_bar + 8 * s, CONV_WARPS);
+            if (I8) mbar_init(raw_bar + 8 * s, 1);
         }
+        if (I8)
+            for (int k = 0; k < p.slots; ++k) {
+                mbar_init(conv_bar + 8 * k, CONV_WARPS * CG);
+                mbar_init(slot_bar + 8 * k, 1);
+            }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar + 8 * b, 1);
             mbar_init(tempty_bar + 8 * b, EPI_WARPS * CG);
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             const int q_cta = p.bn / CG;  // rows of Q this CTA stages
-            const uint32_t tx = static_cast<uint32_t>(CONV ? P_RAW + p.q_bytes / 2 : CG * (P_BYTES + p.q_bytes));
+            const uint32_t tx = static_cast<uint32_t>(CG * ((I8 ? 0 : P_BYTES) + p.q_bytes));  // 8-bit: Q alone
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
@@ -407,7 +421,9 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                     const uint32_t fb = CG == 2 ? mapa_shared(fb_local, 0) : fb_local;
                     const uint32_t p_st = sbase + s * p.stage_bytes;
                     const uint32_t q_st = p_st + P_BYTES;
+                    const uint32_t rb = raw_bar + 8 * s;
                     if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                    if (I8) mbar_arrive_expect_tx(rb, P_BYTES);
                     if (++s == static_cast<uint32_t>(p.stages)) {
                         s = 0;
                         ph ^= 1u;
@@ -446,11 +462,17 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                         }
                         continue;
                     }
-                    const int kx = (t.ks + kt) * (MX ? 128 : BK);  // 4-bit views count bytes
-                    if (CONV) {  // the bytes lie behind the stage's converted operands
-                        const uint32_t raw = q_st + p.q_bytes;
-                        tma_load_3d(raw, &tmP, fb, kx, p0, t.g);
-                        tma_load_2d(raw + P_RAW, &tmQ, fb, kx, qx);
+                    const int kx = (t.ks + kt) * (MX ? 128 : BK);  // the views of 4-bit operands count bytes
+                    if (I8) {
+                        tma_load_3d(p_st, &tmP, rb, kx, p0, t.g);  // each CTA's own
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t dst = q_st + j * (p.q_bytes / 2);
+                            if (CG == 2)
+                                tma_load_2d_pair(dst, &tmQ, fb, kx + j * 64, qx);
+                            else
+                                tma_load_2d(dst, &tmQ, fb, kx + j * 64, qx);
+                        }
                         continue;
                     }
                     if (P_MN) {
@@ -491,6 +513,7 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                     // after an abort: leave no copy in flight (the even CTA's
                     // barriers count both CTAs' operand bytes)
                     if (leader) mbar_wait(full_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
+                    if (I8) mbar_wait(raw_bar + 8 * ds, dph, &dummy, nullptr, kWaitDrain, p.timeout_ns);
                 }
                 if (++ds == static_cast<uint32_t>(p.stages)) {
                     ds = 0;
@@ -501,7 +524,7 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (even CTA)
         if (leader) {
-            uint32_t it = 0, s = 0, ph = 0, acc_it = 0, sup = 0;
+            uint32_t it = 0, s = 0, ph = 0, acc_it = 0, sup = 0, slot = 0, slot_ph = 0;
             bool ok = true, issued = false;
             for (int u = first_unit; ok && u < num_units; u += unit_step) {
                 const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
@@ -517,8 +540,12 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                     tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + abuf * acc1;
                     for (int kt = seg0; kt < seg1; ++kt, ++it) {
-                        if (!mbar_wait_warp((CONV ? conv_bar : full_bar) + 8 * s, ph, abort_flag, p.status, kWaitMmaFull,
-                                            p.timeout_ns)) {
+                        if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitMmaFull, p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        if (I8 &&
+                            !mbar_wait_warp(conv_bar + 8 * slot, slot_ph, abort_flag, p.status, kWaitMmaConv, p.timeout_ns)) {
                             ok = false;
                             break;
                         }
@@ -531,6 +558,7 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                         tc_fence_after_sync();
                         const uint32_t p_st = sbase + s * p.stage_bytes;
                         const uint32_t q_st = p_st + P_BYTES;
+                        const uint32_t p_tmem = tmem_base + 2 * acc1 + slot * SLOT_COLS;  // 8-bit operands
                         uint64_t pd[K_STEPS], qd[K_STEPS];
     #pragma unroll
                         for (int kk = 0; kk < K_STEPS; ++kk) {
@@ -538,6 +566,7 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                             pd[kk] = P_MN ? smem_desc(p_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
                                           : smem_desc(p_st + kk * 32, 16, 1024, kLayoutSw128);
                             qd[kk] = Q_MN ? smem_desc(q_st + kr, BOX_BYTES, MN_SBO, MN_LAYOUT)
+                                     : I8 ? smem_desc(q_st + (kk >> 2) * (p.q_bytes / 2) + (kk & 3) * 32, 16, 1024, kLayoutSw128)
                                           : smem_desc(q_st + kk * 32, 16, 1024, kLayoutSw128);
                         }
                         const uint32_t acc0 = kt > seg0 ? 1u : 0u;
@@ -569,7 +598,12 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                                         tc_mma_mx4_pair(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
                                     else
                                         tc_mma_mx4(d_tmem, pd[kk], qd[kk], id, sp, sq, acc);
-                                } else if (KIND == kRaggedBf16 || I8) {
+                                } else if (I8) {
+                                    if (CG == 2)
+                                        tc_mma_f16_ta_pair(d_tmem, p_tmem + kk * 8, qd[kk], idesc, acc);
+                                    else
+                                        tc_mma_f16_ta(d_tmem, p_tmem + kk * 8, qd[kk], idesc, acc);
+                                } else if (KIND == kRaggedBf16) {
                                     if (CG == 2)
                                         tc_mma_f16_pair(d_tmem, pd[kk], qd[kk], idesc, acc);
                                     else
@@ -585,6 +619,12 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                                 tc_commit_pair_multicast(empty_bar + 8 * s, 0x3);
                             else
                                 tc_commit(empty_bar + 8 * s);
+                            if (I8) {
+                                if (CG == 2)
+                                    tc_commit_pair_multicast(slot_bar + 8 * slot, 0x3);
+                                else
+                                    tc_commit(slot_bar + 8 * slot);
+                            }
                             if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) {
                                 if (CG == 2)
                                     tc_commit_pair_multicast(sfree_bar + 8 * (sup & 1u), 0x3);
@@ -595,6 +635,10 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
                         __syncwarp();
                         if (MX && (kt % SUP == SUP - 1 || kt == t.kt - 1)) ++sup;
                         issued = true;
+                        if (I8 && ++slot == static_cast<uint32_t>(p.slots)) {
+                            slot = 0;
+                            slot_ph ^= 1u;
+                        }
                         if (++s == static_cast<uint32_t>(p.stages)) {
                             s = 0;
                             ph ^= 1u;
@@ -811,38 +855,51 @@ __global__ void __launch_bounds__(32 * warps_of(KIND), 1)
             }
             __syncwarp();
         }
-    } else if (CONV) {
+    } else if (I8) {
         // ------------------------------------------------------ conversion
-        // Item i of a stage: 16 bytes of K of row i / 4 of P, then of Q; they
-        // lie behind one another.  A quarter of a warp stores two rows' even (or
-        // odd) 16-byte pieces, which the swizzle spreads over all banks.
-        const int team = (warp - WARPS) / CONV_WARPS;
-        const int first = threadIdx.x - 32 * (WARPS + team * CONV_WARPS);
-        uint32_t it = 0, s = 0, ph = 0;
+        // A thread takes half a row of P, 64 bytes, for the lane of tensor memory
+        // that its warp may write.  Swizzled as TMA leaves them, 16-byte piece c of
+        // row r at c ^ (r % 8), eight rows' pieces lie in different banks.
+        const int half = (warp - WARPS) >> 2, q = warp & 3;
+        const uint32_t row = static_cast<uint32_t>(q * 32 + lane);
+        const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + 2 * acc1 + half * 32;
+        uint32_t s = 0, ph = 0, slot = 0, slot_ph = 0;
         bool ok = true;
         for (int u = first_unit; ok && u < num_units; u += unit_step) {
-            const Tile t = tile_at<BK, RAGGED_K>(p, table, u, krank);
-            const int items = 4 * (BP + mma_n<CG, RAGGED_K>(p, t));
-            for (int kt = 0; kt < t.kt; ++kt, ++it) {
-                if (it % CONV_TEAMS == static_cast<uint32_t>(team)) {
-                    if (!mbar_wait_warp(full_bar + 8 * s, ph, abort_flag, p.status, kWaitConvFull, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t p_st = sbase + s * p.stage_bytes;
-                    const uint32_t raw = p_st + P_BYTES + p.q_bytes;
-#pragma unroll 4
-                    for (int i = first; i < items; i += 32 * CONV_WARPS) {
-                        uint4 lo, hi;
-                        i8_to_f16(lds_u4(raw + i * 16), lo, hi);
-                        const uint32_t row = i >> 2, piece = (i & 3) * 2;
-                        const uint32_t at = p_st + row * 128;  // Q's rows follow P's
-                        sts_u4(at + ((piece ^ (row & 7)) * 16), lo);
-                        sts_u4(at + (((piece + 1) ^ (row & 7)) * 16), hi);
-                    }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(conv_bar + 8 * s);
+            const int kts = tile_at<BK, RAGGED_K>(p, table, u, krank).kt;
+            for (int kt = 0; kt < kts; ++kt) {
+                if (!mbar_wait_warp(raw_bar + 8 * s, ph, abort_flag, p.status, kWaitConvFull, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = sbase + s * p.stage_bytes + row * 128;
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint4 lo, hi;
+                    i8_to_f16(lds_u4(src + (((half * 4 + c) ^ (row & 7u)) * 16)), lo, hi);
+                    v[8 * c] = lo.x, v[8 * c + 1] = lo.y, v[8 * c + 2] = lo.z, v[8 * c + 3] = lo.w;
+                    v[8 * c + 4] = hi.x, v[8 * c + 5] = hi.y, v[8 * c + 6] = hi.z, v[8 * c + 7] = hi.w;
+                }
+                if (!mbar_wait_warp(slot_bar + 8 * slot, slot_ph ^ 1u, abort_flag, p.status, kWaitConvEmpty,
+                                    p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                tmem_store_32cols(dst + slot * SLOT_COLS, v);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive_relaxed(conv_bar + 8 * slot);
+                    else
+                        mbar_arrive_cluster_relaxed(mapa_shared(conv_bar + 8 * slot, 0));
+                }
+                if (++slot == static_cast<uint32_t>(p.slots)) {
+                    slot = 0;
+                    slot_ph ^= 1u;
                 }
                 if (++s == static_cast<uint32_t>(p.stages)) {
                     s = 0;
@@ -1068,12 +1125,12 @@ cudaError_t dispatch(int kind, int ctas, bool p_mn, bool ragged_k, bool sum, con
     if (kind == kRaggedMx4)
         return ctas == 2 ? op.template apply<kRaggedMx4, 2, false, false, false>()
                          : op.template apply<kRaggedMx4, 1, false, false, false>();
+    if (kind == kRaggedI8 && ctas == 2)
+        return sum ? op.template apply<kRaggedI8, 2, false, false, true>()
+                   : op.template apply<kRaggedI8, 2, false, false, false>();
     if (kind == kRaggedI8)
         return sum ? op.template apply<kRaggedI8, 1, false, false, true>()
                    : op.template apply<kRaggedI8, 1, false, false, false>();
-    if (kind == kRaggedI8Wide)
-        return sum ? op.template apply<kRaggedI8Wide, 2, false, false, true>()
-                   : op.template apply<kRaggedI8Wide, 2, false, false, false>();
     if (kind == kRaggedTf32)
         return ctas == 2 ? dispatch_form<kRaggedTf32, 2>(p_mn, ragged_k, sum, op)
                          : dispatch_form<kRaggedTf32, 1>(p_mn, ragged_k, sum, op);
@@ -1153,9 +1210,9 @@ cudaError_t prepare_ragged()
 cudaError_t prepare_ragged_i8()
 {
     cudaError_t e = prepare_ragged();  // the clusters that run at the same time
-    for (int kind : {kRaggedI8, kRaggedI8Wide})
+    for (int ctas = 1; ctas <= 2; ++ctas)
         for (bool sum : {false, true})
-            if (e == cudaSuccess) e = dispatch(kind, 1, false, false, sum, SetAttrs());
+            if (e == cudaSuccess) e = dispatch(kRaggedI8, ctas, false, false, sum, SetAttrs());
     return e;
 }
 
@@ -1178,7 +1235,7 @@ bool ragged_tile_ok(int split, int ctas, int bn)
 // is no multiple of the chunk): 13 + 10 us for the TF32 gradients of 2011 rows and
 // 13 experts of 1020 x 520, which take 24 + 27.
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
-                            int sm_count, bool may_split, double *cycles)
+                            int sm_count, bool may_split, int most_bn)
 {
     const double es = kind == kRaggedMx4 ? 17.0 / 32 : kind == kRaggedTf32 ? 4 : kind == kRaggedI8 ? 1 : 2;
     const double eo = ragged_k ? 4 : 2;
@@ -1192,19 +1249,20 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
     RaggedTile best;
     double best_t = 0;
     for (int ctas = 1; ctas <= 2; ++ctas)
-        for (int bn : {32, 64, 128, kind == kRaggedMx4 ? ACC1_MX : 256})
+        for (int bn : {32, 64, 128, kind == kRaggedMx4 ? ACC1_MX : kind == kRaggedI8 ? I8_MOST_BN : 256})
             for (int split = 1; split <= 8; split *= 2) {
                 if (ragged_k && bn < 128) continue;  // whole 128-byte column chunks per CTA
-                if (kind == kRaggedI8 && (ctas > 1 || bn > 128)) continue;
-                if (kind == kRaggedI8Wide && ctas < 2) continue;
+                if (bn > most_bn || (kind == kRaggedI8 && bn > 128 && ctas == 1)) continue;
                 const int64_t units = max_units(ragged_k, rows, groups, P, Q, ctas, bn);
                 if (split > 1 && (!may_split || ctas > 1 || bn > 128 || units > max_clusters(split) || units * split > sm_count ||
                                   kt < 4 * split))
                     continue;
                 const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
-                const double arrival = (P_BYTES + bn / ctas * 128) / 55.0 * (kind == kRaggedI8 ? 0.5 : 1);
-                const double convert = kind == kRaggedI8 ? (bn == 32 ? 650 : 870) : 0;
-                const double stage = std::max({4 * mma, arrival, convert}) * (kind == kRaggedMx4 ? 1.1 : 1);
+                // 8-bit operands: stages of eight instructions, and 450 cycles of conversion
+                const double stage =
+                    kind == kRaggedI8
+                        ? std::max({8 * mma, (P_BYTES + bn / ctas * 256) / 55.0, 450.0})
+                        : std::max(4 * mma, (P_BYTES + bn / ctas * 128) / 55.0) * (kind == kRaggedMx4 ? 1.1 : 1);
                 const double tiles_p = static_cast<double>((P + ctas * BP - 1) / (ctas * BP));
                 const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
                                        : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
@@ -1224,7 +1282,6 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
                     best.split = split;
                 }
             }
-    if (cycles) *cycles = best_t;
     return best;
 }
 
@@ -1242,16 +1299,15 @@ cudaError_t launch_ragged(int kind, bool ragged_k, bool p_mn, const RaggedTile &
     p.tiles_p = (a.P + t.ctas * BP - 1) / (t.ctas * BP);
     p.tiles_q = ragged_k ? (a.Q + t.bn - 1) / t.bn : 0;
     p.split = t.split;
-    p.q_bytes = t.bn / t.ctas * 128;
-    p.stage_bytes = P_BYTES + p.q_bytes + (kind == kRaggedI8 ? P_RAW + p.q_bytes / 2 : 0);
+    p.q_bytes = t.bn / t.ctas * (kind == kRaggedI8 ? 256 : 128);
+    p.stage_bytes = P_BYTES + p.q_bytes;
     p.sf_parts = 1 + (t.bn + 127) / 128;
     p.table_bytes = ragged_k ? 0 : (4 * (a.groups + 1) + 15) / 16 * 16;
     const int sf_bytes = kind == kRaggedMx4 ? 2 * SUP * p.sf_parts * SF_PART : 0;
     const int fixed = 1024 + sf_bytes + EPI_BYTES + p.table_bytes + bar_bytes(kind) + tail_bytes(kind);
     p.stages = std::min(MAX_STAGES, (SMEM_MAX - fixed) / p.stage_bytes);
-    // A team of converter warps keeps to its own ring stages: it sees all of their
-    // phases, and none of the others'.
-    if (kind == kRaggedI8) p.stages -= p.stages % CONV_TEAMS;
+    p.acc1 = std::max(128, t.bn);
+    p.slots = std::min(MAX_SLOTS, (TMEM_COLS - 2 * p.acc1) / SLOT_COLS);
     p.C = a.C;
     p.ldc = a.ldc;
     p.stride_c = a.stride_c;

@@ -9,11 +9,9 @@
 
 namespace dg {
 
-// Operand kinds of the grouped kernel.  8-bit integers are multiplied as FP16,
-// in which they are exact: kRaggedI8 converts both operands on their way through
-// shared memory (one CTA a tile), kRaggedI8Wide takes operands converted before
-// (CTA pairs).
-enum RaggedKind : int { kRaggedBf16 = 0, kRaggedTf32 = 1, kRaggedMx4 = 2, kRaggedI8 = 3, kRaggedI8Wide = 4 };
+// Operand kinds of the grouped kernel.  8-bit integers are multiplied as FP16, in
+// which they are exact: P as bytes, converted inside the kernel, Q converted before.
+enum RaggedKind : int { kRaggedBf16 = 0, kRaggedTf32 = 1, kRaggedMx4 = 2, kRaggedI8 = 3 };
 
 // The kernel computes, for every group g, D[p][q] = sum_k P_g[p][k] Q_g[q][k]
 // and stores D[p][q] at C[row(q) * ldc + p]: P is the operand whose index runs
@@ -63,12 +61,11 @@ constexpr int kRaggedP = 128;    // rows of P one CTA stages
 constexpr int kRaggedBlock = 32;  // elements that share a 4-bit scale
 
 bool ragged_tile_ok(int split, int ctas, int bn);  // split 0: none
-// cycles (may be null): the estimated time that the choice is made by
 RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, int64_t P, int64_t Q, int64_t K,
-                            int sm_count, bool may_split, double *cycles = nullptr);
+                            int sm_count, bool may_split, int most_bn = 256);
 
-// K elements of one ring stage (128 bytes of a K-major row as it is multiplied).
-inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : 64; }
+// K elements of one ring stage (128 bytes of a K-major row).
+inline int ragged_bk(int kind) { return kind == kRaggedMx4 ? 256 : kind == kRaggedTf32 ? 32 : kind == kRaggedI8 ? 128 : 64; }
 
 // Sets the kernels' attributes on the current device: once per handle, before
 // its first product (1.5 ms for the first handle of a process, whose creation
@@ -95,11 +92,11 @@ cudaError_t launch_i8_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t
                                cudaStream_t stream);
 cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
                                  void *dst, int64_t ldd, bool dst_bf16, int sm_count, cudaStream_t stream);
-// rows_a rows of A's codes and rows_b of B's as FP16, at pitches of K rounded up
-// to 16; with offsets only B's rows of groups (rows_per each) that own rows.
-cudaError_t launch_i8_widen(const int8_t *a, int64_t lda, int64_t rows_a, const int8_t *b, int64_t ldb, int64_t rows_b,
-                            int64_t K, void *a16, void *b16, const int64_t *offsets, int64_t rows_per, int sm_count,
+// Rows of codes as FP16, at a pitch of K rounded up to 16.
+cudaError_t launch_i8_widen(const int8_t *src, int64_t ld, int64_t rows, int64_t K, void *dst, int sm_count,
                             cudaStream_t stream);
+// Rows of a tile at most, by the type of C.
+constexpr int kRaggedI8Rows = 192, kRaggedI8RowsF32 = 128;
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
                                   int64_t lds, void *dst, int64_t ldd, bool dst_bf16, int sm_count,
                                   cudaStream_t stream);

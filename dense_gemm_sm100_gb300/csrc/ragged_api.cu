@@ -508,30 +508,6 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     return GEMM_OK;
 }
 
-// Converting the operands first (2 bytes written and read for each one read)
-// costs a launch of its own and its traffic, and the product then reads 16-bit
-// operands; converting inside the product costs every tile that reads them.  The
-// estimates of both decide (cycles of 1.9 GHz, 3370 bytes each), as the tile's.
-dg::RaggedTile i8_tile(const gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, int *kind)
-{
-    dg::RaggedTile t;
-    if (h->ragged_tile) {
-        t = tile_for(h, dg::kRaggedI8, false, rows, groups, N, 0, K);
-        *kind = t.ctas == 2 ? dg::kRaggedI8Wide : dg::kRaggedI8;
-        if (t.ctas == 1) t.bn = std::min(t.bn, 128);
-        return t;
-    }
-    const int g = static_cast<int>(groups);
-    double narrow = 0, wide = 0;
-    t = dg::ragged_pick_tile(dg::kRaggedI8, false, rows, g, N, 0, K, usable_sms(h), h->split_k == 0, &narrow);
-    const dg::RaggedTile w =
-        dg::ragged_pick_tile(dg::kRaggedI8Wide, false, rows, g, N, 0, K, usable_sms(h), false, &wide);
-    const double busy = static_cast<double>(std::min(groups, rows));
-    wide += (static_cast<double>(rows) + busy * N) * K * 3 / 3370 + 5000;
-    *kind = wide < narrow ? dg::kRaggedI8Wide : dg::kRaggedI8;
-    return wide < narrow ? w : t;
-}
-
 int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const int8_t *ac,
            int64_t aq, const float *as, const int8_t *bc, int64_t bq, const float *bs, void *C, int64_t ldc,
            int c_dtype, cudaStream_t stream)
@@ -543,41 +519,37 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
     dg::DeviceGuard guard(h->device);
     int rc = prepare(h, true);
     if (rc) return rc;
-    int kind;
-    const dg::RaggedTile t = i8_tile(h, groups, rows, N, K, &kind);
+    const int kind = dg::kRaggedI8, most = c_dtype == GEMM_BF16 ? dg::kRaggedI8Rows : dg::kRaggedI8RowsF32;
+    dg::RaggedTile t;
+    if (h->ragged_tile) {
+        t = tile_for(h, kind, false, rows, groups, N, 0, K);
+        t.bn = std::min(t.bn, t.ctas == 2 ? most : 128);
+    } else {
+        t = dg::ragged_pick_tile(kind, false, rows, static_cast<int>(groups), N, 0, K, usable_sms(h), h->split_k == 0,
+                                 most);
+    }
     dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
     a.row_scale_p = bs;
     a.row_scale_q = as;
     alignas(64) CUtensorMap tmP = {}, tmQ = {};
     dg::WorkspaceUse ws(h, stream);
-    const bool wide = kind == dg::kRaggedI8Wide;
-    if (K > 0 && wide) {
-        const int64_t ld = round_up(K, 16), a_bytes = round_up(rows * ld * 2, 256);
-        if ((rc = ws.acquire(static_cast<size_t>(a_bytes + groups * N * ld * 2)))) return rc;
-        uint8_t *a16 = static_cast<uint8_t *>(h->ws), *b16 = a16 + a_bytes;
-        const cudaError_t e = dg::launch_i8_widen(ac, aq, rows, bc, bq, groups * N, K, a16, b16, offsets, N, h->sm_count,
-                                                  stream);
+    if (K > 0) {
+        const int64_t ld = round_up(K, 16);
+        if ((rc = ws.acquire(static_cast<size_t>(rows * ld * 2)))) return rc;
+        const cudaError_t e = dg::launch_i8_widen(ac, aq, rows, K, h->ws, h->sm_count, stream);
         if (e != cudaSuccess) return cuda_fail(h, e, "conversion launch");
         ++h->launches;
-        rc = encode_k_major(h, &tmP, float_type(2), 2, b16, K, N, ld, groups, N * ld, 64, dg::kRaggedP,
-                            CU_TENSOR_MAP_SWIZZLE_128B, true, "B in 16 bits");
+        rc = encode_k_major(h, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, bc, K, N, bq, groups, N * bq, 128, dg::kRaggedP,
+                            CU_TENSOR_MAP_SWIZZLE_128B, true, "the codes of B");
         if (!rc)
-            rc = encode_k_major(h, &tmQ, float_type(2), 2, a16, K, rows, ld, 1, 0, 64, t.bn / t.ctas,
+            rc = encode_k_major(h, &tmQ, float_type(2), 2, h->ws, K, rows, ld, 1, 0, 64, t.bn / t.ctas,
                                 CU_TENSOR_MAP_SWIZZLE_128B, false, "A in 16 bits");
-        if (rc) return rc;
-    } else if (K > 0) {
-        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        rc = encode_k_major(h, &tmP, u8, 1, bc, K, N, bq, groups, N * bq, 64, dg::kRaggedP, CU_TENSOR_MAP_SWIZZLE_NONE,
-                            true, "the codes of B");
-        if (!rc)
-            rc = encode_k_major(h, &tmQ, u8, 1, ac, K, rows, aq, 1, 0, 64, t.bn, CU_TENSOR_MAP_SWIZZLE_NONE, false,
-                                "the codes of A");
         if (rc) return rc;
     }
     const cudaError_t e = dg::launch_ragged(kind, false, false, t, tmP, tmQ, a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
     ++h->launches;
-    set_path(h, offsets ? "grouped" : "tc", kind, t, wide ? "_widened" : "", false, false);
+    set_path(h, offsets ? "grouped" : "tc", kind, t, "", false, false);
     return ws.done();
 }
 

@@ -160,8 +160,7 @@ extern "C" {
  * (default) = the least estimated time for the average group; else 1000 * CTAs
  * + rows, CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile
  * of 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at
- * most 224, 8-bit products of one CTA at most 128 and convert their operands on
- * the way, of a pair before), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
+ * most 224, 8-bit products at most 128, of a pair with BF16 results 192), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
  * 8 CTAs (CTAs 1, rows at most 128).  By default the contraction is cut where
  * the tiles would leave SMs idle; GEMM_OPT_SPLIT_K = 1 (or more) forbids it. */
 #define GEMM_OPT_GROUPED_TILE 16

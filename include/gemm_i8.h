@@ -34,9 +34,8 @@
  *                      group g is multiplied by rows g*N .. g*N + N - 1 of B.
  *
  * The products run on the tensor cores in FP16, which holds every code exactly.
- * c_dtype is GEMM_F32 or GEMM_BF16.  Products with many rows first convert both
- * operands into the handle's workspace (2 bytes an element); the others convert
- * on the way through shared memory and use none.  Handles, streams, asynchrony,
+ * c_dtype is GEMM_F32 or GEMM_BF16.  A is first converted into the handle's
+ * workspace (2 bytes an element), B inside the product.  Handles, streams, asynchrony,
  * errors and in-kernel time limits are those of gemm_run; results are
  * bit-identical from call to call.  The rows of a matrix times a pitch stay
  * within 2^44, and a group's codes below 2^40 bytes.

@@ -242,17 +242,17 @@ def test_grouped_product(gm, h, sizes, tile):
         assert (got[:2] == 7).all() and (got[bounds[-1]:] == 7).all()
 
 
-def test_the_choice_of_form(gm, h):
-    """Few rows convert on the way, very many first."""
-    for M, N, widened in ((4, 2048, False), (64, 2048, False), (5000, 8192, True)):
-        A, a, sa = operand(gm, M, 1024, 13)
-        B, b, sb = operand(gm, N, 1024, 14)
-        C = torch.empty((M, N), device="cuda")
+@pytest.mark.parametrize("M,N", [(4, 2048), (64, 2048), (700, 3000), (5000, 8192)])
+def test_chosen_tiles(gm, h, M, N):
+    A, a, sa = operand(gm, M, 1024, 13)
+    B, b, sb = operand(gm, N, 1024, 14)
+    some = torch.arange(0, M, max(1, M // 64))
+    want = expected(product(a[some], b), sa[some], sb)
+    for out in (torch.float32, torch.bfloat16):
+        C = torch.empty((M, N), device="cuda", dtype=out)
         h.run_i8(A, B, C)
         h.sync_status()
-        assert ("widened" in h.last_path) == widened, h.last_path
-        some = torch.arange(0, M, max(1, M // 64))
-        assert torch.equal(C[some].cpu(), expected(product(a[some], b), sa[some], sb))
+        assert torch.equal(C[some].cpu(), want.to(out))
 
 
 def test_empty_sums_and_empty_calls(gm, h):
