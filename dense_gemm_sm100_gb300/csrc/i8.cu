@@ -1,8 +1,8 @@
 // 8-bit integers with one FP32 scale a row: s = max|x| / 127 rounded to FP32,
 // codes x / s rounded to the nearest integer, ties to even, within -127 .. 127.
-// The quotient is taken as if in infinite precision: x * (1 / s) in FP32 is off
-// by 1.5e-5 at most, and where that leaves the rounding open (4e-5 on either
-// side of a half) the exact remainder x - c * s decides.  A row of zeros has scale
+// The quotient is taken as if in infinite precision: it lies between x times a
+// reciprocal of s rounded down and one rounded up, and where these two round to
+// different integers (one element in 20000) the exact remainder x - c * s decides.  A row of zeros has scale
 // 0; one that holds an infinity or a NaN has scale NaN; both have codes 0.
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -29,6 +29,13 @@ struct Raw;
 template <>
 struct Raw<float> {
     float4 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    // from shared memory, the second half `pitch` bytes behind (n elements are there)
+    __device__ __forceinline__ void fetch(uint32_t from, int pitch, int n)
+    {
+        a = lds_f4(from);
+        if (n > 4) b = lds_f4(from + pitch);
+    }
     __device__ __forceinline__ void load(const float *s, int n, bool vec)
     {
         if (vec && n >= 8) {
@@ -42,6 +49,15 @@ struct Raw<float> {
             b = make_float4(v[4], v[5], v[6], v[7]);
         }
     }
+    // the largest magnitude's bits, and the most of two such
+    __device__ __forceinline__ uint32_t top(uint32_t m) const
+    {
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t whole(uint32_t m) { return m; }
     __device__ __forceinline__ void widen(float (&v)[8]) const
     {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -50,6 +66,8 @@ struct Raw<float> {
 template <>
 struct Raw<__nv_bfloat16> {
     uint4 a;
+    __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void fetch(uint32_t from, int, int) { a = lds_u4(from); }
     __device__ __forceinline__ void load(const __nv_bfloat16 *s, int n, bool vec)
     {
         if (vec && n >= 8) {
@@ -63,6 +81,15 @@ struct Raw<__nv_bfloat16> {
             a = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
+    // as above, of the even and the odd elements in the halves of a word
+    __device__ __forceinline__ uint32_t top(uint32_t m) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t whole(uint32_t m) { return max(m & 0xffff0000u, m << 16); }
     __device__ __forceinline__ void widen(float (&v)[8]) const
     {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -83,21 +110,22 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits)
 
 // Codes of values by a row's scale.
 struct Coder {
-    float scale, inverse;
+    float scale, low, high;  // reciprocals, 2^-22 below and above
     bool none, small;
     __device__ __forceinline__ explicit Coder(float s) : scale(s)
     {
         none = !(s > 0.0f);
         small = s < 1e-30f;  // no FP32 reciprocal to rely on
-        inverse = none || small ? 0.0f : 1.0f / s;
+        const float inverse = none || small ? 0.0f : 1.0f / s;
+        low = inverse * (1.0f - 0x1p-22f);
+        high = inverse * (1.0f + 0x1p-22f);
     }
-    // Where the estimate leaves the rounding open.  The remainder is exact: a
-    // multiple of half a unit of the scale's last place, and little more than
-    // half the scale.
+    // Where the rounding is open.  The remainder is exact: a multiple of half a
+    // unit of the scale's last place, and little more than half the scale.
     __device__ __forceinline__ int settle(float x) const
     {
         if (small) return static_cast<int>(fmin(fmax(rint(static_cast<double>(x) / scale), -127.0), 127.0));
-        float c = rintf(x * inverse);
+        float c = rintf(x * low);
         const float d = fmaf(-c, scale, x), twice = 2.0f * fabsf(d);
         if (twice > scale || (twice == scale && (static_cast<int>(c) & 1))) c += copysignf(1.0f, d);
         return static_cast<int>(c);
@@ -108,20 +136,20 @@ struct Coder {
     {
         if (none) return make_uint2(0u, 0u);
         constexpr float ROUND = 12582912.0f;
-        uint32_t w[8];
-        float far = small ? 1.0f : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = fmaf(v[i], inverse, ROUND);
-            far = fmaxf(far, fabsf(fmaf(v[i], inverse, -(t - ROUND))));
-            w[i] = __float_as_uint(t);
-        }
-        if (far > 0.49996f)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = static_cast<uint32_t>(settle(v[i]));
         const auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
         };
+        const auto codes = [&](float r) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(fmaf(v[i], r, ROUND));
+            return make_uint2(four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7]));
+        };
+        const uint2 a = codes(low), b = codes(high);
+        if (a.x == b.x && a.y == b.y && !small) return a;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = static_cast<uint32_t>(settle(v[i]));
         return make_uint2(four(w[0], w[1], w[2], w[3]), four(w[4], w[5], w[6], w[7]));
     }
 };
@@ -137,52 +165,88 @@ __device__ __forceinline__ void store8(int8_t *dst, uint2 c, int n)
     }
 }
 
-// TPR threads a row, U pieces of eight elements a thread kept in registers
-// between the maximum and the codes (U = 0: the row is read again).
-template <typename T, int TPR, int U>
-__global__ void __launch_bounds__(THREADS)
+__host__ __device__ constexpr int quantise_threads(int tpr) { return tpr > THREADS ? tpr : THREADS; }
+
+// TPR threads a row, U pieces of eight elements a thread (U = 0: any number, and
+// the row is read again for the codes).  Few pieces a thread: eight left so few
+// warps that 8192 x 14336 took 270 us.  S > 0 (rows on 16-byte boundaries): a
+// thread's pieces of the next S - 1 rows are on their way into shared memory while
+// it works on one, each thread's own, so that no barrier comes into it.  Memory sets
+// the time then.
+template <typename T, int TPR, int U, int S>
+__global__ void __launch_bounds__(quantise_threads(TPR))
     quantise_kernel(const T *src, long long ld, long long stride, long long rows, long long all, int K, bool vec,
                     int8_t *codes, long long ldq, float *scales)
 {
-    __shared__ uint32_t part[THREADS / 32];
-    constexpr int ROWS = THREADS / TPR;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ uint32_t part[32];
+    constexpr int NT = quantise_threads(TPR), ROWS = NT / TPR, WORDS = sizeof(Raw<T>) / 16, RING = S > 0 ? S : 1;
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int pieces = (K + 7) / 8;
+    const long long step = static_cast<long long>(gridDim.x) * ROWS;
     griddep_wait();
     griddep_launch_dependents();
-    for (long long r0 = static_cast<long long>(blockIdx.x) * ROWS; r0 < all; r0 += static_cast<long long>(gridDim.x) * ROWS) {
+    const auto row_at = [&](long long r) {
+        const long long b = r / rows;
+        return src + b * stride + (r - b * rows) * ld;
+    };
+    const uint32_t mine = S > 0 ? smem_addr(ring) + threadIdx.x * 16 : 0u;
+    const auto slot = [&](int s, int u, int w) { return mine + static_cast<uint32_t>(((s * U + u) * WORDS + w) * NT * 16); };
+    const auto request = [&](long long r, int s) {
+        if (r < all) {
+            const T *row = row_at(r);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w) {
+                    constexpr int N = 16 / sizeof(T);
+                    const int k = (u * TPR + t) * 8 + w * N, left = (K - k) * static_cast<int>(sizeof(T));
+                    if (left > 0) cp_async_16(slot(s, u, w), row + k, left < 16 ? static_cast<uint32_t>(left) : 16u);
+                }
+        }
+        cp_async_commit();
+    };
+    if (S > 0) {
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) request(static_cast<long long>(blockIdx.x) * ROWS + sub + s * step, s);
+    }
+    int stage = 0;
+    for (long long r0 = static_cast<long long>(blockIdx.x) * ROWS; r0 < all; r0 += step) {
         const long long r = r0 + sub;
         const bool there = r < all;
-        const long long b = there ? r / rows : 0;
-        const T *row = src + (there ? b * stride + (r - b * rows) * ld : 0);
+        const T *row = there ? row_at(r) : src;
         Raw<T> kept[U > 0 ? U : 1];
         uint32_t amax = 0;
-        const auto top = [&](const Raw<T> &raw) {
-            float v[8];
-            raw.widen(v);
+        if (S > 0) {
+            request(r + (S - 1) * step, (stage + S - 1) % RING);
+            cp_async_wait<S - 1>();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-        };
-        if (U > 0) {
+            for (int u = 0; u < U; ++u) {
+                kept[u].clear();
+                if (there && (u * TPR + t) * 8 < K) kept[u].fetch(slot(stage, u, 0), NT * 16, K - (u * TPR + t) * 8);
+                amax = kept[u].top(amax);
+            }
+            stage = (stage + 1) % RING;
+        } else if (U > 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = (u * TPR + t) * 8;
                 kept[u].load(row + k, there ? K - k : 0, vec);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) top(kept[u]);
+            for (int u = 0; u < U; ++u) amax = kept[u].top(amax);
         } else if (there) {
             for (int i = t; i < pieces; i += TPR) {
                 kept[0].load(row + i * 8, K - i * 8, vec);
-                top(kept[0]);
+                amax = kept[0].top(amax);
             }
         }
-        amax = __reduce_max_sync(0xffffffffu, amax);
+        amax = __reduce_max_sync(0xffffffffu, Raw<T>::whole(amax));
         if (TPR > 32) {
             if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) amax = max(amax, part[w]);
+            for (int w = 0; w < TPR / 32; ++w) amax = max(amax, part[sub * (TPR / 32) + w]);
             __syncthreads();  // part is written again for the next row
         }
         const Coder q(scale_of(amax));
@@ -354,18 +418,35 @@ int grid_for(long long units, int per_cta, int per_sm, int sm_count)
     return static_cast<int>(std::max(1LL, std::min<long long>((units + per_cta - 1) / per_cta, int64_t{per_sm} * sm_count)));
 }
 
+template <typename T, int TPR, int U, int S>
+cudaError_t launch_quantise_form(const void *src, int64_t ld, int64_t stride, int64_t batch, int64_t rows, int64_t K,
+                                 bool vec, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                                 cudaStream_t stream)
+{
+    constexpr int NT = quantise_threads(TPR);
+    constexpr size_t SMEM = static_cast<size_t>(S) * U * NT * sizeof(Raw<T>);
+    const cudaError_t e = kernel_ready<quantise_kernel<T, TPR, U, S>>(SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(quantise_kernel<T, TPR, U, S>, grid_for(batch * rows, NT / TPR, 2048 / NT, sm_count), NT, SMEM,
+                      stream, 1, static_cast<const T *>(src), static_cast<long long>(ld),
+                      static_cast<long long>(stride), static_cast<long long>(rows),
+                      static_cast<long long>(batch * rows), static_cast<int>(K), vec, codes,
+                      static_cast<long long>(ldq), scales);
+}
+
 template <typename T, int TPR, int U>
 cudaError_t launch_quantise(const void *src, int64_t ld, int64_t stride, int64_t batch, int64_t rows, int64_t K,
                             int8_t *codes, int64_t ldq, float *scales, int sm_count, cudaStream_t stream)
 {
     const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (ld * sizeof(T)) % 16 == 0 &&
                      (stride * sizeof(T)) % 16 == 0;
-    const cudaError_t e = kernel_ready<quantise_kernel<T, TPR, U>>(0);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(quantise_kernel<T, TPR, U>, grid_for(batch * rows, THREADS / TPR, 8, sm_count), THREADS, 0, stream,
-                      1, static_cast<const T *>(src), static_cast<long long>(ld), static_cast<long long>(stride),
-                      static_cast<long long>(rows), static_cast<long long>(batch * rows), static_cast<int>(K), vec, codes,
-                      static_cast<long long>(ldq), scales);
+    // more rows than run at once: those that follow are fetched ahead
+    constexpr int S = sizeof(T) == 2 ? 4 : 3;
+    if (U > 0 && vec && batch * rows > static_cast<int64_t>(quantise_threads(TPR) / TPR) * 2 * sm_count)
+        return launch_quantise_form<T, TPR, U, U == 0 ? 0 : S>(src, ld, stride, batch, rows, K, vec, codes, ldq, scales,
+                                                               sm_count, stream);
+    return launch_quantise_form<T, TPR, U, 0>(src, ld, stride, batch, rows, K, vec, codes, ldq, scales, sm_count,
+                                              stream);
 }
 
 template <typename T>
@@ -384,9 +465,11 @@ cudaError_t launch_quantise_for(bool k_rows, int64_t batch, int64_t rows, int64_
     const auto run = [&](auto f) { return f(src, ld, stride, batch, rows, K, codes, ldq, scales, sm_count, stream); };
     if (K <= 256) return run(launch_quantise<T, 32, 1>);
     if (K <= 1024) return run(launch_quantise<T, 32, 4>);
+    if (K <= 2048) return run(launch_quantise<T, 256, 1>);
     if (K <= 4096) return run(launch_quantise<T, 256, 2>);
-    if (K <= 16384) return run(launch_quantise<T, 256, 8>);
-    return run(launch_quantise<T, 256, 0>);
+    if (K <= 8192) return run(launch_quantise<T, 512, 2>);
+    if (K <= 16384) return run(launch_quantise<T, 1024, 2>);
+    return run(launch_quantise<T, 1024, 0>);
 }
 
 }  // namespace
