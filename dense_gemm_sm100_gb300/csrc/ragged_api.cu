@@ -508,6 +508,8 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     return GEMM_OK;
 }
 
+constexpr int64_t kFewRows = 8;
+
 int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const int8_t *ac,
            int64_t aq, const float *as, const int8_t *bc, int64_t bq, const float *bs, void *C, int64_t ldc,
            int c_dtype, cudaStream_t stream)
@@ -519,6 +521,19 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
     dg::DeviceGuard guard(h->device);
     int rc = prepare(h, true);
     if (rc) return rc;
+    // Few rows a group: B is read once by integer dot products.
+    const int64_t each = offsets ? (rows + groups - 1) / groups : rows;
+    const int mr = each <= (offsets ? 1 : 4) ? 4 : 8;
+    if (!h->ragged_tile && each <= kFewRows && dg::i8_rows_fit(K, mr)) {
+        dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
+        a.row_scale_p = bs;
+        a.row_scale_q = as;
+        const cudaError_t e = dg::launch_i8_rows(a, mr, ac, aq, bc, bq, usable_sms(h));
+        if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
+        ++h->launches;
+        h->last_path = offsets ? "grouped_i8_rows" : "i8_rows";
+        return GEMM_OK;
+    }
     const int kind = dg::kRaggedI8, most = c_dtype == GEMM_BF16 ? dg::kRaggedI8Rows : dg::kRaggedI8RowsF32;
     dg::RaggedTile t;
     if (h->ragged_tile) {

@@ -255,6 +255,65 @@ def test_chosen_tiles(gm, h, M, N):
         assert torch.equal(C[some].cpu(), want.to(out))
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 33, 15), (2, 100, 17), (3, 31, 496), (4, 130, 512), (5, 257, 1000),
+                                   (7, 64, 2100), (8, 300, 4096), (1, 40, 11000), (4, 77, 24000), (8, 5000, 130)])
+def test_few_rows(gm, h, M, N, K, out):
+    A, a, sa = operand(gm, M, K, 31)
+    B, b, sb = operand(gm, N, K, 32, pad=1)
+    sums = product(a, b)
+    assert sums.abs().max() < 2 ** 24
+    C = torch.full((M + 2, N + 3), 7.0, device="cuda", dtype=out)
+    h.run_i8(A, B, C[1:M + 1, 2:N + 2])
+    h.sync_status()
+    assert h.last_path == ("i8_rows" if K < 13000 or M <= 4 else h.last_path)
+    assert torch.equal(C[1:M + 1, 2:N + 2].cpu(), expected(sums, sa, sb).to(out))
+    assert (C[0] == 7).all() and (C[M + 1] == 7).all() and (C[:, :2] == 7).all() and (C[:, N + 2:] == 7).all()
+
+
+@pytest.mark.parametrize("sizes", [[1] * 40, [0, 3, 0, 9, 1, 20, 0], [17, 0, 0, 0, 0, 0], [0, 0, 0], [8, 8, 1]],
+                         ids=lambda s: f"{len(s)}groups{sum(s)}rows")
+def test_few_rows_grouped(gm, h, sizes):
+    """Groups of many rows among them: they are taken eight (four) at a time."""
+    G, rows, N, K = len(sizes), sum(sizes) + 3, 70, 330
+    bounds = [2]
+    for s in sizes:
+        bounds.append(bounds[-1] + s)
+    A, a, sa = operand(gm, rows, K, 33)
+    B, b, sb = operand(gm, G * N, K, 34)
+    C = torch.full((rows, N), 7.0, device="cuda")
+    h.run_i8_grouped(A, B, torch.tensor(bounds, device="cuda"), C)
+    h.sync_status()
+    assert h.last_path == "grouped_i8_rows"
+    for g in range(G):
+        lo, hi = bounds[g], bounds[g + 1]
+        w = slice(g * N, (g + 1) * N)
+        assert torch.equal(C[lo:hi].cpu(), expected(product(a[lo:hi], b[w]), sa[lo:hi], sb[w]))
+    assert (C[:2] == 7).all() and (C[bounds[-1]:] == 7).all()
+    for bad in ([0, 5, 3] + [rows] * (G - 2), [-1] * G + [2], [0] * G + [rows + 1]):
+        C.fill_(7.0)
+        h.run_i8_grouped(A, B, torch.tensor(bad, device="cuda"), C)
+        with pytest.raises(gm.GemmError) as e:
+            h.sync_status()
+        assert e.value.code == gm.GEMM_ERR_INVALID and (C == 7).all()
+
+
+def test_few_rows_largest_sums(gm, h):
+    """131071 products of 2^14: an integer sum just below 2^31, rounded once to FP32."""
+    A, a, sa = operand(gm, 1, 20000, 35)
+    for K in (20000, 131071):
+        if K > 20000 and not K * 4 < 96 * 1024:
+            continue  # the row does not fit the kernel; the tensor-core one takes it
+        B, b, sb = operand(gm, 9, K, 36)
+        A.codes.fill_(-128)
+        B.codes.fill_(-128)
+        C = torch.empty((1, 9), device="cuda")
+        h.run_i8(A, B, C)
+        h.sync_status()
+        assert h.last_path == "i8_rows"
+        assert torch.equal(C.cpu(), expected(torch.full((1, 9), K * 2 ** 14), sa, sb))
+
+
 def test_empty_sums_and_empty_calls(gm, h):
     C = torch.full((3, 5), 7.0, device="cuda")
     z = lambda n: gm.I8(torch.empty((n, 16), dtype=torch.int8, device="cuda"),
