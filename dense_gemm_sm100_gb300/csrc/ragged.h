@@ -98,8 +98,7 @@ cudaError_t launch_i8_widen(const int8_t *src, int64_t ld, int64_t rows, int64_t
 // Products of few rows a group (i8_rows.cu), mr (4 or 8) of them at a time: whether
 // they fit the kernel's shared memory and integers, and the launch (B's rows are
 // P's, A's Q's).
-constexpr int kI8RowsBytes = 96 * 1024;
-bool i8_rows_fit(int64_t K, int mr);
+bool i8_rows_fit(int64_t rows, int64_t K, int mr);
 cudaError_t launch_i8_rows(const RaggedArgs &a, int mr, const int8_t *codes_a, int64_t lda, const int8_t *codes_b,
                            int64_t ldb, int sm_count);
 // Rows of a tile at most, by the type of C.

@@ -508,7 +508,13 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     return GEMM_OK;
 }
 
-constexpr int64_t kFewRows = 8;
+// Rows up to which integer dot products (i8_rows.cu) are faster than the tensor
+// cores.  One product, us, 4 / 8 rows against the tensor cores' 8: 2048 x 2048
+// 4.7 / 5.0 and 9, 14336 x 4096 14.7 / 17 and 19, 28672 x 8192 43 / 52 and 60,
+// 8192 x 8192 17.7 / 24 and 21.  Groups of uneven sizes, 0.5 / 2 / 4 rows each on
+// average: 128 of 768 x 2048 18 / 34 / 44 and 21 / 41 / 42, 8 of 14336 x 4096 40 /
+// 61 / 109 and 51 / 72 / 85; all rows in one of the 128 groups 7 / 16 / 27 and 13.
+constexpr int64_t kFewRows = 8, kFewRowsOfGroup = 2;
 
 int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const int8_t *ac,
            int64_t aq, const float *as, const int8_t *bc, int64_t bq, const float *bs, void *C, int64_t ldc,
@@ -521,10 +527,9 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
     dg::DeviceGuard guard(h->device);
     int rc = prepare(h, true);
     if (rc) return rc;
-    // Few rows a group: B is read once by integer dot products.
-    const int64_t each = offsets ? (rows + groups - 1) / groups : rows;
-    const int mr = each <= (offsets ? 1 : 4) ? 4 : 8;
-    if (!h->ragged_tile && each <= kFewRows && dg::i8_rows_fit(K, mr)) {
+    const bool few = offsets ? rows <= kFewRowsOfGroup * groups : rows <= kFewRows;
+    const int mr = offsets || rows <= 4 ? 4 : 8;
+    if (!h->ragged_tile && few && dg::i8_rows_fit(rows, K, mr)) {
         dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
         a.row_scale_p = bs;
         a.row_scale_q = as;

@@ -25,21 +25,23 @@
  *                      i < M, j < N: both operands hold K values a row (B the
  *                      channels of a column-major weight); all 256 codes may
  *                      occur.  The sum of the codes' products is exact while
- *                      it fits 24 bits.  Beyond that, where M is at most 8 (and
- *                      K within 131071 and the kernel's shared memory) it is a
- *                      32-bit integer, rounded once; else an FP32 result is the
+ *                      it fits 24 bits.  Beyond that it is a 32-bit integer,
+ *                      rounded once, where M is at most 4 (8) and K at most
+ *                      24576 (12288); else an FP32 result is the
  *                      sum of exact parts of 768 products each, rounded to FP32
  *                      as they are added (at most one half step of FP32 each),
  *                      and a BF16 result loses less than 2^-23 of the largest
  *                      partial sum for every 16 products past it.
  * gemm_i8_grouped_run  The same over row groups (see gemm_grouped.h): row r of
  *                      group g is multiplied by rows g*N .. g*N + N - 1 of B.
+ *                      Sums are 32-bit integers where rows is at most 1536 and
+ *                      twice the groups and K at most 24576.
  *
  * The products run on the tensor cores in FP16, which holds every code exactly,
- * or, with at most 8 rows (a group, on average), on integer dot products.  c_dtype
- * is GEMM_F32 or GEMM_BF16.  On the tensor cores A is first converted into the
- * handle's workspace (2 bytes an element), B inside the product.  Handles, streams, asynchrony,
- * errors and in-kernel time limits are those of gemm_run; results are
+ * or, where sums are 32-bit integers, on integer dot products.  c_dtype is GEMM_F32
+ * or GEMM_BF16.  On the tensor cores A is first converted into the handle's
+ * workspace (2 bytes an element), B inside the product.  Handles, streams,
+ * asynchrony, errors and in-kernel time limits are those of gemm_run; results are
  * bit-identical from call to call.  The rows of a matrix times a pitch stay
  * within 2^44, and a group's codes below 2^40 bytes.
  */

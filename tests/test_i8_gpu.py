@@ -274,8 +274,11 @@ def test_few_rows(gm, h, M, N, K, out):
 @pytest.mark.parametrize("sizes", [[1] * 40, [0, 3, 0, 9, 1, 20, 0], [17, 0, 0, 0, 0, 0], [0, 0, 0], [8, 8, 1]],
                          ids=lambda s: f"{len(s)}groups{sum(s)}rows")
 def test_few_rows_grouped(gm, h, sizes):
-    """Groups of many rows among them: they are taken eight (four) at a time."""
-    G, rows, N, K = len(sizes), sum(sizes) + 3, 70, 330
+    """Groups of many rows among them: they are taken four at a time.  Empty groups
+    behind make the groups' average small."""
+    rows, N, K = sum(sizes) + 3, 70, 330
+    sizes = sizes + [0] * max(0, (rows + 1) // 2 - len(sizes))
+    G = len(sizes)
     bounds = [2]
     for s in sizes:
         bounds.append(bounds[-1] + s)
@@ -290,7 +293,7 @@ def test_few_rows_grouped(gm, h, sizes):
         w = slice(g * N, (g + 1) * N)
         assert torch.equal(C[lo:hi].cpu(), expected(product(a[lo:hi], b[w]), sa[lo:hi], sb[w]))
     assert (C[:2] == 7).all() and (C[bounds[-1]:] == 7).all()
-    for bad in ([0, 5, 3] + [rows] * (G - 2), [-1] * G + [2], [0] * G + [rows + 1]):
+    for bad in ([0, 3, 2] + [rows] * (G - 2), [-1] * G + [2], [0] * G + [rows + 1]):
         C.fill_(7.0)
         h.run_i8_grouped(A, B, torch.tensor(bad, device="cuda"), C)
         with pytest.raises(gm.GemmError) as e:
@@ -298,20 +301,38 @@ def test_few_rows_grouped(gm, h, sizes):
         assert e.value.code == gm.GEMM_ERR_INVALID and (C == 7).all()
 
 
-def test_few_rows_largest_sums(gm, h):
-    """131071 products of 2^14: an integer sum just below 2^31, rounded once to FP32."""
-    A, a, sa = operand(gm, 1, 20000, 35)
-    for K in (20000, 131071):
-        if K > 20000 and not K * 4 < 96 * 1024:
-            continue  # the row does not fit the kernel; the tensor-core one takes it
-        B, b, sb = operand(gm, 9, K, 36)
-        A.codes.fill_(-128)
-        B.codes.fill_(-128)
-        C = torch.empty((1, 9), device="cuda")
-        h.run_i8(A, B, C)
+@pytest.mark.parametrize("rows,K", [(4, 24576), (8, 12288)])
+def test_few_rows_largest_sums(gm, h, rows, K):
+    """Products of 2^14 as long as the kernel takes them, and one off: sums past 24
+    bits, rounded once to FP32."""
+    A, a, sa = operand(gm, rows, K, 35)
+    B, b, sb = operand(gm, 9, K, 36)
+    A.codes.fill_(-128)
+    B.codes.fill_(-128)
+    B.codes[:, 5] = 1
+    C = torch.empty((rows, 9), device="cuda")
+    h.run_i8(A, B, C)
+    h.sync_status()
+    assert h.last_path == "i8_rows"
+    assert torch.equal(C.cpu(), expected(torch.full((rows, 9), (K - 1) * 2 ** 14 - 128), sa, sb))
+
+
+@pytest.mark.parametrize("rows,groups", [(1536, 768), (1537, 769), (1, 1024), (300, 150)])
+def test_few_rows_most_passes(gm, h, rows, groups):
+    """A pass for every row, and every row in one group."""
+    N, K = 9, 40
+    A, a, sa = operand(gm, rows, K, 37)
+    B, b, sb = operand(gm, groups * N, K, 38)
+    for bounds in ([min(rows, g) for g in range(groups)] + [rows], [0] * (groups // 2) + [rows] * (groups - groups // 2 + 1)):
+        C = torch.full((rows, N), 7.0, device="cuda")
+        h.run_i8_grouped(A, B, torch.tensor(bounds, device="cuda"), C)
         h.sync_status()
-        assert h.last_path == "i8_rows"
-        assert torch.equal(C.cpu(), expected(torch.full((1, 9), K * 2 ** 14), sa, sb))
+        assert (h.last_path == "grouped_i8_rows") == (rows <= 1536)
+        for g in range(groups):
+            lo, hi = bounds[g], bounds[g + 1]
+            w = slice(g * N, (g + 1) * N)
+            if hi > lo:
+                assert torch.equal(C[lo:hi].cpu(), expected(product(a[lo:hi], b[w]), sa[lo:hi], sb[w]))
 
 
 def test_empty_sums_and_empty_calls(gm, h):
