@@ -202,10 +202,11 @@ __device__ __noinline__ int choose_exactly(const RouteParams &p, const T *row, i
 
 // How far two scores plus biases may be off, together, from what they stand for:
 // FP32 exp (2 ulp), addition and division of a sigmoid and the bias's addition; for
-// a softmax also the sum of up to V / 32 + 5 roundings and the exponent's.
+// a softmax also the sum of up to V / 32 + 5 roundings and the exponent's.  Below
+// 2^-125 a fast division gives zero: 2^-126 for each of a group's two best.
 __device__ __forceinline__ float score_bound(const RouteParams &p, float most, float bias_max)
 {
-    return (most + bias_max) * (p.sigmoid ? 1e-6f : 4e-6f);
+    return (most + bias_max) * (p.sigmoid ? 1e-6f : 4e-6f) + 4e-38f;
 }
 
 // Routes one token with one warp, however close its values are.

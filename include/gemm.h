@@ -156,13 +156,14 @@ extern "C" {
  * 1 = never; 2 = for every FP32 problem (tests). */
 #define GEMM_OPT_SIMT_SMALL 15
 /* Tile of the grouped, 4-bit and 8-bit products (gemm_grouped.h, gemm_mx4.h,
- * gemm_i8.h): 0
- * (default) = the least estimated time for the average group; else 1000 * CTAs
- * + rows, CTAs 1 or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile
- * of 128 * CTAs columns (weight gradients take 128 or 256, 4-bit products at
- * most 224, 8-bit products at most 128, of a pair with BF16 results 192), plus 10000 * S to cut the contraction over clusters of S = 2, 4 or
- * 8 CTAs (CTAs 1, rows at most 128).  By default the contraction is cut where
- * the tiles would leave SMs idle; GEMM_OPT_SPLIT_K = 1 (or more) forbids it. */
+ * gemm_i8.h): 0 (default) = the least estimated time for the average group (8-bit
+ * products of few rows take another kernel then); else 1000 * CTAs + rows, CTAs 1
+ * or 2 (a pair) and rows 32, 64, 128, 224 or 256 of C per tile of 128 * CTAs
+ * columns (weight gradients take 128 or 256, 4-bit products at most 224, 8-bit
+ * products at most 128, of a pair with BF16 results 192), plus 10000 * S to cut the
+ * contraction over clusters of S = 2, 4 or 8 CTAs (CTAs 1, rows at most 128).  By
+ * default the contraction is cut where the tiles would leave SMs idle;
+ * GEMM_OPT_SPLIT_K = 1 (or more) forbids it. */
 #define GEMM_OPT_GROUPED_TILE 16
 /* Tile of the products of gemm_ortho.h: 0 (default) = the least estimated time
  * of each; else 1000 * CTAs + columns, CTAs 1 or 2 and columns 32, 64, 128 or 256

@@ -218,6 +218,19 @@ def test_close_sums_are_decided_in_64_bits(gm, h, scoring):
         assert torch.equal(r.expert.cpu(), e)
 
 
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("E,groups", [(16, 4), (256, 8), (640, 8)])
+def test_scores_near_the_smallest_number(gm, h, E, groups, biased):
+    """Sigmoids of 1e-39 to 1e-36, some of which FP32 has only as zero."""
+    gen = torch.Generator().manual_seed(12)
+    x = -90 + 6 * torch.rand((100, E), generator=gen)
+    bias = torch.zeros(E) if biased else None
+    r = fresh(gm, 100, E, 4)
+    h.route(x.cuda(), r, "sigmoid", bias.cuda() if biased else None, groups, 2)
+    _, e = definition(x, 4, "sigmoid", bias, groups, 2)
+    assert torch.equal(r.expert.cpu(), e)
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_neighbouring_logits_keep_their_order(gm, h, sign):
     """FP32 logits one unit in the last place apart, and equal ones."""
