@@ -7,11 +7,14 @@
 // key, its order-preserving bits above the expert's index, so that every key is
 // different and a comparison is one instruction; a lane sorts its keys by a
 // network, keeps eight, and the lanes merge their lists in 3 to 5 exchanges.  BF16
-// logits fit their key whole; of FP32 values it holds 22 bits, and the chosen are
+// logits fit their key whole; of FP32 values it holds 23 bits, and the chosen are
 // put in order by their full values afterwards.  (One pick after another by
 // warp-wide maxima took 780 instructions a token of 128 experts and 2300 of 256 in
-// groups, and their issue set the time: 38 and 84 us for 32768 and 16384 tokens.)
-// What the keys, or FP32 itself, leave open (a key equal in its 22 bits to the last
+// groups; 200 and 900 now.)  The issue of instructions, at 45 to 50 % of its rate
+// with the 32 warps an SM that 64 registers leave, sets the time, not memory (8 to
+// 10 % of its rate): 16384 tokens of 256 experts 23 us, 32768 of 128 11 us, both
+// without the sorting by expert (6 us).
+// What the keys, or FP32 itself, leave open (a key equal in its 23 bits to the last
 // choice's, or a sum with a bias nearer than a bound on the rounding of the scores:
 // one token in a hundred) is settled by settle_token: the few experts that may be
 // among the chosen, one a lane, are ranked by their values in FP64.  Groups whose
@@ -198,6 +201,20 @@ __device__ __noinline__ int choose_exactly(const RouteParams &p, const T *row, i
     int index;
     pick<V>(key, p.k, lane, unused, index);
     return index;
+}
+
+// For the ranking alone: e^x to 2^-22 and x * 2^-24, 1 / x to an ulp, flushed.
+__device__ __forceinline__ float exp_near(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950409f));
+    return y;
+}
+__device__ __forceinline__ float inverse_near(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // How far two scores plus biases may be off, together, from what they stand for:
@@ -433,26 +450,37 @@ __device__ __forceinline__ F token_reduce(F x, const Op &op)
 }
 
 constexpr int kScratch = 32;  // candidates of settle_token, per warp
+constexpr uint32_t kIndex = 511;            // the index in a key of an FP32 value
 constexpr uint32_t kLowest = 0x00800000u;  // key of the lowest finite value, its index cut off
 
 // The choice among n <= 32 experts of token t (scratch[0 .. n - 1]), the only ones
-// that may be chosen, by logits or by sigmoid scores with a bias in FP64.  top,
-// sum: of the row's softmax.
+// that may be chosen, by logits or by sigmoid scores with a bias, in FP64 where
+// two are within `bound`.  top, sum: of the row's softmax.
 template <typename T>
 __device__ __noinline__ void settle_token(const RouteParams &p, int t, int n, const int *scratch, float top, float sum,
-                                          int *count, int lane)
+                                          float bound, int *count, int lane)
 {
     const T *row = static_cast<const T *>(p.logits) + static_cast<long long>(t) * p.ld;
     const int index = lane < n ? scratch[lane] : -1;
     const float x = index >= 0 ? to_float(row[index]) : -INFINITY;
-    double d = x;
-    if (p.bias && index >= 0)
-        d = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(__ldg(p.bias + index));
+    const float v = p.bias && index >= 0 ? 1.0f / (1.0f + expf(-x)) + __ldg(p.bias + index) : x;
     int rank = 0;
+    bool close = false;
     for (int i = 0; i < n; ++i) {
-        const double o = __shfl_sync(kFull, d, i);
+        const float o = __shfl_sync(kFull, v, i);
         const int oi = __shfl_sync(kFull, index, i);
-        rank += o > d || (o == d && oi < index) ? 1 : 0;
+        rank += o > v || (o == v && oi < index) ? 1 : 0;
+        close |= i != lane && !(fabsf(o - v) > bound);
+    }
+    if (p.bias && __any_sync(kFull, close && index >= 0)) {
+        double d = -INFINITY;
+        if (index >= 0) d = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(__ldg(p.bias + index));
+        rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const double o = __shfl_sync(kFull, d, i);
+            const int oi = __shfl_sync(kFull, index, i);
+            rank += o > d || (o == d && oi < index) ? 1 : 0;
+        }
     }
     const bool in = index >= 0 && rank < p.k;
     float score = 0.0f;
@@ -515,7 +543,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
     }
     uint32_t key[V];
     bool close = false, open = true, slow_group = false;
-    float bound = 0.0f;
+    float bound = 0.0f, rough = 0.0f;  // of scores by expf, and of v
     if (scored) {
         float most = 0.0f, v[V], offset[V];
         const float scale = 1.0f / sum;
@@ -526,12 +554,15 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float s = p.sigmoid ? __fdividef(1.0f, 1.0f + expf(-x[j])) : expf(x[j] - top) * scale;
+            const float s = p.sigmoid ? inverse_near(1.0f + exp_near(-x[j])) : exp_near(x[j] - top) * scale;
             v[j] = x[j] == -INFINITY ? -INFINITY : s + offset[j];
             odd |= v[j] != v[j];
             if (x[j] != -INFINITY) most = fmaxf(most, s);
         }
-        bound = score_bound(p, token_reduce<L>(most, fmax_), bias_max);
+        most = token_reduce<L>(most, fmax_);
+        bound = score_bound(p, most, bias_max);
+        // two scores by exp_near: (|x| + 7) 2^-24 of a sigmoid each, |x| up to 88
+        rough = bound + most * (p.sigmoid ? 1.2e-5f : 1e-6f);
         if (p.groups > 1) {
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -550,7 +581,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
             for (int g = 0; g < p.groups; ++g) {
                 const float o = __shfl_sync(kFull, score, (lane / L) * L + g * y.lanes);
                 rank += o > score || (o == score && g < group) ? 1 : 0;
-                near |= g != group && !(fabsf(o - score) > 2.0f * bound) && o != -INFINITY;
+                near |= g != group && !(fabsf(o - score) > 2.0f * rough) && o != -INFINITY;
             }
             open = rank < p.top_groups && score != -INFINITY;
             // the last group in and the first one out may change places
@@ -559,7 +590,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
                 slow_group = near;
             } else if (__any_sync(kFull, near)) {
                 // the sums again in FP64, of all that may be a group's two best
-                const float least = (b == -INFINITY ? a : b) - bound;
+                const float least = (b == -INFINITY ? a : b) - rough;
                 uint32_t which = 0;
 #pragma unroll
                 for (int j = 0; j < V; ++j) which |= v[j] != -INFINITY && v[j] >= least ? 1u << j : 0u;
@@ -601,13 +632,13 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
     }
     // Minus infinity, what is past the row's end and closed groups come out below
     // kLowest, the key of the lowest finite value.
-    const uint32_t keep = open ? (whole_key ? 0xffff0000u : ~1023u) : 0u;
-    const uint32_t base = (whole_key ? 0xffffu : 1023u) - static_cast<uint32_t>(first);
+    const uint32_t keep = open ? (whole_key ? 0xffff0000u : ~kIndex) : 0u;
+    const uint32_t base = (whole_key ? 0xffffu : kIndex) - static_cast<uint32_t>(first);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint32_t u = __float_as_uint(x[j] + 0.0f);
         key[j] = ((u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u)) & keep) |
-                 ((base - j) & (whole_key ? 0xffffu : 1023u));
+                 ((base - j) & (whole_key ? 0xffffu : kIndex));
     }
     uint32_t list[8];
     if (V == 16) {
@@ -647,13 +678,13 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
     uint32_t low = kLowest;
     if (!whole_key && full) {
         // whatever is not chosen and may belong before the last choice
-        low = last & ~1023u;
-        if (biased) low = min(low, key_of(key_value(low) - bound) & ~1023u);
+        low = last & ~kIndex;
+        if (biased) low = min(low, key_of(key_value(low) - rough) & ~kIndex);
         low = max(low, kLowest);
 #pragma unroll
         for (int j = 0; j < V; ++j) close |= key[j] < last && key[j] >= low;
     }
-    const int index = mine < kLowest ? -1 : static_cast<int>(whole_key ? 0xffffu - (mine & 0xffffu) : 1023u - (mine & 1023u));
+    const int index = mine < kLowest ? -1 : static_cast<int>(whole_key ? 0xffffu - (mine & 0xffffu) : kIndex - (mine & kIndex));
     const float chosen = index >= 0 ? to_float(row[index]) : -INFINITY;
     float score = 0.0f;
     if (p.sigmoid) {
@@ -721,8 +752,8 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
             for (int j = 0; j < V; ++j)
                 if (key[j] >= low) scratch[at++] = first + j;
         __syncwarp();
-        settle_token<T>(p, t0 + i, n, scratch, __shfl_sync(kFull, top, i * L), __shfl_sync(kFull, sum, i * L), count,
-                        lane);
+        settle_token<T>(p, t0 + i, n, scratch, __shfl_sync(kFull, top, i * L), __shfl_sync(kFull, sum, i * L),
+                        __shfl_sync(kFull, bound, i * L), count, lane);
         __syncwarp();
     }
 }
@@ -754,20 +785,40 @@ __device__ void block_scan(int *v, int n, int *warp_sums)
     __syncthreads();
 }
 
-// Places the choices lo .. hi - 1 (rows t * k + i) by expert.  base[b]: where
-// the first of bin b = expert + 1 goes.  hist: [warps][bins] of scratch.
+// A warp's run of the choices lo .. hi - 1 (rows t * k + i), whole 32s, and the bins
+// (expert + 1) of its first KEEP * 32, a lane's own.
 template <int NT>
-__device__ void place(const RouteParams &p, int lo, int hi, int bins, const int *base, int *hist)
+struct Run {
+    static constexpr int KEEP = 4;
+    int first, last, bin[KEEP];
+    __device__ __forceinline__ void load(const RouteParams &p, int lo, int hi)
+    {
+        constexpr int W = NT / 32;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int per = ((hi - lo + W - 1) / W + 31) & ~31;
+        first = lo + warp * per;
+        last = min(hi, first + per);
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j) bin[j] = at(p, first + j * 32 + lane);
+    }
+    __device__ __forceinline__ int at(const RouteParams &p, int i) const
+    {
+        return i < last ? static_cast<int>(p.expert[i]) + 1 : -1;
+    }
+};
+
+// Places the choices of all warps' runs by expert.  base[b]: where the first of bin
+// b goes.  hist: [warps][bins] of zeros.
+template <int NT>
+__device__ void place(const RouteParams &p, const Run<NT> &run, int bins, const int *base, int *hist)
 {
-    constexpr int W = NT / 32;
+    constexpr int W = NT / 32, KEEP = Run<NT>::KEEP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < W * bins; i += NT) hist[i] = 0;
-    __syncthreads();
-    // a contiguous run of whole 32s a warp
-    const int per = ((hi - lo + W - 1) / W + 31) & ~31;
-    const int first = lo + warp * per, last = min(hi, first + per);
     int *mine = hist + warp * bins;
-    for (int i = first + lane; i < last; i += 32) atomicAdd(mine + static_cast<int>(p.expert[i]) + 1, 1);
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+        if (run.bin[j] >= 0) atomicAdd(mine + run.bin[j], 1);
+    for (int i = run.first + KEEP * 32 + lane; i < run.last; i += 32) atomicAdd(mine + run.at(p, i), 1);
     __syncthreads();
     for (int b = tid; b < bins; b += NT) {
         int at = base[b];
@@ -779,9 +830,7 @@ __device__ void place(const RouteParams &p, int lo, int hi, int bins, const int 
         }
     }
     __syncthreads();
-    for (int i0 = first; i0 < last; i0 += 32) {
-        const int i = i0 + lane;
-        const int bin = i < last ? static_cast<int>(p.expert[i]) + 1 : -1;
+    const auto put = [&](int i, int bin) {
         const unsigned same = __match_any_sync(kFull, bin);
         const int rank = __popc(same & ((1u << lane) - 1u));
         const int at = bin >= 0 ? mine[bin] : 0;
@@ -791,7 +840,11 @@ __device__ void place(const RouteParams &p, int lo, int hi, int bins, const int 
             p.order[at + rank] = i;
         }
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+        if (run.first + j * 32 < run.last) put(run.first + j * 32 + lane, run.bin[j]);
+    for (int i0 = run.first + KEEP * 32; i0 < run.last; i0 += 32) put(i0 + lane, run.at(p, i0 + lane));
 }
 
 __device__ __forceinline__ float largest_bias(const RouteParams &p, int lane)
@@ -816,7 +869,7 @@ __global__ void __launch_bounds__(NT, 1) route_kernel(const RouteParams p, const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bins = p.experts + 1;
     int *count = smem, *hist = smem + bins;  // ONE: a counter a warp and bin
-    for (int i = tid; i < bins; i += NT) count[i] = 0;
+    for (int i = tid; i < (ONE ? bins * (1 + W) : bins); i += NT) smem[i] = 0;
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
@@ -843,7 +896,9 @@ __global__ void __launch_bounds__(NT, 1) route_kernel(const RouteParams p, const
         for (int b = tid; b < bins; b += NT)  // bin e + 1 starts where expert e does
             if (b > 0) p.offsets[b - 1] = count[b];
         if (tid == 0) p.offsets[p.experts] = static_cast<long long>(p.tokens) * p.k;
-        place<NT>(p, 0, p.tokens * p.k, bins, count, hist);
+        Run<NT> run;
+        run.load(p, 0, p.tokens * p.k);
+        place<NT>(p, run, bins, count, hist);
     } else {
         for (int b = tid; b < p.pitch; b += NT)
             p.counts[static_cast<long long>(blockIdx.x) * p.pitch + b] = b < bins ? count[b] : 0;
@@ -859,10 +914,13 @@ __global__ void __launch_bounds__(NT, 1) place_kernel(const RouteParams p)
     const int tid = threadIdx.x;
     const int bins = p.experts + 1;
     int *total = smem, *before = smem + bins, *hist = smem + 2 * bins;
-    for (int i = tid; i < 2 * bins; i += NT) smem[i] = 0;
+    for (int i = tid; i < (2 + NT / 32) * bins; i += NT) smem[i] = 0;
+    const int t0 = blockIdx.x * p.per_chunk, t1 = min(p.tokens, t0 + p.per_chunk);
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
+    Run<NT> run;
+    run.load(p, t0 * p.k, max(t0, t1) * p.k);
     // four bins a thread, as many runs of CTAs side by side as there are threads
     const int quads = p.pitch / 4, parts = NT / quads;
     if (tid < parts * quads) {
@@ -894,8 +952,7 @@ __global__ void __launch_bounds__(NT, 1) place_kernel(const RouteParams p)
     }
     for (int b = tid; b < bins; b += NT) before[b] += total[b];
     __syncthreads();
-    const int t0 = blockIdx.x * p.per_chunk, t1 = min(p.tokens, t0 + p.per_chunk);
-    place<NT>(p, t0 * p.k, max(t0, t1) * p.k, bins, before, hist);
+    place<NT>(p, run, bins, before, hist);
 }
 
 __global__ void zero_offsets_kernel(long long *offsets, int n)
