@@ -90,6 +90,7 @@
 #include <cuda_bf16.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -1257,23 +1258,28 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
                 if (bn > most_bn || (kind == kRaggedI8 && bn > 128 && ctas == 1)) continue;
                 const int64_t units = max_units(ragged_k, rows, groups, P, Q, ctas, bn);
                 if (split > 1 && (!may_split || ctas > 1 || bn > 128 || units > max_clusters(split) || units * split > sm_count ||
-                                  kt < 4 * split))
+                                  kt < (kind == kRaggedI8 ? 1 : 4) * split))
                     continue;
                 const double mma = bn == 32 ? 40 : bn == 64 ? 48 : bn / 2;
-                // 8-bit operands: stages of eight instructions, and 450 cycles of conversion
+                // 8-bit operands: stages of eight instructions, and 700 cycles of hand-overs
+                // (301 x 2047 x 1000, FP32: tiles of 64 rows 11.1 us, of 32, one more than
+                // there are SMs for, 14.3)
                 const double stage =
                     kind == kRaggedI8
-                        ? std::max({8 * mma, (P_BYTES + bn / ctas * 256) / 55.0, 450.0})
+                        ? std::max({8 * mma, (P_BYTES + bn / ctas * 256) / 55.0, 700.0})
                         : std::max(4 * mma, (P_BYTES + bn / ctas * 128) / 55.0) * (kind == kRaggedMx4 ? 1.1 : 1);
                 const double tiles_p = static_cast<double>((P + ctas * BP - 1) / (ctas * BP));
                 const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
                                        : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
                                                     : double((rows + bn - 1) / bn);
-                const double tile = static_cast<double>((kt + split - 1) / split) * stage +
+                const int64_t slice = (kt + split - 1) / split;  // of 8-bit stages an even number
+                const double tile = static_cast<double>(kind == kRaggedI8 && split > 1 ? (slice + 1) & ~1 : slice) * stage +
                                     (kind == kRaggedMx4 && ctas > 1 ? 3000 : 0);
                 const double epi = 600 + bn * 12.0;
                 const double fill = tiles_q * tiles_p * ctas * split / sm_count;
-                const double run = (fill <= 1 ? 1 : fill + 0.3) * std::max(tile, epi) + std::min(tile, epi) +
+                // whole waves of 8-bit tiles where there is one group, the rows of each known
+                const double waves = fill <= 1 ? 1 : kind == kRaggedI8 && busy <= 1.5 ? std::ceil(fill) : fill + 0.3;
+                const double run = waves * std::max(tile, epi) + std::min(tile, epi) +
                                    (split > 1 || ctas > 1 ? 1500 : 0);
                 const double mem = bytes / 3370;
                 const double t = std::max(run, mem) + 0.1 * std::min(run, mem) + 6000;

@@ -17,8 +17,10 @@
 // What the keys, or FP32 itself, leave open (a key equal in its 23 bits to the last
 // choice's, or a sum with a bias nearer than a bound on the rounding of the scores:
 // one token in a hundred) is settled by settle_token: the few experts that may be
-// among the chosen, one a lane, are ranked by their values in FP64.  Groups whose
-// sums are as near, more choices and more experts take route_slowly, a warp a token.
+// among the chosen, one a lane, are ranked by their values, in FP64 where FP32
+// cannot tell two apart.  Sums of groups that are as near are taken again in FP64;
+// softmax scores that near, more choices and more experts take route_slowly, a warp
+// a token.
 //
 // Sorting by expert is a counting sort, stable and without atomics whose order
 // would matter: CTA c routes a run of tokens and counts its choices by expert;
