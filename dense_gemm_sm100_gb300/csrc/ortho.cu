@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // With the powers of two of what is read and written in the constants, a
             // value is acc * scale (A), + e * (row + column) (B; e an element of A,
             // row and column from the diagonal), or + x * row (X).
-            float scale, row_c[4], column_c = 0.0f;  // rows i0 + sub, + 8, ...
+            float scale, row_c[4], row_d[4], column_c = 0.0f;  // rows i0 + sub, + 8, ...
             if (XSTEP) {
                 const float post = (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
                 scale = post / SCALE_B;
@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = i0 + sub + 8 * r;
-                    row_c[r] = i < p.m ? fmaf(p.cc, p.da[mat * p.ldm + i], p.cb) * (SCALE_B / SCALE_A) : 0.0f;
+                    row_d[r] = i < p.m ? p.da[mat * p.ldm + i] : 0.0f;
+                    row_c[r] = fmaf(p.cc, row_d[r], p.cb) * (SCALE_B / SCALE_A);
                 }
             }
             const int width = XSTEP ? p.n : p.m, ld = XSTEP ? p.ldn : p.ldm;
@@ -440,8 +441,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             // The operands that the epilogue adds: X, or A where B is made.
             uint4 extra[2][4];
+            float4 diagonal[2];  // A's, at a lane's columns; ahead where registers allow
             const bool reads = XSTEP || p.mode == kOrthoB;
             const bool two = SPLIT || (XSTEP && p.has_rest);
+            const auto load_diagonal = [&](int j) {
+                const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
+                diagonal[0] = d[0];
+                diagonal[1] = d[1];
+            };
             const auto fetch = [&](int k) {
                 if (!reads) return;
                 const int j = column(k) + piece * 8;
@@ -454,6 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     extra[0][r] = in ? *reinterpret_cast<const uint4 *>(from[0] + o) : make_uint4(0u, 0u, 0u, 0u);
                     if (two) extra[1][r] = in ? *reinterpret_cast<const uint4 *>(from[1] + o) : make_uint4(0u, 0u, 0u, 0u);
                 }
+                if (!SPLIT && !XSTEP && j < width) load_diagonal(j);
             };
             const bool back = XSTEP ? p.last && p.turned : t.mirror;  // results are needed column by column
             __half *const *planes = XSTEP ? p.x_out : p.mode == kOrthoA ? p.a : p.b;
@@ -465,8 +473,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 float dj[8];
                 if (!XSTEP && p.mode == kOrthoB && j < width) {
-                    const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
-                    const float4 d0 = d[0], d1 = d[1];
+                    if (SPLIT) load_diagonal(j);
+                    const float4 d0 = diagonal[0], d1 = diagonal[1];
                     dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
                     dj[4] = d1.x, dj[5] = d1.y, dj[6] = d1.z, dj[7] = d1.w;
 #pragma unroll
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (p.mode == kOrthoA) {
                                     p.da[mat * p.ldm + i] = v[c] * scale * (1.0f / SCALE_A);
                                 } else {
-                                    const float d = p.da[mat * p.ldm + i];
+                                    const float d = SPLIT ? p.da[mat * p.ldm + i] : row_d[r];
                                     p.db[mat * p.ldm + i] =
                                         p.cb * d + p.cc * fmaf(d, d, v[c] * (1.0f / (SCALE_A * SCALE_A)));
                                 }
@@ -692,57 +700,58 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16 *src, float (&x)[8]
     }
 }
 
-// From the norm of a matrix: the factors of its products and the power of two
-// of X (two factors, whose product may leave FP32's range).
-__device__ void write_factors(double norm, double eps, float *f)
+__device__ __forceinline__ double power_of_two(int k)  // |k| < 1022
+{
+    return __longlong_as_double(static_cast<long long>(k + 1023) << 52);
+}
+
+// From the sum of squares of a matrix: the factors of its products and the power
+// of two of X (two factors, whose product may leave FP32's range).  FP64 operations
+// are slow here (sqrt, division and frexp took 2 us of a call): FP32 results with
+// one correction each.
+__device__ void write_factors(double sum, double eps, float *f)
 {
     // |G| 2^e in [1, 2); 1 / ((|G| + eps) 2^e) = rest 2^-down, down > 0 only where eps outweighs |G|
     int e = 0, down = 0;
-    double rest = 1.0;
-    if (!(norm < INFINITY)) {
-        rest = __longlong_as_double(0x7fffffffffffffffLL);  // NaN
-    } else if (norm > 0.0) {
-        int top;
-        frexp(norm, &top);
-        e = 1 - top;
-        rest = 1.0 / ldexp(norm + eps, e);
-        if (rest < 0.25) {
-            int low;
-            rest = 2.0 * frexp(rest, &low);
-            down = 1 - low;
+    float rest = 1.0f;
+    if (!(sum < INFINITY)) {
+        rest = __int_as_float(0x7fffffff);  // NaN
+    } else if (sum > 0.0) {
+        int two = static_cast<int>(__double_as_longlong(sum) >> 52) - 1023;  // sums of FP32 squares are no FP64 denormals
+        two -= two & 1;
+        e = -(two / 2);
+        const double g = sum * power_of_two(-two);  // in [1, 4)
+        const float root = sqrtf(static_cast<float>(g));
+        const double r = root, near = r + 0.5f * static_cast<float>(fma(-r, r, g)) / root;
+        double h = near + eps * power_of_two(e);
+        if (h > 4.0) {
+            const int q = static_cast<int>(__double_as_longlong(h) >> 52) - 1023;
+            h *= 0.5 * power_of_two(-q);
+            down = q + 1;
         }
+        rest = 1.0f / static_cast<float>(h);
+        rest = fmaf(rest, static_cast<float>(fma(-h, static_cast<double>(rest), 1.0)), rest);
     }
     // X may grow by the steps' factors where A is too small to hold it back
     const int storage = SCALE_X_LOG - min(down, 9), up = e + storage, up0 = max(-126, min(126, up));
-    const double s2 = ldexp(1.0, -2 * storage - 2 * down);
-    f[kFactorA0] = static_cast<float>(s2 * rest * rest);
-    f[kFactorA] = static_cast<float>(s2);
-    f[kFactorX0] = static_cast<float>(rest);
-    f[kFactorOut] = static_cast<float>(ldexp(1.0, -storage - down));
+    f[kFactorA0] = ldexpf(rest * rest, -2 * (storage + down));
+    f[kFactorA] = ldexpf(1.0f, -2 * (storage + down));
+    f[kFactorX0] = rest;
+    f[kFactorOut] = ldexpf(1.0f, -storage - down);
     f[kFactorUp0] = ldexpf(1.0f, up0);
     f[kFactorUp1] = ldexpf(1.0f, max(-126, min(126, up - up0)));
 }
 
-// Sums of squares of the rows of a part of a matrix.  A thread adds in FP32, the
-// threads in FP64.  Where squares would leave FP32 (largest magnitude above 2^50
-// or below 2^-40) the part is summed again, scaled by a power of two.  A matrix
-// of one part has its factors written here.
+// The sum of squares of rows r0 .. r1 - 1, by a whole CTA.  A thread adds in FP32,
+// the threads in FP64.  Where squares would leave FP32 (largest magnitude above
+// 2^50 or below 2^-40) the rows are summed again, scaled by a power of two.
 template <typename T>
-__global__ void __launch_bounds__(NORM_THREADS)
-    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, float eps, bool vec,
-                double *parts, float *factors)
+__device__ double squares(const T *base, long long ldg, int r0, int r1, int cols, bool vec)
 {
     constexpr int N = 16 / sizeof(T);
     __shared__ double sums[NORM_THREADS / 32];
     __shared__ float tops[NORM_THREADS / 32];
-    griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long b = blockIdx.x / num_parts;
-    const int part = static_cast<int>(blockIdx.x - b * num_parts);
-    const int per = (rows + num_parts - 1) / num_parts;
-    const int r0 = min(rows, part * per), r1 = min(rows, r0 + per);
-    const T *base = g + b * stride;
     float scale = 1.0f;
     for (int pass = 0;; ++pass) {
         float top = 0.0f;
@@ -793,10 +802,9 @@ __global__ void __launch_bounds__(NORM_THREADS)
         __syncthreads();
         const bool again = pass == 0 && top > 0.0f && top < INFINITY && (top > 0x1p50f || top < 0x1p-40f);
         if (!again) {
-            total /= static_cast<double>(scale) * scale;
-            if (threadIdx.x == 0 && num_parts == 1) write_factors(sqrt(total), eps, factors + b * FACTORS);
-            if (threadIdx.x == 0 && num_parts > 1) parts[b * num_parts + part] = total;
-            return;
+            if (scale == 1.0f) return total;
+            const double undo = 1.0 / scale;  // a power of two
+            return total * undo * undo;
         }
         int e;
         frexpf(top, &e);
@@ -804,32 +812,34 @@ __global__ void __launch_bounds__(NORM_THREADS)
     }
 }
 
-__global__ void factors_kernel(const double *parts, int num_parts, float eps, float *factors)
+template <typename T>
+__global__ void __launch_bounds__(NORM_THREADS)
+    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, bool vec, double *parts)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const long long b = blockIdx.x;
-    double sum = 0.0;
-    for (int k = threadIdx.x; k < num_parts; k += 32) sum += parts[b * num_parts + k];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (threadIdx.x == 0) write_factors(sqrt(sum), eps, factors + b * FACTORS);
+    const long long b = blockIdx.x / num_parts;
+    const int part = static_cast<int>(blockIdx.x - b * num_parts);
+    const int per = (rows + num_parts - 1) / num_parts;
+    const int r0 = min(rows, part * per), r1 = min(rows, r0 + per);
+    const double sum = squares(g + b * stride, ldg, r0, r1, cols, vec);
+    if (threadIdx.x == 0) parts[b * num_parts + part] = sum;
 }
 
-// X in two FP16 numbers from G, turned where rows > cols.  A CTA takes 64 x 64
-// elements.
+// X in two FP16 numbers from G, turned where rows > cols, and the matrix's factors,
+// which every CTA makes from the sums of the norm's parts (one part: of the matrix
+// itself) for a launch less.  A CTA takes 64 x 64 elements.
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
     start_kernel(const T *g, long long ldg, long long stride, bool vec, int turned, int m, int n, int ldn, int tiles_j,
-                 int tiles, __half *x0, __half *x1, const float *factors)
+                 int tiles, __half *x0, __half *x1, const double *parts, int num_parts, float eps, float *factors)
 {
-    __shared__ float tile[64][65];
+    __shared__ float tile[64][65], f[FACTORS];
     griddep_wait();
     griddep_launch_dependents();
     const long long b = blockIdx.x / tiles;
     const int t = static_cast<int>(blockIdx.x - b * tiles);
     const int i0 = t / tiles_j * 64, j0 = t % tiles_j * 64;
-    const float s0 = factors[b * FACTORS + kFactorUp0], s1 = factors[b * FACTORS + kFactorUp1];
     constexpr int N = 16 / sizeof(T);
     const T *base = g + b * stride;
     // tile[a][c]: row a of G's part (64 x 64), turned on the way out
@@ -847,23 +857,37 @@ __global__ void __launch_bounds__(NORM_THREADS)
                     x[i] = ga + a < rows && gc + c + i < cols ? to_f32(base[(ga + a) * ldg + gc + c + i]) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) tile[a][c + i] = x[i] * s0 * s1;
+            for (int i = 0; i < N; ++i) tile[a][c + i] = x[i];
         }
     } else {
 #pragma unroll 4
         for (int k = threadIdx.x; k < 64 * 64; k += NORM_THREADS) {
             const int a = k >> 6, c = k & 63;
-            tile[a][c] = (ga + a < rows && gc + c < cols ? to_f32(base[(ga + a) * ldg + gc + c]) : 0.0f) * s0 * s1;
+            tile[a][c] = ga + a < rows && gc + c < cols ? to_f32(base[(ga + a) * ldg + gc + c]) : 0.0f;
         }
     }
+    double sum = 0.0;
+    if (num_parts == 1) {
+        sum = squares(base, ldg, 0, rows, cols, vec);
+    } else if (threadIdx.x < 32) {
+        for (int k = threadIdx.x; k < num_parts; k += 32) sum += parts[b * num_parts + k];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+    if (threadIdx.x == 0) {
+        write_factors(sum, eps, f);
+        if (t == 0)
+            for (int k = 0; k < FACTORS; ++k) factors[b * FACTORS + k] = f[k];
+    }
     __syncthreads();
+    const float s0 = f[kFactorUp0], s1 = f[kFactorUp1];
 #pragma unroll
     for (int k = threadIdx.x; k < 64 * 8; k += NORM_THREADS) {
         const int r = k >> 3, c = (k & 7) * 8;  // 16 bytes of X
         if (i0 + r >= m) continue;
         float v[8], rest[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = turned ? tile[c + i][r] : tile[r][c + i];
+        for (int i = 0; i < 8; ++i) v[i] = (turned ? tile[c + i][r] : tile[r][c + i]) * s0 * s1;
         const long long at = (b * m + i0 + r) * ldn + j0 + c;
         *reinterpret_cast<uint4 *>(x0 + at) = round8(v, rest);
         if (x1) *reinterpret_cast<uint4 *>(x1 + at) = round8(rest);
@@ -943,7 +967,6 @@ cudaError_t prepare_ortho()
 {
     cudaError_t e = kernel_ready<norm_kernel<float>>(0);
     if (e == cudaSuccess) e = kernel_ready<norm_kernel<__nv_bfloat16>>(0);
-    if (e == cudaSuccess) e = kernel_ready<factors_kernel>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<float>>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<__nv_bfloat16>>(0);
     if (e == cudaSuccess) e = ready_for<1>();
@@ -954,33 +977,30 @@ cudaError_t prepare_ortho()
 cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, cudaStream_t stream,
                                int *launches)
 {
-    // one part below 8192 elements: a launch less
+    // one part below 8192 elements: the start sums it up, a launch less
     const int64_t size = int64_t{u.rows} * u.cols;
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ORTHO_PARTS, size / 4096)));
     const int es = u.bf16 ? 2 : 4;
     const bool vec = reinterpret_cast<uintptr_t>(u.g) % 16 == 0 && (u.ldg * es) % 16 == 0 && (u.stride_g * es) % 16 == 0;
     const __nv_bfloat16 *gb = static_cast<const __nv_bfloat16 *>(u.g);
     const float *gf = static_cast<const float *>(u.g);
-    cudaError_t e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb,
-                                        u.ldg, u.stride_g, u.rows, u.cols, parts, u.eps, vec, w.parts, w.factors)
-                           : launch_pdl(norm_kernel<float>, parts * w.batch, NORM_THREADS, 0, stream, 1, gf, u.ldg,
-                                        u.stride_g, u.rows, u.cols, parts, u.eps, vec, w.parts, w.factors);
-    if (e != cudaSuccess) return e;
-    ++*launches;
+    cudaError_t e = cudaSuccess;
     if (parts > 1) {
-        const double *sums = w.parts;
-        e = launch_pdl(factors_kernel, w.batch, 32, 0, stream, 1, sums, parts, u.eps, w.factors);
+        e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb, u.ldg,
+                                u.stride_g, u.rows, u.cols, parts, vec, w.parts)
+                   : launch_pdl(norm_kernel<float>, parts * w.batch, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g,
+                                u.rows, u.cols, parts, vec, w.parts);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
     const int tiles_j = (w.n + 63) / 64, tiles = (w.m + 63) / 64 * tiles_j;
     const int grid = tiles * w.batch, turned = u.rows > u.cols;
     __half *x0 = reinterpret_cast<__half *>(w.x[0][0]), *x1 = split ? reinterpret_cast<__half *>(w.x[0][1]) : nullptr;
-    const float *factors = w.factors;
+    const double *sums = w.parts;
     e = u.bf16 ? launch_pdl(start_kernel<__nv_bfloat16>, grid, NORM_THREADS, 0, stream, 1, gb, u.ldg, u.stride_g,
-                            vec, turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, factors)
+                            vec, turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, sums, parts, u.eps, w.factors)
                : launch_pdl(start_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, vec, turned, w.m,
-                            w.n, w.ldn, tiles_j, tiles, x0, x1, factors);
+                            w.n, w.ldn, tiles_j, tiles, x0, x1, sums, parts, u.eps, w.factors);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
