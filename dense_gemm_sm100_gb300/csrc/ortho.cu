@@ -367,7 +367,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // 4096 x 2048 500 us, B 150 us.)
         const int q = warp & 3;            // tensor-memory lane quarter
         const int half = (warp - 2) >> 2;  // 0: even chunks of 32 columns, 1: odd ones
-        const int mine = (p.bn / 32 + 1 - half) / 2;
+        // Tiles of 32 columns: both halves take the one chunk, 16 of its rows each (with
+        // half of the warps idle one matrix of 256 x 384 took 83.7 us, 80.3 now).
+        const bool narrow = !XSTEP && p.bn == 32;
+        const int mine = narrow ? 1 : (p.bn / 32 + 1 - half) / 2;
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 4096;
         const int sub = lane >> 2, piece = lane & 3;
         // 16 bytes c of row r: bank conflicts are spread over the rows
@@ -430,7 +433,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_load_16cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc_it & 1u) * ACC1 + unit * 16, v);
             };
             // Chunk k of this warp: columns from column(k) on.
-            const auto column = [&](int k) { return t.j0 + (2 * k + half) * 32; };
+            const auto column = [&](int k) { return narrow ? t.j0 : t.j0 + (2 * k + half) * 32; };
+            const auto skips = [&](int r) { return narrow && (r >> 1) != half; };
             const auto turn = [&](const uint32_t(&lo)[16], const uint32_t(&hi)[16]) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -455,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const __half *const *from = XSTEP ? p.x : p.a;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
+                    if (skips(r)) continue;
                     const int i = i0 + sub + 8 * r;
                     const bool in = i < p.m && j < width;
                     const long long o = (rows + i) * ld + j;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = sub + 8 * r, i = i0 + row;
-                    if (i >= p.m || j >= width) continue;
+                    if (i >= p.m || j >= width || skips(r)) continue;
                     const float4 a0 = lds_f4(at(row, 2 * piece)), a1 = lds_f4(at(row, 2 * piece + 1));
                     float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}, e[8] = {};
                     if (reads) {
@@ -559,7 +564,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 if (!back) return;
-                if (!XSTEP) {
+                if (narrow) {
+                    // as below, 8 pairs of rows and 4 columns an instruction
+                    const int r = half * 16 + (lane & 7) * 2, h = lane >> 3;
+                    const uint32_t base = stage + r * 128 + h * 4;
+                    __half *to = planes[0] + (rows + jc + h) * p.ldm + i0 + r;
+                    const long long step = 4LL * p.ldm, rest = SPLIT ? planes[1] - planes[0] : 0;
+                    const int left = i0 + r < p.m ? p.m - jc - h : 0;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const uint32_t c = n ^ (r & 7);
+                        const float v0 = lds_f1(base + c * 16), v1 = lds_f1(base + 128 + (c ^ 1) * 16);
+                        if (4 * n < left) {
+                            const __half2 b = __floats2half2_rn(v0, v1);
+                            *reinterpret_cast<__half2 *>(to) = b;
+                            if (SPLIT) {
+                                const float2 w = __half22float2(b);
+                                *reinterpret_cast<__half2 *>(to + rest) = __floats2half2_rn(v0 - w.x, v1 - w.y);
+                            }
+                        }
+                        to += step;
+                    }
+                } else if (!XSTEP) {
                     // Column c of the result is row jc + c of the mirrored half: rows r and
                     // r + 1 of the tile a lane, columns 2 n and 2 n + 1 an instruction.
                     const int r = (lane & 15) * 2, h = lane >> 4;
@@ -612,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < UNITS; ++k) {
                         if (k >= 2 * mine) continue;
-                        const int unit = 4 * (k >> 1) + 2 * half + (k & 1);
+                        const int unit = narrow ? k : 4 * (k >> 1) + 2 * half + (k & 1);
                         if (seg0 == 0) {
                             load(unit, sum[k]);
                         } else {
@@ -645,8 +671,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
                 for (int k = 0; k == 0 || k < mine; ++k) {
                     if (k < mine) {
-                        load(4 * k + 2 * half, v[0]);
-                        load(4 * k + 2 * half + 1, v[1]);
+                        const int unit = narrow ? 0 : 4 * k + 2 * half;
+                        load(unit, v[0]);
+                        load(unit + 1, v[1]);
                         tmem_wait_ld();
                     }
                     if (k + 1 >= mine) release();
