@@ -150,7 +150,8 @@ __device__ __forceinline__ uint4 round8(const float (&v)[8])
 // SPLIT: operands of two FP16 numbers.  XSTEP: X' = a X + B X, Q = X with its
 // rows as K; else A or B, symmetric, P and Q the same matrix along K.
 // UNITS: 16-column units of a tile that a warp adds up (SPLIT; 8 for tiles of more
-// than 128 columns, whose sums take 128 registers a thread and leave some spilled).
+// than 128 columns, whose sums take 128 registers a thread and leave some spilled);
+// else 2 for tiles of 32 columns.
 template <int CG, bool SPLIT, bool XSTEP, int UNITS>
 __global__ void __launch_bounds__(THREADS, 1)
     ortho_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
@@ -368,8 +369,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp & 3;            // tensor-memory lane quarter
         const int half = (warp - 2) >> 2;  // 0: even chunks of 32 columns, 1: odd ones
         // Tiles of 32 columns: both halves take the one chunk, 16 of its rows each (with
-        // half of the warps idle one matrix of 256 x 384 took 83.7 us, 80.3 now).
-        const bool narrow = !XSTEP && p.bn == 32;
+        // half of the warps idle one matrix of 256 x 384 took 83.7 us, 80.3 now; in the
+        // kernel of the other tiles the choice cost 3 % of 16 matrices of 4096 x 2048).
+        constexpr bool narrow = !SPLIT && UNITS == 2;
         const int mine = narrow ? 1 : (p.bn / 32 + 1 - half) / 2;
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 4096;
         const int sub = lane >> 2, piece = lane & 3;
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             // The operands that the epilogue adds: X, or A where B is made.
             uint4 extra[2][4];
-            float4 diagonal[2];  // A's, at a lane's columns; ahead where registers allow
+            float4 diagonal[2];  // A's, at a lane's columns (narrow: loaded ahead)
             const bool reads = XSTEP || p.mode == kOrthoB;
             const bool two = SPLIT || (XSTEP && p.has_rest);
             const auto load_diagonal = [&](int j) {
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     extra[0][r] = in ? *reinterpret_cast<const uint4 *>(from[0] + o) : make_uint4(0u, 0u, 0u, 0u);
                     if (two) extra[1][r] = in ? *reinterpret_cast<const uint4 *>(from[1] + o) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (!SPLIT && !XSTEP && j < width) load_diagonal(j);
+                if (narrow && j < width) load_diagonal(j);
             };
             const bool back = XSTEP ? p.last && p.turned : t.mirror;  // results are needed column by column
             __half *const *planes = XSTEP ? p.x_out : p.mode == kOrthoA ? p.a : p.b;
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 float dj[8];
                 if (!XSTEP && p.mode == kOrthoB && j < width) {
-                    if (SPLIT) load_diagonal(j);
+                    if (!narrow) load_diagonal(j);
                     const float4 d0 = diagonal[0], d1 = diagonal[1];
                     dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
                     dj[4] = d1.x, dj[5] = d1.y, dj[6] = d1.z, dj[7] = d1.w;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (p.mode == kOrthoA) {
                                     p.da[mat * p.ldm + i] = v[c] * scale * (1.0f / SCALE_A);
                                 } else {
-                                    const float d = SPLIT ? p.da[mat * p.ldm + i] : row_d[r];
+                                    const float d = narrow ? row_d[r] : p.da[mat * p.ldm + i];
                                     p.db[mat * p.ldm + i] =
                                         p.cb * d + p.cc * fmaf(d, d, v[c] * (1.0f / (SCALE_A * SCALE_A)));
                                 }
@@ -564,25 +566,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 if (!back) return;
-                if (narrow) {
+                if constexpr (narrow) {
                     // as below, 8 pairs of rows and 4 columns an instruction
                     const int r = half * 16 + (lane & 7) * 2, h = lane >> 3;
                     const uint32_t base = stage + r * 128 + h * 4;
                     __half *to = planes[0] + (rows + jc + h) * p.ldm + i0 + r;
-                    const long long step = 4LL * p.ldm, rest = SPLIT ? planes[1] - planes[0] : 0;
-                    const int left = i0 + r < p.m ? p.m - jc - h : 0;
+                    const long long step = 4LL * p.ldm, left = i0 + r < p.m ? p.m - jc - h : 0;
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         const uint32_t c = n ^ (r & 7);
                         const float v0 = lds_f1(base + c * 16), v1 = lds_f1(base + 128 + (c ^ 1) * 16);
-                        if (4 * n < left) {
-                            const __half2 b = __floats2half2_rn(v0, v1);
-                            *reinterpret_cast<__half2 *>(to) = b;
-                            if (SPLIT) {
-                                const float2 w = __half22float2(b);
-                                *reinterpret_cast<__half2 *>(to + rest) = __floats2half2_rn(v0 - w.x, v1 - w.y);
-                            }
-                        }
+                        if (4 * n < left) *reinterpret_cast<__half2 *>(to) = __floats2half2_rn(v0, v1);
                         to += step;
                     }
                 } else if (!XSTEP) {
@@ -638,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < UNITS; ++k) {
                         if (k >= 2 * mine) continue;
-                        const int unit = narrow ? k : 4 * (k >> 1) + 2 * half + (k & 1);
+                        const int unit = 4 * (k >> 1) + 2 * half + (k & 1);
                         if (seg0 == 0) {
                             load(unit, sum[k]);
                         } else {
@@ -968,6 +962,7 @@ template <int CG>
 static cudaError_t ready_for()
 {
     cudaError_t e = kernel_ready<ortho_kernel<CG, false, false, 8>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, false, 2>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, true, 8>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, false, 4>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, true, 4>>(SMEM_MAX);
@@ -981,8 +976,9 @@ static cudaError_t launch_for(bool split, bool x, int bn, const CUtensorMap (&ma
                               cudaStream_t stream)
 {
     if (!split)
-        return x ? launch_one<CG, false, true, 8>(maps, p, grid, stream)
-                 : launch_one<CG, false, false, 8>(maps, p, grid, stream);
+        return x          ? launch_one<CG, false, true, 8>(maps, p, grid, stream)
+               : bn == 32 ? launch_one<CG, false, false, 2>(maps, p, grid, stream)
+                          : launch_one<CG, false, false, 8>(maps, p, grid, stream);
     if (bn <= 128)
         return x ? launch_one<CG, true, true, 4>(maps, p, grid, stream)
                  : launch_one<CG, true, false, 4>(maps, p, grid, stream);
