@@ -29,6 +29,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.h"
 #include "ortho.h"
@@ -59,7 +60,7 @@ constexpr int FACTORS = ORTHO_FACTORS;
 
 struct Params {
     int m, n, ldm, ldn, batch;
-    int mode, bn, tiles_i, tiles, stages, stage_bytes, q_bytes, kt;
+    int bn, tiles_i, tiles, stages, stage_bytes, q_bytes, kt;
     int first, last, has_rest;
     float ca, cb, cc;
     const __half *x[2];  // planes of X as read
@@ -147,17 +148,18 @@ __device__ __forceinline__ uint4 round8(const float (&v)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// SPLIT: operands of two FP16 numbers.  XSTEP: X' = a X + B X, Q = X with its
+// SPLIT: operands of two FP16 numbers.  STEP: X' = a X + B X, Q = X with its
 // rows as K; else A or B, symmetric, P and Q the same matrix along K.
 // UNITS: 16-column units of a tile that a warp adds up (SPLIT; 8 for tiles of more
 // than 128 columns, whose sums take 128 registers a thread and leave some spilled);
 // else 2 for tiles of 32 columns.
-template <int CG, bool SPLIT, bool XSTEP, int UNITS>
+template <int CG, bool SPLIT, int STEP, int UNITS>
 __global__ void __launch_bounds__(THREADS, 1)
     ortho_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                  const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1, const Params p)
 {
     constexpr int PLANES = SPLIT ? 2 : 1;
+    constexpr bool XSTEP = STEP == kOrthoX;
     // FP16 operands, FP32 accumulator; Q MN-major for X
     constexpr uint32_t IDESC = (1u << 4) | ((XSTEP ? 1u : 0u) << 16) | (static_cast<uint32_t>((CG * BP) >> 4) << 24);
     extern __shared__ uint8_t smem_raw[];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int i = i0 + sub + 8 * r;
                     row_c[r] = i < p.m ? (p.ca + p.db[mat * p.ldm + i]) * post : 0.0f;
                 }
-            } else if (p.mode == kOrthoA) {
+            } else if (STEP == kOrthoA) {
                 scale = f[p.first ? kFactorA0 : kFactorA] * SCALE_A;
             } else {
                 scale = p.cc * (SCALE_B / (SCALE_A * SCALE_A));
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The operands that the epilogue adds: X, or A where B is made.
             uint4 extra[2][4];
             float4 diagonal[2];  // A's, at a lane's columns (narrow: loaded ahead)
-            const bool reads = XSTEP || p.mode == kOrthoB;
+            const bool reads = XSTEP || STEP == kOrthoB;
             const bool two = SPLIT || (XSTEP && p.has_rest);
             const auto load_diagonal = [&](int j) {
                 const float4 *d = reinterpret_cast<const float4 *>(p.da + mat * p.ldm + j);
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (narrow && j < width) load_diagonal(j);
             };
             const bool back = XSTEP ? p.last && p.turned : t.mirror;  // results are needed column by column
-            __half *const *planes = XSTEP ? p.x_out : p.mode == kOrthoA ? p.a : p.b;
+            __half *const *planes = XSTEP ? p.x_out : STEP == kOrthoA ? p.a : p.b;
             const auto finish = [&](int k) {
                 const int jc = column(k), j = jc + piece * 8;
                 if (jc >= width) {
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return;
                 }
                 float dj[8];
-                if (!XSTEP && p.mode == kOrthoB && j < width) {
+                if (!XSTEP && STEP == kOrthoB && j < width) {
                     if (!narrow) load_diagonal(j);
                     const float4 d0 = diagonal[0], d1 = diagonal[1];
                     dj[0] = d0.x, dj[1] = d0.y, dj[2] = d0.z, dj[3] = d0.w;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             if (j + c == i) {
-                                if (p.mode == kOrthoA) {
+                                if (STEP == kOrthoA) {
                                     p.da[mat * p.ldm + i] = v[c] * scale * (1.0f / SCALE_A);
                                 } else {
                                     const float d = narrow ? row_d[r] : p.da[mat * p.ldm + i];
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         v[c] *= scale;
                         if (XSTEP)
                             v[c] = fmaf(e[c], rc, v[c]);
-                        else if (p.mode == kOrthoB)
+                        else if (STEP == kOrthoB)
                             v[c] = fmaf(e[c], rc + dj[c], v[c]);
                     }
                     const long long o = (rows + i) * ld + j;
@@ -915,10 +917,10 @@ __global__ void __launch_bounds__(NORM_THREADS)
     }
 }
 
-template <int CG, bool SPLIT, bool XSTEP, int UNITS>
+template <int CG, bool SPLIT, int STEP, int UNITS>
 cudaError_t launch_one(const CUtensorMap (&maps)[4], const Params &p, int grid, cudaStream_t stream)
 {
-    return launch_pdl(ortho_kernel<CG, SPLIT, XSTEP, UNITS>, grid, THREADS, SMEM_MAX, stream, CG, maps[0], maps[1], maps[2],
+    return launch_pdl(ortho_kernel<CG, SPLIT, STEP, UNITS>, grid, THREADS, SMEM_MAX, stream, CG, maps[0], maps[1], maps[2],
                       maps[3], p);
 }
 
@@ -958,32 +960,27 @@ void ortho_layout(OrthoBuffers &o, uint8_t *base, bool split)
     o.factors = reinterpret_cast<float *>(take(static_cast<size_t>(o.batch) * ORTHO_FACTORS * 4));
 }
 
-template <int CG>
+template <int CG, int STEP>
 static cudaError_t ready_for()
 {
-    cudaError_t e = kernel_ready<ortho_kernel<CG, false, false, 8>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, false, 2>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, true, 8>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, false, 4>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, true, 4>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, false, 8>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, true, 8>>(SMEM_MAX);
+    cudaError_t e = cudaSuccess;
+    if constexpr (STEP != kOrthoX) e = kernel_ready<ortho_kernel<CG, false, STEP, 2>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, STEP, 8>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 4>>(SMEM_MAX);
+    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 8>>(SMEM_MAX);
     return e;
 }
 
-template <int CG>
-static cudaError_t launch_for(bool split, bool x, int bn, const CUtensorMap (&maps)[4], const Params &p, int grid,
+template <int CG, int STEP>
+static cudaError_t launch_for(bool split, int bn, const CUtensorMap (&maps)[4], const Params &p, int grid,
                               cudaStream_t stream)
 {
-    if (!split)
-        return x          ? launch_one<CG, false, true, 8>(maps, p, grid, stream)
-               : bn == 32 ? launch_one<CG, false, false, 2>(maps, p, grid, stream)
-                          : launch_one<CG, false, false, 8>(maps, p, grid, stream);
-    if (bn <= 128)
-        return x ? launch_one<CG, true, true, 4>(maps, p, grid, stream)
-                 : launch_one<CG, true, false, 4>(maps, p, grid, stream);
-    return x ? launch_one<CG, true, true, 8>(maps, p, grid, stream)
-             : launch_one<CG, true, false, 8>(maps, p, grid, stream);
+    if (split)
+        return bn <= 128 ? launch_one<CG, true, STEP, 4>(maps, p, grid, stream)
+                         : launch_one<CG, true, STEP, 8>(maps, p, grid, stream);
+    if constexpr (STEP != kOrthoX)
+        if (bn == 32) return launch_one<CG, false, STEP, 2>(maps, p, grid, stream);
+    return launch_one<CG, false, STEP, 8>(maps, p, grid, stream);
 }
 
 cudaError_t prepare_ortho()
@@ -992,8 +989,12 @@ cudaError_t prepare_ortho()
     if (e == cudaSuccess) e = kernel_ready<norm_kernel<__nv_bfloat16>>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<float>>(0);
     if (e == cudaSuccess) e = kernel_ready<start_kernel<__nv_bfloat16>>(0);
-    if (e == cudaSuccess) e = ready_for<1>();
-    if (e == cudaSuccess) e = ready_for<2>();
+    if (e == cudaSuccess) e = ready_for<1, kOrthoA>();
+    if (e == cudaSuccess) e = ready_for<1, kOrthoB>();
+    if (e == cudaSuccess) e = ready_for<1, kOrthoX>();
+    if (e == cudaSuccess) e = ready_for<2, kOrthoA>();
+    if (e == cudaSuccess) e = ready_for<2, kOrthoB>();
+    if (e == cudaSuccess) e = ready_for<2, kOrthoX>();
     return e;
 }
 
@@ -1066,7 +1067,6 @@ cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, 
     p.ldm = w.ldm;
     p.ldn = w.ldn;
     p.batch = w.batch;
-    p.mode = r.step;
     p.bn = r.tile.bn;
     p.tiles_i = (w.m + cg * BP - 1) / (cg * BP);
     const int64_t tiles = product_tiles(r.step, cg, r.tile.bn, w.m, w.n);
@@ -1103,9 +1103,13 @@ cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, 
     p.debug_drop = r.debug_drop;
     const int64_t slots = std::max(1, (max_ctas > 0 ? std::min(max_ctas, sm_count) : sm_count) / cg);
     const int grid = static_cast<int>(cg * std::min<int64_t>(tiles * w.batch, slots));
-    const bool x = r.step == kOrthoX;
-    return cg == 2 ? launch_for<2>(r.split, x, r.tile.bn, maps, p, grid, r.stream)
-                   : launch_for<1>(r.split, x, r.tile.bn, maps, p, grid, r.stream);
+    const auto launch = [&](auto pair) {
+        constexpr int CG = decltype(pair)::value;
+        return r.step == kOrthoA   ? launch_for<CG, kOrthoA>(r.split, r.tile.bn, maps, p, grid, r.stream)
+               : r.step == kOrthoB ? launch_for<CG, kOrthoB>(r.split, r.tile.bn, maps, p, grid, r.stream)
+                                   : launch_for<CG, kOrthoX>(r.split, r.tile.bn, maps, p, grid, r.stream);
+    };
+    return cg == 2 ? launch(std::integral_constant<int, 2>()) : launch(std::integral_constant<int, 1>());
 }
 
 }  // namespace dg
