@@ -152,7 +152,9 @@ __device__ __forceinline__ uint4 round8(const float (&v)[8])
 // rows as K; else A or B, symmetric, P and Q the same matrix along K.
 // UNITS: 16-column units of a tile that a warp adds up (SPLIT; 8 for tiles of more
 // than 128 columns, whose sums take 128 registers a thread and leave some spilled);
-// else 2 for tiles of 32 columns.
+// 2 for tiles of 32 columns.  What the epilogue adds is loaded right before it is
+// added where sums are held: loaded a chunk ahead, it spilled (13 FP32 matrices of
+// 1020 x 520 466 -> 516 us replayed).
 template <int CG, bool SPLIT, int STEP, int UNITS>
 __global__ void __launch_bounds__(THREADS, 1)
     ortho_kernel(const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Tiles of 32 columns: both halves take the one chunk, 16 of its rows each (with
         // half of the warps idle one matrix of 256 x 384 took 83.7 us, 80.3 now; in the
         // kernel of the other tiles the choice cost 3 % of 16 matrices of 4096 x 2048).
-        constexpr bool narrow = !SPLIT && UNITS == 2;
+        constexpr bool narrow = UNITS == 2;
         const int mine = narrow ? 1 : (p.bn / 32 + 1 - half) / 2;
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 4096;
         const int sub = lane >> 2, piece = lane & 3;
@@ -573,12 +575,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int r = half * 16 + (lane & 7) * 2, h = lane >> 3;
                     const uint32_t base = stage + r * 128 + h * 4;
                     __half *to = planes[0] + (rows + jc + h) * p.ldm + i0 + r;
-                    const long long step = 4LL * p.ldm, left = i0 + r < p.m ? p.m - jc - h : 0;
+                    const long long step = 4LL * p.ldm, left = i0 + r < p.m ? p.m - jc - h : 0,
+                                    rest = SPLIT ? planes[1] - planes[0] : 0;
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         const uint32_t c = n ^ (r & 7);
                         const float v0 = lds_f1(base + c * 16), v1 = lds_f1(base + 128 + (c ^ 1) * 16);
-                        if (4 * n < left) *reinterpret_cast<__half2 *>(to) = __floats2half2_rn(v0, v1);
+                        if (4 * n < left) {
+                            const __half2 b = __floats2half2_rn(v0, v1);
+                            *reinterpret_cast<__half2 *>(to) = b;
+                            if (SPLIT) {
+                                const float2 w = __half22float2(b);
+                                *reinterpret_cast<__half2 *>(to + rest) = __floats2half2_rn(v0 - w.x, v1 - w.y);
+                            }
+                        }
                         to += step;
                     }
                 } else if (!XSTEP) {
@@ -629,21 +639,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (SPLIT) {
                 uint32_t sum[UNITS][16];
                 for (int seg0 = 0; seg0 < p.kt; seg0 += SEG) {
-                    if (UNITS == 4 && seg0 + SEG >= p.kt) fetch(0);
+                    if (narrow && seg0 + SEG >= p.kt) fetch(0);
                     if (!await()) break;
 #pragma unroll
-                    for (int k = 0; k < UNITS; ++k) {
+                    for (int k = 0; k < UNITS; k += 2) {
                         if (k >= 2 * mine) continue;
-                        const int unit = 4 * (k >> 1) + 2 * half + (k & 1);
+                        const int unit = 2 * k + (narrow ? 0 : 2 * half);
                         if (seg0 == 0) {
                             load(unit, sum[k]);
+                            load(unit + 1, sum[k + 1]);
                         } else {
-                            uint32_t v[16];
-                            load(unit, v);
-                            tmem_wait_ld();
+                            constexpr int AT_ONCE = UNITS > 4 ? 1 : 2;  // as registers allow
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                sum[k][c] = __float_as_uint(__uint_as_float(sum[k][c]) + __uint_as_float(v[c]));
+                            for (int n = 0; n < 2; n += AT_ONCE) {
+                                uint32_t v[AT_ONCE][16];
+#pragma unroll
+                                for (int i = 0; i < AT_ONCE; ++i) load(unit + n + i, v[i]);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c)
+                                        sum[k + n + i][c] = __float_as_uint(__uint_as_float(sum[k + n + i][c]) +
+                                                                            __uint_as_float(v[i][c]));
+                            }
                         }
                     }
                     tmem_wait_ld();
@@ -656,9 +675,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int n = 0; n < UNITS / 2; ++n)
                         if (k == n) turn(sum[2 * n], sum[2 * n + 1]);
-                    if (UNITS > 4) fetch(k);
+                    if (!narrow) fetch(k);
                     finish(k);
-                    if (UNITS == 4 && k + 1 < mine) fetch(k + 1);
                 }
             } else {
                 fetch(0);
@@ -964,7 +982,10 @@ template <int CG, int STEP>
 static cudaError_t ready_for()
 {
     cudaError_t e = cudaSuccess;
-    if constexpr (STEP != kOrthoX) e = kernel_ready<ortho_kernel<CG, false, STEP, 2>>(SMEM_MAX);
+    if constexpr (STEP != kOrthoX) {
+        e = kernel_ready<ortho_kernel<CG, false, STEP, 2>>(SMEM_MAX);
+        if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 2>>(SMEM_MAX);
+    }
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, STEP, 8>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 4>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 8>>(SMEM_MAX);
@@ -975,11 +996,13 @@ template <int CG, int STEP>
 static cudaError_t launch_for(bool split, int bn, const CUtensorMap (&maps)[4], const Params &p, int grid,
                               cudaStream_t stream)
 {
+    if constexpr (STEP != kOrthoX)
+        if (bn == 32)
+            return split ? launch_one<CG, true, STEP, 2>(maps, p, grid, stream)
+                         : launch_one<CG, false, STEP, 2>(maps, p, grid, stream);
     if (split)
         return bn <= 128 ? launch_one<CG, true, STEP, 4>(maps, p, grid, stream)
                          : launch_one<CG, true, STEP, 8>(maps, p, grid, stream);
-    if constexpr (STEP != kOrthoX)
-        if (bn == 32) return launch_one<CG, false, STEP, 2>(maps, p, grid, stream);
     return launch_one<CG, false, STEP, 8>(maps, p, grid, stream);
 }
 
