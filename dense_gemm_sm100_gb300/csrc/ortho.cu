@@ -152,7 +152,7 @@ __device__ __forceinline__ uint4 round8(const float (&v)[8])
 // rows as K; else A or B, symmetric, P and Q the same matrix along K.
 // UNITS: 16-column units of a tile that a warp adds up (SPLIT; 8 for tiles of more
 // than 128 columns, whose sums take 128 registers a thread and leave some spilled);
-// 2 for tiles of 32 columns.  What the epilogue adds is loaded right before it is
+// 2 for tiles of 32 columns (X: 64).  What the epilogue adds is loaded right before it is
 // added where sums are held: loaded a chunk ahead, it spilled (13 FP32 matrices of
 // 1020 x 520 466 -> 516 us replayed).
 template <int CG, bool SPLIT, int STEP, int UNITS>
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Tiles of 32 columns: both halves take the one chunk, 16 of its rows each (with
         // half of the warps idle one matrix of 256 x 384 took 83.7 us, 80.3 now; in the
         // kernel of the other tiles the choice cost 3 % of 16 matrices of 4096 x 2048).
-        constexpr bool narrow = UNITS == 2;
-        const int mine = narrow ? 1 : (p.bn / 32 + 1 - half) / 2;
+        constexpr bool narrow = UNITS == 2 && !XSTEP;
+        const int mine = UNITS == 2 ? 1 : (p.bn / 32 + 1 - half) / 2;
         const uint32_t stage = epi_base + static_cast<uint32_t>(warp - 2) * 4096;
         const int sub = lane >> 2, piece = lane & 3;
         // 16 bytes c of row r: bank conflicts are spread over the rows
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (SPLIT) {
                 uint32_t sum[UNITS][16];
                 for (int seg0 = 0; seg0 < p.kt; seg0 += SEG) {
-                    if (narrow && seg0 + SEG >= p.kt) fetch(0);
+                    if (UNITS == 2 && seg0 + SEG >= p.kt) fetch(0);
                     if (!await()) break;
 #pragma unroll
                     for (int k = 0; k < UNITS; k += 2) {
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int n = 0; n < UNITS / 2; ++n)
                         if (k == n) turn(sum[2 * n], sum[2 * n + 1]);
-                    if (!narrow) fetch(k);
+                    if (UNITS > 2) fetch(k);
                     finish(k);
                 }
             } else {
@@ -982,7 +982,7 @@ template <int CG, int STEP>
 static cudaError_t ready_for()
 {
     cudaError_t e = cudaSuccess;
-    if constexpr (STEP != kOrthoX) {
+    if constexpr (CG == 1 || STEP != kOrthoX) {
         e = kernel_ready<ortho_kernel<CG, false, STEP, 2>>(SMEM_MAX);
         if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 2>>(SMEM_MAX);
     }
@@ -996,8 +996,8 @@ template <int CG, int STEP>
 static cudaError_t launch_for(bool split, int bn, const CUtensorMap (&maps)[4], const Params &p, int grid,
                               cudaStream_t stream)
 {
-    if constexpr (STEP != kOrthoX)
-        if (bn == 32)
+    if constexpr (CG == 1 || STEP != kOrthoX)  // pairs take 128 columns of X at least
+        if (bn == (STEP == kOrthoX ? 64 : 32))
             return split ? launch_one<CG, true, STEP, 2>(maps, p, grid, stream)
                          : launch_one<CG, false, STEP, 2>(maps, p, grid, stream);
     if (split)
