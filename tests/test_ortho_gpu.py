@@ -106,6 +106,17 @@ def test_large_matrix(gm, h, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(40, 300, 400), (30, 500, 290)])
+def test_many_matrices_of_different_norms(gm, h, shape, dtype):
+    G = updates(shape, dtype, 23)
+    G = (G.float() * (2.0 ** (torch.arange(shape[0]) % 9 - 4))[:, None, None]).to(dtype)
+    out = torch.empty_like(G, device="cuda")
+    h.orthogonalise(G.cuda(), out)
+    h.sync_status()
+    assert_near(out, definition(G.cuda().double()), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_one_step_and_coefficients_of_each(gm, h, dtype):
     G = updates((70, 90), dtype, 4)
     out = torch.empty_like(G, device="cuda")
