@@ -1008,7 +1008,8 @@ static cudaError_t ready_for()
     }
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, false, STEP, 8>>(SMEM_MAX);
     if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 4>>(SMEM_MAX);
-    if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 8>>(SMEM_MAX);
+    if constexpr (CG == 2 || STEP == kOrthoX)
+        if (e == cudaSuccess) e = kernel_ready<ortho_kernel<CG, true, STEP, 8>>(SMEM_MAX);
     return e;
 }
 
@@ -1020,9 +1021,9 @@ static cudaError_t launch_for(bool split, int bn, const CUtensorMap (&maps)[4], 
         if (bn == (STEP == kOrthoX ? 64 : 32))
             return split ? launch_one<CG, true, STEP, 2>(maps, p, grid, stream)
                          : launch_one<CG, false, STEP, 2>(maps, p, grid, stream);
-    if (split)
-        return bn <= 128 ? launch_one<CG, true, STEP, 4>(maps, p, grid, stream)
-                         : launch_one<CG, true, STEP, 8>(maps, p, grid, stream);
+    if constexpr (CG == 2 || STEP == kOrthoX)  // a CTA alone takes 128 columns of A and B at most
+        if (split && bn > 128) return launch_one<CG, true, STEP, 8>(maps, p, grid, stream);
+    if (split) return launch_one<CG, true, STEP, 4>(maps, p, grid, stream);
     return launch_one<CG, false, STEP, 8>(maps, p, grid, stream);
 }
 
