@@ -18,10 +18,14 @@
 // take both FP16 numbers of every operand: three products (the fourth is below
 // 2^-22 of the first), and sums cut into segments that are added to nearest.
 //
-// The norm.  X is stored as Y = G 2^e with the norm of Y in [1, 2): exact for
-// BF16 and FP32 alike, the rest of 1 / (|G| + eps) enters A's and X's first
-// epilogues.  Where eps outweighs |G| the result is tiny; its power of two
-// stays out of Y until the result is written.
+// The norm.  X is stored as Y = G 2^e with the norm of Y in [2^12, 2^13): exact
+// for BF16 and FP32 alike, the rest of 1 / (|G| + eps) enters A's and X's first
+// epilogues.  X is Y 2^-q, q = 12 where |G| outweighs eps.  Where eps outweighs
+// |G|, X is tiny and q larger, and as long as A is too small to hold it back X
+// grows by a = 3.4 or more a step: every X epilogue takes out of Y, and of q, the
+// whole powers of two by which a bound on Y's norm has grown past 2^14, until q is
+// 12.  Each matrix has its own q and bound, in turn in two places, so that a launch
+// writes what the next one reads.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,20 +58,20 @@ constexpr int SEG = 4;                // ring stages of a segment of a two-term 
 constexpr float SCALE_A = 2048.0f, SCALE_B = 1024.0f;
 constexpr int SCALE_X_LOG = 12;
 
-// factors of a matrix, see below
-enum Factor : int { kFactorA0 = 0, kFactorA, kFactorX0, kFactorOut, kFactorUp0, kFactorUp1 };
+// factors of a matrix, see below; the last two twice, by X's buffer that is read
+enum Factor : int { kFactorRest = 0, kFactorUp0, kFactorUp1, kFactorLog, kFactorMost = kFactorLog + 2 };
 constexpr int FACTORS = ORTHO_FACTORS;
 
 struct Params {
     int m, n, ldm, ldn, batch;
     int bn, tiles_i, tiles, stages, stage_bytes, q_bytes, kt;
-    int first, last, has_rest;
+    int first, last, has_rest, from;
     float ca, cb, cc;
     const __half *x[2];  // planes of X as read
     __half *x_out[2];
     __half *a[2], *b[2];
     float *da, *db;
-    const float *factors;
+    float *factors;
     void *o;
     long long ldo, stride_o;
     int turned, o_bf16, o_vec;
@@ -109,6 +113,9 @@ __device__ __forceinline__ Tile tile_at(const Params &p, int u)
     t.some = t.j0 < (SYM ? p.m : p.n);
     return t;
 }
+
+// 2^-k for k >= 0; 0 past FP32's normal numbers.
+__device__ __forceinline__ float power_down(int k) { return __int_as_float(max(0, 127 - k) << 23); }
 
 // Eight FP16 numbers added to v.
 __device__ __forceinline__ void add8(uint4 w, float (&v)[8])
@@ -388,13 +395,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!t.some) continue;
             const int i0 = t.i0 + static_cast<int>(rank) * BP + q * 32;  // the warp's first row
             const long long mat = t.b;
-            const float *f = p.factors + mat * FACTORS;
+            float *f = p.factors + mat * FACTORS;
+            const int log_x = static_cast<int>(f[kFactorLog + p.from]);  // X = Y 2^-log_x
+            const float rest = p.first ? f[kFactorRest] : 1.0f;
             // With the powers of two of what is read and written in the constants, a
             // value is acc * scale (A), + e * (row + column) (B; e an element of A,
             // row and column from the diagonal), or + x * row (X).
             float scale, row_c[4], row_d[4], column_c = 0.0f;  // rows i0 + sub, + 8, ...
             if (XSTEP) {
-                const float post = (p.first ? f[kFactorX0] : 1.0f) * (p.last ? f[kFactorOut] : 1.0f);
+                int take = 0;  // powers of two taken out of Y
+                float most = 0.0f;
+                if (log_x > SCALE_X_LOG) {
+                    most = f[kFactorMost + p.from];
+                    const float s = most * power_down(log_x), s2 = s * s;  // no singular value of X is larger
+                    most *= fabsf(p.ca) + s2 * (fabsf(p.cb) + s2 * fabsf(p.cc));
+                    const int log_most = (__float_as_int(most) >> 23) - 127;  // rounded down
+                    take = max(0, min(log_x - SCALE_X_LOG, log_most - SCALE_X_LOG - 1));
+                }
+                if (!p.last && i0 == 0 && t.j0 == 0 && half == 0 && lane == 0) {
+                    f[kFactorLog + (p.from ^ 1)] = static_cast<float>(log_x - take);
+                    f[kFactorMost + (p.from ^ 1)] = most * power_down(take);
+                }
+                // a result may lie below FP32's normal numbers
+                const float post = rest * (p.last ? ldexpf(1.0f, -log_x) : power_down(take));
                 scale = post / SCALE_B;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     row_c[r] = i < p.m ? (p.ca + p.db[mat * p.ldm + i]) * post : 0.0f;
                 }
             } else if (STEP == kOrthoA) {
-                scale = f[p.first ? kFactorA0 : kFactorA] * SCALE_A;
+                scale = rest * rest * power_down(2 * log_x) * SCALE_A;
             } else {
                 scale = p.cc * (SCALE_B / (SCALE_A * SCALE_A));
                 column_c = p.cc * (SCALE_B / SCALE_A);
@@ -746,13 +769,13 @@ __device__ __forceinline__ double power_of_two(int k)  // |k| < 1022
     return __longlong_as_double(static_cast<long long>(k + 1023) << 52);
 }
 
-// From the sum of squares of a matrix: the factors of its products and the power
-// of two of X (two factors, whose product may leave FP32's range).  FP64 operations
+// From the sum of squares of a matrix: the factor of its first products, the power
+// of two that makes Y (two factors, whose product may leave FP32's range), and X's.  FP64 operations
 // are slow here (sqrt, division and frexp took 2 us of a call): FP32 results with
 // one correction each.
 __device__ void write_factors(double sum, double eps, float *f)
 {
-    // |G| 2^e in [1, 2); 1 / ((|G| + eps) 2^e) = rest 2^-down, down > 0 only where eps outweighs |G|
+    // |G| 2^e in [1, 2); 1 / ((|G| + eps) 2^e) = rest 2^-down, rest <= 2, down > 0 only where eps outweighs |G|
     int e = 0, down = 0;
     float rest = 1.0f;
     if (!(sum < INFINITY)) {
@@ -773,14 +796,13 @@ __device__ void write_factors(double sum, double eps, float *f)
         rest = 1.0f / static_cast<float>(h);
         rest = fmaf(rest, static_cast<float>(fma(-h, static_cast<double>(rest), 1.0)), rest);
     }
-    // X may grow by the steps' factors where A is too small to hold it back
-    const int storage = SCALE_X_LOG - min(down, 9), up = e + storage, up0 = max(-126, min(126, up));
-    f[kFactorA0] = ldexpf(rest * rest, -2 * (storage + down));
-    f[kFactorA] = ldexpf(1.0f, -2 * (storage + down));
-    f[kFactorX0] = rest;
-    f[kFactorOut] = ldexpf(1.0f, -storage - down);
+    const int up = e + SCALE_X_LOG, up0 = max(-126, min(126, up));
+    f[kFactorRest] = rest;
     f[kFactorUp0] = ldexpf(1.0f, up0);
     f[kFactorUp1] = ldexpf(1.0f, max(-126, min(126, up - up0)));
+    f[kFactorLog] = static_cast<float>(SCALE_X_LOG + down);
+    f[kFactorMost] = rest * 8192.0f;  // of rest Y
+    f[kFactorLog + 1] = f[kFactorMost + 1] = 0.0f;
 }
 
 // The sum of squares of rows r0 .. r1 - 1, by a whole CTA.  A thread adds in FP32,
@@ -1133,6 +1155,7 @@ cudaError_t launch_ortho_product(const OrthoBuffers &w, const OrthoMatrices &u, 
     p.first = r.first;
     p.last = r.last;
     p.has_rest = r.split || !r.first;  // BF16 input is exact in FP16
+    p.from = r.from;
     p.ca = r.ca;
     p.cb = r.cb;
     p.cc = r.cc;

@@ -21,7 +21,7 @@ struct OrthoBuffers {
     double *parts = nullptr;             // batch x ORTHO_PARTS sums of squares
     float *factors = nullptr;            // batch x ORTHO_FACTORS
 };
-constexpr int ORTHO_PARTS = 64, ORTHO_FACTORS = 6;
+constexpr int ORTHO_PARTS = 64, ORTHO_FACTORS = 7;
 
 size_t ortho_bytes(int64_t m, int64_t n, bool split);  // of one matrix
 void ortho_layout(OrthoBuffers &o, uint8_t *base, bool split);

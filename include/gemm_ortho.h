@@ -22,9 +22,12 @@
  * that holds an infinity or a NaN gives NaN, and its neighbours in the batch are
  * not touched by that.
  *
- * FP16 bounds what may come up on the way: singular values of X up to 8, and
+ * FP16 bounds what may come up on the way: singular values of X up to 7.9, and
  * |b| s^2 + |c| s^4 up to 60 for the largest one s (the usual coefficients stay
- * below 1.3 and 8); past that results may be infinite or NaN.
+ * below 1.3 and 8); past that results may be infinite or NaN.  Elements of A off
+ * the diagonal below 2^-36 count as zero, so that a step with a = 0 makes zeros of
+ * a matrix that lies as far below eps.  There is no other lower bound: a matrix
+ * far below eps grows by a every step, as the formula has it.
  *
  * steps is 1 .. GEMM_ORTHO_MAX_STEPS; the coefficients are finite, eps >= 0.
  * rows and cols are at most 2^20.  O may be G itself (same strides); no other
