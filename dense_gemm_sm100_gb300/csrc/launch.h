@@ -26,7 +26,7 @@ inline cudaError_t kernel_ready(size_t smem)
     if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, Kernel);
-    if (e == cudaSuccess && smem > 48 * 1024)
+    if (e == cudaSuccess && smem + attr.sharedSizeBytes > 48 * 1024)  // with the kernel's static shared memory
         e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
