@@ -148,11 +148,12 @@ def _weights_of(logits, expert, scoring, renormalise, scale):
     chosen, x = expert >= 0, logits.float()
     index = expert.clamp(min=0)
     if scoring == "sigmoid":
-        score = torch.sigmoid(torch.gather(x, 1, index)).masked_fill(~chosen, 0.0)
+        # a finite stand-in where there is no choice: 0 * nan would stay in the gradient
+        score = torch.sigmoid(torch.gather(x, 1, index).masked_fill(~chosen, 0.0)).masked_fill(~chosen, 0.0)
         if renormalise:
             score = score / (score.sum(-1, keepdim=True) + 1e-20)
     elif renormalise:
-        # a finite stand-in where there is no choice: 0 * nan would stay in the gradient
+        # the same stand-in, below every chosen logit
         score = torch.softmax(torch.gather(x, 1, index).masked_fill(~chosen, -1e30), -1).masked_fill(~chosen, 0.0)
     else:
         x = x.masked_fill(~chosen.any(-1, keepdim=True), 0.0)
