@@ -153,8 +153,10 @@ def _weights_of(logits, expert, scoring, renormalise, scale):
         if renormalise:
             score = score / (score.sum(-1, keepdim=True) + 1e-20)
     elif renormalise:
-        # the same stand-in, below every chosen logit
-        score = torch.softmax(torch.gather(x, 1, index).masked_fill(~chosen, -1e30), -1).masked_fill(~chosen, 0.0)
+        # finite in rows without any choice, below every logit in the others
+        x = torch.gather(x, 1, index).masked_fill(~chosen, -float("inf"))
+        x = x.masked_fill(~chosen.any(-1, keepdim=True), 0.0)
+        score = torch.softmax(x, -1).masked_fill(~chosen, 0.0)
     else:
         x = x.masked_fill(~chosen.any(-1, keepdim=True), 0.0)
         score = torch.gather(torch.softmax(x, -1), 1, index).masked_fill(~chosen, 0.0)

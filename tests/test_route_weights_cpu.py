@@ -31,3 +31,19 @@ def test_rows_without_choices_have_zero_gradients(scoring, renormalise, bad):
                              create_graph=True)
     b, = torch.autograd.grad(a.square().sum(), alone)
     assert torch.equal(first[[0, 2]], a) and torch.equal(second[[0, 2]], b)
+
+
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_choices_far_below_the_other_slots(renormalise):
+    """Two equal choices share the weight however low their logits are, with a slot that
+    holds no choice beside them."""
+    x = torch.full((3, 4), -math.inf)
+    x[:, 1:3] = torch.tensor([[-1e31], [-3e38], [5.0]])
+    expert = torch.tensor([[1, 2, -1]] * 3)
+    leaf = x.clone().requires_grad_()
+    w = _weights_of(leaf, expert, "softmax", renormalise, 1.0)
+    assert torch.equal(w, torch.tensor([[0.5, 0.5, 0.0]] * 3))
+    first, = torch.autograd.grad(w, leaf, torch.tensor([[1.0, -1.0, 9.0]] * 3), create_graph=True)
+    second, = torch.autograd.grad(first.square().sum(), leaf)
+    assert torch.equal(first.detach(), torch.tensor([[0.0, 0.5, -0.5, 0.0]] * 3))
+    assert torch.isfinite(second).all()
