@@ -14,9 +14,13 @@
 #include "../../include/gemm.h"
 #include "gemm_internal.h"
 #include "handle.h"
+#include "launch.h"
 #include "ragged.h"
 
 PFN_cuTensorMapEncodeTiled_v12000 dg::g_encode = nullptr;
+PFN_cuCtxGetCurrent_v4000 dg::g_get_context = nullptr;
+PFN_cuCtxSetCurrent_v4000 dg::g_set_context = nullptr;
+PFN_cuCtxGetId_v12000 dg::g_context_id = nullptr;
 
 using dg::cuda_fail;
 using dg::DeviceGuard;
@@ -30,16 +34,24 @@ using dg::tma_ready;
 
 namespace {
 
-std::once_flag g_encode_once;
+std::once_flag g_driver_once;
 
-void load_encode()
+template <typename F>
+void load(F &f, const char *name, unsigned version)
 {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
+    if (cudaGetDriverEntryPointByVersion(name, &fn, version, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        f = reinterpret_cast<F>(fn);
+}
+
+void load_driver()
+{
+    load(dg::g_get_context, "cuCtxGetCurrent", 4000);
+    load(dg::g_set_context, "cuCtxSetCurrent", 4000);
+    load(dg::g_context_id, "cuCtxGetId", 12000);
+    load(g_encode, "cuTensorMapEncodeTiled", 12000);
 }
 
 int elem_bytes(int dtype) { return dtype == GEMM_BF16 ? 2 : 4; }
@@ -395,13 +407,15 @@ int gemm_create(gemm_handle_t *out, int device)
         return GEMM_ERR_DEVICE;
     }
     if (prop.major != 10 || prop.minor != 3) return GEMM_ERR_DEVICE;  // built for sm_103a only
+    std::call_once(g_driver_once, load_driver);
+    if (!g_encode || !dg::g_get_context || !dg::g_set_context || !dg::g_context_id) return GEMM_ERR_CUDA;
     gemm_ctx *h = new (std::nothrow) gemm_ctx;
     if (!h) return GEMM_ERR_NOMEM;
     h->device = device;
     h->sm_count = prop.multiProcessorCount;
     DeviceGuard guard(device);
-    std::call_once(g_encode_once, load_encode);
-    cudaError_t e = g_encode ? cudaSuccess : cudaErrorNotSupported;
+    h->context = dg::current_context();
+    cudaError_t e = h->context ? cudaSuccess : cudaErrorNotSupported;
     if (e == cudaSuccess) e = dg::prepare_simt();
     if (e == cudaSuccess) e = dg::prepare_tc();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_status, sizeof(int));
@@ -422,7 +436,7 @@ int gemm_destroy(gemm_handle_t h)
 {
     if (!h) return GEMM_OK;
     {
-        DeviceGuard guard(h->device);
+        DeviceGuard guard(h);
         cudaDeviceSynchronize();
         // cudaFree takes blocks of the stream-ordered pool and of cudaMalloc (captures)
         for (void *old : h->ws_retired) cudaFree(old);
@@ -458,7 +472,7 @@ int gemm_run(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K, con
     std::string why;
     int rc = check_args(layout_b, M, N, K, A, lda, B, ldb, C, ldc, dtype, &why);
     if (rc) return fail(h, rc, why);
-    DeviceGuard guard(h->device);
+    DeviceGuard guard(h);
     const PackPlan pp = plan_pack(h, layout_b, M, N, K, A, lda, B, ldb, dtype);
     dg::WorkspaceUse ws(h, stream);
     if (pp.total() && (rc = ws.acquire(pp.total()))) return rc;
@@ -616,7 +630,7 @@ int gemm_run_host(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K
         h->last_path = "noop";
         return GEMM_OK;
     }
-    DeviceGuard guard(h->device);
+    DeviceGuard guard(h);
     rc = ensure_pipeline(h);
     if (rc) return rc;
     const int es = elem_bytes(dtype);
@@ -727,7 +741,7 @@ int gemm_run_host(gemm_handle_t h, int layout_b, int64_t M, int64_t N, int64_t K
 int gemm_sync_status(gemm_handle_t h, cudaStream_t stream)
 {
     if (!h) return GEMM_ERR_INVALID;
-    DeviceGuard guard(h->device);
+    DeviceGuard guard(h);
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaStreamSynchronize");
     int st = 0;

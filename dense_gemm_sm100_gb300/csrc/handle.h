@@ -17,6 +17,7 @@
 
 struct gemm_ctx {
     int device = 0;
+    CUcontext context = nullptr;  // the one it was made in; its memory and events belong to that
     int sm_count = 0;
     int *d_status = nullptr;
     void *ws = nullptr;
@@ -66,8 +67,10 @@ namespace dg {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;  // kernels index tiles with int
 constexpr int64_t kMaxLd = int64_t{1} << 36;
 
-// cuTensorMapEncodeTiled, looked up once by gemm_create.
+// The driver's functions, looked up once by gemm_create.
 extern PFN_cuTensorMapEncodeTiled_v12000 g_encode;
+extern PFN_cuCtxGetCurrent_v4000 g_get_context;
+extern PFN_cuCtxSetCurrent_v4000 g_set_context;
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -275,25 +278,56 @@ inline int encode(gemm_ctx *h, CUtensorMap *map, CUtensorMapDataType type, int r
     return fail(h, GEMM_ERR_CUDA, msg);
 }
 
-// The handle's device for the length of a call.  Set even where it is the
-// thread's already: a thread that has made no CUDA call yet (one of an autograd
-// engine's, say) reports device 0 without a context, and tensor maps cannot be
-// encoded without one.
+inline CUcontext current_context()
+{
+    CUcontext c = nullptr;
+    return g_get_context(&c) == CUDA_SUCCESS ? c : nullptr;
+}
+
+// The handle's context for the length of a call.  A thread that has made no CUDA
+// call yet (one of an autograd engine's, say) has none, though it reports device 0,
+// and tensor maps cannot be encoded without one; it keeps the handle's where that is
+// the device it reports.  A thread that has another one, of its own making perhaps,
+// gets it back.
 class DeviceGuard {
   public:
-    explicit DeviceGuard(int dev)
+    explicit DeviceGuard(const gemm_ctx *h) : before_(current_context())
     {
-        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        cudaSetDevice(dev);
+        if (before_ == h->context) return;
+        moved_ = true;
+        if (!before_) remember(h->device);
+        g_set_context(h->context);
+    }
+    // For a handle to be made: the thread's own context where it is one of that
+    // device, else the device's primary one.
+    explicit DeviceGuard(int device) : before_(current_context())
+    {
+        int now = -1;
+        if (before_ && cudaGetDevice(&now) == cudaSuccess && now == device) return;
+        moved_ = true;
+        if (!before_) remember(device);
+        cudaSetDevice(device);
     }
     ~DeviceGuard()
     {
-        int cur = -1;
-        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
+        if (!moved_) return;
+        if (before_)
+            g_set_context(before_);
+        else if (device_ >= 0)
+            cudaSetDevice(device_);
     }
+    DeviceGuard(const DeviceGuard &) = delete;
+    DeviceGuard &operator=(const DeviceGuard &) = delete;
 
   private:
-    int prev_ = -1;
+    void remember(int other_than)
+    {
+        if (cudaGetDevice(&device_) != cudaSuccess || device_ == other_than) device_ = -1;
+    }
+
+    CUcontext before_;
+    bool moved_ = false;
+    int device_ = -1;  // to be set again
 };
 
 }  // namespace dg

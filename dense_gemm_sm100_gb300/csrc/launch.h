@@ -2,6 +2,8 @@
 // update: programmatic stream serialisation, and kernels loaded before use.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -10,18 +12,22 @@
 
 namespace dg {
 
-// Loads a kernel on the current device and allows it `smem` bytes of dynamic
+extern PFN_cuCtxGetId_v12000 g_context_id;  // looked up by gemm_create
+
+// Loads a kernel in the current context and allows it `smem` bytes of dynamic
 // shared memory, the first time it is used there: the call may be captured in a
-// graph, and loading is no part of that.
+// graph, and loading is no part of that.  Remembered is the last context of every
+// device; contexts that take turns on one cost a few microseconds at each change.
 template <auto Kernel>
 inline cudaError_t kernel_ready(size_t smem)
 {
-    static std::atomic<unsigned long long> done{0};
+    static std::atomic<unsigned long long> ready[64];  // a context's id + 1
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    unsigned long long id = 0;
+    const bool known = dev < 64 && g_context_id(nullptr, &id) == CUDA_SUCCESS;
+    if (known && ready[dev].load(std::memory_order_acquire) == id + 1) return cudaSuccess;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // of this thread, for these calls
     if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
     cudaFuncAttributes attr;
@@ -29,7 +35,7 @@ inline cudaError_t kernel_ready(size_t smem)
     if (e == cudaSuccess && smem + attr.sharedSizeBytes > 48 * 1024)  // with the kernel's static shared memory
         e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    if (e == cudaSuccess && known) ready[dev].store(id + 1, std::memory_order_release);
     return e;
 }
 

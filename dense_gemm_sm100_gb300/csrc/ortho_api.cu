@@ -171,7 +171,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     cudaError_t e = dg::prepare_ortho();
     if (e != cudaSuccess) return cuda_fail(h, e, "preparing the orthogonalisation's kernels");
     const bool split = dtype == GEMM_F32;

@@ -480,7 +480,7 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     int rc = prepare(h);
     if (rc) return rc;
     const int kind = dg::kRaggedMx4;
@@ -524,7 +524,7 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     int rc = prepare(h, true);
     if (rc) return rc;
     const bool few = offsets ? rows <= kFewRowsOfGroup * groups : rows <= kFewRows;
@@ -606,7 +606,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     if ((rc = prepare(h))) return rc;
     const int es = dtype == GEMM_BF16 ? 2 : 4;
     const int kind = dtype == GEMM_BF16 ? dg::kRaggedBf16 : dg::kRaggedTf32;
@@ -665,7 +665,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     if ((rc = prepare(h))) return rc;
     const int es = dtype == GEMM_BF16 ? 2 : 4;
     const int kind = dtype == GEMM_BF16 ? dg::kRaggedBf16 : dg::kRaggedTf32;
@@ -746,7 +746,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     const cudaError_t e = dg::launch_mx4_quantise(layout == GEMM_B_ROW_MAJOR, batch, rows, K, src, ld,
                                                   batch > 1 ? stride : 0, src_dtype == GEMM_BF16,
                                                   static_cast<uint8_t *>(codes), ldq, static_cast<uint8_t *>(scales),
@@ -770,7 +770,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     const cudaError_t e =
         dg::launch_mx4_dequantise(rows, K, static_cast<const uint8_t *>(codes), ldq,
                                   static_cast<const uint8_t *>(scales), lds, dst, ldd, dst_dtype == GEMM_BF16,
@@ -853,7 +853,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     const cudaError_t e = dg::launch_i8_quantise(layout == GEMM_B_ROW_MAJOR, batch, rows, K, src, ld,
                                                  batch > 1 ? stride : 0, src_dtype == GEMM_BF16, codes, ldq, scales,
                                                  h->sm_count, stream);
@@ -878,7 +878,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     const cudaError_t e =
         dg::launch_i8_dequantise(rows, K, codes, ldq, scales, dst, ldd, dst_dtype == GEMM_BF16, h->sm_count, stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "dequantisation launch");

@@ -108,7 +108,7 @@ try {
     int rc = check_route(tokens, experts, k, logits, ld, dtype, bias, groups, top_groups, flags, weights, expert,
                          order, offsets, &why);
     if (rc) return fail(h, rc, why);
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     const int sms = h->max_ctas > 0 ? std::min(h->max_ctas, h->sm_count) : h->sm_count;
     dg::RouteArgs a;
     a.logits = logits;
@@ -156,7 +156,7 @@ try {
         h->last_path = "noop";
         return GEMM_OK;
     }
-    dg::DeviceGuard guard(h->device);
+    dg::DeviceGuard guard(h);
     dg::RouteGradArgs a;
     a.logits = logits;
     a.ld = ld;

@@ -173,9 +173,12 @@ extern "C" {
 typedef struct gemm_ctx *gemm_handle_t;
 
 /*
- * Create a handle bound to CUDA device `device` (which becomes current on the
- * calling thread).  Fails with GEMM_ERR_DEVICE when the device is missing or
- * is not compute capability 10.3 (GB300).  *out is set only on success.
+ * Create a handle bound to CUDA device `device`, in the calling thread's current
+ * context where that is one of this device, else in the device's primary context.
+ * Every call on the handle works in that context, and puts back the one that the
+ * thread had; a thread that had none keeps the handle's.  Fails with
+ * GEMM_ERR_DEVICE when the device is missing or is not compute capability 10.3
+ * (GB300).  *out is set only on success.
  */
 int gemm_create(gemm_handle_t *out, int device);
 
