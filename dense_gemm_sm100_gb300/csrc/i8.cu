@@ -273,12 +273,12 @@ __global__ void __launch_bounds__(quantise_threads(TPR))
 }
 
 // Row-major weights: element (r, k) at src[k * ld + r].  A CTA takes 32 rows of
-// the output: the maxima of its 32 columns, then 128 values of K at a time
-// through shared memory.
+// the output at a time: the maxima of its 32 columns, then 128 values of K at a
+// time through shared memory.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    quantise_turn_kernel(const T *src, long long ld, long long stride, int rows, int K, int8_t *codes, long long ldq,
-                         float *scales)
+    quantise_turn_kernel(const T *src, long long ld, long long stride, int rows, long long all, int K, int8_t *codes,
+                         long long ldq, float *scales)
 {
     constexpr int W = THREADS / 32;
     __shared__ uint32_t part[W][32];
@@ -286,45 +286,47 @@ __global__ void __launch_bounds__(THREADS)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const int blocks = (rows + 31) / 32;
-    const long long b = blockIdx.x / blocks;
-    const int r0 = static_cast<int>(blockIdx.x - b * blocks) * 32, r = r0 + lane;
-    const T *col = src + b * stride + r;
-    uint32_t amax = 0;
-    if (r < rows)
-#pragma unroll 8
-        for (int k = warp; k < K; k += W)
-            amax = max(amax, __float_as_uint(to_f32(col[static_cast<long long>(k) * ld])) & 0x7fffffffu);
-    part[warp][lane] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) amax = max(amax, part[w][lane]);
-    const Coder q(scale_of(amax));
-    const long long first = b * rows + r0;
-    if (warp == 0 && r < rows) scales[first + lane] = q.scale;
+    const int blocks = (rows + 31) / 32;  // of a matrix
     const int out_row = threadIdx.x >> 3, piece = (threadIdx.x & 7) * 16;
-    for (int k0 = 0; k0 < K; k0 += 128) {
-#pragma unroll
-        for (int j = warp * 8; j < 128; j += W * 8) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = r < rows && k0 + j + i < K ? to_f32(col[static_cast<long long>(k0 + j + i) * ld]) : 0.0f;
-            *reinterpret_cast<uint2 *>(&tile[lane][j]) = q(v);
-        }
+    for (long long u = blockIdx.x; u < all; u += gridDim.x) {
+        const long long b = u / blocks;
+        const int r0 = static_cast<int>(u - b * blocks) * 32, r = r0 + lane;
+        const T *col = src + b * stride + r;
+        uint32_t amax = 0;
+        if (r < rows)
+#pragma unroll 8
+            for (int k = warp; k < K; k += W)
+                amax = max(amax, __float_as_uint(to_f32(col[static_cast<long long>(k) * ld])) & 0x7fffffffu);
+        part[warp][lane] = amax;
         __syncthreads();
-        if (r0 + out_row < rows) {
-            int8_t *dst = codes + (first + out_row) * ldq + k0 + piece;
-            const int n = K - k0 - piece;
-            const uint4 v = *reinterpret_cast<const uint4 *>(&tile[out_row][piece]);
-            if (n >= 16) {
-                *reinterpret_cast<uint4 *>(dst) = v;
-            } else {
-                store8(dst, make_uint2(v.x, v.y), n);
-                store8(dst + 8, make_uint2(v.z, v.w), n - 8);
+#pragma unroll
+        for (int w = 0; w < W; ++w) amax = max(amax, part[w][lane]);
+        const Coder q(scale_of(amax));
+        const long long first = b * rows + r0;
+        if (warp == 0 && r < rows) scales[first + lane] = q.scale;
+        for (int k0 = 0; k0 < K; k0 += 128) {
+#pragma unroll
+            for (int j = warp * 8; j < 128; j += W * 8) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = r < rows && k0 + j + i < K ? to_f32(col[static_cast<long long>(k0 + j + i) * ld]) : 0.0f;
+                *reinterpret_cast<uint2 *>(&tile[lane][j]) = q(v);
             }
+            __syncthreads();
+            if (r0 + out_row < rows) {
+                int8_t *dst = codes + (first + out_row) * ldq + k0 + piece;
+                const int n = K - k0 - piece;
+                const uint4 v = *reinterpret_cast<const uint4 *>(&tile[out_row][piece]);
+                if (n >= 16) {
+                    *reinterpret_cast<uint4 *>(dst) = v;
+                } else {
+                    store8(dst, make_uint2(v.x, v.y), n);
+                    store8(dst + 8, make_uint2(v.z, v.w), n - 8);
+                }
+            }
+            __syncthreads();  // tile, and after the last part, is written again
         }
-        __syncthreads();
     }
 }
 
@@ -413,21 +415,21 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-int grid_for(long long units, int per_cta, int per_sm, int sm_count)
+int grid_for(long long units, int per_cta, int per_sm, int sm_count, int max_ctas)
 {
-    return static_cast<int>(std::max(1LL, std::min<long long>((units + per_cta - 1) / per_cta, int64_t{per_sm} * sm_count)));
+    return capped(std::max(1LL, std::min<long long>((units + per_cta - 1) / per_cta, int64_t{per_sm} * sm_count)), max_ctas);
 }
 
 template <typename T, int TPR, int U, int S>
 cudaError_t launch_quantise_form(const void *src, int64_t ld, int64_t stride, int64_t batch, int64_t rows, int64_t K,
-                                 bool vec, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                                 bool vec, int8_t *codes, int64_t ldq, float *scales, int sm_count, int max_ctas,
                                  cudaStream_t stream)
 {
     constexpr int NT = quantise_threads(TPR);
     constexpr size_t SMEM = static_cast<size_t>(S) * U * NT * sizeof(Raw<T>);
     const cudaError_t e = kernel_ready<quantise_kernel<T, TPR, U, S>>(SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(quantise_kernel<T, TPR, U, S>, grid_for(batch * rows, NT / TPR, 2048 / NT, sm_count), NT, SMEM,
+    return launch_pdl(quantise_kernel<T, TPR, U, S>, grid_for(batch * rows, NT / TPR, 2048 / NT, sm_count, max_ctas), NT, SMEM,
                       stream, 1, static_cast<const T *>(src), static_cast<long long>(ld),
                       static_cast<long long>(stride), static_cast<long long>(rows),
                       static_cast<long long>(batch * rows), static_cast<int>(K), vec, codes,
@@ -436,7 +438,8 @@ cudaError_t launch_quantise_form(const void *src, int64_t ld, int64_t stride, in
 
 template <typename T, int TPR, int U>
 cudaError_t launch_quantise(const void *src, int64_t ld, int64_t stride, int64_t batch, int64_t rows, int64_t K,
-                            int8_t *codes, int64_t ldq, float *scales, int sm_count, cudaStream_t stream)
+                            int8_t *codes, int64_t ldq, float *scales, int sm_count, int max_ctas,
+                            cudaStream_t stream)
 {
     const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (ld * sizeof(T)) % 16 == 0 &&
                      (stride * sizeof(T)) % 16 == 0;
@@ -444,25 +447,28 @@ cudaError_t launch_quantise(const void *src, int64_t ld, int64_t stride, int64_t
     constexpr int S = sizeof(T) == 2 ? 4 : 3;
     if (U > 0 && vec && batch * rows > static_cast<int64_t>(quantise_threads(TPR) / TPR) * 2 * sm_count)
         return launch_quantise_form<T, TPR, U, U == 0 ? 0 : S>(src, ld, stride, batch, rows, K, vec, codes, ldq, scales,
-                                                               sm_count, stream);
+                                                               sm_count, max_ctas, stream);
     return launch_quantise_form<T, TPR, U, 0>(src, ld, stride, batch, rows, K, vec, codes, ldq, scales, sm_count,
-                                              stream);
+                                              max_ctas, stream);
 }
 
 template <typename T>
 cudaError_t launch_quantise_for(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
-                                int64_t stride, int8_t *codes, int64_t ldq, float *scales, int sm_count,
+                                int64_t stride, int8_t *codes, int64_t ldq, float *scales, int sm_count, int max_ctas,
                                 cudaStream_t stream)
 {
     if (k_rows) {
-        const int64_t grid = batch * ((rows + 31) / 32);
+        const int64_t all = batch * ((rows + 31) / 32);
         const cudaError_t e = kernel_ready<quantise_turn_kernel<T>>(0);
         if (e != cudaSuccess) return e;
-        return launch_pdl(quantise_turn_kernel<T>, static_cast<int>(grid), THREADS, 0, stream, 1,
+        return launch_pdl(quantise_turn_kernel<T>, capped(all, max_ctas), THREADS, 0, stream, 1,
                           static_cast<const T *>(src), static_cast<long long>(ld), static_cast<long long>(stride),
-                          static_cast<int>(rows), static_cast<int>(K), codes, static_cast<long long>(ldq), scales);
+                          static_cast<int>(rows), static_cast<long long>(all), static_cast<int>(K), codes,
+                          static_cast<long long>(ldq), scales);
     }
-    const auto run = [&](auto f) { return f(src, ld, stride, batch, rows, K, codes, ldq, scales, sm_count, stream); };
+    const auto run = [&](auto f) {
+        return f(src, ld, stride, batch, rows, K, codes, ldq, scales, sm_count, max_ctas, stream);
+    };
     if (K <= 256) return run(launch_quantise<T, 32, 1>);
     if (K <= 1024) return run(launch_quantise<T, 32, 4>);
     if (K <= 2048) return run(launch_quantise<T, 256, 1>);
@@ -476,20 +482,21 @@ cudaError_t launch_quantise_for(bool k_rows, int64_t batch, int64_t rows, int64_
 
 cudaError_t launch_i8_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
                                int64_t stride, bool src_bf16, int8_t *codes, int64_t ldq, float *scales, int sm_count,
-                               cudaStream_t stream)
+                               int max_ctas, cudaStream_t stream)
 {
     return src_bf16 ? launch_quantise_for<__nv_bfloat16>(k_rows, batch, rows, K, src, ld, stride, codes, ldq, scales,
-                                                         sm_count, stream)
+                                                         sm_count, max_ctas, stream)
                     : launch_quantise_for<float>(k_rows, batch, rows, K, src, ld, stride, codes, ldq, scales, sm_count,
-                                                 stream);
+                                                 max_ctas, stream);
 }
 
 cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
-                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, cudaStream_t stream)
+                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, int max_ctas,
+                                 cudaStream_t stream)
 {
     const int es = dst_bf16 ? 2 : 4;
     const bool vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && (ldd * es) % 16 == 0;
-    const int grid = grid_for(rows * ((K + 255) / 256), THREADS / 32, 8, sm_count);
+    const int grid = grid_for(rows * ((K + 255) / 256), THREADS / 32, 8, sm_count, max_ctas);
     cudaError_t e;
     if (dst_bf16) {
         e = kernel_ready<dequantise_kernel<__nv_bfloat16>>(0);
@@ -508,12 +515,12 @@ cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, i
 }
 
 cudaError_t launch_i8_widen(const int8_t *src, int64_t ld, int64_t rows, int64_t K, void *dst, int sm_count,
-                            cudaStream_t stream)
+                            int max_ctas, cudaStream_t stream)
 {
     const int64_t chunks = (K + 512 * WIDEN - 1) / (512 * WIDEN);
     const cudaError_t e = kernel_ready<widen_kernel>(0);
     if (e != cudaSuccess) return e;
-    return launch_pdl(widen_kernel, grid_for(rows * chunks, THREADS / 32, 8, sm_count), THREADS, 0, stream, 1, src,
+    return launch_pdl(widen_kernel, grid_for(rows * chunks, THREADS / 32, 8, sm_count, max_ctas), THREADS, 0, stream, 1, src,
                       static_cast<long long>(ld), static_cast<long long>(rows), static_cast<int>(K),
                       static_cast<__half *>(dst));
 }

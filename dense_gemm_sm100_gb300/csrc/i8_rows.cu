@@ -231,14 +231,14 @@ int64_t padded(int64_t K, int mr)
 }
 
 template <int MR, typename T>
-cudaError_t launch(const RowsParams &p, int sm_count, cudaStream_t stream)
+cudaError_t launch(const RowsParams &p, int sm_count, int max_ctas, cudaStream_t stream)
 {
     constexpr size_t MOST = A_BYTES + MAX_PASSES * sizeof(int2);
     const cudaError_t e = kernel_ready<rows_kernel<MR, T>>(MOST);
     if (e != cudaSuccess) return e;
     constexpr int CH = SUMS / MR;
     const long long units = static_cast<long long>(p.rows) * ((p.N + CH - 1) / CH);  // at most
-    const int grid = static_cast<int>(std::min<long long>((units + WARPS - 1) / WARPS, 2LL * sm_count));
+    const int grid = capped(std::min<long long>((units + WARPS - 1) / WARPS, 2LL * sm_count), max_ctas);
     const size_t smem = static_cast<size_t>(MR) * p.kpad + static_cast<size_t>(p.rows) * sizeof(int2);
     return launch_pdl(rows_kernel<MR, T>, grid, THREADS, smem, stream, 1, p);
 }
@@ -251,7 +251,7 @@ bool i8_rows_fit(int64_t rows, int64_t K, int mr)
 }
 
 cudaError_t launch_i8_rows(const RaggedArgs &r, int mr, const int8_t *a, int64_t lda, const int8_t *b, int64_t ldb,
-                           int sm_count)
+                           int sm_count, int max_ctas)
 {
     RowsParams p;
     p.offsets = reinterpret_cast<const long long *>(r.offsets);
@@ -271,8 +271,10 @@ cudaError_t launch_i8_rows(const RaggedArgs &r, int mr, const int8_t *a, int64_t
     p.ldc = r.ldc;
     p.status = r.status;
     if (mr == 4)
-        return r.out_bf16 ? launch<4, __nv_bfloat16>(p, sm_count, r.stream) : launch<4, float>(p, sm_count, r.stream);
-    return r.out_bf16 ? launch<8, __nv_bfloat16>(p, sm_count, r.stream) : launch<8, float>(p, sm_count, r.stream);
+        return r.out_bf16 ? launch<4, __nv_bfloat16>(p, sm_count, max_ctas, r.stream)
+                          : launch<4, float>(p, sm_count, max_ctas, r.stream);
+    return r.out_bf16 ? launch<8, __nv_bfloat16>(p, sm_count, max_ctas, r.stream)
+                      : launch<8, float>(p, sm_count, max_ctas, r.stream);
 }
 
 }  // namespace dg

@@ -6,8 +6,10 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
+#include <cstdint>
 #include <type_traits>
 
 namespace dg {
@@ -37,6 +39,12 @@ inline cudaError_t kernel_ready(size_t smem)
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e == cudaSuccess && known) ready[dev].store(id + 1, std::memory_order_release);
     return e;
+}
+
+// The grid of a kernel whose CTAs take one unit after another (max_ctas 0: no cap).
+inline int capped(int64_t grid, int max_ctas)
+{
+    return static_cast<int>(max_ctas > 0 ? std::min<int64_t>(grid, max_ctas) : grid);
 }
 
 // cluster: CTAs of a cluster (1: none).

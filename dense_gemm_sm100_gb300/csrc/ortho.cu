@@ -877,16 +877,19 @@ __device__ double squares(const T *base, long long ldg, int r0, int r1, int cols
 
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
-    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, bool vec, double *parts)
+    norm_kernel(const T *g, long long ldg, long long stride, int rows, int cols, int num_parts, int all, bool vec,
+                double *parts)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const long long b = blockIdx.x / num_parts;
-    const int part = static_cast<int>(blockIdx.x - b * num_parts);
     const int per = (rows + num_parts - 1) / num_parts;
-    const int r0 = min(rows, part * per), r1 = min(rows, r0 + per);
-    const double sum = squares(g + b * stride, ldg, r0, r1, cols, vec);
-    if (threadIdx.x == 0) parts[b * num_parts + part] = sum;
+    for (int u = blockIdx.x; u < all; u += gridDim.x) {
+        const long long b = u / num_parts;
+        const int part = static_cast<int>(u - b * num_parts);
+        const int r0 = min(rows, part * per), r1 = min(rows, r0 + per);
+        const double sum = squares(g + b * stride, ldg, r0, r1, cols, vec);
+        if (threadIdx.x == 0) parts[u] = sum;
+    }
 }
 
 // The sum of a matrix's parts, by a warp.
@@ -899,81 +902,85 @@ __device__ double sum_of_parts(const double *parts, int num_parts)
     return sum;
 }
 
-__global__ void factors_kernel(const double *parts, int num_parts, float eps, float *factors)
+__global__ void factors_kernel(const double *parts, int num_parts, int batch, float eps, float *factors)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const long long b = blockIdx.x;
-    const double sum = sum_of_parts(parts + b * num_parts, num_parts);
-    if (threadIdx.x == 0) write_factors(sum, eps, factors + b * FACTORS);
+    for (long long b = blockIdx.x; b < batch; b += gridDim.x) {
+        const double sum = sum_of_parts(parts + b * num_parts, num_parts);
+        if (threadIdx.x == 0) write_factors(sum, eps, factors + b * FACTORS);
+    }
 }
 
 // X in two FP16 numbers from G, turned where rows > cols.  A CTA takes 64 x 64
-// elements.  With num_parts > 0 every CTA also makes the matrix's factors from the
+// elements at a time.  With num_parts > 0 every CTA also makes the matrix's factors from the
 // sums of the norm's parts (one part: of the matrix itself), for a launch less.
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
     start_kernel(const T *g, long long ldg, long long stride, bool vec, int turned, int m, int n, int ldn, int tiles_j,
-                 int tiles, __half *x0, __half *x1, const double *parts, int num_parts, float eps, float *factors)
+                 int tiles, int all, __half *x0, __half *x1, const double *parts, int num_parts, float eps, float *factors)
 {
     __shared__ float tile[64][65], f[FACTORS];
     griddep_wait();
     griddep_launch_dependents();
-    const long long b = blockIdx.x / tiles;
-    const int t = static_cast<int>(blockIdx.x - b * tiles);
-    const int i0 = t / tiles_j * 64, j0 = t % tiles_j * 64;
-    constexpr int N = 16 / sizeof(T);
-    const T *base = g + b * stride;
-    // tile[a][c]: row a of G's part (64 x 64), turned on the way out
-    const int ga = turned ? j0 : i0, gc = turned ? i0 : j0, rows = turned ? n : m, cols = turned ? m : n;
-    if (vec) {
+    for (int u = blockIdx.x; u < all; u += gridDim.x) {
+        if (u != static_cast<int>(blockIdx.x)) __syncthreads();  // the shared arrays have been read
+        const long long b = u / tiles;
+        const int t = static_cast<int>(u - b * tiles);
+        const int i0 = t / tiles_j * 64, j0 = t % tiles_j * 64;
+        constexpr int N = 16 / sizeof(T);
+        const T *base = g + b * stride;
+        // tile[a][c]: row a of G's part (64 x 64), turned on the way out
+        const int ga = turned ? j0 : i0, gc = turned ? i0 : j0, rows = turned ? n : m, cols = turned ? m : n;
+        if (vec) {
 #pragma unroll
-        for (int k = threadIdx.x; k < 64 * 64 / N; k += NORM_THREADS) {
-            const int a = k / (64 / N), c = k % (64 / N) * N;
-            float x[N];
-            if (ga + a < rows && gc + c + N <= cols) {
-                load_vec(base + (ga + a) * ldg + gc + c, x);
-            } else {
+            for (int k = threadIdx.x; k < 64 * 64 / N; k += NORM_THREADS) {
+                const int a = k / (64 / N), c = k % (64 / N) * N;
+                float x[N];
+                if (ga + a < rows && gc + c + N <= cols) {
+                    load_vec(base + (ga + a) * ldg + gc + c, x);
+                } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    x[i] = ga + a < rows && gc + c + i < cols ? to_f32(base[(ga + a) * ldg + gc + c + i]) : 0.0f;
+                    for (int i = 0; i < N; ++i)
+                        x[i] = ga + a < rows && gc + c + i < cols ? to_f32(base[(ga + a) * ldg + gc + c + i]) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) tile[a][c + i] = x[i];
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) tile[a][c + i] = x[i];
-        }
-    } else {
+        } else {
 #pragma unroll 4
-        for (int k = threadIdx.x; k < 64 * 64; k += NORM_THREADS) {
-            const int a = k >> 6, c = k & 63;
-            tile[a][c] = ga + a < rows && gc + c < cols ? to_f32(base[(ga + a) * ldg + gc + c]) : 0.0f;
+            for (int k = threadIdx.x; k < 64 * 64; k += NORM_THREADS) {
+                const int a = k >> 6, c = k & 63;
+                tile[a][c] = ga + a < rows && gc + c < cols ? to_f32(base[(ga + a) * ldg + gc + c]) : 0.0f;
+            }
         }
-    }
-    if (num_parts > 0) {
-        double sum = 0.0;
-        if (num_parts == 1)
-            sum = squares(base, ldg, 0, rows, cols, vec);
-        else if (threadIdx.x < 32)
-            sum = sum_of_parts(parts + b * num_parts, num_parts);
-        if (threadIdx.x == 0) {
-            write_factors(sum, eps, f);
-            if (t == 0)
-                for (int k = 0; k < FACTORS; ++k) factors[b * FACTORS + k] = f[k];
+        if (num_parts > 0) {
+            double sum = 0.0;
+            if (num_parts == 1)
+                sum = squares(base, ldg, 0, rows, cols, vec);
+            else if (threadIdx.x < 32)
+                sum = sum_of_parts(parts + b * num_parts, num_parts);
+            if (threadIdx.x == 0) {
+                write_factors(sum, eps, f);
+                if (t == 0)
+                    for (int k = 0; k < FACTORS; ++k) factors[b * FACTORS + k] = f[k];
+            }
+        } else if (threadIdx.x < FACTORS) {
+            f[threadIdx.x] = factors[b * FACTORS + threadIdx.x];
         }
-    } else if (threadIdx.x < FACTORS) {
-        f[threadIdx.x] = factors[b * FACTORS + threadIdx.x];
-    }
-    __syncthreads();
-    const float s0 = f[kFactorUp0], s1 = f[kFactorUp1];
+        __syncthreads();
+        const float s0 = f[kFactorUp0], s1 = f[kFactorUp1];
 #pragma unroll
-    for (int k = threadIdx.x; k < 64 * 8; k += NORM_THREADS) {
-        const int r = k >> 3, c = (k & 7) * 8;  // 16 bytes of X
-        if (i0 + r >= m) continue;
-        float v[8], rest[8];
+        for (int k = threadIdx.x; k < 64 * 8; k += NORM_THREADS) {
+            const int r = k >> 3, c = (k & 7) * 8;  // 16 bytes of X
+            if (i0 + r >= m) continue;
+            float v[8], rest[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (turned ? tile[c + i][r] : tile[r][c + i]) * s0 * s1;
-        const long long at = (b * m + i0 + r) * ldn + j0 + c;
-        *reinterpret_cast<uint4 *>(x0 + at) = round8(v, rest);
-        if (x1) *reinterpret_cast<uint4 *>(x1 + at) = round8(rest);
+            for (int i = 0; i < 8; ++i) v[i] = (turned ? tile[c + i][r] : tile[r][c + i]) * s0 * s1;
+            const long long at = (b * m + i0 + r) * ldn + j0 + c;
+            *reinterpret_cast<uint4 *>(x0 + at) = round8(v, rest);
+            if (x1) *reinterpret_cast<uint4 *>(x1 + at) = round8(rest);
+        }
     }
 }
 
@@ -1065,8 +1072,8 @@ cudaError_t prepare_ortho()
     return e;
 }
 
-cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, cudaStream_t stream,
-                               int *launches)
+cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, int max_ctas,
+                               cudaStream_t stream, int *launches)
 {
     // one part below 8192 elements: the start sums it up, a launch less
     const int64_t size = int64_t{u.rows} * u.cols;
@@ -1077,30 +1084,32 @@ cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bo
     const float *gf = static_cast<const float *>(u.g);
     cudaError_t e = cudaSuccess;
     if (parts > 1) {
-        e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, parts * w.batch, NORM_THREADS, 0, stream, 1, gb, u.ldg,
-                                u.stride_g, u.rows, u.cols, parts, vec, w.parts)
-                   : launch_pdl(norm_kernel<float>, parts * w.batch, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g,
-                                u.rows, u.cols, parts, vec, w.parts);
+        const int all = parts * w.batch, grid = capped(all, max_ctas);
+        e = u.bf16 ? launch_pdl(norm_kernel<__nv_bfloat16>, grid, NORM_THREADS, 0, stream, 1, gb, u.ldg, u.stride_g,
+                                u.rows, u.cols, parts, all, vec, w.parts)
+                   : launch_pdl(norm_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, u.rows,
+                                u.cols, parts, all, vec, w.parts);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
     const int tiles_j = (w.n + 63) / 64, tiles = (w.m + 63) / 64 * tiles_j;
-    const int grid = tiles * w.batch, turned = u.rows > u.cols;
+    const int all = tiles * w.batch, grid = capped(all, max_ctas), turned = u.rows > u.cols;
     __half *x0 = reinterpret_cast<__half *>(w.x[0][0]), *x1 = split ? reinterpret_cast<__half *>(w.x[0][1]) : nullptr;
     const double *sums = w.parts;
     // Factors made by the start's CTAs save a launch of 2 us, and cost 22 us where
     // there are 32768 of them (16 matrices of 4096 x 2048).
     int start_parts = parts;
-    if (parts > 1 && grid > 1024) {
-        e = launch_pdl(factors_kernel, w.batch, 32, 0, stream, 1, sums, parts, u.eps, w.factors);
+    if (parts > 1 && all > 1024) {
+        e = launch_pdl(factors_kernel, capped(w.batch, max_ctas), 32, 0, stream, 1, sums, parts, w.batch, u.eps,
+                       w.factors);
         if (e != cudaSuccess) return e;
         ++*launches;
         start_parts = 0;
     }
     e = u.bf16 ? launch_pdl(start_kernel<__nv_bfloat16>, grid, NORM_THREADS, 0, stream, 1, gb, u.ldg, u.stride_g,
-                            vec, turned, w.m, w.n, w.ldn, tiles_j, tiles, x0, x1, sums, start_parts, u.eps, w.factors)
+                            vec, turned, w.m, w.n, w.ldn, tiles_j, tiles, all, x0, x1, sums, start_parts, u.eps, w.factors)
                : launch_pdl(start_kernel<float>, grid, NORM_THREADS, 0, stream, 1, gf, u.ldg, u.stride_g, vec, turned, w.m,
-                            w.n, w.ldn, tiles_j, tiles, x0, x1, sums, start_parts, u.eps, w.factors);
+                            w.n, w.ldn, tiles_j, tiles, all, x0, x1, sums, start_parts, u.eps, w.factors);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

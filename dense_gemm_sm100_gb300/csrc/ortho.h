@@ -39,8 +39,8 @@ struct OrthoMatrices {
 
 cudaError_t prepare_ortho();  // kernel attributes on the current device
 // X = G / (|G| + eps), up to the factors; *launches counts kernels.
-cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, cudaStream_t stream,
-                               int *launches);
+cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bool split, int max_ctas,
+                               cudaStream_t stream, int *launches);
 
 enum OrthoStep : int { kOrthoA = 0, kOrthoB = 1, kOrthoX = 2 };
 

@@ -84,7 +84,7 @@ int run_group(gemm_ctx *h, const dg::OrthoBuffers &w, const dg::OrthoMatrices &u
     const bool split = !u.bf16;
     const int sms = h->max_ctas > 0 ? std::min(h->max_ctas, h->sm_count) : h->sm_count;
     int launches = 0;
-    cudaError_t e = dg::launch_ortho_start(w, u, split, stream, &launches);
+    cudaError_t e = dg::launch_ortho_start(w, u, split, h->max_ctas, stream, &launches);
     h->launches += launches;
     if (e != cudaSuccess) return cuda_fail(h, e, "orthogonalisation launch");
     dg::OrthoProduct r;

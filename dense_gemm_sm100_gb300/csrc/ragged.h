@@ -89,18 +89,19 @@ cudaError_t launch_mx4_quantise(bool k_rows, int64_t batch, int64_t rows, int64_
 // 8-bit integers (i8.cu): batch * rows output rows of codes, one scale a row.
 cudaError_t launch_i8_quantise(bool k_rows, int64_t batch, int64_t rows, int64_t K, const void *src, int64_t ld,
                                int64_t stride, bool src_bf16, int8_t *codes, int64_t ldq, float *scales, int sm_count,
-                               cudaStream_t stream);
+                               int max_ctas, cudaStream_t stream);
 cudaError_t launch_i8_dequantise(int64_t rows, int64_t K, const int8_t *codes, int64_t ldq, const float *scales,
-                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, cudaStream_t stream);
+                                 void *dst, int64_t ldd, bool dst_bf16, int sm_count, int max_ctas,
+                                 cudaStream_t stream);
 // Rows of codes as FP16, at a pitch of K rounded up to 16.
 cudaError_t launch_i8_widen(const int8_t *src, int64_t ld, int64_t rows, int64_t K, void *dst, int sm_count,
-                            cudaStream_t stream);
+                            int max_ctas, cudaStream_t stream);
 // Products of few rows a group (i8_rows.cu), mr (4 or 8) of them at a time: whether
 // they fit the kernel's shared memory and integers, and the launch (B's rows are
 // P's, A's Q's).
 bool i8_rows_fit(int64_t rows, int64_t K, int mr);
 cudaError_t launch_i8_rows(const RaggedArgs &a, int mr, const int8_t *codes_a, int64_t lda, const int8_t *codes_b,
-                           int64_t ldb, int sm_count);
+                           int64_t ldb, int sm_count, int max_ctas);
 // Rows of a tile at most, by the type of C.
 constexpr int kRaggedI8Rows = 192, kRaggedI8RowsF32 = 128;
 cudaError_t launch_mx4_dequantise(int64_t rows, int64_t K, const uint8_t *codes, int64_t ldq, const uint8_t *scales,

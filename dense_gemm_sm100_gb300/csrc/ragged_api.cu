@@ -533,7 +533,7 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
         dg::RaggedArgs a = common_args(h, offsets, groups, rows, N, 0, K, C, ldc, c_dtype, stream);
         a.row_scale_p = bs;
         a.row_scale_q = as;
-        const cudaError_t e = dg::launch_i8_rows(a, mr, ac, aq, bc, bq, usable_sms(h));
+        const cudaError_t e = dg::launch_i8_rows(a, mr, ac, aq, bc, bq, h->sm_count, h->max_ctas);
         if (e != cudaSuccess) return cuda_fail(h, e, "8-bit product launch");
         ++h->launches;
         h->last_path = offsets ? "grouped_i8_rows" : "i8_rows";
@@ -556,7 +556,7 @@ int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, cons
     if (K > 0) {
         const int64_t ld = round_up(K, 16);
         if ((rc = ws.acquire(static_cast<size_t>(rows * ld * 2)))) return rc;
-        const cudaError_t e = dg::launch_i8_widen(ac, aq, rows, K, h->ws, h->sm_count, stream);
+        const cudaError_t e = dg::launch_i8_widen(ac, aq, rows, K, h->ws, h->sm_count, h->max_ctas, stream);
         if (e != cudaSuccess) return cuda_fail(h, e, "conversion launch");
         ++h->launches;
         rc = encode_k_major(h, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, bc, K, N, bq, groups, N * bq, 128, dg::kRaggedP,
@@ -856,7 +856,7 @@ try {
     dg::DeviceGuard guard(h);
     const cudaError_t e = dg::launch_i8_quantise(layout == GEMM_B_ROW_MAJOR, batch, rows, K, src, ld,
                                                  batch > 1 ? stride : 0, src_dtype == GEMM_BF16, codes, ldq, scales,
-                                                 h->sm_count, stream);
+                                                 h->sm_count, h->max_ctas, stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "quantisation launch");
     ++h->launches;
     h->last_path = layout == GEMM_B_ROW_MAJOR ? "i8_quantise_rowB" : "i8_quantise_colB";
@@ -880,7 +880,8 @@ try {
     }
     dg::DeviceGuard guard(h);
     const cudaError_t e =
-        dg::launch_i8_dequantise(rows, K, codes, ldq, scales, dst, ldd, dst_dtype == GEMM_BF16, h->sm_count, stream);
+        dg::launch_i8_dequantise(rows, K, codes, ldq, scales, dst, ldd, dst_dtype == GEMM_BF16, h->sm_count,
+                                 h->max_ctas, stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "dequantisation launch");
     ++h->launches;
     h->last_path = "i8_dequantise";

@@ -1129,12 +1129,12 @@ __global__ void __launch_bounds__(GRAD_THREADS) route_grad_kernel(const GradPara
 }
 
 template <typename T>
-cudaError_t launch_grad(const RouteGradArgs &a, const GradParams &p, int sm_count)
+cudaError_t launch_grad(const RouteGradArgs &a, const GradParams &p, int sm_count, int max_ctas)
 {
     const bool vec = p.experts % 4 == 0 && p.ldd % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % (4 * sizeof(T)) == 0;
     const int warps = GRAD_THREADS / 32;
     const size_t smem = static_cast<size_t>(warps) * ((p.experts + 3) & ~3) * 4;
-    const int grid = std::min((p.tokens + warps - 1) / warps, 8 * sm_count);
+    const int grid = capped(std::min((p.tokens + warps - 1) / warps, 8 * sm_count), max_ctas);
     const cudaError_t e = vec ? kernel_ready<route_grad_kernel<T, 4>>(0) : kernel_ready<route_grad_kernel<T, 1>>(0);
     if (e != cudaSuccess) return e;
     return vec ? launch_pdl(route_grad_kernel<T, 4>, grid, GRAD_THREADS, smem, a.stream, 1, p)
@@ -1190,7 +1190,7 @@ cudaError_t launch_route(const RouteArgs &a, int sm_count, int *launches)
     return a.bf16 ? launch_for<__nv_bfloat16>(p, a.stream, launches) : launch_for<float>(p, a.stream, launches);
 }
 
-cudaError_t launch_route_grad(const RouteGradArgs &a, int sm_count)
+cudaError_t launch_route_grad(const RouteGradArgs &a, int sm_count, int max_ctas)
 {
     GradParams p;
     p.logits = a.logits;
@@ -1205,7 +1205,8 @@ cudaError_t launch_route_grad(const RouteGradArgs &a, int sm_count)
     p.scale = a.scale;
     p.dlogits = a.dlogits;
     p.ldd = a.ldd;
-    return a.bf16 ? launch_grad<__nv_bfloat16>(a, p, sm_count) : launch_grad<float>(a, p, sm_count);
+    return a.bf16 ? launch_grad<__nv_bfloat16>(a, p, sm_count, max_ctas)
+                  : launch_grad<float>(a, p, sm_count, max_ctas);
 }
 
 }  // namespace dg

@@ -42,6 +42,6 @@ struct RouteGradArgs {
     long long ldd = 0;
     cudaStream_t stream = nullptr;
 };
-cudaError_t launch_route_grad(const RouteGradArgs &a, int sm_count);
+cudaError_t launch_route_grad(const RouteGradArgs &a, int sm_count, int max_ctas);
 
 }  // namespace dg

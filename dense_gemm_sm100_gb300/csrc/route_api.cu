@@ -172,7 +172,7 @@ try {
     a.dlogits = dlogits;
     a.ldd = ldd;
     a.stream = stream;
-    const cudaError_t e = dg::launch_route_grad(a, h->sm_count);
+    const cudaError_t e = dg::launch_route_grad(a, h->sm_count, h->max_ctas);
     if (e != cudaSuccess) return cuda_fail(h, e, "router gradient launch");
     ++h->launches;
     h->last_path = "route_grad";

@@ -98,7 +98,10 @@ extern "C" {
 #define GEMM_OPT_WAIT_TIMEOUT_NS 2 /* limit of every in-kernel wait, nanoseconds (default 4e9) */
 #define GEMM_OPT_SIMT_GROUP_M 3   /* tile-order group height in tiles for the FP32 kernel */
 #define GEMM_OPT_TC_GROUP_M 4     /* tile-order group height in tiles for the tensor-core kernel */
-#define GEMM_OPT_MAX_CTAS 5       /* cap on persistent CTAs (0 = SMs x resident CTAs per SM) */
+/* Cap on persistent CTAs (0 = SMs x resident CTAs per SM), and on those of every
+ * launch of the router, the 8-bit operators and the orthogonalised update; kernels
+ * that re-pack operands and the 4-bit conversions take what they need. */
+#define GEMM_OPT_MAX_CTAS 5
 /* FP32 tile configuration: 0 = chosen per shape (least estimated time), else
  * 1..8 = 128x128, 128x128 scalar FMA, 64x128, 64x64, 128x256 (8x16 per
  * thread), 192x128 (12 consumer warps, the usual row-major choice), 128x128
