@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 
 #include "../../include/gemm_route.h"
@@ -228,6 +229,14 @@ __device__ __forceinline__ float score_bound(const RouteParams &p, float most, f
     return (most + bias_max) * (p.sigmoid ? 1e-6f : 4e-6f) + 4e-38f;
 }
 
+// A group's score from its two best (minus infinity: none).  Biases of the type's
+// lowest value exclude nothing, so that their sum stays above minus infinity; what
+// ends there as one value is near, and told apart in FP64.
+__device__ __forceinline__ float group_score(float a, float b)
+{
+    return b == -INFINITY ? a : fmaxf(a + b, -FLT_MAX);
+}
+
 // Routes one token with one warp, however close its values are.
 template <int V, typename T>
 __device__ __noinline__ void route_slowly(const RouteParams &p, int t, float bias_max, int *count, int lane)
@@ -286,7 +295,7 @@ __device__ __noinline__ void route_slowly(const RouteParams &p, int t, float bia
                         a = fmaxf(a, x[j]);
                     }
                 warp_top2(a, b);
-                if (lane == g) score = b == -INFINITY ? a : a + b;
+                if (lane == g) score = group_score(a, b);
             }
             uint32_t gkey[1] = {lane < p.groups ? key_of(score) : 0u}, mine;
             int open;
@@ -577,7 +586,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams &p, const Layout 
                 b = fmaxf(fminf(a, a2), fmaxf(b, b2));
                 a = fmaxf(a, a2);
             }
-            const float score = b == -INFINITY ? a : a + b;
+            const float score = group_score(a, b);
             int rank = 0;
             bool near = false;
             for (int g = 0; g < p.groups; ++g) {

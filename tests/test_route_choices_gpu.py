@@ -157,3 +157,23 @@ def test_close_sums_of_different_rows(gm, h, scoring, draw):
         w, e = definition(x, k, scoring, bias, groups, top)
         assert torch.equal(r.expert.cpu(), e)
         weights_near(r, w, x)
+
+
+@pytest.mark.parametrize("low", [-3.4028234663852886e38, -1e38, -1e9])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k", [(8, 4, 4, 8), (8, 4, 2, 4), (64, 8, 6, 8), (96, 8, 8, 31), (640, 8, 3, 9),
+                                           (12, 1, 1, 8)])
+def test_biases_of_the_lowest_value(gm, h, E, groups, top, k, scoring, low):
+    """A finite bias, the type's lowest one too, ranks last and excludes nothing: sums
+    of a group's two best may leave FP32."""
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn((40, E), generator=gen)
+    x[20:, ::3] = -math.inf
+    for masked in (torch.arange(E) % (E // groups) < E, torch.arange(E) >= E // 2,
+                   torch.rand(E, generator=gen) < 0.8):
+        bias = torch.where(masked, low, 0.1 * torch.randn(E, generator=gen))
+        bias[E // 3] = low / 2
+        r = routed(gm, h, x, k, scoring, bias=bias, groups=groups, top_groups=top)
+        w, e = definition(x, k, scoring, bias, groups, top)
+        assert torch.equal(r.expert.cpu(), e)
+        weights_near(r, w, x)
