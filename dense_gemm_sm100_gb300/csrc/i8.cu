@@ -171,8 +171,9 @@ __host__ __device__ constexpr int quantise_threads(int tpr) { return tpr > THREA
 // the row is read again for the codes).  Few pieces a thread: eight left so few
 // warps that 8192 x 14336 took 270 us.  S > 0 (rows on 16-byte boundaries): a
 // thread's pieces of the next S - 1 rows are on their way into shared memory while
-// it works on one, each thread's own, so that no barrier comes into it.  Memory sets
-// the time then.
+// it works on one, each thread's own, so that no barrier comes into it.  The issue
+// of instructions is 74 % used then, memory 36 to 43 % (8192 x 4096 and 12001 x 4096
+// BF16: 25 and 34 us).
 template <typename T, int TPR, int U, int S>
 __global__ void __launch_bounds__(quantise_threads(TPR))
     quantise_kernel(const T *src, long long ld, long long stride, long long rows, long long all, int K, bool vec,

@@ -5,8 +5,9 @@
 //
 // A pass takes up to MR rows of one group; the units of work are CH neighbouring
 // rows of B in a pass, shared out evenly over the CTAs, so that a group of many rows
-// (all 256 rows in one of 128 groups: 16 us) is spread as well as many groups of
-// one (37 us).  More passes over a group read B out of the L2 cache.
+// (all 256 rows in one of 128 groups of 768 x 2048, in the L2 cache: 16 us) is spread
+// as well as many groups of one (37 us).  More passes over a group read B out of the
+// L2 cache, four rows of A at a time: that is the worst case, see kFewRowsOfGroup.
 //
 // A warp takes a unit at a time, 16 bytes of each row a lane and step; AHEAD loads
 // of a lane, two to four steps, are under way while it works on one, across the

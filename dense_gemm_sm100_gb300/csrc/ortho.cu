@@ -913,8 +913,9 @@ __global__ void factors_kernel(const double *parts, int num_parts, int batch, fl
 }
 
 // X in two FP16 numbers from G, turned where rows > cols.  A CTA takes 64 x 64
-// elements at a time.  With num_parts > 0 every CTA also makes the matrix's factors from the
-// sums of the norm's parts (one part: of the matrix itself), for a launch less.
+// elements at a time.  With num_parts > 0 every CTA also makes the matrix's factors
+// from the sums of the norm's parts (one part: of the matrix itself), for a launch
+// less.
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
     start_kernel(const T *g, long long ldg, long long stride, bool vec, int turned, int m, int n, int ldn, int tiles_j,
@@ -1096,8 +1097,11 @@ cudaError_t launch_ortho_start(const OrthoBuffers &w, const OrthoMatrices &u, bo
     const int all = tiles * w.batch, grid = capped(all, max_ctas), turned = u.rows > u.cols;
     __half *x0 = reinterpret_cast<__half *>(w.x[0][0]), *x1 = split ? reinterpret_cast<__half *>(w.x[0][1]) : nullptr;
     const double *sums = w.parts;
-    // Factors made by the start's CTAs save a launch of 2 us, and cost 22 us where
-    // there are 32768 of them (16 matrices of 4096 x 2048).
+    // Factors made by the start's CTAs save a launch of 2 us, but all of them make
+    // them.  One step, us, with a launch of their own / in the start: 1152 CTAs (2 of
+    // 1536 x 1536) 67.8 / 69.8, 1872 (13 of 520 x 1020) 97.7 / 97.5, 2048 95.0 / 97.4,
+    // 4096 141.6 / 145.7, 8192 235 / 244, 32768 (16 of 2048 x 4096) 794 to 812 / 799 to
+    // 802.
     int start_parts = parts;
     if (parts > 1 && all > 1024) {
         e = launch_pdl(factors_kernel, capped(w.batch, max_ctas), 32, 0, stream, 1, sums, parts, w.batch, u.eps,

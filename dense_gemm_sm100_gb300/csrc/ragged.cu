@@ -1272,7 +1272,8 @@ RaggedTile ragged_pick_tile(int kind, bool ragged_k, int64_t rows, int groups, i
                 const double tiles_q = ragged_k     ? double(groups) * ((Q + bn - 1) / bn)
                                        : busy > 1.5 ? busy * std::max(1.0, per_group / bn + 0.5)
                                                     : double((rows + bn - 1) / bn);
-                const int64_t slice = (kt + split - 1) / split;  // of 8-bit stages an even number
+                // shares are even (tile_at), which counts where they are few stages
+                const int64_t slice = (kt + split - 1) / split;
                 const double tile = static_cast<double>(kind == kRaggedI8 && split > 1 ? (slice + 1) & ~1 : slice) * stage +
                                     (kind == kRaggedMx4 && ctas > 1 ? 3000 : 0);
                 const double epi = 600 + bn * 12.0;

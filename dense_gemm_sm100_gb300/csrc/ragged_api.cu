@@ -508,12 +508,18 @@ int run_mx4(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, con
     return GEMM_OK;
 }
 
-// Rows up to which integer dot products (i8_rows.cu) are faster than the tensor
-// cores.  One product, us, 4 / 8 rows against the tensor cores' 8: 2048 x 2048
+// Rows up to which integer dot products (i8_rows.cu) are taken, whose sums are exact,
+// and which are the faster ones for most sizes.  One product, us, 4 / 8 rows against the tensor cores' 8: 2048 x 2048
 // 4.7 / 5.0 and 9, 14336 x 4096 14.7 / 17 and 19, 28672 x 8192 43 / 52 and 60,
 // 8192 x 8192 17.7 / 24 and 21.  Groups of uneven sizes, 0.5 / 2 / 4 rows each on
 // average: 128 of 768 x 2048 18 / 34 / 44 and 21 / 41 / 42, 8 of 14336 x 4096 40 /
 // 61 / 109 and 51 / 72 / 85; all rows in one of the 128 groups 7 / 16 / 27 and 13.
+// Where they lose (operands from memory, against the best tile): long rows, 8 of
+// 8192 x 8192 33 and 29, 8 of 1024 x 12288 25 and 19, 8 of 8192 x 12288 46 and 35; and
+// two rows a group on average that are all in one group, which is read once for
+// every four: 256, 512, 1024, 1536 rows of 2048 x 2048 40, 68, 124, 181 and 19, 21,
+// 23, 31.  Rows spread evenly over those groups: 107, 183, 331, 480 and 113, 201,
+// 388, 576; unevenly, as a router does: 87, 169, 294, 433 and 87, 167, 300, 451.
 constexpr int64_t kFewRows = 8, kFewRowsOfGroup = 2;
 
 int run_i8(gemm_ctx *h, int64_t groups, int64_t rows, int64_t N, int64_t K, const int64_t *offsets, const int8_t *ac,

@@ -10,9 +10,10 @@
 // logits fit their key whole; of FP32 values it holds 23 bits, and the chosen are
 // put in order by their full values afterwards.  (One pick after another by
 // warp-wide maxima took 780 instructions a token of 128 experts and 2300 of 256 in
-// groups; 200 and 900 now.)  The issue of instructions, at 45 to 50 % of its rate
-// with the 32 warps an SM that 64 registers leave, sets the time, not memory (8 to
-// 10 % of its rate): 16384 tokens of 256 experts 23 us, 32768 of 128 11 us, both
+// groups; 194 and 847 now.)  Neither memory (8 to 10 % of its rate) nor the issue of
+// instructions (47 to 52 %) is used up: with the 32 warps an SM that 64 registers
+// leave, the latency of loads and exchanges and the slowest warp before a CTA's
+// barrier set the time: 16384 tokens of 256 experts 23 us, 32768 of 128 11 us, both
 // without the sorting by expert (6 us).
 // What the keys, or FP32 itself, leave open (a key equal in its 23 bits to the last
 // choice's, or a sum with a bias nearer than a bound on the rounding of the scores:
@@ -20,7 +21,10 @@
 // among the chosen, one a lane, are ranked by their values, in FP64 where FP32
 // cannot tell two apart.  Sums of groups that are as near are taken again in FP64;
 // softmax scores that near, more choices and more experts take route_slowly, a warp
-// a token.
+// a token: 16384 tokens with 9 choices of 128 experts 39 us (8 choices 15), with 10
+// of 512 45 us, with 8 of 256 by softmax and a bias 58 us (by sigmoid 28).  The
+// bound on the rounding goes by the largest finite bias: with one of -1e9 every
+// sum is near another, and those tokens take 0.4 to 1.1 ms (minus infinity: 30 us).
 //
 // Sorting by expert is a counting sort, stable and without atomics whose order
 // would matter: CTA c routes a run of tokens and counts its choices by expert;

@@ -24,7 +24,9 @@
  * gemm_i8_run          C[i*ldc + j] = (sum_k a(i, k) * b(j, k)) * sa[i] * sb[j],
  *                      i < M, j < N: both operands hold K values a row (B the
  *                      channels of a column-major weight); all 256 codes may
- *                      occur.  The sum of the codes' products is exact while
+ *                      occur.  The sum is multiplied by sa[i], the product by
+ *                      sb[j], each rounded to FP32 (both have to lie in its
+ *                      range).  The sum of the codes' products is exact while
  *                      it fits 24 bits.  Beyond that it is a 32-bit integer,
  *                      rounded once, where M is at most 4 (8) and K at most
  *                      24576 (12288); else an FP32 result is the

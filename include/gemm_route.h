@@ -24,7 +24,9 @@
  *                  weights[t*k + i] and expert[t*k + i] hold choice i.  Sums
  *                  with a bias, and of groups, that FP32 cannot tell apart are
  *                  decided in 64 bits.  An expert whose logit (or bias) is
- *                  minus infinity is no choice: where fewer than k are left
+ *                  minus infinity is no choice (a finite bias, however low,
+ *                  excludes nothing, and one far above the scores' range makes
+ *                  every sum a close one): where fewer than k are left
  *                  the last choices are expert -1 with weight 0.  A row of
  *                  padding is a row of minus infinities.  A row that holds a
  *                  NaN (for softmax: or plus infinity), or meets a bias
